@@ -1,0 +1,174 @@
+// attend.cuh -- the work split and the joining of partial results that both
+// attention kernels (attend_simt.cu, attend_tc.cu) share.
+//
+// Rows: the G query heads of a KV head stand side by side, row r of a list =
+// token r / G, query head r % G of the group, so every key tile is read once
+// for all of them.  A unit is (list, block of unit_rows rows); its cost is
+// its number of steps over the keys its last row sees (one at least, so that
+// somebody writes the zeros of a row that sees none).  The flat sequence of all
+// units' steps is cut into equal runs, one per CTA: lists of any lengths keep
+// every SM busy to the end, and a CTA shares at most its first and its last
+// unit with others.  For those it leaves rows' (max, sum, unnormalised output)
+// in a slot of its own; the CTA that finishes last adds the unit's slots up in
+// CTA order, so the result does not depend on the order of finishing.
+#pragma once
+
+#include <climits>
+
+#include "cache.cuh"
+
+namespace kvc {
+
+struct AttendParams {
+    int n_seqs, n_q_heads, n_kv_heads, group, dim;
+    int n_pages, max_pages, shift;
+    int64_t n_tokens;
+    int max_new;
+    int unit_rows;       // rows of a unit
+    int blocks;          // units per list
+    int64_t n_units;
+    int step_keys;       // keys per step
+    int slot_rows;       // row capacity of a slot
+    int64_t q_stride;
+    const void *q, *k_pool, *v_pool;
+    const int32_t *q_start, *table, *len;
+    void *out;
+    float *lse;
+    float scale_log2;    // scale * log2(e)
+    uint32_t *status;
+    uint32_t *arrived;   // [grid], zero between calls
+    float2 *stat;        // [2 grid][slot_rows] (max in log2 units, sum)
+    float *part;         // [2 grid][slot_rows][dim]
+};
+
+struct AttendUnit {
+    int list, b, h;
+    int q0, n;        // the sequence's first token and number of tokens
+    int row0, rows;   // this unit's rows among the list's n * group
+    int len;          // the list's cached rows
+    int hi;           // cached rows that the unit's last row sees
+    int steps;        // 0: no such unit
+};
+
+__device__ __forceinline__ AttendUnit attend_unit(const AttendParams &p, int64_t u) {
+    AttendUnit a;
+    a.list = (int)(u / p.blocks);
+    const int block = (int)(u - (int64_t)a.list * p.blocks);
+    a.b = a.list / p.n_kv_heads;
+    a.h = a.list - a.b * p.n_kv_heads;
+    int q0 = p.q_start[a.b], q1 = p.q_start[a.b + 1];
+    a.len = p.len[a.list];
+    const int64_t most = (int64_t)p.max_pages << p.shift;
+    if (q0 < 0 || q1 < q0 || q1 > p.n_tokens || q1 - q0 > p.max_new || a.len < 0 || a.len > most) {
+        set_status(p.status, KVC_DEV_BAD_LIST);
+        q0 = max(q0, 0);
+        q1 = (int)min((int64_t)min(q1, q0 > INT_MAX - p.max_new ? INT_MAX : q0 + p.max_new), p.n_tokens);
+        a.len = (int)max((int64_t)0, min((int64_t)a.len, most));
+    }
+    a.q0 = q0;
+    a.n = max(0, q1 - q0);
+    a.row0 = block * p.unit_rows;
+    a.rows = min(p.unit_rows, a.n * p.group - a.row0);
+    a.hi = a.rows <= 0 ? 0 : max(0, a.len - a.n + (a.row0 + a.rows - 1) / p.group + 1);
+    a.steps = a.rows <= 0 ? 0 : max(1, (a.hi + p.step_keys - 1) / p.step_keys);
+    return a;
+}
+
+// Cached rows that row r of the unit sees.
+__device__ __forceinline__ int attend_sees(const AttendParams &p, const AttendUnit &a, int r) {
+    return max(0, a.len - a.n + (a.row0 + r) / p.group + 1);
+}
+// Its row of out [n_tokens][n_q_heads].
+__device__ __forceinline__ int64_t attend_out_row(const AttendParams &p, const AttendUnit &a, int r) {
+    const int token = (a.row0 + r) / p.group;
+    return (int64_t)(a.q0 + token) * p.n_q_heads + a.h * p.group + (a.row0 + r - token * p.group);
+}
+
+// A page number that may be used: the pool's, or -1 (rows of zeros).
+__device__ __forceinline__ int attend_page(const AttendParams &p, int list, int j) {
+    const int page = p.table[(int64_t)list * p.max_pages + j];
+    if (page < 0 || page >= p.n_pages) {
+        set_status(p.status, KVC_DEV_BAD_PAGE);
+        return -1;
+    }
+    return page;
+}
+
+// The CTA's run of steps and the unit it begins in.
+struct AttendRun {
+    int64_t total, lo, hi;   // steps in all; this CTA's
+    int grid;                // CTAs with work
+    int64_t unit, unit_lo;   // first unit and its first step
+};
+
+__device__ __forceinline__ int64_t attend_cut(int64_t total, int grid, int64_t c) {
+    return total * c / grid;
+}
+// The CTA whose run holds step x.
+__device__ __forceinline__ int attend_cta_of(int64_t total, int grid, int64_t x) {
+    return (int)(((x + 1) * grid - 1) / total);
+}
+
+// Every thread of a block of NT threads calls it; scratch: NT / 32 + 4 int64.
+template <int NT>
+__device__ AttendRun attend_plan(const AttendParams &p, int64_t *scratch) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t per = (p.n_units + NT - 1) / NT;
+    const int64_t u0 = min(p.n_units, per * threadIdx.x), u1 = min(p.n_units, u0 + per);
+    int64_t mine = 0;
+    for (int64_t u = u0; u < u1; ++u) mine += attend_unit(p, u).steps;
+    int64_t x = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += y;
+    }
+    if (lane == 31) scratch[warp] = x;
+    __syncthreads();
+    int64_t before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) {
+        if (w < warp) before += scratch[w];
+        total += scratch[w];
+    }
+    int64_t *found = scratch + NT / 32;
+    AttendRun r;
+    r.total = total;
+    r.grid = (int)min((int64_t)gridDim.x, total);
+    const bool works = (int)blockIdx.x < r.grid;
+    r.lo = works ? attend_cut(total, r.grid, blockIdx.x) : 0;
+    r.hi = works ? attend_cut(total, r.grid, blockIdx.x + 1) : 0;
+    int64_t at = before + x - mine;
+    if (works && r.lo >= at && r.lo < at + mine) {
+        for (int64_t u = u0; u < u1; ++u) {
+            const int s = attend_unit(p, u).steps;
+            if (r.lo < at + s) {
+                found[0] = u;
+                found[1] = at;
+                break;
+            }
+            at += s;
+        }
+    }
+    __syncthreads();
+    r.unit = works ? found[0] : 0;
+    r.unit_lo = works ? found[1] : 0;
+    return r;
+}
+
+// The unit behind u; blocks behind a sequence's last row are passed over.
+__device__ __forceinline__ int64_t attend_next(const AttendParams &p, const AttendUnit &a, int64_t u) {
+    return a.steps == 0 || a.row0 + a.rows >= a.n * p.group ? ((int64_t)a.list + 1) * p.blocks : u + 1;
+}
+
+// ln of the row's sum = ln 2 (m + log2 l).
+__device__ __forceinline__ void attend_store_lse(const AttendParams &p, int64_t row, float m, float l,
+                                                 bool sees) {
+    if (p.lse) p.lse[row] = sees ? (m + log2f(l)) * 0.693147180559945309f : -INFINITY;
+}
+
+// attend_simt.cu; fills the units' shape in.
+int launch_attend_simt(AttendParams &p, bool f32, int grid, cudaStream_t st);
+constexpr int kSimtSlotRows = 64;
+
+}  // namespace kvc

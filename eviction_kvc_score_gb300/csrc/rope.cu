@@ -1,0 +1,200 @@
+// rope.cu -- rotary positions of new tokens' queries and keys, and of kept
+// keys that move to other positions.
+//
+// A pair (a, b) of a head at position p turns by the angle 2 pi p u, u turns
+// per position.  u is held as a 64-bit fraction, and the product with the
+// integer p modulo 2^64 IS the angle modulo a full turn, exactly: no position
+// is too far and the reduction is one integer multiply.  What is left is one
+// sincospi of a 32-bit fraction of half a turn, within 2^-24.
+//
+// Each block takes a few tokens, computes every (token, pair) angle once into
+// shared memory and turns all their heads with 16-byte loads and stores.
+#include <algorithm>
+
+#include "cache.cuh"
+
+namespace kvc {
+
+namespace {
+
+constexpr int kRopeThreads = 256;
+constexpr int kRopePairs = 512;   // (token, pair) angles of a block
+
+__global__ void rope_table_kernel(int rot, double theta, double factor, double alpha, double beta,
+                                  double context, uint64_t *table) {
+    const int i = threadIdx.x;
+    if (i >= rot / 2) return;
+    constexpr double kTwoPi = 6.283185307179586476925286766559;
+    double f = pow(theta, -2.0 * i / rot);
+    if (factor > 1.0) {
+        const double turns = context * f / kTwoPi;
+        double g;
+        if (turns >= beta)
+            g = 1.0;
+        else if (turns <= alpha)
+            g = 0.0;
+        else
+            g = (turns - alpha) / (beta - alpha);
+        f *= g + (1.0 - g) / factor;
+    }
+    table[i] = __double2ull_rn(f / kTwoPi * 18446744073709551616.0);
+}
+
+struct RopeSide {
+    const void *x;
+    void *y;
+    int64_t xs, ys;   // elements from token to token
+    int heads;
+};
+
+struct RopeParams {
+    RopeSide q, k;
+    const int32_t *pos;
+    const uint64_t *table;
+    int64_t n_tokens;
+    int dim, rot, per_block;
+    float amplitude;
+    bool inverse;
+    int turn_units, units;   // threads of a head: turning, turning + copying
+};
+
+template <typename T>
+__device__ __forceinline__ float to_f(T x);
+template <>
+__device__ __forceinline__ float to_f(float x) { return x; }
+template <>
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <typename T>
+__device__ __forceinline__ T from_f(float x);
+template <>
+__device__ __forceinline__ float from_f(float x) { return x; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f(float x) { return __float2bfloat16_rn(x); }
+
+template <typename T, int N>
+struct alignas(N * sizeof(T)) Pack {
+    T v[N];
+};
+
+// Element i of the pair and its partner, turned (cs = amplitude cos, amplitude sin).
+template <typename T>
+__device__ __forceinline__ void turn(T &a, T &b, float2 cs) {
+    const float x = to_f(a), y = to_f(b);
+    a = from_f<T>(x * cs.x - y * cs.y);
+    b = from_f<T>(x * cs.y + y * cs.x);
+}
+
+// N elements per thread and access: 16 bytes where sizes, strides and
+// alignment allow, else 1.  threadIdx.x walks the units of one head,
+// threadIdx.y the (token, head) rows.
+template <typename T, int N, bool INTER>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeParams p) {
+    __shared__ float2 cs[kRopePairs];
+    const int pairs = p.rot / 2;
+    const int64_t t0 = (int64_t)blockIdx.x * p.per_block;
+    const int nt = (int)min((int64_t)p.per_block, p.n_tokens - t0);
+    const int tid = threadIdx.y * blockDim.x + threadIdx.x, nthr = blockDim.x * blockDim.y;
+    for (int i = tid; i < nt * pairs; i += nthr) {
+        const int t = i / pairs, j = i - t * pairs;
+        const uint64_t turns = (uint64_t)(int64_t)p.pos[t0 + t] * p.table[j];
+        float s, c;
+        sincospif((float)(int64_t)turns * 0x1p-63f, &s, &c);
+        cs[i] = make_float2(p.amplitude * c, p.amplitude * (p.inverse ? -s : s));
+    }
+    __syncthreads();
+    const int unit = threadIdx.x;
+    const int heads = p.q.heads + p.k.heads;
+    for (int row = threadIdx.y; row < nt * heads; row += blockDim.y) {
+        const int t = row / heads, h = row - t * heads;
+        const bool is_k = h >= p.q.heads;
+        const RopeSide &side = is_k ? p.k : p.q;
+        const int64_t at = (int64_t)(is_k ? h - p.q.heads : h) * p.dim;
+        const T *x = static_cast<const T *>(side.x) + (t0 + t) * side.xs + at;
+        T *y = static_cast<T *>(side.y) + (t0 + t) * side.ys + at;
+        const float2 *c = cs + t * pairs;
+        using P = Pack<T, N>;
+        if (unit >= p.turn_units) {   // behind the turned part
+            const int i = p.rot + (unit - p.turn_units) * N;
+            *reinterpret_cast<P *>(y + i) = *reinterpret_cast<const P *>(x + i);
+        } else if constexpr (INTER) {
+            constexpr int M = N < 2 ? 2 : N;   // whole pairs
+            alignas(16) T v[M];
+            const int i = unit * M;
+#pragma unroll
+            for (int j = 0; j < M; j += N)
+                *reinterpret_cast<P *>(v + j) = *reinterpret_cast<const P *>(x + i + j);
+#pragma unroll
+            for (int j = 0; j < M; j += 2) turn(v[j], v[j + 1], c[(i + j) / 2]);
+#pragma unroll
+            for (int j = 0; j < M; j += N)
+                *reinterpret_cast<P *>(y + i + j) = *reinterpret_cast<const P *>(v + j);
+        } else {
+            const int i = unit * N;
+            P a = *reinterpret_cast<const P *>(x + i);
+            P b = *reinterpret_cast<const P *>(x + i + pairs);
+#pragma unroll
+            for (int j = 0; j < N; ++j) turn(a.v[j], b.v[j], c[i + j]);
+            *reinterpret_cast<P *>(y + i) = a;
+            *reinterpret_cast<P *>(y + i + pairs) = b;
+        }
+    }
+}
+
+template <typename T, int N, bool INTER>
+void launch(RopeParams &p, bool in_place, int sms, cudaStream_t st) {
+    p.turn_units = INTER ? p.rot / (N < 2 ? 2 : N) : p.rot / 2 / N;
+    p.units = p.turn_units + (in_place ? 0 : (p.dim - p.rot) / N);
+    // tokens of a block: enough blocks for four per SM before angles are
+    // shared by more rows, and never more angles than the array holds
+    const int64_t want = (p.n_tokens + 4 * sms - 1) / (4 * sms);
+    p.per_block = (int)std::min<int64_t>({std::max<int64_t>(1, want), kRopePairs / (p.rot / 2), 8});
+    const dim3 block(p.units, std::max(1, kRopeThreads / p.units));
+    rope_kernel<T, N, INTER><<<(unsigned)((p.n_tokens + p.per_block - 1) / p.per_block), block, 0, st>>>(p);
+}
+
+template <typename T>
+void launch_type(RopeParams &p, bool inter, bool in_place, bool wide, int sms, cudaStream_t st) {
+    constexpr int N = 16 / sizeof(T);
+    if (wide)
+        inter ? launch<T, N, true>(p, in_place, sms, st) : launch<T, N, false>(p, in_place, sms, st);
+    else
+        inter ? launch<T, 1, true>(p, in_place, sms, st) : launch<T, 1, false>(p, in_place, sms, st);
+}
+
+}  // namespace
+
+int launch_rope_table(int32_t rot, double theta, double factor, double alpha, double beta,
+                      double context, uint64_t *table, cudaStream_t st) {
+    rope_table_kernel<<<1, 128, 0, st>>>(rot, theta, factor, alpha, beta, context, table);
+    return cache_launched("kvc_rope_table");
+}
+
+int launch_rope(const RopeArgs &a, int sms, cudaStream_t st) {
+    RopeParams p;
+    p.q = {a.q, a.q_out, a.q_stride, a.q_out_stride, a.n_q_heads};
+    p.k = {a.k, a.k_out, a.k_stride, a.k_out_stride, a.n_k_heads};
+    p.pos = a.positions;
+    p.table = a.table;
+    p.n_tokens = a.n_tokens;
+    p.dim = a.head_dim;
+    p.rot = a.rot_dim;
+    p.amplitude = a.amplitude;
+    p.inverse = a.flags & KVC_ROPE_INVERSE;
+    const bool inter = a.flags & KVC_ROPE_INTERLEAVED;
+    const bool in_place = (a.n_q_heads == 0 || a.q == a.q_out) && (a.n_k_heads == 0 || a.k == a.k_out);
+    const int n = a.dtype == KVC_F32 ? 4 : 8;
+    // 16-byte accesses: every head, half and tail starts on a boundary
+    bool wide = a.head_dim % n == 0 && a.rot_dim % n == 0 && (inter || (a.rot_dim / 2) % n == 0);
+    const RopeSide *sides[2] = {&p.q, &p.k};
+    for (const RopeSide *s : sides)
+        if (s->heads)
+            wide = wide && ((reinterpret_cast<uintptr_t>(s->x) | reinterpret_cast<uintptr_t>(s->y)) & 15) == 0 &&
+                   s->xs % n == 0 && s->ys % n == 0;
+    if (a.dtype == KVC_F32)
+        launch_type<float>(p, inter, in_place, wide, sms, st);
+    else
+        launch_type<__nv_bfloat16>(p, inter, in_place, wide, sms, st);
+    return cache_launched("kvc_rope");
+}
+
+}  // namespace kvc

@@ -34,6 +34,8 @@ KVC_F32, KVC_BF16 = 0, 1
 DEV_TIMEOUT, DEV_BAD_SCORE, DEV_BAD_BUDGET, DEV_OUT_CAPACITY = 0x1, 0x2, 0x4, 0x8
 VALUE_REUSE_SCORE_STATS = 0x1   # kvc_channel_prune_value_ex flag
 DEV_INVARIANT = 0x10   # bounds-checking builds only
+DEV_BAD_LIST, DEV_BAD_PAGE, DEV_PAGES_FULL = 0x20, 0x40, 0x80   # paged cache
+ROPE_INTERLEAVED, ROPE_INVERSE = 0x1, 0x2
 
 
 class KvcError(RuntimeError):
@@ -48,8 +50,15 @@ class KvcShape(C.Structure):
                 ("dtype", C.c_int32)]
 
 
+class KvcCache(C.Structure):
+    _fields_ = [("n_pages", C.c_int32), ("page_rows", C.c_int32), ("head_dim", C.c_int32),
+                ("dtype", C.c_int32), ("max_pages", C.c_int32)]
+
+
 _p, _sz, _i32, _i64, _u32, _d = C.c_void_p, C.c_size_t, C.c_int32, C.c_int64, C.c_uint32, C.c_double
 _sp = C.POINTER(KvcShape)
+_cp = C.POINTER(KvcCache)
+_f = C.c_float
 _SIGS = {
     "kvc_workspace_size": (_sz, [_sp, _i32]),
     "kvc_workspace_init": (C.c_int, [_p, _sz, _p]),
@@ -73,14 +82,27 @@ _SIGS = {
                                           _p]),
     "kvc_channel_prune_value_ex": (C.c_int, [_sp, _p, _p, _p, _p, _p, _d, _p, _p, _p, _i64,
                                              C.c_uint32, _p, _sz, _p]),
+    "kvc_pages_size": (_sz, [_cp, _i32]),
+    "kvc_pages_init": (C.c_int, [_cp, _p, _sz, _p]),
+    "kvc_pages_status": (C.c_int, [_cp, _p, _sz, C.POINTER(_u32), C.POINTER(_i32), _p]),
+    "kvc_pages_append": (C.c_int, [_cp, _p, _p, _i32, _p, _p, _i64, _p, _p, _i64, _p, _p, _p, _sz, _p]),
+    "kvc_pages_fork": (C.c_int, [_cp, _p, _p, _i32, _p, _p, _sz, _p]),
+    "kvc_pages_compact": (C.c_int, [_cp, _p, _p, _i32, _p, _i32, _p, _p, _p, _p, _sz, _p]),
+    "kvc_pages_truncate": (C.c_int, [_cp, _p, _p, _i32, _p, _p, _sz, _p]),
+    "kvc_rope_table": (C.c_int, [_i32, _d, _d, _d, _d, _d, _p, _p]),
+    "kvc_rope": (C.c_int, [_i32, _i64, _i32, _i32, _i32, _i32, _u32, _f, _p, _p, _p, _i64, _p, _i64,
+                           _p, _i64, _p, _i64, _p]),
+    "kvc_attend_workspace_size": (_sz, [_cp, _i32, _i32, _i32, _i32]),
+    "kvc_attend": (C.c_int, [_cp, _i32, _i32, _i32, _i32, _i64, _p, _i64, _p, _p, _p, _p, _p, _f, _p,
+                             _p, _p, _sz, _p]),
     "kvc_keep_channels": (_i32, [_d, _i32]),
     "kvc_status_string": (C.c_char_p, [C.c_int]),
     "kvc_last_error": (C.c_char_p, []),
 }
 for _name, (_res, _args) in _SIGS.items():
-    _f = getattr(_lib, _name)
-    _f.restype = _res
-    _f.argtypes = _args
+    _fn = getattr(_lib, _name)
+    _fn.restype = _res
+    _fn.argtypes = _args
 
 
 def _check(fn, rc):
@@ -278,6 +300,199 @@ def kvc_channel_prune_value_ex(s: KvcShape, q_obs, k, v, v_out, budget, lam: flo
 
 def kvc_keep_channels(lam: float, head_dim: int) -> int:
     return int(_lib.kvc_keep_channels(float(lam), int(head_dim)))
+
+
+# --- the paged cache --------------------------------------------------------
+
+_DTYPES = {KVC_F32: torch.float32, KVC_BF16: torch.bfloat16}
+
+
+def cache(n_pages, page_rows, head_dim, max_pages, dtype) -> KvcCache:
+    """Description of a page pool and its tables (kvc_cache in kvc.h)."""
+    if isinstance(dtype, torch.dtype):
+        if dtype not in _DTYPES.values():
+            raise ValueError(f"pages hold float32 or bfloat16 rows, not {dtype}")
+        dt = KVC_F32 if dtype == torch.float32 else KVC_BF16
+    else:
+        dt = KVC_F32 if dtype in ("f32", KVC_F32) else KVC_BF16
+    return KvcCache(int(n_pages), int(page_rows), int(head_dim), dt, int(max_pages))
+
+
+def _tensor(t, name, dtype, numel=None, strided=False):
+    """Pointer of a device tensor of the given type, on the current device,
+    contiguous (but for strided ones) and with numel elements at least."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current device")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if not strided and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if numel is not None and t.numel() < numel:
+        raise ValueError(f"{name} has {t.numel()} elements, needs {numel}")
+    return t.data_ptr()
+
+
+def _lists(c: KvcCache, table, lens):
+    """Pointers of a table and its lengths, and the number of lists."""
+    if table.dim() != 2 or table.shape[1] != c.max_pages:
+        raise ValueError(f"table must be [n_lists][{c.max_pages}]")
+    n = table.shape[0]
+    return _tensor(table, "table", torch.int32), _tensor(lens, "len", torch.int32, n), n
+
+
+def _pools(c: KvcCache, k_pool, v_pool):
+    n, dt = c.n_pages * c.page_rows * c.head_dim, _DTYPES[c.dtype]
+    return _tensor(k_pool, "k_pool", dt, n), _tensor(v_pool, "v_pool", dt, n)
+
+
+def _state(state):
+    return _tensor(state, "state", torch.uint8), state.numel()
+
+
+def kvc_pages_size(c: KvcCache, n_lists: int) -> int:
+    n = _lib.kvc_pages_size(C.byref(c), int(n_lists))
+    if n == 0:
+        raise KvcError("kvc_pages_size", -1, _lib.kvc_last_error().decode())
+    return n
+
+
+def kvc_pages_init(c: KvcCache, state, stream=None) -> None:
+    _check("kvc_pages_init", _lib.kvc_pages_init(C.byref(c), *_state(state), _stream(stream)))
+
+
+def kvc_pages_status(c: KvcCache, state, stream=None):
+    """(status bits, free pages); waits for the stream."""
+    st, free = _u32(0), _i32(0)
+    _check("kvc_pages_status", _lib.kvc_pages_status(
+        C.byref(c), *_state(state), C.byref(st), C.byref(free), _stream(stream)))
+    return st.value, free.value
+
+
+def kvc_pages_append(c: KvcCache, table, lens, counts, src_row, src_step: int, k_src, v_src,
+                     k_pool, v_pool, state, stream=None) -> None:
+    """Append counts[i] rows of k_src / v_src (rows of head_dim elements) behind
+    every list i: rows src_row[i] + r * src_step.  Rows inside a fused projection
+    are taken where they lie: k_src and v_src start at the first key and value
+    row of the first token, src_step is the heads of a whole token."""
+    t, n_len, n = _lists(c, table, lens)
+    dt = _DTYPES[c.dtype]
+    rows = min(k_src.numel(), v_src.numel()) // c.head_dim
+    _check("kvc_pages_append", _lib.kvc_pages_append(
+        C.byref(c), t, n_len, n, _tensor(counts, "counts", torch.int32, n),
+        _tensor(src_row, "src_row", torch.int64, n), int(src_step), _tensor(k_src, "k_src", dt),
+        _tensor(v_src, "v_src", dt), rows, *_pools(c, k_pool, v_pool),
+        *_state(state), _stream(stream)))
+
+
+def kvc_pages_fork(c: KvcCache, table, lens, src, state, stream=None) -> None:
+    """Make every list i with src[i] >= 0 a second holder of list src[i]'s pages."""
+    t, n_len, n = _lists(c, table, lens)
+    _check("kvc_pages_fork", _lib.kvc_pages_fork(
+        C.byref(c), t, n_len, n, _tensor(src, "src", torch.int32, n), *_state(state),
+        _stream(stream)))
+
+
+def kvc_pages_compact(c: KvcCache, table, lens, idx, counts, k_pool, v_pool, state,
+                      stream=None) -> None:
+    """Keep rows idx[i][:counts[i]] of every list i with counts[i] >= 0."""
+    t, n_len, n = _lists(c, table, lens)
+    k_max = idx.shape[-1]
+    _check("kvc_pages_compact", _lib.kvc_pages_compact(
+        C.byref(c), t, n_len, n, _tensor(idx, "idx", torch.int32, n * k_max), k_max,
+        _tensor(counts, "counts", torch.int32, n), *_pools(c, k_pool, v_pool), *_state(state),
+        _stream(stream)))
+
+
+def kvc_pages_truncate(c: KvcCache, table, lens, new_len, state, stream=None) -> None:
+    """Cut every list i with new_len[i] >= 0 to at most new_len[i] rows (0 frees it)."""
+    t, n_len, n = _lists(c, table, lens)
+    _check("kvc_pages_truncate", _lib.kvc_pages_truncate(
+        C.byref(c), t, n_len, n, _tensor(new_len, "new_len", torch.int32, n), *_state(state),
+        _stream(stream)))
+
+
+def kvc_rope_table(rot_dim: int, theta: float, table, factor: float = 1.0, alpha: float = 1.0,
+                   beta: float = 4.0, context: float = 8192.0, stream=None) -> None:
+    """Fill table (rot_dim / 2 int64 or uint64) with the pairs' frequencies;
+    factor > 1 slows the slow pairs down for longer contexts (see kvc.h)."""
+    dt = torch.uint64 if table.dtype == torch.uint64 else torch.int64
+    _check("kvc_rope_table", _lib.kvc_rope_table(
+        int(rot_dim), float(theta), float(factor), float(alpha), float(beta), float(context),
+        _tensor(table, "table", dt, max(0, int(rot_dim)) // 2), _stream(stream)))
+
+
+def _heads(x, name, dtype, n_tokens, dim):
+    """(heads, pointer, token stride) of x [n_tokens][heads][dim], whose heads
+    are contiguous; tokens may be further apart."""
+    if x is None:
+        return 0, None, 0
+    if x.dim() != 3 or x.shape[0] != n_tokens or x.shape[2] != dim:
+        raise ValueError(f"{name} must be [{n_tokens}][heads][{dim}]")
+    if x.numel() and (x.stride(2) != 1 or (x.shape[1] > 1 and x.stride(1) != dim)):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    stride = x.stride(0) if n_tokens > 1 else x.shape[1] * dim
+    return x.shape[1], _tensor(x, name, dtype, strided=True), stride
+
+
+def kvc_rope(table, positions, q, k, q_out, k_out, rot_dim: int, interleaved: bool = False,
+             inverse: bool = False, amplitude: float = 1.0, stream=None) -> None:
+    """Turn the first rot_dim elements of the heads of q and k [n_tokens][heads][D]
+    (either may be None) by their tokens' positions (int32)."""
+    x = q if q is not None else k
+    if x is None:
+        raise ValueError("kvc_rope needs q or k")
+    if x.dtype not in _DTYPES.values():
+        raise ValueError(f"kvc_rope takes float32 or bfloat16 tensors, not {x.dtype}")
+    if (q is None) != (q_out is None) or (k is None) != (k_out is None):
+        raise ValueError("kvc_rope needs an output for each input")
+    if x.dim() != 3:
+        raise ValueError("kvc_rope takes [n_tokens][heads][D] tensors")
+    n, dim, dt = x.shape[0], x.shape[2], x.dtype
+    hq, qp, qs = _heads(q, "q", dt, n, dim)
+    hqo, qop, qos = _heads(q_out, "q_out", dt, n, dim)
+    hk, kp, ks = _heads(k, "k", dt, n, dim)
+    hko, kop, kos = _heads(k_out, "k_out", dt, n, dim)
+    if hq != hqo or hk != hko:
+        raise ValueError("kvc_rope: outputs must have their inputs' heads")
+    tdt = torch.uint64 if table.dtype == torch.uint64 else torch.int64
+    flags = (ROPE_INTERLEAVED if interleaved else 0) | (ROPE_INVERSE if inverse else 0)
+    _check("kvc_rope", _lib.kvc_rope(
+        KVC_F32 if dt == torch.float32 else KVC_BF16, n, hq, hk, dim, int(rot_dim), flags,
+        float(amplitude), _tensor(positions, "positions", torch.int32, n),
+        _tensor(table, "table", tdt, max(0, int(rot_dim)) // 2), qp, qs, qop, qos, kp, ks, kop, kos,
+        _stream(stream)))
+
+
+def kvc_attend_workspace_size(c: KvcCache, n_q_heads: int, n_kv_heads: int, n_seqs: int,
+                              max_new: int) -> int:
+    n = _lib.kvc_attend_workspace_size(C.byref(c), int(n_q_heads), int(n_kv_heads), int(n_seqs),
+                                       int(max_new))
+    if n == 0:
+        raise KvcError("kvc_attend_workspace_size", -1, _lib.kvc_last_error().decode())
+    return n
+
+
+def kvc_attend(c: KvcCache, q, q_start, table, lens, k_pool, v_pool, max_new: int, out, ws,
+               lse=None, scale: Optional[float] = None, stream=None) -> None:
+    """Attention of new tokens q [n_tokens][H_q][D] over the paged lists of one
+    layer, table [n_seqs * H_kv][max_pages]; scale defaults to 1 / sqrt(D)."""
+    t, n_len, n_lists = _lists(c, table, lens)
+    n_seqs = q_start.numel() - 1
+    if n_seqs < 1 or n_lists % n_seqs:
+        raise ValueError("table must hold the same number of lists for every sequence of q_start")
+    dt = _DTYPES[c.dtype]
+    if q.dim() != 3:
+        raise ValueError("q must be [n_tokens][n_q_heads][head_dim]")
+    hq, qp, qs = _heads(q, "q", dt, q.shape[0], c.head_dim)
+    n = q.shape[0]
+    _check("kvc_attend", _lib.kvc_attend(
+        C.byref(c), hq, n_lists // n_seqs, n_seqs, int(max_new), n, qp, qs,
+        _tensor(q_start, "q_start", torch.int32), t, n_len, *_pools(c, k_pool, v_pool),
+        c.head_dim ** -0.5 if scale is None else float(scale), _tensor(out, "out", dt, q.numel()),
+        None if lse is None else _tensor(lse, "lse", torch.float32, n * hq),
+        _tensor(ws, "workspace", torch.uint8), ws.numel(), _stream(stream)))
 
 
 def kvc_status_string(code: int) -> str:

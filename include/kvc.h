@@ -98,6 +98,12 @@ typedef enum { KVC_F32 = 0, KVC_BF16 = 1 } kvc_dtype;
                                       ascending or outside [0, D).  The check
                                       records the bit and the kernel goes on; it
                                       never traps. */
+#define KVC_DEV_BAD_LIST     0x20u /* a list length, row count, row index, source
+                                      list or q_start entry outside its range */
+#define KVC_DEV_BAD_PAGE     0x40u /* a page-table entry outside the pool, or a
+                                      page released more often than it is held */
+#define KVC_DEV_PAGES_FULL   0x80u /* more free pages or page-table entries
+                                      needed than there are; nothing was done */
 
 typedef struct {
     int32_t n_layers;    /* L >= 1 */
@@ -386,6 +392,160 @@ int kvc_channel_prune_value_ex(const kvc_shape *shape, const void *q_obs, const 
 /* floor((1 - lambda) * head_dim) computed in double; 0 if lambda is outside
  * [0,1). */
 int32_t kvc_keep_channels(double lambda, int32_t head_dim);
+
+/* ------------------------------------------------------------------------
+ * The paged cache: what a compressed prompt is decoded from.
+ *
+ * A pool holds n_pages pages, each of page_rows consecutive cached rows (K
+ * rows in one pool, V rows in the other, same page numbers) of ONE KV head.
+ * A list is the cache of one (layer, sequence, KV head): its row r lies in
+ * page table[list][r / page_rows] at row r % page_rows of the page.  Lists
+ * have lengths of their own, because the budgets above differ from layer to
+ * layer and, optionally, from head to head; keys are stored with their rotary
+ * positions applied, so rows may be dropped without moving the others.
+ *
+ *  k_pool, v_pool  [n_pages][page_rows][D]  16-byte aligned
+ *  table           [n_lists][max_pages]     int32 page numbers; entries at and
+ *                                           after ceil(len / page_rows) are
+ *                                           neither read nor changed
+ *  len             [n_lists]                int32 rows of each list
+ *
+ * All tables, lengths and pools are DEVICE memory of the caller.  Calls take
+ * the lists [0, n_lists) of the arrays they are given: a layer's lists are
+ * passed by pointing into a larger table.  Which pages are free and how many
+ * lists hold each page is kept in an opaque device buffer, the pages' state,
+ * shared by every list of a pool.  Calls on one state (and its pools) must be
+ * ordered on one stream or by events.  No call waits for the device, and every
+ * call but kvc_pages_status can be captured into a graph.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+    int32_t n_pages;    /* pages per pool, 1..2^30 */
+    int32_t page_rows;  /* rows per page: 16, 32, 64 or 128 */
+    int32_t head_dim;   /* D: a multiple of 8, 8..256 */
+    int32_t dtype;      /* kvc_dtype of the rows */
+    int32_t max_pages;  /* entries of one page-table row, >= 1; max_pages *
+                           page_rows < 2^31 */
+} kvc_cache;
+
+/* Bytes of state for `cache` and calls of up to n_lists lists (0 if either is
+ * invalid; n_lists 1..2^20). */
+size_t kvc_pages_size(const kvc_cache *cache, int32_t n_lists);
+
+/* Make every page free and clear the status word.  Lists that held pages are
+ * the caller's to empty (len = 0).  state is 256-byte aligned. */
+int kvc_pages_init(const kvc_cache *cache, void *state, size_t state_bytes, cudaStream_t stream);
+
+/* Synchronise `stream`; *status = the KVC_DEV_* bits since kvc_pages_init,
+ * *n_free = free pages.  Either may be NULL. */
+int kvc_pages_status(const kvc_cache *cache, const void *state, size_t state_bytes,
+                     uint32_t *status, int32_t *n_free, cudaStream_t stream);
+
+/* Append counts[i] rows (none where <= 0) behind every list i.  Row r of list i
+ * is row src_row[i] + r * src_step of k_src and v_src, [src_rows][D]: packed
+ * rows (kvc_compact's) have src_step 1; token-major rows [tokens][heads][D]
+ * have src_step = heads and src_row = token * heads + head.  New pages are the
+ * free pages of the lowest numbers, in list order.  A partly filled last page
+ * that other lists hold too is copied to a page of the list's own first, so
+ * the others keep their rows.  All lists or none: with too few free pages or
+ * table entries (KVC_DEV_PAGES_FULL), or a length or source row out of range
+ * (KVC_DEV_BAD_LIST), or a last page outside the pool (KVC_DEV_BAD_PAGE), the
+ * call changes nothing but the status word.  src_step >= 0.  k_src and v_src
+ * must not overlap the pools; they are 16-byte aligned. */
+int kvc_pages_append(const kvc_cache *cache, int32_t *table, int32_t *len, int32_t n_lists,
+                     const int32_t *counts, const int64_t *src_row, int64_t src_step,
+                     const void *k_src, const void *v_src, int64_t src_rows, void *k_pool,
+                     void *v_pool, void *state, size_t state_bytes, cudaStream_t stream);
+
+/* Make every list i with src[i] >= 0 a second holder of list src[i]'s pages:
+ * no rows are copied; whichever list appends first copies the last page.
+ * List i must be empty, src[i] < n_lists, and list src[i] not itself forked
+ * into by the same call; an entry that breaks this is skipped
+ * (KVC_DEV_BAD_LIST).  Several lists may fork from one. */
+int kvc_pages_fork(const kvc_cache *cache, int32_t *table, int32_t *len, int32_t n_lists,
+                   const int32_t *src, void *state, size_t state_bytes, cudaStream_t stream);
+
+/* Keep only rows idx[i][0..counts[i]) (any order, [n_lists][k_max] int32) of
+ * every list i with counts[i] >= 0, in that order: the rows are gathered into
+ * new pages (the lowest free ones, in list order) and the list lets go of its
+ * old ones, which other holders keep unchanged.  The new pages must be free
+ * before the old ones are: all lists or none, as in kvc_pages_append;
+ * counts[i] > k_max is KVC_DEV_BAD_LIST.  An index outside the list gives a
+ * row of zeros and KVC_DEV_BAD_LIST.  idx may be kvc_topk_select's. */
+int kvc_pages_compact(const kvc_cache *cache, int32_t *table, int32_t *len, int32_t n_lists,
+                      const int32_t *idx, int32_t k_max, const int32_t *counts, void *k_pool,
+                      void *v_pool, void *state, size_t state_bytes, cudaStream_t stream);
+
+/* Cut every list i with new_len[i] >= 0 to min(len[i], new_len[i]) rows; pages
+ * that no list holds any more become free.  new_len 0 frees the list.  A
+ * length out of range is skipped (KVC_DEV_BAD_LIST). */
+int kvc_pages_truncate(const kvc_cache *cache, int32_t *table, int32_t *len, int32_t n_lists,
+                       const int32_t *new_len, void *state, size_t state_bytes,
+                       cudaStream_t stream);
+
+/* Rotary frequencies of the rot_dim / 2 pairs, as turns per position in units
+ * of 2^-64 (device array of rot_dim / 2 uint64): pair i makes f_i / (2 pi)
+ * turns per position, f_i = theta^(-2 i / rot_dim).  With factor > 1, for
+ * contexts longer than the `context` positions the model was trained on, pairs
+ * that make fewer than alpha turns in `context` positions are slowed down by
+ * factor, those that make beta or more are kept, and between the two
+ *   f_i (g + (1 - g) / factor),  g = (turns - alpha) / (beta - alpha)
+ * (alpha = beta = infinity slows every pair).  theta >= 1, factor >= 1,
+ * 0 <= alpha <= beta, context > 0 (alpha, beta and context are ignored at
+ * factor 1), rot_dim even, 2..256. */
+int kvc_rope_table(int32_t rot_dim, double theta, double factor, double alpha, double beta,
+                   double context, uint64_t *table, cudaStream_t stream);
+
+/* kvc_rope: turn the first rot_dim elements of every head of q [n_tokens]
+ * [n_q_heads][D] and k [n_tokens][n_k_heads][D] by the token's angles:
+ *   (a, b) -> amplitude (a cos t - b sin t, a sin t + b cos t),
+ * t = positions[token] * f_i of the table; the pair (a, b) is elements
+ * (i, i + rot_dim / 2), or (2i, 2i + 1) with KVC_ROPE_INTERLEAVED.
+ * KVC_ROPE_INVERSE turns by -t (which is also the gradient's way back).  The
+ * angle is reduced exactly in 64-bit fixed point, so far positions (any int32,
+ * negative ones too) lose nothing.  Elements from rot_dim on are copied.
+ * Arithmetic is fp32, rounded once.  q_stride and the others count elements
+ * from token to token (>= heads * D); heads are contiguous.  q_out may be q
+ * (then with the same stride), k_out may be k; other overlaps are not
+ * allowed.  n_q_heads or n_k_heads may be 0 with NULL tensors.  D is 2..256. */
+#define KVC_ROPE_INTERLEAVED 0x1u
+#define KVC_ROPE_INVERSE     0x2u
+int kvc_rope(int32_t dtype, int64_t n_tokens, int32_t n_q_heads, int32_t n_k_heads,
+             int32_t head_dim, int32_t rot_dim, uint32_t flags, float amplitude,
+             const int32_t *positions, const uint64_t *table, const void *q, int64_t q_stride,
+             void *q_out, int64_t q_out_stride, const void *k, int64_t k_stride, void *k_out,
+             int64_t k_out_stride, cudaStream_t stream);
+
+/* Bytes of workspace kvc_attend needs on the CURRENT device (0 if an argument
+ * is invalid).  Initialise it once with kvc_workspace_init; read its status
+ * word with kvc_workspace_status. */
+size_t kvc_attend_workspace_size(const kvc_cache *cache, int32_t n_q_heads, int32_t n_kv_heads,
+                                 int32_t n_seqs, int32_t max_new);
+
+/* Attention of new tokens over the paged lists of one layer.  Tokens
+ * q_start[b] .. q_start[b+1]-1 (device array [n_seqs + 1] int32) of q
+ * [n_tokens][n_q_heads][D] belong to sequence b; n = their number, at most
+ * max_new.  List b * n_kv_heads + h holds KV head h of sequence b, the n new
+ * tokens' own rows appended; query head j reads KV head j / (n_q_heads /
+ * n_kv_heads).  Token i of n sees rows r < len - n + i + 1 of each list:
+ *   out = sum_r softmax_r(scale q . k_r) v_r,  lse = ln sum_r exp(scale q . k_r)
+ * A token that sees no row gets zeros and lse -infinity.  Rows at and after
+ * len, and rows a token does not see, never reach its outputs, whatever they
+ * hold.  Tokens outside [q_start[0], q_start[n_seqs]) are left as they were.
+ * n = 1 is a decode step.  q_stride counts elements from token to token; out
+ * is [n_tokens][n_q_heads][D] contiguous, lse [n_tokens][n_q_heads] fp32 or
+ * NULL.  Logits, softmax and sums are fp32.  bf16 with D 64 or 128 and at most
+ * 128 query heads per KV head runs on the tensor cores (the probabilities
+ * rounded to bf16 for the product with V); everything else on the CUDA cores
+ * in fp32.  Lengths and q_start out of range are cut to it
+ * (KVC_DEV_BAD_LIST); a page outside the pool counts as rows of zeros
+ * (KVC_DEV_BAD_PAGE).  Long lists are split over the GPU and joined in a fixed
+ * order, so results do not vary from run to run.  q, out and the pools are
+ * 16-byte aligned, q_stride a multiple of 8. */
+int kvc_attend(const kvc_cache *cache, int32_t n_q_heads, int32_t n_kv_heads, int32_t n_seqs,
+               int32_t max_new, int64_t n_tokens, const void *q, int64_t q_stride,
+               const int32_t *q_start, const int32_t *table, const int32_t *len,
+               const void *k_pool, const void *v_pool, float scale, void *out, float *lse,
+               void *ws, size_t ws_bytes, cudaStream_t stream);
 
 const char *kvc_status_string(int status);
 

@@ -69,22 +69,25 @@ int state_of(const kvc_cache &c, int32_t n_lists, void *state, size_t bytes, con
     return KVC_OK;
 }
 
-// kvc_attend's workspace: header | arrival counters | slots' (max, sum) | slots' rows.
+// The kernel that takes a call, and its workspace: header | arrival counters |
+// slots' (max, sum) | slots' rows.
 struct AttendWs {
+    bool tc;
+    AttendNeeds needs;
     size_t arrived, stat, part, total;
 };
 
-AttendWs attend_ws(const kvc_cache &c, int slot_rows, int grid) {
+AttendWs attend_ws(const kvc_cache &c, int group) {
     AttendWs w;
+    w.tc = attend_tc_takes(c.dtype, c.head_dim, group);
+    w.needs = w.tc ? attend_tc_needs(device_sms()) : attend_simt_needs(device_sms());
+    const size_t rows = (size_t)w.needs.grid * w.needs.slots * w.needs.slot_rows;
     w.arrived = kWsHeader;
-    w.stat = w.arrived + cache_align((size_t)grid * 4);
-    w.part = w.stat + cache_align((size_t)2 * grid * slot_rows * sizeof(float2));
-    w.total = w.part + cache_align((size_t)2 * grid * slot_rows * c.head_dim * sizeof(float));
+    w.stat = w.arrived + cache_align((size_t)w.needs.grid * 2 * sizeof(uint32_t));
+    w.part = w.stat + cache_align(rows * sizeof(float2));
+    w.total = w.part + cache_align(rows * c.head_dim * sizeof(float));
     return w;
 }
-
-// CTAs of the attention launch, a function of the device alone.
-int attend_grid() { return 2 * device_sms(); }
 
 bool attend_shape_ok(const kvc_cache *c, int32_t n_q_heads, int32_t n_kv_heads, int32_t n_seqs,
                      int32_t max_new, const char *fn) {
@@ -274,7 +277,7 @@ size_t kvc_attend_workspace_size(const kvc_cache *cache, int32_t n_q_heads, int3
                                  int32_t n_seqs, int32_t max_new) {
     if (!attend_shape_ok(cache, n_q_heads, n_kv_heads, n_seqs, max_new, "kvc_attend_workspace_size"))
         return 0;
-    return attend_ws(*cache, kSimtSlotRows, attend_grid()).total;
+    return attend_ws(*cache, n_q_heads / n_kv_heads).total;
 }
 
 int kvc_attend(const kvc_cache *cache, int32_t n_q_heads, int32_t n_kv_heads, int32_t n_seqs,
@@ -298,9 +301,8 @@ int kvc_attend(const kvc_cache *cache, int32_t n_q_heads, int32_t n_kv_heads, in
         return fail(KVC_ERR_INVALID_ARG,
                     "kvc_attend: q_stride must be a multiple of 8 and >= n_q_heads * head_dim");
     if (!std::isfinite(scale)) return fail(KVC_ERR_INVALID_ARG, "kvc_attend: scale must be finite");
-    const int grid = attend_grid();
-    if (grid == 0) return fail(KVC_ERR_CUDA, "kvc_attend: no usable CUDA device");
-    const AttendWs w = attend_ws(c, kSimtSlotRows, grid);
+    const AttendWs w = attend_ws(c, n_q_heads / n_kv_heads);
+    if (w.needs.grid == 0) return fail(KVC_ERR_CUDA, "kvc_attend: no usable CUDA device");
     if (!ws) return fail(KVC_ERR_WORKSPACE, "kvc_attend: workspace is NULL");
     if (reinterpret_cast<uintptr_t>(ws) % 256)
         return fail(KVC_ERR_WORKSPACE, "kvc_attend: workspace must be 256-byte aligned");
@@ -318,7 +320,8 @@ int kvc_attend(const kvc_cache *cache, int32_t n_q_heads, int32_t n_kv_heads, in
     while ((1 << p.shift) < c.page_rows) ++p.shift;
     p.n_tokens = n_tokens;
     p.max_new = max_new;
-    p.slot_rows = kSimtSlotRows;
+    p.slots = w.needs.slots;
+    p.slot_rows = w.needs.slot_rows;
     p.q_stride = q_stride;
     p.q = q;
     p.k_pool = k_pool;
@@ -333,7 +336,8 @@ int kvc_attend(const kvc_cache *cache, int32_t n_q_heads, int32_t n_kv_heads, in
     p.arrived = reinterpret_cast<uint32_t *>(base + w.arrived);
     p.stat = reinterpret_cast<float2 *>(base + w.stat);
     p.part = reinterpret_cast<float *>(base + w.part);
-    return launch_attend_simt(p, c.dtype == KVC_F32, grid, stream);
+    return w.tc ? launch_attend_tc(p, w.needs.grid, stream)
+                : launch_attend_simt(p, c.dtype == KVC_F32, w.needs.grid, stream);
 }
 
 }  // extern "C"

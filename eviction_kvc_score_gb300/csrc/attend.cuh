@@ -27,7 +27,9 @@ struct AttendParams {
     int unit_rows;       // rows of a unit
     int blocks;          // units per list
     int64_t n_units;
-    int step_keys;       // keys per step
+    int step_keys;       // keys per step ...
+    int split_rows;      // ... twice as many for units of at most so many rows
+    int slots;           // slots per CTA
     int slot_rows;       // row capacity of a slot
     int64_t q_stride;
     const void *q, *k_pool, *v_pool;
@@ -36,9 +38,9 @@ struct AttendParams {
     float *lse;
     float scale_log2;    // scale * log2(e)
     uint32_t *status;
-    uint32_t *arrived;   // [grid], zero between calls
-    float2 *stat;        // [2 grid][slot_rows] (max in log2 units, sum)
-    float *part;         // [2 grid][slot_rows][dim]
+    uint32_t *arrived;   // [grid][2], zero between calls
+    float2 *stat;        // [grid][slots][slot_rows] (max in log2 units, sum)
+    float *part;         // [grid][slots][slot_rows][dim]
 };
 
 struct AttendUnit {
@@ -70,7 +72,8 @@ __device__ __forceinline__ AttendUnit attend_unit(const AttendParams &p, int64_t
     a.row0 = block * p.unit_rows;
     a.rows = min(p.unit_rows, a.n * p.group - a.row0);
     a.hi = a.rows <= 0 ? 0 : max(0, a.len - a.n + (a.row0 + a.rows - 1) / p.group + 1);
-    a.steps = a.rows <= 0 ? 0 : max(1, (a.hi + p.step_keys - 1) / p.step_keys);
+    const int keys = a.rows <= p.split_rows ? 2 * p.step_keys : p.step_keys;
+    a.steps = a.rows <= 0 ? 0 : max(1, (a.hi + keys - 1) / keys);
     return a;
 }
 
@@ -167,8 +170,18 @@ __device__ __forceinline__ void attend_store_lse(const AttendParams &p, int64_t 
     if (p.lse) p.lse[row] = sees ? (m + log2f(l)) * 0.693147180559945309f : -INFINITY;
 }
 
-// attend_simt.cu; fills the units' shape in.
+// Slots of a CTA: its first unit's (begun by an earlier CTA), its last unit's.
+constexpr int kSlotFirst = 0, kSlotLast = 1;
+
+// What a launch needs of the workspace.
+struct AttendNeeds {
+    int grid, slots, slot_rows;
+};
+AttendNeeds attend_simt_needs(int sms);
+AttendNeeds attend_tc_needs(int sms);
+bool attend_tc_takes(int dtype, int dim, int group);
+// Both fill the units' shape in.
 int launch_attend_simt(AttendParams &p, bool f32, int grid, cudaStream_t st);
-constexpr int kSimtSlotRows = 64;
+int launch_attend_tc(AttendParams &p, int grid, cudaStream_t st);
 
 }  // namespace kvc

@@ -17,6 +17,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kKeys = 64;
+constexpr int kSlotRows = 64;
 
 template <int ROWS, int DMAX>
 struct SimtSmem {
@@ -179,7 +180,7 @@ __global__ void __launch_bounds__(kThreads) attend_simt_kernel(AttendParams p) {
         }
         // whole units go straight out, shared ones through the slots
         const bool whole = t0 == 0 && t1 == a.steps;
-        const int slot = 2 * blockIdx.x + (t0 == 0 ? 1 : 0);
+        const int slot = 2 * blockIdx.x + (t0 == 0 ? kSlotLast : kSlotFirst);
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
             const int r = ty * RT + i;
@@ -205,9 +206,9 @@ __global__ void __launch_bounds__(kThreads) attend_simt_kernel(AttendParams p) {
             __threadfence();
             __syncthreads();
             if (tid == 0) {
-                const uint32_t before = atomicAdd(&p.arrived[c0], 1u);
+                const uint32_t before = atomicAdd(&p.arrived[2 * c0], 1u);
                 s.last = before == (uint32_t)(c1 - c0);
-                if (s.last) p.arrived[c0] = 0;
+                if (s.last) p.arrived[2 * c0] = 0;
             }
             __syncthreads();
             if (s.last) {
@@ -269,13 +270,16 @@ int launch_rows(AttendParams &p, int rows, int grid, cudaStream_t st) {
 
 }  // namespace
 
+AttendNeeds attend_simt_needs(int sms) { return {2 * sms, 2, kSlotRows}; }
+
 int launch_attend_simt(AttendParams &p, bool f32, int grid, cudaStream_t st) {
     // 16 rows per block where a list's tokens fill no more
-    const int rows = p.max_new * p.group <= 16 ? 16 : kSimtSlotRows;
+    const int rows = p.max_new * p.group <= 16 ? 16 : kSlotRows;
     p.unit_rows = rows;
     p.blocks = (p.max_new * p.group + rows - 1) / rows;
     p.n_units = (int64_t)p.n_seqs * p.n_kv_heads * p.blocks;
     p.step_keys = kKeys;
+    p.split_rows = 0;
     return f32 ? launch_rows<float>(p, rows, grid, st) : launch_rows<__nv_bfloat16>(p, rows, grid, st);
 }
 

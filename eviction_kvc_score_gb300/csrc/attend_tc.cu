@@ -1,0 +1,780 @@
+// attend_tc.cu -- attention of new tokens over the paged cache on the sm_103a
+// tensor cores: bf16, head size 64 or 128, up to 128 query heads per KV head.
+//
+// A CTA walks its run of steps (attend.cuh).  Per 128-key tile of a list and
+// per tile t of up to 128 rows (tokens x the KV head's query heads):
+//   MMA   S_t = Q_t K^T        128 x 128, D deep, both operands in shared memory
+//   soft  p = 2^(S c - m), c = scale log2 e, rounded to bf16 and written over
+//         S_t in TMEM; l += sum of the unrounded p
+//   MMA   O_t += P_t V         128 x D, P straight from TMEM, V as TMA left it
+//                              (channel-contiguous: the MN-major layout)
+// The reference m only follows the running maximum when that has grown by more
+// than 8 (p then stays below 2^8, far from any limit of bf16 or fp32); O and l
+// are rescaled then, which after the first tiles hardly ever happens.
+//
+// Two row tiles share every K and V tile of a step (256 rows per read of the
+// cache); while the softmax of one runs, the tensor cores work on the other.
+// A unit of at most one tile's rows -- decode -- gives both halves the same
+// rows and every other key tile each, so the two chains still overlap, and
+// joins the halves at the end: 256 keys per step.
+//
+// Pages go to shared memory by TMA, one box of page_rows x 64 elements each;
+// a page outside the pool is a box outside the tensor and comes as zeros.
+// Nothing a row does not see reaches it: its S is masked, and in tiles that
+// some row sees only part of, V's elements that are not finite are taken out
+// before the product (p = 0 would not cancel them) and given back at the end
+// to the rows that see them.
+//
+// Roles: warps 0-3 and 4-7 softmax of t = 0 and 1, a thread per row; warp 8
+// loads; warp 9 issues the MMAs.  TMEM: S_0 | S_1 | O_0 | O_1, 128 columns each.
+// Shared memory: two Q tiles and a ring of five tiles (D = 128: 64 + 160 KB) that
+// K and V tiles pass through in the order the MMAs use them.  Every wait is
+// bounded and nothing waits on a barrier without a limit, so a wait that runs
+// out ends the kernel with KVC_DEV_TIMEOUT (the workspace then has to be
+// initialised again).
+#include "attend.cuh"
+
+namespace kvc {
+
+namespace {
+
+constexpr int kThreads = 384;
+// Registers per thread: 168 at launch (64,512 of the SM's 65,536), moved from
+// the loading and issuing warpgroup to the two that hold a row of 128 logits
+// per thread.  256 x 216 + 128 x 72 = 384 x 168: the launch checks the 168,
+// because an increase beyond what the block was launched with never returns.
+constexpr int kRegsLaunch = 168, kRegsSoftmax = 216, kRegsOther = 72;
+static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreads * kRegsLaunch, "register split");
+constexpr int kTile = 128;              // rows of Q, keys of K and V
+constexpr int kStages = 5;
+constexpr int kLoadWarp = 8, kMmaWarp = 9;
+constexpr int kBox = kTile * 128;       // bytes of 128 rows x 64 bf16
+constexpr uint32_t kColS = 0, kColO = 256;
+constexpr float kGrow = 8.f;            // log2 units m may lag behind
+constexpr int kSlotsTc = 3;             // first, last, exchange of the halves
+constexpr int kSlotExchange = 2;
+
+struct Bars {
+    uint64_t full[kStages], empty[kStages];
+    uint64_t q_full, q_empty;
+    uint64_t s_full[2], p_full[2], o_full[2];
+    uint64_t half_full, wg[2], drain;
+    uint32_t tmem;
+    volatile int abort_flag;
+    int dirty;            // some value taken out of V
+    int last[2];
+    int64_t plan[kThreads / 32 + 4];
+};
+
+template <int KH>
+constexpr size_t smem_bytes() {
+    return 1024 + (size_t)(2 + kStages) * KH * kBox + sizeof(Bars);
+}
+
+__device__ __forceinline__ void tma_load_4d(const CUtensorMap *map, uint64_t *bar, void *dst, int c0,
+                                            int c1, int c2, int c3) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
+}
+
+// O += P V: A (bf16 pairs along K) in TMEM, B in shared memory.
+__device__ __forceinline__ void tc_mma_bf16_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                                   uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Operand in the 128-byte swizzled layout TMA writes.  K-major: lbo unused,
+// sbo between 8-row groups.  MN-major: lbo between blocks of 64 elements of MN,
+// sbo between groups of 8 rows of K.
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+    return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | static_cast<uint64_t>(lbo >> 4) << 16 |
+           static_cast<uint64_t>(sbo >> 4) << 32 | static_cast<uint64_t>(1) << 46 |
+           static_cast<uint64_t>(2) << 61;
+}
+
+__device__ __forceinline__ void fence_async_shared() {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// The bounded wait, its outcome the same for the whole warp (what follows is
+// warp-wide).
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *stop,
+                                          uint32_t *status) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, stop, status));
+}
+
+// What a CTA does of one unit: key tiles [first, first + n) of the list; half t
+// takes cnt[t] of them, every one (paired) or every other (split).
+struct Segment {
+    bool split, whole, begins;   // begins: the unit's first step is in it
+    int first, n, cnt[2];
+};
+
+__device__ __forceinline__ Segment segment_of(const AttendParams &p, const AttendUnit &a, int s0, int s1) {
+    Segment g;
+    g.split = a.rows <= p.split_rows;
+    g.whole = s0 == 0 && s1 == a.steps;
+    g.begins = s0 == 0;
+    const int tiles = (a.hi + kTile - 1) / kTile;
+    if (g.split) {
+        g.first = 2 * s0;
+        g.n = max(0, min(2 * s1, tiles) - g.first);
+        g.cnt[0] = (g.n + 1) / 2;
+        g.cnt[1] = g.n / 2;
+    } else {
+        const int t0 = (attend_sees(p, a, p.split_rows - 1) + kTile - 1) / kTile;
+        g.first = s0;
+        g.cnt[0] = max(0, min(s1, t0) - s0);
+        g.cnt[1] = max(0, min(s1, tiles) - s0);
+        g.n = g.cnt[1];
+    }
+    return g;
+}
+
+// Order of the ring: paired K0 V0 K1 V1 ..; split K0 K1 V0 K2 V1 K3 .. V.
+__device__ __forceinline__ void load_at(const Segment &g, int l, bool *is_v, int *tile) {
+    if (!g.split) {
+        *is_v = l & 1;
+        *tile = l >> 1;
+        return;
+    }
+    const int lead = min(2, g.n), m = l - lead;
+    if (m < 0) {
+        *is_v = false;
+        *tile = l;
+    } else if (m < 2 * (g.n - lead)) {
+        *is_v = !(m & 1);
+        *tile = (m >> 1) + ((m & 1) ? 2 : 0);
+    } else {
+        *is_v = true;
+        *tile = m - (g.n - lead);
+    }
+}
+// Place in it of V of the segment's tile i.
+__device__ __forceinline__ int v_at(const Segment &g, int i) {
+    return g.split ? min(2, g.n) + i + min(i, max(g.n - 2, 0)) : 2 * i + 1;
+}
+
+// Walks the units of the CTA's run.
+struct Walk {
+    AttendRun run;
+    int64_t pos, u, u_lo;
+    AttendUnit a;
+    Segment g;
+    __device__ explicit Walk(const AttendRun &r) : run(r), pos(r.lo), u(r.unit), u_lo(r.unit_lo) {}
+    __device__ bool next(const AttendParams &p) {
+        while (pos < run.hi) {
+            a = attend_unit(p, u);
+            if (a.steps == 0) {
+                u = attend_next(p, a, u);
+                continue;
+            }
+            const int64_t end = min(run.hi, u_lo + a.steps);
+            g = segment_of(p, a, (int)(pos - u_lo), (int)(end - u_lo));
+            lo = u_lo;
+            pos = end;
+            u_lo += a.steps;
+            u = attend_next(p, a, u);
+            return true;
+        }
+        return false;
+    }
+    int64_t lo;   // the unit's first step
+};
+
+template <int KH>
+__global__ void __launch_bounds__(kThreads, 1)
+    attend_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                     const __grid_constant__ CUtensorMap tv, const AttendParams p) {
+    constexpr int D = 64 * KH;
+    constexpr int kStageBytes = KH * kBox;
+    extern __shared__ uint8_t raw[];
+    uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *sq = base;                              // [2][KH][128 rows][128 B]
+    uint8_t *ring = base + 2 * kStageBytes;          // [stage][KH][128 keys][128 B]
+    Bars &b = *reinterpret_cast<Bars *>(ring + kStages * kStageBytes);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int R = p.split_rows;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&b.full[i], 1);
+            mbar_init(&b.empty[i], 1);
+        }
+        mbar_init(&b.q_full, 1);
+        mbar_init(&b.q_empty, 1);
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&b.s_full[t], 1);
+            mbar_init(&b.p_full[t], 4);
+            mbar_init(&b.o_full[t], 1);
+            mbar_init(&b.wg[t], 4);
+        }
+        mbar_init(&b.half_full, 4);
+        mbar_init(&b.drain, 1);
+        b.abort_flag = 0;
+        b.dirty = 0;
+        fence_barrier_init();
+    }
+    const AttendRun run = attend_plan<kThreads>(p, b.plan);
+    if (run.lo >= run.hi) return;   // more CTAs than steps
+    if (warp == kMmaWarp) {
+        tmem_alloc(&b.tmem, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = b.tmem;
+    volatile int *stop = &b.abort_flag;
+
+    if (warp >= kLoadWarp) {
+    regs_dec<kRegsOther>();
+    if (warp == kLoadWarp) {
+        // ------------------------------------------------ loads
+        if (lane == 0) {
+            tma_prefetch_desc(&tq);
+            tma_prefetch_desc(&tk);
+            tma_prefetch_desc(&tv);
+        }
+        uint32_t fill = 0, segs = 0;   // ring stages filled, segments
+        bool ok = true;
+        const int per_tile = kTile >> p.shift, ps = 1 << p.shift;
+        Walk w(run);
+        while (ok && w.next(p)) {
+            const Segment &g = w.g;
+            if (g.n == 0) continue;
+            // Q once the segment before has used it
+            ok = segs == 0 || warp_wait(&b.q_empty, (segs - 1) & 1, stop, p.status);
+            if (!ok) break;
+            if (lane == 0) {
+                const int tiles = g.split ? 1 : 2;
+                mbar_arrive_expect_tx(&b.q_full, (uint32_t)(tiles * KH * R * 128));
+                for (int t = 0; t < tiles; ++t)
+                    for (int kh = 0; kh < KH; ++kh)
+                        tma_load_4d(&tq, &b.q_full, sq + t * kStageBytes + kh * kBox, kh * 64, 0, w.a.h,
+                                    w.a.q0 + (w.a.row0 + t * R) / p.group);
+            }
+            ++segs;
+            const int loads = 2 * g.n;
+            for (int l = 0; l < loads; ++l, ++fill) {
+                bool is_v;
+                int tile;
+                load_at(g, l, &is_v, &tile);
+                tile += g.first;
+                // the tile's pages that hold visible rows
+                const int left = w.a.hi - tile * kTile;
+                const int pages = min(per_tile, (left + ps - 1) >> p.shift);
+                int page = 0;
+                if (lane < pages) {
+                    page = attend_page(p, w.a.list, tile * per_tile + lane);
+                    if (page < 0) page = p.n_pages;   // outside the tensor: zeros
+                }
+                const uint32_t st = fill % kStages;
+                ok = fill < kStages || warp_wait(&b.empty[st], (fill / kStages - 1) & 1, stop, p.status);
+                if (!ok) break;
+                if (lane == 0) mbar_arrive_expect_tx(&b.full[st], (uint32_t)(pages * ps * D * 2));
+                __syncwarp();
+                if (lane < pages) {
+                    uint8_t *dst = ring + st * kStageBytes + (lane << p.shift) * 128;
+#pragma unroll
+                    for (int kh = 0; kh < KH; ++kh)
+                        tma_load_3d(is_v ? &tv : &tk, &b.full[st], dst + kh * kBox, kh * 64, 0, page);
+                }
+            }
+        }
+        if (*stop) {   // unwind: every copy started must land
+            for (uint32_t f = fill > kStages ? fill - kStages : 0; f < fill; ++f)
+                mbar_drain(&b.full[f % kStages], (f / kStages) & 1);
+            if (segs) mbar_drain(&b.q_full, (segs - 1) & 1);
+        }
+    } else if (warp == kMmaWarp) {
+        // ------------------------------------------------ MMA issue
+        if (lane == 0) {
+            constexpr uint32_t kIdS = idesc_bf16_f32(kTile, kTile);
+            constexpr uint32_t kIdO = idesc_bf16_f32(kTile, D) | (1u << 16);   // B MN-major
+            uint32_t use = 0, segs = 0, np[2] = {0, 0};   // ring stages used, P tiles seen
+            const uint64_t qd = desc_sw128(smem_u32(sq), 16, 1024);
+            auto stage_full = [&](uint32_t f) {
+                return mbar_wait(&b.full[f % kStages], (f / kStages) & 1, stop, p.status);
+            };
+            auto issue_s = [&](int t, bool split, uint32_t f) {
+                const uint64_t a = qd + (split ? 0 : (uint64_t)((t * kStageBytes) >> 4));
+                const uint64_t k = desc_sw128(smem_u32(ring + (f % kStages) * kStageBytes), 16, 1024);
+#pragma unroll
+                for (int ks = 0; ks < 4 * KH; ++ks) {
+                    const uint64_t off = (uint64_t)(((ks >> 2) * kBox + (ks & 3) * 32) >> 4);
+                    tc_mma_bf16(tmem + kColS + t * 128, a + off, k + off, kIdS, ks > 0);
+                }
+                tc_commit(&b.s_full[t]);
+            };
+            auto issue_o = [&](int t, uint32_t f, bool add) {
+                const uint64_t v = desc_sw128(smem_u32(ring + (f % kStages) * kStageBytes), kBox, 1024);
+#pragma unroll
+                for (int ks = 0; ks < kTile / 16; ++ks)
+                    tc_mma_bf16_tmem_a(tmem + kColO + t * 128, tmem + kColS + t * 128 + ks * 8,
+                                       v + (uint64_t)(ks * (16 * 128 >> 4)), kIdO, add || ks > 0);
+            };
+            bool ok = true;
+            Walk w(run);
+            while (ok && w.next(p)) {
+                const Segment &g = w.g;
+                if (g.n == 0) continue;
+                if (!(ok = mbar_wait(&b.q_full, segs & 1, stop, p.status))) break;
+                ++segs;
+                tc_fence_after();
+                if (!g.split) {
+                    for (int i = -1; ok && i < g.n; ++i) {
+                        // ring: V i at use, K i+1 behind it
+                        const uint32_t fv = use, fk = use + (i >= 0 ? 1 : 0);
+                        const bool more = i + 1 < g.n;
+                        if (i >= 0 && !(ok = stage_full(fv))) break;
+                        for (int t = 0; ok && t < 2; ++t) {
+                            if (i >= 0 && i < g.cnt[t]) {
+                                if (!(ok = mbar_wait(&b.p_full[t], np[t] & 1, stop, p.status))) break;
+                                ++np[t];
+                                tc_fence_after();
+                                issue_o(t, fv, i > 0);
+                                if (i + 1 == g.cnt[t]) tc_commit(&b.o_full[t]);
+                            }
+                            if (t == 1 && i >= 0) tc_commit(&b.empty[fv % kStages]);
+                            if (i + 1 < g.cnt[t]) {
+                                if (!(ok = stage_full(fk))) break;
+                                tc_fence_after();
+                                issue_s(t, false, fk);
+                            }
+                        }
+                        if (!ok) break;
+                        if (more) {
+                            tc_commit(&b.empty[fk % kStages]);
+                            if (i + 2 == g.n) tc_commit(&b.q_empty);
+                        }
+                        use = fk + (more ? 1 : 0);
+                    }
+                } else {
+                    const int lead = min(2, g.n);
+                    for (int i = 0; ok && i < lead; ++i, ++use) {
+                        if (!(ok = stage_full(use))) break;
+                        tc_fence_after();
+                        issue_s(i, true, use);
+                        tc_commit(&b.empty[use % kStages]);
+                        if (i + 1 == g.n) tc_commit(&b.q_empty);
+                    }
+                    for (int i = 0; ok && i < g.n; ++i) {
+                        const int t = i & 1;
+                        if (!(ok = stage_full(use))) break;
+                        if (!(ok = mbar_wait(&b.p_full[t], np[t] & 1, stop, p.status))) break;
+                        ++np[t];
+                        tc_fence_after();
+                        issue_o(t, use, i >= 2);
+                        tc_commit(&b.empty[use % kStages]);
+                        ++use;
+                        if (i + 2 < g.n) {
+                            if (!(ok = stage_full(use))) break;
+                            tc_fence_after();
+                            issue_s(t, true, use);
+                            tc_commit(&b.empty[use % kStages]);
+                            ++use;
+                            if (i + 3 == g.n) tc_commit(&b.q_empty);
+                        } else {
+                            tc_commit(&b.o_full[t]);
+                        }
+                    }
+                }
+            }
+            tc_commit(&b.drain);
+            mbar_drain(&b.drain, 0);
+        }
+    }
+    } else {
+        // ------------------------------------------------ softmax and output
+        regs_inc<kRegsSoftmax>();
+        const int t = warp >> 2, quarter = warp & 3;
+        const int r = quarter * 32 + lane;   // row of the tile
+        const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+        const uint32_t cs = tmem + lanes + kColS + t * 128, co = tmem + lanes + kColO + t * 128;
+        const bool flip = p.scale_log2 < 0.f;   // maxima are taken of S itself
+        const float c = fabsf(p.scale_log2);
+        const unsigned long long c2 = f2_pack(c, c);
+        uint32_t ns = 0, no = 0, nwg = 0, nhalf = 0, filled = 0;
+        bool ok = true;
+        Walk w(run);
+        while (ok && w.next(p)) {
+            const AttendUnit &a = w.a;
+            const Segment &g = w.g;
+            const int rt = g.split ? r : t * R + r;
+            const bool real = r < R && rt < a.rows;
+            const bool any = __any_sync(0xffffffffu, real);
+            const int sees = real ? attend_sees(p, a, rt) : 0;
+            const int sees0 = attend_sees(p, a, g.split ? 0 : t * R);   // the tile's first row's
+            float m = -INFINITY, l = 0.f;
+            const int cnt = g.cnt[t];
+            for (int i = 0; i < cnt; ++i) {
+                const int ti = g.split ? 2 * i + t : i;
+                const int k0 = (g.first + ti) * kTile;
+                if (!(ok = warp_wait(&b.s_full[t], ns & 1, stop, p.status))) break;
+                ++ns;
+                tc_fence_after();
+                const bool edge = k0 + kTile > sees0;
+                if (any) {
+                    float v[4][32];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) tmem_ld32(cs + q * 32, v[q]);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) reg_fence(v[q]);
+                    const int lim = sees - k0;   // keys of the tile the row sees
+                    if (flip) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) v[q][j] = -v[q][j];
+                    }
+                    if (edge) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (q * 32 + j >= lim) v[q][j] = -INFINITY;
+                    }
+                    float x[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        x[q] = fmax3(v[q][0], v[q][1], v[q][2]);
+#pragma unroll
+                        for (int j = 3; j < 31; j += 2) x[q] = fmax3(x[q], v[q][j], v[q][j + 1]);
+                        x[q] = fmaxf(x[q], v[q][31]);
+                    }
+                    const float s_top = fmaxf(fmax3(x[0], x[1], x[2]), x[3]);
+                    // -inf where the row sees nothing yet, also at c = 0
+                    const float top = s_top == -INFINITY ? -INFINITY : s_top * c;
+                    if (i == 0) {
+                        m = top;
+                    } else {
+                        const bool grow = top > m + kGrow;
+                        if (__any_sync(0xffffffffu, grow)) {
+                            // every product of this half up to the tile before is done: S came after it
+                            const float down = grow ? ex2(m - top) : 1.f;
+                            if (grow) m = top;
+                            l *= down;
+#pragma unroll 1
+                            for (int d = 0; d < D; d += 32) {
+                                float o[32];
+                                uint32_t ou[32];
+                                tmem_ld32(co + d, o);
+                                tmem_ld_wait();
+                                reg_fence(o);
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) ou[j] = __float_as_uint(o[j] * down);
+                                tmem_st32(co + d, ou);
+                            }
+                        }
+                    }
+                    const float nm = m == -INFINITY ? 0.f : -m;
+                    const unsigned long long nm2 = f2_pack(nm, nm);
+                    unsigned long long sum2[2] = {0, 0};
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t pw[32];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            const int q = 2 * h + (j >> 4), e = 2 * (j & 15);
+                            float y0, y1;
+                            f2_unpack(f2_fma(f2_pack(v[q][e], v[q][e + 1]), c2, nm2), y0, y1);
+                            float p0 = ex2(y0), p1 = ex2(y1);
+                            if (edge) {   // -inf * 0 is no number: mask again
+                                if (64 * h + 2 * j >= lim) p0 = 0.f;
+                                if (64 * h + 2 * j + 1 >= lim) p1 = 0.f;
+                            }
+                            sum2[j & 1] = f2_add(sum2[j & 1], f2_pack(p0, p1));
+                            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(pw[j]) : "f"(p1), "f"(p0));
+                        }
+                        tmem_st32(cs + h * 32, pw);
+                    }
+                    float s0, s1;
+                    f2_unpack(f2_add(sum2[0], sum2[1]), s0, s1);
+                    l += s0 + s1;
+                    tmem_st_wait();
+                }
+                if (edge) {
+                    // V's rows from the first that some row of the tile does not see
+                    const uint32_t f = filled + v_at(g, ti);
+                    if (!(ok = warp_wait(&b.full[f % kStages], (f / kStages) & 1, stop, p.status))) break;
+                    if (k0 + r >= sees0) {
+                        uint8_t *row = ring + (f % kStages) * kStageBytes + r * 128;
+                        const bool inside = k0 + r < a.len;
+                        bool found = false;
+                        for (int kh = 0; kh < KH; ++kh)
+                            for (int ch = 0; ch < 8; ++ch) {
+                                uint4 *at = reinterpret_cast<uint4 *>(row + kh * kBox + ch * 16);
+                                uint4 x = *at;
+                                uint32_t *xs = &x.x;
+                                bool put = false;
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    if ((xs[e] & 0x7f80u) == 0x7f80u) {
+                                        xs[e] &= 0xffff0000u;
+                                        put = true;
+                                    }
+                                    if ((xs[e] & 0x7f800000u) == 0x7f800000u) {
+                                        xs[e] &= 0xffffu;
+                                        put = true;
+                                    }
+                                }
+                                if (put) *at = x;
+                                found |= put;
+                            }
+                        if (found && inside) *static_cast<volatile int *>(&b.dirty) = 1;
+                    }
+                    fence_async_shared();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&b.p_full[t]);
+            }
+            if (!ok) break;
+            if (cnt > 0) {
+                if (!(ok = warp_wait(&b.o_full[t], no & 1, stop, p.status))) break;
+                ++no;
+                tc_fence_after();
+            }
+            filled += 2 * g.n;
+            // where this half's rows go: straight out, to the other half, or to a slot
+            const bool direct = g.whole && !g.split;
+            const bool hand = g.whole && g.split && t == 1;
+            const bool keep = g.whole && g.split && t == 0;
+            const int slot_of_cta = g.whole ? kSlotExchange : g.begins ? kSlotLast : kSlotFirst;
+            const int half = slot_of_cta == kSlotExchange ? (int)(nhalf & 1) : t;
+            const int64_t slot = ((int64_t)blockIdx.x * kSlotsTc + slot_of_cta) * p.slot_rows + half * kTile + r;
+            if (keep && g.cnt[1] > 0) {   // the other half's rows of this unit
+                if (!(ok = warp_wait(&b.half_full, nhalf & 1, stop, p.status))) break;
+            }
+            if (any && !(hand && cnt == 0)) {
+                float other_w = 0.f, mine_w = 1.f;
+                if (keep && g.cnt[1] > 0 && real) {
+                    const float2 st = __ldcg(&p.stat[slot]);
+                    const float top = fmaxf(m, st.x), ref = top == -INFINITY ? 0.f : top;
+                    mine_w = ex2(m - ref);
+                    other_w = ex2(st.x - ref);
+                    l = l * mine_w + st.y * other_w;
+                    m = top;
+                }
+                const float inv = sees > 0 ? 1.f / l : 0.f;
+                const int64_t out_row = real ? attend_out_row(p, a, rt) : 0;
+                const int from = attend_sees(p, a, 0);   // first key taken out of V
+                const bool dirty = *static_cast<volatile int *>(&b.dirty);
+#pragma unroll 1
+                for (int d = 0; d < D; d += 32) {
+                    __syncwarp();
+                    float o[32];
+                    if (cnt > 0) {
+                        tmem_ld32(co + d, o);
+                        tmem_ld_wait();
+                        reg_fence(o);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) o[j] = 0.f;
+                    }
+                    if (dirty && real) {   // what was taken out, for rows that see it
+                        const int k1 = min(sees, (g.first + g.n) * kTile);
+                        for (int k = max(from, g.first * kTile); k < k1; ++k) {
+                            if (g.split && ((k / kTile - g.first) & 1) != t) continue;
+                            const int page = p.table[(int64_t)a.list * p.max_pages + (k >> p.shift)];
+                            if (page < 0 || page >= p.n_pages) continue;
+                            const uint16_t *vr = static_cast<const uint16_t *>(p.v_pool) +
+                                (((int64_t)page << p.shift) + (k & ((1 << p.shift) - 1))) * D + d;
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) {
+                                const uint32_t bits = vr[j];
+                                if ((bits & 0x7f80u) == 0x7f80u) o[j] += __uint_as_float(bits << 16);
+                            }
+                        }
+                    }
+                    if (!real) continue;
+                    if (direct || keep) {
+                        if (keep && g.cnt[1] > 0) {
+                            const float4 *src = reinterpret_cast<const float4 *>(p.part + slot * D + d);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                const float4 y = __ldcg(src + j);
+                                o[4 * j] = o[4 * j] * mine_w + y.x * other_w;
+                                o[4 * j + 1] = o[4 * j + 1] * mine_w + y.y * other_w;
+                                o[4 * j + 2] = o[4 * j + 2] * mine_w + y.z * other_w;
+                                o[4 * j + 3] = o[4 * j + 3] * mine_w + y.w * other_w;
+                            }
+                        }
+                        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + out_row * D + d);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            uint32_t q[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                // a row that sees nothing: zeros, whatever O holds
+                                const float y0 = sees > 0 ? o[8 * j + 2 * e] * inv : 0.f;
+                                const float y1 = sees > 0 ? o[8 * j + 2 * e + 1] * inv : 0.f;
+                                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(q[e]) : "f"(y1), "f"(y0));
+                            }
+                            dst[j] = make_uint4(q[0], q[1], q[2], q[3]);
+                        }
+                    } else {
+                        float4 *dst = reinterpret_cast<float4 *>(p.part + slot * D + d);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            dst[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                    }
+                }
+                if (real) {
+                    if (direct || keep)
+                        attend_store_lse(p, out_row, m, l, sees > 0);
+                    else
+                        p.stat[slot] = make_float2(m, l);
+                }
+            }
+            __syncwarp();
+            tc_fence_before();   // O is read: the next unit's products may overwrite it
+            if (g.whole && g.split) {
+                if (g.cnt[1] > 0) {
+                    if (hand) {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&b.half_full);
+                    }
+                    ++nhalf;
+                }
+            } else if (!g.whole) {
+                // the last of the CTAs (and, where both halves hold the same rows, halves) joins
+                const int c0 = attend_cta_of(run.total, run.grid, w.lo);
+                const int c1 = attend_cta_of(run.total, run.grid, w.lo + a.steps - 1);
+                __threadfence();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&b.wg[t]);
+                if (!(ok = warp_wait(&b.wg[t], nwg++ & 1, stop, p.status))) break;
+                if (quarter == 0 && lane == 0) {
+                    uint32_t *count = &p.arrived[2 * c0 + (g.split ? 0 : t)];
+                    const uint32_t all = (uint32_t)(c1 - c0 + 1) * (g.split ? 2u : 1u);
+                    const bool last = atomicAdd(count, 1u) == all - 1;
+                    if (last) *count = 0;
+                    __threadfence();
+                    b.last[t] = last;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&b.wg[t]);
+                if (!(ok = warp_wait(&b.wg[t], nwg++ & 1, stop, p.status))) break;
+                if (*static_cast<volatile int *>(&b.last[t])) {
+                    __threadfence();
+                    const int first_row = g.split ? 0 : t * R;
+                    const int rows = min(a.rows - first_row, R);
+                    const int halves = g.split ? 2 : 1;
+                    constexpr int kVec = D / 4;
+                    for (int x = r; x < rows * kVec; x += kTile) {
+                        const int rr = x / kVec, d = (x - rr * kVec) * 4;
+                        auto at = [&](int cta, int h) {
+                            return ((int64_t)cta * kSlotsTc + (cta == c0 ? kSlotLast : kSlotFirst)) * p.slot_rows +
+                                   (g.split ? h : t) * kTile + rr;
+                        };
+                        float top = -INFINITY;
+                        for (int cta = c0; cta <= c1; ++cta)
+                            for (int h = 0; h < halves; ++h) top = fmaxf(top, __ldcg(&p.stat[at(cta, h)]).x);
+                        const float ref = top == -INFINITY ? 0.f : top;
+                        float sum = 0.f;
+                        float4 acc = make_float4(0, 0, 0, 0);
+                        for (int cta = c0; cta <= c1; ++cta)
+                            for (int h = 0; h < halves; ++h) {
+                                const int64_t s = at(cta, h);
+                                const float2 st = __ldcg(&p.stat[s]);
+                                const float4 y = __ldcg(reinterpret_cast<const float4 *>(p.part + s * D + d));
+                                const float wgt = ex2(st.x - ref);
+                                sum = fmaf(st.y, wgt, sum);
+                                acc.x = fmaf(y.x, wgt, acc.x);
+                                acc.y = fmaf(y.y, wgt, acc.y);
+                                acc.z = fmaf(y.z, wgt, acc.z);
+                                acc.w = fmaf(y.w, wgt, acc.w);
+                            }
+                        const bool see = attend_sees(p, a, first_row + rr) > 0;
+                        const float inv = 1.f / sum;
+                        const int64_t row = attend_out_row(p, a, first_row + rr);
+                        uint32_t q0, q1;
+                        const float y0 = see ? acc.x * inv : 0.f, y1 = see ? acc.y * inv : 0.f;
+                        const float y2 = see ? acc.z * inv : 0.f, y3 = see ? acc.w * inv : 0.f;
+                        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(q0) : "f"(y1), "f"(y0));
+                        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(q1) : "f"(y3), "f"(y2));
+                        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + row * D + d) = make_uint2(q0, q1);
+                        if (d == 0) attend_store_lse(p, row, top, sum, see);
+                    }
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int KH>
+int launch(AttendParams &p, int grid, cudaStream_t st) {
+    const uint64_t D = 64 * KH, G = p.group;
+    const uint32_t tokens = kTile / p.group;
+    CUtensorMap tq, tk, tv;
+    const uint64_t dims[4] = {D, G, (uint64_t)p.n_kv_heads, (uint64_t)p.n_tokens};
+    const uint64_t strides[3] = {D * 2, G * D * 2, (uint64_t)p.q_stride * 2};
+    const uint32_t box[4] = {64, (uint32_t)G, 1, tokens};
+    const uint64_t ps = (uint64_t)1 << p.shift;
+    if (!make_tma_map_nd(&tq, p.q, 4, dims, strides, box) ||
+        !make_tma_map(&tk, p.k_pool, D, ps, (uint64_t)p.n_pages, (uint32_t)ps) ||
+        !make_tma_map(&tv, p.v_pool, D, ps, (uint64_t)p.n_pages, (uint32_t)ps)) {
+        set_error("kvc_attend: cuTensorMapEncodeTiled failed (alignment or driver)");
+        return KVC_ERR_CUDA;
+    }
+    constexpr size_t bytes = smem_bytes<KH>();
+    static_assert(bytes <= 232448, "shared memory of one block");
+    static const int regs = [] {
+        cudaFuncAttributes at{};
+        return cudaFuncGetAttributes(&at, attend_tc_kernel<KH>) == cudaSuccess ? at.numRegs : 0;
+    }();
+    if (regs != kRegsLaunch) {
+        set_error("kvc_attend: the tensor-core kernel has %d registers per thread, its split needs %d", regs,
+                  kRegsLaunch);
+        return KVC_ERR_UNSUPPORTED;
+    }
+    cudaFuncSetAttribute(attend_tc_kernel<KH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    attend_tc_kernel<KH><<<grid, kThreads, bytes, st>>>(tq, tk, tv, p);
+    return cache_launched("kvc_attend");
+}
+
+}  // namespace
+
+AttendNeeds attend_tc_needs(int sms) { return {sms, kSlotsTc, 2 * kTile}; }
+
+bool attend_tc_takes(int dtype, int dim, int group) {
+    return dtype == KVC_BF16 && (dim == 64 || dim == 128) && group <= kTile;
+}
+
+int launch_attend_tc(AttendParams &p, int grid, cudaStream_t st) {
+    const int R = kTile / p.group * p.group;   // whole tokens
+    p.unit_rows = 2 * R;
+    p.split_rows = R;
+    p.step_keys = kTile;
+    p.blocks = (p.max_new * p.group + 2 * R - 1) / (2 * R);
+    p.n_units = (int64_t)p.n_seqs * p.n_kv_heads * p.blocks;
+    return p.dim == 64 ? launch<1>(p, grid, st) : launch<2>(p, grid, st);
+}
+
+}  // namespace kvc

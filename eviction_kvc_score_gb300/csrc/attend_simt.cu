@@ -6,52 +6,90 @@
 // log2 units, so that one ex2 gives a probability):
 //   m' = max(m, max_j x_j),  l' = l 2^(m - m') + sum_j 2^(x_j - m'),
 //   o' = o 2^(m - m') + sum_j 2^(x_j - m') v_j,  out = o / l.
-// A block holds kRows rows (tokens x query heads of one KV head) and walks 64-key
-// tiles through shared memory; 16 x 16 threads each own kRows/16 rows x 4 keys of
-// the logits and kRows/16 rows x D/16 columns of o.
+//
+// A block of 128 threads holds ROWS rows (tokens x query heads of one KV head)
+// and walks 64-key tiles; a thread owns 4 rows x 64/TX keys of the logits and
+// the same 4 rows x D/TX columns of o, TX = 8 for 64 rows, 32 for 16.  With 64
+// rows the work is bound by the FMA pipe: 12 16-byte shared loads feed 128 FMAs
+// (as 64 two-wide ones) of the logits, 5 feed 64 of the output at D = 128.  With
+// 16 (decode) it is bound by reading the cache.  K of the next tile is on its
+// way (cp.async) during the product with V, V of the next during the logits.
+// K and V stay in shared memory in their own type; a row is padded by 16 bytes,
+// which spreads 8 rows' loads over all banks for every D that is a multiple of 8.
+#include <algorithm>
+#include <type_traits>
+
 #include "attend.cuh"
 
 namespace kvc {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kKeys = 64;
 constexpr int kSlotRows = 64;
-
-template <int ROWS, int DMAX>
-struct SimtSmem {
-    float q[ROWS][DMAX + 4];
-    float k[kKeys][DMAX + 4];
-    float v[kKeys][DMAX];
-    float pr[ROWS][kKeys + 4];
-    int64_t plan[kThreads / 32 + 4];
-    uint32_t last;
-};
+constexpr int kBlocksPerSm = 4;   // at most: the workspace's slots are sized by it
 
 template <typename T>
-__device__ __forceinline__ float4 load4(const T *p);
-template <>
-__device__ __forceinline__ float4 load4(const float *p) {
-    return *reinterpret_cast<const float4 *>(p);
+constexpr int row_bytes(int dim) {
+    return dim * (int)sizeof(T) + 16;
 }
-template <>
-__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
-    const uint2 w = *reinterpret_cast<const uint2 *>(p);
-    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
-                       __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
+template <typename T, int ROWS>
+size_t smem_bytes(int dim) {
+    return (size_t)ROWS * (dim + 4) * 4 + 2 * (size_t)kKeys * row_bytes<T>(dim) +
+           (size_t)kKeys * (ROWS + 4) * 4 + (kThreads / 32 + 6) * 8;
 }
-__device__ __forceinline__ void store1(float *p, float x) { *p = x; }
-__device__ __forceinline__ void store1(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
 
-template <typename T, int ROWS, int DMAX>
-__global__ void __launch_bounds__(kThreads) attend_simt_kernel(AttendParams p) {
+// Four elements as two pairs.
+struct Quad {
+    unsigned long long a, b;
+};
+__device__ __forceinline__ Quad quad(const float *p) {
+    const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(p);
+    return {x.x, x.y};
+}
+__device__ __forceinline__ Quad quad(const __nv_bfloat16 *p) {
+    const uint2 w = *reinterpret_cast<const uint2 *>(p);
+    return {f2_pack(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u)),
+            f2_pack(__uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u))};
+}
+__device__ __forceinline__ void store4(float *p, float4 x) { *reinterpret_cast<float4 *>(p) = x; }
+__device__ __forceinline__ void store4(__nv_bfloat16 *p, float4 x) {
+    uint32_t a, b;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(a) : "f"(x.y), "f"(x.x));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(b) : "f"(x.w), "f"(x.z));
+    *reinterpret_cast<uint2 *>(p) = make_uint2(a, b);
+}
+
+// 16 bytes global -> shared, zeros where !valid (src is then not read).
+__device__ __forceinline__ void copy16(void *dst, const void *src, bool valid) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
+                 "r"(valid ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// CT: 16-byte (fp32) column chunks of a thread, CT * TX * 4 >= D.
+template <typename T, int ROWS, int CT>
+__global__ void __launch_bounds__(kThreads) attend_simt_kernel(const AttendParams p) {
+    constexpr int TX = ROWS == 64 ? 8 : 32, KT = kKeys / TX;
+    static_assert(TX * (ROWS / 4) == kThreads, "four rows per thread");
     extern __shared__ __align__(16) uint8_t raw[];
-    auto &s = *reinterpret_cast<SimtSmem<ROWS, DMAX> *>(raw);
-    constexpr int RT = ROWS / 16, CT = DMAX / 16;   // rows and columns of a thread
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-    const int D = p.dim, D4 = D / 4;
-    const AttendRun run = attend_plan<kThreads>(p, s.plan);
+    const int D = p.dim, rb = row_bytes<T>(D), vecs = D * (int)sizeof(T) / 16;
+    float *sq = reinterpret_cast<float *>(raw);            // [ROWS][D + 4]
+    uint8_t *sk = raw + ROWS * (D + 4) * 4;                // [64][rb]
+    uint8_t *sv = sk + kKeys * rb;
+    float *sp = reinterpret_cast<float *>(sv + kKeys * rb);   // [64 keys][ROWS + 4]
+    int64_t *plan = reinterpret_cast<int64_t *>(sp + kKeys * (ROWS + 4));
+    uint32_t *s_last = reinterpret_cast<uint32_t *>(plan + kThreads / 32 + 4);
+    const int tid = threadIdx.x, tx = tid % TX, ty = tid / TX;
+    const int pr = 1 << p.shift;
+
+    const AttendRun run = attend_plan<kThreads>(p, plan);
     if (run.lo >= run.hi) return;
     int64_t u = run.unit, u_lo = run.unit_lo;
     for (int64_t pos = run.lo; pos < run.hi;) {
@@ -62,142 +100,192 @@ __global__ void __launch_bounds__(kThreads) attend_simt_kernel(AttendParams p) {
         }
         const int64_t end = min(run.hi, u_lo + a.steps);
         const int t0 = (int)(pos - u_lo), t1 = (int)(end - u_lo);
-        const int rows = a.rows;
-        __syncthreads();   // the unit before is done with q
-        for (int i = tid; i < ROWS * D4; i += kThreads) {
-            const int r = i / D4, c = (i - r * D4) * 4;
-            float4 x = make_float4(0, 0, 0, 0);
-            if (r < rows) {
-                const int token = (a.row0 + r) / p.group, g = a.row0 + r - token * p.group;
-                x = load4(static_cast<const T *>(p.q) + (a.q0 + token) * p.q_stride +
-                          (int64_t)(a.h * p.group + g) * D + c);
-            }
-            *reinterpret_cast<float4 *>(&s.q[r][c]) = x;
-        }
-        float m[RT], l[RT], o[RT][CT];
-        int sees[RT];
+        // eight threads copy a row, 16 rows at a time; pages are looked up
+        // ahead of the copies that use them
+        int page[4];
+        auto look_up = [&](int t) {
 #pragma unroll
-        for (int i = 0; i < RT; ++i) {
-            const int r = ty * RT + i;
+            for (int i = 0; i < 4; ++i) {
+                const int j = t * kKeys + 16 * i + (tid >> 3);
+                page[i] = j < a.hi ? attend_page(p, a.list, j >> p.shift) : -1;
+            }
+        };
+        auto fetch = [&](uint8_t *dst, const void *pool, int t) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = 16 * i + (tid >> 3), j = t * kKeys + r;
+                const bool valid = page[i] >= 0;
+                const T *src = static_cast<const T *>(pool) +
+                               (((int64_t)(valid ? page[i] : 0) << p.shift) + (j & (pr - 1))) * D;
+                for (int v = tid & 7; v < vecs; v += 8)
+                    copy16(dst + r * rb + v * 16, reinterpret_cast<const uint4 *>(src) + v, valid);
+            }
+            copies_done();
+        };
+        __syncthreads();   // the unit before is done with shared memory
+        look_up(t0);
+        fetch(sk, p.k_pool, t0);
+        fetch(sv, p.v_pool, t0);
+        for (int i = tid; i < ROWS * (D / 4); i += kThreads) {
+            const int r = i / (D / 4), c = (i - r * (D / 4)) * 4;
+            Quad x{0, 0};
+            if (r < a.rows) {
+                const int token = (a.row0 + r) / p.group, g = a.row0 + r - token * p.group;
+                x = quad(static_cast<const T *>(p.q) + (a.q0 + token) * p.q_stride +
+                         (int64_t)(a.h * p.group + g) * D + c);
+            }
+            *reinterpret_cast<ulonglong2 *>(sq + r * (D + 4) + c) = make_ulonglong2(x.a, x.b);
+        }
+        float m[4], l[4];
+        unsigned long long o[4][2 * CT];
+        int sees[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = ty * 4 + i;
             m[i] = -INFINITY;
             l[i] = 0.f;
-            sees[i] = r < rows ? attend_sees(p, a, r) : 0;
+            sees[i] = r < a.rows ? attend_sees(p, a, r) : 0;
 #pragma unroll
-            for (int c = 0; c < CT; ++c) o[i][c] = 0.f;
+            for (int c = 0; c < 2 * CT; ++c) o[i][c] = 0;
         }
+        const int sees0 = attend_sees(p, a, 0);
+        const bool some = (tid & ~31) / TX * 4 < a.rows;   // the warp has a row
         for (int t = t0; t < t1; ++t) {
             const int j0 = t * kKeys;
-            __syncthreads();   // the tile before is done with k, v and pr
-            for (int i = tid; i < kKeys * D4; i += kThreads) {
-                const int j = i / D4, c = (i - j * D4) * 4;
-                float4 kk = make_float4(0, 0, 0, 0), vv = kk;
-                if (j0 + j < a.hi) {
-                    const int page = attend_page(p, a.list, (j0 + j) >> p.shift);
-                    if (page >= 0) {
-                        const int64_t at = ((((int64_t)page << p.shift) + ((j0 + j) & ((1 << p.shift) - 1))) * D) + c;
-                        kk = load4(static_cast<const T *>(p.k_pool) + at);
-                        vv = load4(static_cast<const T *>(p.v_pool) + at);
-                    }
-                }
-                *reinterpret_cast<float4 *>(&s.k[j][c]) = kk;
-                *reinterpret_cast<float4 *>(&s.v[j][c]) = vv;
-            }
-            __syncthreads();
-            // logits of rows ty*RT.. and keys tx, tx+16, tx+32, tx+48
-            float x[RT][4];
+            const bool more = t + 1 < t1, edge = j0 + kKeys > sees0;
+            copies_wait<1>();
+            __syncthreads();   // K and q are here
+            if (more) look_up(t + 1);
+            if (some) {
+                unsigned long long x2[4][KT];
 #pragma unroll
-            for (int i = 0; i < RT; ++i)
+                for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) x[i][j] = 0.f;
-            for (int c = 0; c < D; c += 4) {
-                float4 kk[4];
+                    for (int j = 0; j < KT; ++j) x2[i][j] = 0;
+                const float *q = sq + ty * 4 * (D + 4);
+#pragma unroll 2
+                for (int c = 0; c < D; c += 4) {
+                    Quad qq[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) kk[j] = *reinterpret_cast<const float4 *>(&s.k[tx + 16 * j][c]);
+                    for (int i = 0; i < 4; ++i) qq[i] = quad(q + i * (D + 4) + c);
 #pragma unroll
-                for (int i = 0; i < RT; ++i) {
-                    const float4 qq = *reinterpret_cast<const float4 *>(&s.q[ty * RT + i][c]);
+                    for (int j = 0; j < KT; ++j) {
+                        const Quad kk = quad(reinterpret_cast<const T *>(sk + (tx + TX * j) * rb) + c);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        x[i][j] = fmaf(qq.x, kk[j].x, x[i][j]);
-                        x[i][j] = fmaf(qq.y, kk[j].y, x[i][j]);
-                        x[i][j] = fmaf(qq.z, kk[j].z, x[i][j]);
-                        x[i][j] = fmaf(qq.w, kk[j].w, x[i][j]);
-                    }
-                }
-            }
-            bool cut = false;   // some row of the thread sees only part of the tile
-#pragma unroll
-            for (int i = 0; i < RT; ++i) {
-                const int left = sees[i] - j0;
-                cut |= left < kKeys;
-                float top = m[i];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    x[i][j] = tx + 16 * j < left ? x[i][j] * p.scale_log2 : -INFINITY;
-                    top = fmaxf(top, x[i][j]);
-                }
-#pragma unroll
-                for (int d = 8; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-                // all -inf so far: any finite reference gives 2^-inf = 0
-                const float ref = top == -INFINITY ? 0.f : top;
-                const float down = ex2(m[i] - ref);
-                float sum = 0.f;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float e = ex2(x[i][j] - ref);
-                    sum += e;
-                    s.pr[ty * RT + i][tx + 16 * j] = e;
-                }
-#pragma unroll
-                for (int d = 8; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-                l[i] = l[i] * down + sum;
-                m[i] = top;
-#pragma unroll
-                for (int c = 0; c < CT; ++c) o[i][c] *= down;
-            }
-            __syncthreads();
-            const int nk = min(kKeys, a.hi - j0);
-            for (int j = 0; j < nk; ++j) {
-                float e[RT];
-#pragma unroll
-                for (int i = 0; i < RT; ++i) e[i] = s.pr[ty * RT + i][j];
-#pragma unroll
-                for (int c = 0; c < CT; ++c) {
-                    const int col = tx + 16 * c;
-                    if (col < D) {
-                        const float vv = s.v[j][col];
-                        if (!cut) {
-#pragma unroll
-                            for (int i = 0; i < RT; ++i) o[i][c] = fmaf(e[i], vv, o[i][c]);
-                        } else {   // a value a row does not see may be anything
-#pragma unroll
-                            for (int i = 0; i < RT; ++i)
-                                if (j0 + j < sees[i]) o[i][c] = fmaf(e[i], vv, o[i][c]);
+                        for (int i = 0; i < 4; ++i) {
+                            x2[i][j] = f2_fma(qq[i].a, kk.a, x2[i][j]);
+                            x2[i][j] = f2_fma(qq[i].b, kk.b, x2[i][j]);
                         }
                     }
                 }
+                float x[4][KT];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float top = m[i];
+#pragma unroll
+                    for (int j = 0; j < KT; ++j) {
+                        float lo, hi;
+                        f2_unpack(x2[i][j], lo, hi);
+                        x[i][j] = (lo + hi) * p.scale_log2;
+                        if (edge && j0 + tx + TX * j >= sees[i]) x[i][j] = -INFINITY;
+                        top = fmaxf(top, x[i][j]);
+                    }
+#pragma unroll
+                    for (int d = TX / 2; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                    // all -inf so far: any finite reference gives 2^-inf = 0
+                    const float ref = top == -INFINITY ? 0.f : top;
+                    const float down = ex2(m[i] - ref);
+                    float sum = 0.f;
+#pragma unroll
+                    for (int j = 0; j < KT; ++j) {
+                        x[i][j] = ex2(x[i][j] - ref);
+                        sum += x[i][j];
+                    }
+#pragma unroll
+                    for (int d = TX / 2; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                    l[i] = l[i] * down + sum;
+                    m[i] = top;
+                    const unsigned long long down2 = f2_pack(down, down);
+#pragma unroll
+                    for (int c = 0; c < 2 * CT; ++c) o[i][c] = f2_mul(o[i][c], down2);
+                }
+#pragma unroll
+                for (int j = 0; j < KT; ++j)
+                    *reinterpret_cast<float4 *>(sp + (tx + TX * j) * (ROWS + 4) + ty * 4) =
+                        make_float4(x[0][j], x[1][j], x[2][j], x[3][j]);
             }
+            __syncthreads();   // K is read, p is here
+            if (more)
+                fetch(sk, p.k_pool, t + 1);
+            else
+                copies_done();   // an empty group keeps the count
+            copies_wait<1>();
+            __syncthreads();   // V is here
+            if (some) {
+                auto product = [&](auto cut) {
+                    const int nk = min(kKeys, a.hi - j0);
+#pragma unroll 2
+                    for (int j = 0; j < nk; ++j) {
+                        const float4 e = *reinterpret_cast<const float4 *>(sp + j * (ROWS + 4) + ty * 4);
+                        const unsigned long long e2[4] = {f2_pack(e.x, e.x), f2_pack(e.y, e.y),
+                                                          f2_pack(e.z, e.z), f2_pack(e.w, e.w)};
+                        const T *v = reinterpret_cast<const T *>(sv + j * rb);
+#pragma unroll
+                        for (int c = 0; c < CT; ++c) {
+                            const int col = (tx + TX * c) * 4;
+                            if (CT * TX * 4 == D || col < D) {
+                                const Quad vv = quad(v + col);
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    // a value that a row does not see may be anything
+                                    if (!decltype(cut)::value || j0 + j < sees[i]) {
+                                        o[i][2 * c] = f2_fma(e2[i], vv.a, o[i][2 * c]);
+                                        o[i][2 * c + 1] = f2_fma(e2[i], vv.b, o[i][2 * c + 1]);
+                                    }
+                            }
+                        }
+                    }
+                };
+                if (edge)
+                    product(std::true_type{});
+                else
+                    product(std::false_type{});
+            }
+            __syncthreads();   // V and p are read
+            if (more)
+                fetch(sv, p.v_pool, t + 1);
+            else
+                copies_done();
         }
         // whole units go straight out, shared ones through the slots
         const bool whole = t0 == 0 && t1 == a.steps;
-        const int slot = 2 * blockIdx.x + (t0 == 0 ? kSlotLast : kSlotFirst);
+        const int64_t slot = (int64_t)blockIdx.x * p.slots + (t0 == 0 ? kSlotLast : kSlotFirst);
 #pragma unroll
-        for (int i = 0; i < RT; ++i) {
-            const int r = ty * RT + i;
-            if (r >= rows) continue;
-            if (whole) {
-                const int64_t row = attend_out_row(p, a, r);
-                T *out = static_cast<T *>(p.out) + row * D;
+        for (int i = 0; i < 4; ++i) {
+            const int r = ty * 4 + i;
+            if (r >= a.rows) continue;
+            const int64_t row = attend_out_row(p, a, r);
+            const float inv = sees[i] > 0 ? 1.f / l[i] : 0.f;
 #pragma unroll
-                for (int c = 0; c < CT; ++c)
-                    if (tx + 16 * c < D) store1(out + tx + 16 * c, sees[i] > 0 ? o[i][c] / l[i] : 0.f);
-                if (tx == 0) attend_store_lse(p, row, m[i], l[i], sees[i] > 0);
-            } else {
-                float *part = p.part + ((int64_t)slot * p.slot_rows + r) * D;
-#pragma unroll
-                for (int c = 0; c < CT; ++c)
-                    if (tx + 16 * c < D) part[tx + 16 * c] = o[i][c];
-                if (tx == 0) p.stat[(int64_t)slot * p.slot_rows + r] = make_float2(m[i], l[i]);
+            for (int c = 0; c < CT; ++c) {
+                const int col = (tx + TX * c) * 4;
+                if (col >= D) continue;
+                float4 y;
+                f2_unpack(o[i][2 * c], y.x, y.y);
+                f2_unpack(o[i][2 * c + 1], y.z, y.w);
+                if (whole) {
+                    y = sees[i] > 0 ? make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv)
+                                    : make_float4(0, 0, 0, 0);
+                    store4(static_cast<T *>(p.out) + row * D + col, y);
+                } else {
+                    *reinterpret_cast<float4 *>(p.part + (slot * p.slot_rows + r) * D + col) = y;
+                }
+            }
+            if (tx == 0) {
+                if (whole)
+                    attend_store_lse(p, row, m[i], l[i], sees[i] > 0);
+                else
+                    p.stat[slot * p.slot_rows + r] = make_float2(m[i], l[i]);
             }
         }
         if (!whole) {
@@ -206,38 +294,43 @@ __global__ void __launch_bounds__(kThreads) attend_simt_kernel(AttendParams p) {
             __threadfence();
             __syncthreads();
             if (tid == 0) {
-                const uint32_t before = atomicAdd(&p.arrived[2 * c0], 1u);
-                s.last = before == (uint32_t)(c1 - c0);
-                if (s.last) p.arrived[2 * c0] = 0;
+                const bool last = atomicAdd(&p.arrived[2 * c0], 1u) == (uint32_t)(c1 - c0);
+                if (last) p.arrived[2 * c0] = 0;
+                *s_last = last;
             }
             __syncthreads();
-            if (s.last) {
+            if (*s_last) {
                 __threadfence();
-                // thread = (row, 16 column lanes), as above
-                for (int r = ty; r < rows; r += 16) {
+                const int chunks = D / 4;
+                for (int x = tid; x < a.rows * chunks; x += kThreads) {
+                    const int r = x / chunks, col = (x - r * chunks) * 4;
+                    auto at = [&](int c) {
+                        return ((int64_t)c * p.slots + (c == c0 ? kSlotLast : kSlotFirst)) * p.slot_rows + r;
+                    };
                     float top = -INFINITY;
-                    for (int c = c0; c <= c1; ++c)
-                        top = fmaxf(top, __ldcg(&p.stat[(int64_t)(2 * c + (c == c0)) * p.slot_rows + r]).x);
+                    for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(&p.stat[at(c)]).x);
                     const float ref = top == -INFINITY ? 0.f : top;
-                    float sum = 0.f, acc[CT];
-#pragma unroll
-                    for (int i = 0; i < CT; ++i) acc[i] = 0.f;
+                    float sum = 0.f;
+                    float4 acc = make_float4(0, 0, 0, 0);
                     for (int c = c0; c <= c1; ++c) {
-                        const int64_t at = (int64_t)(2 * c + (c == c0)) * p.slot_rows + r;
-                        const float2 st = __ldcg(&p.stat[at]);
+                        const float2 st = __ldcg(&p.stat[at(c)]);
+                        const float4 y = __ldcg(reinterpret_cast<const float4 *>(p.part + at(c) * D + col));
                         const float w = ex2(st.x - ref);
                         sum = fmaf(st.y, w, sum);
-#pragma unroll
-                        for (int i = 0; i < CT; ++i)
-                            if (tx + 16 * i < D) acc[i] = fmaf(__ldcg(&p.part[at * D + tx + 16 * i]), w, acc[i]);
+                        acc.x = fmaf(y.x, w, acc.x);
+                        acc.y = fmaf(y.y, w, acc.y);
+                        acc.z = fmaf(y.z, w, acc.z);
+                        acc.w = fmaf(y.w, w, acc.w);
                     }
                     const bool any = attend_sees(p, a, r) > 0;
                     const int64_t row = attend_out_row(p, a, r);
-                    T *out = static_cast<T *>(p.out) + row * D;
-#pragma unroll
-                    for (int i = 0; i < CT; ++i)
-                        if (tx + 16 * i < D) store1(out + tx + 16 * i, any ? acc[i] / sum : 0.f);
-                    if (tx == 0) attend_store_lse(p, row, top, sum, any);
+                    const float inv = 1.f / sum;
+                    if (any)
+                        acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+                    else
+                        acc = make_float4(0, 0, 0, 0);
+                    store4(static_cast<T *>(p.out) + row * D + col, acc);
+                    if (col == 0) attend_store_lse(p, row, top, sum, any);
                 }
             }
         }
@@ -247,40 +340,47 @@ __global__ void __launch_bounds__(kThreads) attend_simt_kernel(AttendParams p) {
     }
 }
 
-template <typename T, int ROWS, int DMAX>
-int launch(AttendParams &p, int grid, cudaStream_t st) {
-    constexpr size_t bytes = sizeof(SimtSmem<ROWS, DMAX>);
-    static_assert(bytes <= 232448, "shared memory of one block");
-    cudaFuncSetAttribute(attend_simt_kernel<T, ROWS, DMAX>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                         (int)bytes);
-    attend_simt_kernel<T, ROWS, DMAX><<<grid, kThreads, bytes, st>>>(p);
+template <typename T, int ROWS, int CT>
+int launch(AttendParams &p, int sms, cudaStream_t st) {
+    const size_t bytes = smem_bytes<T, ROWS>(p.dim);
+    if (bytes > 48 * 1024)
+        cudaFuncSetAttribute(attend_simt_kernel<T, ROWS, CT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             232448);
+    // as many blocks as an SM holds at once (1 KB of shared memory is each block's own cost)
+    static const int by_regs = [] {
+        cudaFuncAttributes at{};
+        return cudaFuncGetAttributes(&at, attend_simt_kernel<T, ROWS, CT>) == cudaSuccess && at.numRegs > 0
+                   ? 65536 / (kThreads * ((at.numRegs + 7) / 8 * 8)) : 1;
+    }();
+    const int per_sm = std::max(1, std::min({kBlocksPerSm, by_regs, (int)(233472 / (bytes + 1024))}));
+    attend_simt_kernel<T, ROWS, CT><<<per_sm * sms, kThreads, bytes, st>>>(p);
     return cache_launched("kvc_attend");
 }
 
 template <typename T>
-int launch_rows(AttendParams &p, int rows, int grid, cudaStream_t st) {
-    if (rows <= 16)
-        return p.dim <= 64    ? launch<T, 16, 64>(p, grid, st)
-               : p.dim <= 128 ? launch<T, 16, 128>(p, grid, st)
-                              : launch<T, 16, 256>(p, grid, st);
-    return p.dim <= 64    ? launch<T, 64, 64>(p, grid, st)
-           : p.dim <= 128 ? launch<T, 64, 128>(p, grid, st)
-                          : launch<T, 64, 256>(p, grid, st);
+int launch_type(AttendParams &p, int rows, int sms, cudaStream_t st) {
+    const int d = p.dim;
+    if (rows == 16) return d <= 128 ? launch<T, 16, 1>(p, sms, st) : launch<T, 16, 2>(p, sms, st);
+    return d <= 64    ? launch<T, 64, 2>(p, sms, st)
+           : d <= 96  ? launch<T, 64, 3>(p, sms, st)
+           : d <= 128 ? launch<T, 64, 4>(p, sms, st)
+                      : launch<T, 64, 8>(p, sms, st);
 }
 
 }  // namespace
 
-AttendNeeds attend_simt_needs(int sms) { return {2 * sms, 2, kSlotRows}; }
+AttendNeeds attend_simt_needs(int sms) { return {kBlocksPerSm * sms, 2, kSlotRows}; }
 
 int launch_attend_simt(AttendParams &p, bool f32, int grid, cudaStream_t st) {
     // 16 rows per block where a list's tokens fill no more
-    const int rows = p.max_new * p.group <= 16 ? 16 : kSlotRows;
+    const int rows = p.max_new * p.group <= 16 ? 16 : 64;
     p.unit_rows = rows;
     p.blocks = (p.max_new * p.group + rows - 1) / rows;
     p.n_units = (int64_t)p.n_seqs * p.n_kv_heads * p.blocks;
     p.step_keys = kKeys;
     p.split_rows = 0;
-    return f32 ? launch_rows<float>(p, rows, grid, st) : launch_rows<__nv_bfloat16>(p, rows, grid, st);
+    const int sms = grid / kBlocksPerSm;
+    return f32 ? launch_type<float>(p, rows, sms, st) : launch_type<__nv_bfloat16>(p, rows, sms, st);
 }
 
 }  // namespace kvc

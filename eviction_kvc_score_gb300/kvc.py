@@ -318,37 +318,58 @@ def cache(n_pages, page_rows, head_dim, max_pages, dtype) -> KvcCache:
     return KvcCache(int(n_pages), int(page_rows), int(head_dim), dt, int(max_pages))
 
 
-def _tensor(t, name, dtype, numel=None, strided=False):
-    """Pointer of a device tensor of the given type, on the current device,
-    contiguous (but for strided ones) and with numel elements at least."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+# The checks of these calls cost more than their launches if written freely
+# (a decode step makes a few of them per layer), so they ask each tensor for as
+# little as possible: one device query per call, one stream handle.
+_get_device = torch._C._cuda_getDevice
+_get_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _device(t, name):
+    """Index of the current device, which t has to be on."""
+    d = t.get_device()
+    if d < 0:
         raise ValueError(f"{name} must be a device tensor")
-    if t.device.index != torch.cuda.current_device():
+    if d != _get_device():
         raise ValueError(f"{name} is on {t.device}, not on the current device")
-    if t.dtype != dtype:
+    return d
+
+
+def _handle(stream, dev):
+    return _get_stream(dev) if stream is None else stream.cuda_stream
+
+
+def _at(t, name, dtype, dev, numel=0):
+    """Address of a contiguous tensor of that type and device with numel
+    elements at least."""
+    if t is None:
+        return None
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a tensor on cuda:{dev}, the current device")
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-    if not strided and not t.is_contiguous():
+    if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if numel is not None and t.numel() < numel:
+    if t.numel() < numel:
         raise ValueError(f"{name} has {t.numel()} elements, needs {numel}")
     return t.data_ptr()
 
 
 def _lists(c: KvcCache, table, lens):
-    """Pointers of a table and its lengths, and the number of lists."""
+    """Device, addresses of a table and its lengths, and the number of lists."""
     if table.dim() != 2 or table.shape[1] != c.max_pages:
         raise ValueError(f"table must be [n_lists][{c.max_pages}]")
-    n = table.shape[0]
-    return _tensor(table, "table", torch.int32), _tensor(lens, "len", torch.int32, n), n
+    n, dev = table.shape[0], _device(table, "table")
+    return dev, _at(table, "table", torch.int32, dev), _at(lens, "len", torch.int32, dev, n), n
 
 
-def _pools(c: KvcCache, k_pool, v_pool):
+def _pools(c: KvcCache, k_pool, v_pool, dev):
     n, dt = c.n_pages * c.page_rows * c.head_dim, _DTYPES[c.dtype]
-    return _tensor(k_pool, "k_pool", dt, n), _tensor(v_pool, "v_pool", dt, n)
+    return _at(k_pool, "k_pool", dt, dev, n), _at(v_pool, "v_pool", dt, dev, n)
 
 
-def _state(state):
-    return _tensor(state, "state", torch.uint8), state.numel()
+def _bytes(t, name, dev):
+    return _at(t, name, torch.uint8, dev), t.numel()
 
 
 def kvc_pages_size(c: KvcCache, n_lists: int) -> int:
@@ -359,14 +380,16 @@ def kvc_pages_size(c: KvcCache, n_lists: int) -> int:
 
 
 def kvc_pages_init(c: KvcCache, state, stream=None) -> None:
-    _check("kvc_pages_init", _lib.kvc_pages_init(C.byref(c), *_state(state), _stream(stream)))
+    dev = _device(state, "state")
+    _check("kvc_pages_init", _lib.kvc_pages_init(C.byref(c), *_bytes(state, "state", dev),
+                                                 _handle(stream, dev)))
 
 
 def kvc_pages_status(c: KvcCache, state, stream=None):
     """(status bits, free pages); waits for the stream."""
-    st, free = _u32(0), _i32(0)
+    st, free, dev = _u32(0), _i32(0), _device(state, "state")
     _check("kvc_pages_status", _lib.kvc_pages_status(
-        C.byref(c), *_state(state), C.byref(st), C.byref(free), _stream(stream)))
+        C.byref(c), *_bytes(state, "state", dev), C.byref(st), C.byref(free), _handle(stream, dev)))
     return st.value, free.value
 
 
@@ -376,93 +399,103 @@ def kvc_pages_append(c: KvcCache, table, lens, counts, src_row, src_step: int, k
     every list i: rows src_row[i] + r * src_step.  Rows inside a fused projection
     are taken where they lie: k_src and v_src start at the first key and value
     row of the first token, src_step is the heads of a whole token."""
-    t, n_len, n = _lists(c, table, lens)
+    dev, t, n_len, n = _lists(c, table, lens)
     dt = _DTYPES[c.dtype]
     rows = min(k_src.numel(), v_src.numel()) // c.head_dim
     _check("kvc_pages_append", _lib.kvc_pages_append(
-        C.byref(c), t, n_len, n, _tensor(counts, "counts", torch.int32, n),
-        _tensor(src_row, "src_row", torch.int64, n), int(src_step), _tensor(k_src, "k_src", dt),
-        _tensor(v_src, "v_src", dt), rows, *_pools(c, k_pool, v_pool),
-        *_state(state), _stream(stream)))
+        C.byref(c), t, n_len, n, _at(counts, "counts", torch.int32, dev, n),
+        _at(src_row, "src_row", torch.int64, dev, n), src_step, _at(k_src, "k_src", dt, dev),
+        _at(v_src, "v_src", dt, dev), rows, *_pools(c, k_pool, v_pool, dev),
+        *_bytes(state, "state", dev), _handle(stream, dev)))
 
 
 def kvc_pages_fork(c: KvcCache, table, lens, src, state, stream=None) -> None:
     """Make every list i with src[i] >= 0 a second holder of list src[i]'s pages."""
-    t, n_len, n = _lists(c, table, lens)
+    dev, t, n_len, n = _lists(c, table, lens)
     _check("kvc_pages_fork", _lib.kvc_pages_fork(
-        C.byref(c), t, n_len, n, _tensor(src, "src", torch.int32, n), *_state(state),
-        _stream(stream)))
+        C.byref(c), t, n_len, n, _at(src, "src", torch.int32, dev, n),
+        *_bytes(state, "state", dev), _handle(stream, dev)))
 
 
 def kvc_pages_compact(c: KvcCache, table, lens, idx, counts, k_pool, v_pool, state,
                       stream=None) -> None:
     """Keep rows idx[i][:counts[i]] of every list i with counts[i] >= 0."""
-    t, n_len, n = _lists(c, table, lens)
+    dev, t, n_len, n = _lists(c, table, lens)
     k_max = idx.shape[-1]
     _check("kvc_pages_compact", _lib.kvc_pages_compact(
-        C.byref(c), t, n_len, n, _tensor(idx, "idx", torch.int32, n * k_max), k_max,
-        _tensor(counts, "counts", torch.int32, n), *_pools(c, k_pool, v_pool), *_state(state),
-        _stream(stream)))
+        C.byref(c), t, n_len, n, _at(idx, "idx", torch.int32, dev, n * k_max), k_max,
+        _at(counts, "counts", torch.int32, dev, n), *_pools(c, k_pool, v_pool, dev),
+        *_bytes(state, "state", dev), _handle(stream, dev)))
 
 
 def kvc_pages_truncate(c: KvcCache, table, lens, new_len, state, stream=None) -> None:
     """Cut every list i with new_len[i] >= 0 to at most new_len[i] rows (0 frees it)."""
-    t, n_len, n = _lists(c, table, lens)
+    dev, t, n_len, n = _lists(c, table, lens)
     _check("kvc_pages_truncate", _lib.kvc_pages_truncate(
-        C.byref(c), t, n_len, n, _tensor(new_len, "new_len", torch.int32, n), *_state(state),
-        _stream(stream)))
+        C.byref(c), t, n_len, n, _at(new_len, "new_len", torch.int32, dev, n),
+        *_bytes(state, "state", dev), _handle(stream, dev)))
+
+
+def _table_at(table, rot_dim, dev):
+    dt = torch.uint64 if table.dtype is torch.uint64 else torch.int64
+    return _at(table, "table", dt, dev, max(0, rot_dim) // 2)
 
 
 def kvc_rope_table(rot_dim: int, theta: float, table, factor: float = 1.0, alpha: float = 1.0,
                    beta: float = 4.0, context: float = 8192.0, stream=None) -> None:
     """Fill table (rot_dim / 2 int64 or uint64) with the pairs' frequencies;
     factor > 1 slows the slow pairs down for longer contexts (see kvc.h)."""
-    dt = torch.uint64 if table.dtype == torch.uint64 else torch.int64
-    _check("kvc_rope_table", _lib.kvc_rope_table(
-        int(rot_dim), float(theta), float(factor), float(alpha), float(beta), float(context),
-        _tensor(table, "table", dt, max(0, int(rot_dim)) // 2), _stream(stream)))
+    dev = _device(table, "table")
+    _check("kvc_rope_table", _lib.kvc_rope_table(rot_dim, theta, factor, alpha, beta, context,
+                                                 _table_at(table, rot_dim, dev), _handle(stream, dev)))
 
 
-def _heads(x, name, dtype, n_tokens, dim):
-    """(heads, pointer, token stride) of x [n_tokens][heads][dim], whose heads
+def _heads(x, name, dtype, dev, n_tokens, dim):
+    """(heads, address, token stride) of x [n_tokens][heads][dim], whose heads
     are contiguous; tokens may be further apart."""
-    if x is None:
-        return 0, None, 0
-    if x.dim() != 3 or x.shape[0] != n_tokens or x.shape[2] != dim:
+    shape, step = x.shape, x.stride()
+    if len(shape) != 3 or shape[0] != n_tokens or shape[2] != dim:
         raise ValueError(f"{name} must be [{n_tokens}][heads][{dim}]")
-    if x.numel() and (x.stride(2) != 1 or (x.shape[1] > 1 and x.stride(1) != dim)):
+    if x.get_device() != dev:
+        raise ValueError(f"{name} must be a tensor on cuda:{dev}, the current device")
+    if x.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, not {x.dtype}")
+    heads = shape[1]
+    if n_tokens and ((step[2] != 1 and dim > 1) or (heads > 1 and step[1] != dim)):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    stride = x.stride(0) if n_tokens > 1 else x.shape[1] * dim
-    return x.shape[1], _tensor(x, name, dtype, strided=True), stride
+    return heads, x.data_ptr(), step[0] if n_tokens > 1 else heads * dim
+
+
+_NO_HEADS = (0, None, 0)
 
 
 def kvc_rope(table, positions, q, k, q_out, k_out, rot_dim: int, interleaved: bool = False,
              inverse: bool = False, amplitude: float = 1.0, stream=None) -> None:
     """Turn the first rot_dim elements of the heads of q and k [n_tokens][heads][D]
     (either may be None) by their tokens' positions (int32)."""
-    x = q if q is not None else k
+    x = k if q is None else q
     if x is None:
         raise ValueError("kvc_rope needs q or k")
-    if x.dtype not in _DTYPES.values():
-        raise ValueError(f"kvc_rope takes float32 or bfloat16 tensors, not {x.dtype}")
     if (q is None) != (q_out is None) or (k is None) != (k_out is None):
         raise ValueError("kvc_rope needs an output for each input")
+    dt = x.dtype
+    if dt is not torch.bfloat16 and dt is not torch.float32:
+        raise ValueError(f"kvc_rope takes float32 or bfloat16 tensors, not {dt}")
     if x.dim() != 3:
         raise ValueError("kvc_rope takes [n_tokens][heads][D] tensors")
-    n, dim, dt = x.shape[0], x.shape[2], x.dtype
-    hq, qp, qs = _heads(q, "q", dt, n, dim)
-    hqo, qop, qos = _heads(q_out, "q_out", dt, n, dim)
-    hk, kp, ks = _heads(k, "k", dt, n, dim)
-    hko, kop, kos = _heads(k_out, "k_out", dt, n, dim)
-    if hq != hqo or hk != hko:
+    n, _, dim = x.shape
+    dev = _device(x, "q" if x is q else "k")
+    qi = _NO_HEADS if q is None else _heads(q, "q", dt, dev, n, dim)
+    qo = qi if q_out is q else _heads(q_out, "q_out", dt, dev, n, dim)
+    ki = _NO_HEADS if k is None else _heads(k, "k", dt, dev, n, dim)
+    ko = ki if k_out is k else _heads(k_out, "k_out", dt, dev, n, dim)
+    if qi[0] != qo[0] or ki[0] != ko[0]:
         raise ValueError("kvc_rope: outputs must have their inputs' heads")
-    tdt = torch.uint64 if table.dtype == torch.uint64 else torch.int64
-    flags = (ROPE_INTERLEAVED if interleaved else 0) | (ROPE_INVERSE if inverse else 0)
     _check("kvc_rope", _lib.kvc_rope(
-        KVC_F32 if dt == torch.float32 else KVC_BF16, n, hq, hk, dim, int(rot_dim), flags,
-        float(amplitude), _tensor(positions, "positions", torch.int32, n),
-        _tensor(table, "table", tdt, max(0, int(rot_dim)) // 2), qp, qs, qop, qos, kp, ks, kop, kos,
-        _stream(stream)))
+        KVC_F32 if dt is torch.float32 else KVC_BF16, n, qi[0], ki[0], dim, rot_dim,
+        (ROPE_INTERLEAVED if interleaved else 0) | (ROPE_INVERSE if inverse else 0), amplitude,
+        _at(positions, "positions", torch.int32, dev, n), _table_at(table, rot_dim, dev),
+        qi[1], qi[2], qo[1], qo[2], ki[1], ki[2], ko[1], ko[2], _handle(stream, dev)))
 
 
 def kvc_attend_workspace_size(c: KvcCache, n_q_heads: int, n_kv_heads: int, n_seqs: int,
@@ -478,21 +511,18 @@ def kvc_attend(c: KvcCache, q, q_start, table, lens, k_pool, v_pool, max_new: in
                lse=None, scale: Optional[float] = None, stream=None) -> None:
     """Attention of new tokens q [n_tokens][H_q][D] over the paged lists of one
     layer, table [n_seqs * H_kv][max_pages]; scale defaults to 1 / sqrt(D)."""
-    t, n_len, n_lists = _lists(c, table, lens)
+    dev, t, n_len, n_lists = _lists(c, table, lens)
     n_seqs = q_start.numel() - 1
     if n_seqs < 1 or n_lists % n_seqs:
         raise ValueError("table must hold the same number of lists for every sequence of q_start")
-    dt = _DTYPES[c.dtype]
-    if q.dim() != 3:
-        raise ValueError("q must be [n_tokens][n_q_heads][head_dim]")
-    hq, qp, qs = _heads(q, "q", dt, q.shape[0], c.head_dim)
-    n = q.shape[0]
+    dt, n, dim = _DTYPES[c.dtype], q.shape[0], c.head_dim
+    hq, qp, qs = _heads(q, "q", dt, dev, n, dim)
     _check("kvc_attend", _lib.kvc_attend(
-        C.byref(c), hq, n_lists // n_seqs, n_seqs, int(max_new), n, qp, qs,
-        _tensor(q_start, "q_start", torch.int32), t, n_len, *_pools(c, k_pool, v_pool),
-        c.head_dim ** -0.5 if scale is None else float(scale), _tensor(out, "out", dt, q.numel()),
-        None if lse is None else _tensor(lse, "lse", torch.float32, n * hq),
-        _tensor(ws, "workspace", torch.uint8), ws.numel(), _stream(stream)))
+        C.byref(c), hq, n_lists // n_seqs, n_seqs, max_new, n, qp, qs,
+        _at(q_start, "q_start", torch.int32, dev), t, n_len, *_pools(c, k_pool, v_pool, dev),
+        dim ** -0.5 if scale is None else scale, _at(out, "out", dt, dev, n * hq * dim),
+        _at(lse, "lse", torch.float32, dev, n * hq), *_bytes(ws, "workspace", dev),
+        _handle(stream, dev)))
 
 
 def kvc_status_string(code: int) -> str:

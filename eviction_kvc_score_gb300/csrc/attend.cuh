@@ -52,14 +52,24 @@ struct AttendUnit {
     int steps;        // 0: no such unit
 };
 
-__device__ __forceinline__ AttendUnit attend_unit(const AttendParams &p, int64_t u) {
+// What a unit is made of in memory, to be asked for before it is needed.
+struct AttendRaw {
+    int q0, q1, len;
+};
+__device__ __forceinline__ AttendRaw attend_raw(const AttendParams &p, int64_t u) {
+    if (u >= p.n_units) return AttendRaw{0, 0, 0};
+    const int list = (int)(u / p.blocks), b = list / p.n_kv_heads;
+    return AttendRaw{p.q_start[b], p.q_start[b + 1], p.len[list]};
+}
+
+__device__ __forceinline__ AttendUnit attend_unit(const AttendParams &p, int64_t u, const AttendRaw &raw) {
     AttendUnit a;
     a.list = (int)(u / p.blocks);
     const int block = (int)(u - (int64_t)a.list * p.blocks);
     a.b = a.list / p.n_kv_heads;
     a.h = a.list - a.b * p.n_kv_heads;
-    int q0 = p.q_start[a.b], q1 = p.q_start[a.b + 1];
-    a.len = p.len[a.list];
+    int q0 = raw.q0, q1 = raw.q1;
+    a.len = raw.len;
     const int64_t most = (int64_t)p.max_pages << p.shift;
     if (q0 < 0 || q1 < q0 || q1 > p.n_tokens || q1 - q0 > p.max_new || a.len < 0 || a.len > most) {
         set_status(p.status, KVC_DEV_BAD_LIST);
@@ -75,6 +85,10 @@ __device__ __forceinline__ AttendUnit attend_unit(const AttendParams &p, int64_t
     const int keys = a.rows <= p.split_rows ? 2 * p.step_keys : p.step_keys;
     a.steps = a.rows <= 0 ? 0 : max(1, (a.hi + keys - 1) / keys);
     return a;
+}
+
+__device__ __forceinline__ AttendUnit attend_unit(const AttendParams &p, int64_t u) {
+    return attend_unit(p, u, attend_raw(p, u));
 }
 
 // Cached rows that row r of the unit sees.

@@ -27,8 +27,8 @@
 //
 // Roles: warps 0-3 and 4-7 softmax of t = 0 and 1, a thread per row; warp 8
 // loads; warp 9 issues the MMAs.  TMEM: S_0 | S_1 | O_0 | O_1, 128 columns each.
-// Shared memory: two Q tiles and a ring of five tiles (D = 128: 64 + 160 KB) that
-// K and V tiles pass through in the order the MMAs use them.  Every wait is
+// Shared memory: two Q tiles and a ring of 5 (D = 128: 64 + 160 KB) or 12 tiles that
+// K and V pass through in the order the MMAs use them.  Every wait is
 // bounded and nothing waits on a barrier without a limit, so a wait that runs
 // out ends the kernel with KVC_DEV_TIMEOUT (the workspace then has to be
 // initialised again).
@@ -46,7 +46,6 @@ constexpr int kThreads = 384;
 constexpr int kRegsLaunch = 168, kRegsSoftmax = 216, kRegsOther = 72;
 static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreads * kRegsLaunch, "register split");
 constexpr int kTile = 128;              // rows of Q, keys of K and V
-constexpr int kStages = 5;
 constexpr int kLoadWarp = 8, kMmaWarp = 9;
 constexpr int kBox = kTile * 128;       // bytes of 128 rows x 64 bf16
 constexpr uint32_t kColS = 0, kColO = 256;
@@ -54,8 +53,12 @@ constexpr float kGrow = 8.f;            // log2 units m may lag behind
 constexpr int kSlotsTc = 3;             // first, last, exchange of the halves
 constexpr int kSlotExchange = 2;
 
+// Ring stages: what shared memory holds beside Q.
+constexpr int stages_of(int kh) { return kh == 2 ? 5 : 12; }
+
+template <int STAGES>
 struct Bars {
-    uint64_t full[kStages], empty[kStages];
+    uint64_t full[STAGES], empty[STAGES];
     uint64_t q_full, q_empty;
     uint64_t s_full[2], p_full[2], o_full[2];
     uint64_t half_full, wg[2], drain;
@@ -68,7 +71,7 @@ struct Bars {
 
 template <int KH>
 constexpr size_t smem_bytes() {
-    return 1024 + (size_t)(2 + kStages) * KH * kBox + sizeof(Bars);
+    return 1024 + (size_t)(2 + stages_of(KH)) * KH * kBox + sizeof(Bars<stages_of(KH)>);
 }
 
 __device__ __forceinline__ void tma_load_4d(const CUtensorMap *map, uint64_t *bar, void *dst, int c0,
@@ -178,12 +181,15 @@ struct Walk {
     int64_t pos, u, u_lo;
     AttendUnit a;
     Segment g;
-    __device__ explicit Walk(const AttendRun &r) : run(r), pos(r.lo), u(r.unit), u_lo(r.unit_lo) {}
+    AttendRaw raw;   // of unit u, asked for while the unit before is worked on
+    __device__ Walk(const AttendParams &p, const AttendRun &r)
+        : run(r), pos(r.lo), u(r.unit), u_lo(r.unit_lo), raw(attend_raw(p, r.unit)) {}
     __device__ bool next(const AttendParams &p) {
         while (pos < run.hi) {
-            a = attend_unit(p, u);
+            a = attend_unit(p, u, raw);
             if (a.steps == 0) {
                 u = attend_next(p, a, u);
+                raw = attend_raw(p, u);
                 continue;
             }
             const int64_t end = min(run.hi, u_lo + a.steps);
@@ -192,6 +198,7 @@ struct Walk {
             pos = end;
             u_lo += a.steps;
             u = attend_next(p, a, u);
+            raw = attend_raw(p, u);
             return true;
         }
         return false;
@@ -204,12 +211,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     attend_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                      const __grid_constant__ CUtensorMap tv, const AttendParams p) {
     constexpr int D = 64 * KH;
-    constexpr int kStageBytes = KH * kBox;
+    constexpr int kStageBytes = KH * kBox, kStages = stages_of(KH);
     extern __shared__ uint8_t raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     uint8_t *sq = base;                              // [2][KH][128 rows][128 B]
     uint8_t *ring = base + 2 * kStageBytes;          // [stage][KH][128 keys][128 B]
-    Bars &b = *reinterpret_cast<Bars *>(ring + kStages * kStageBytes);
+    Bars<kStages> &b = *reinterpret_cast<Bars<kStages> *>(ring + kStages * kStageBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int R = p.split_rows;
 
@@ -255,8 +262,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         uint32_t fill = 0, segs = 0;   // ring stages filled, segments
         bool ok = true;
-        const int per_tile = kTile >> p.shift, ps = 1 << p.shift;
-        Walk w(run);
+        const int tile_shift = 7 - p.shift, per_tile = 1 << tile_shift, ps = 1 << p.shift;
+        Walk w(p, run);
         while (ok && w.next(p)) {
             const Segment &g = w.g;
             if (g.n == 0) continue;
@@ -272,19 +279,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     w.a.q0 + (w.a.row0 + t * R) / p.group);
             }
             ++segs;
+            // page numbers 32 at a time, a lane each: the batch in use, the
+            // one before (V is up to two tiles behind K) and the next, asked
+            // for while the one in use lasts
+            const int page0 = g.first << tile_shift;
+            const int page1 = min((g.first + g.n) << tile_shift, (w.a.hi + ps - 1) >> p.shift);
+            auto look_up = [&](int batch) {
+                const int j = page0 + batch * 32 + lane;
+                return j < page1 ? p.table[(int64_t)w.a.list * p.max_pages + j] : 0;
+            };
+            int batch = 0, before = 0, now = look_up(0), ahead = look_up(1);
             const int loads = 2 * g.n;
             for (int l = 0; l < loads; ++l, ++fill) {
                 bool is_v;
                 int tile;
                 load_at(g, l, &is_v, &tile);
-                tile += g.first;
-                // the tile's pages that hold visible rows
-                const int left = w.a.hi - tile * kTile;
-                const int pages = min(per_tile, (left + ps - 1) >> p.shift);
-                int page = 0;
-                if (lane < pages) {
-                    page = attend_page(p, w.a.list, tile * per_tile + lane);
-                    if (page < 0) page = p.n_pages;   // outside the tensor: zeros
+                const int at = tile << tile_shift;   // the tile's first page, within the segment
+                if (at >> 5 > batch) {
+                    ++batch;
+                    before = now;
+                    now = ahead;
+                    ahead = look_up(batch + 1);
+                }
+                int page = __shfl_sync(0xffffffffu, at >> 5 < batch ? before : now, (at + lane) & 31);
+                // those that hold visible rows
+                const int pages = min(per_tile, page1 - page0 - at);
+                if (lane < pages && (page < 0 || page >= p.n_pages)) {
+                    set_status(p.status, KVC_DEV_BAD_PAGE);
+                    page = p.n_pages;   // outside the tensor: zeros
                 }
                 const uint32_t st = fill % kStages;
                 ok = fill < kStages || warp_wait(&b.empty[st], (fill / kStages - 1) & 1, stop, p.status);
@@ -332,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                        v + (uint64_t)(ks * (16 * 128 >> 4)), kIdO, add || ks > 0);
             };
             bool ok = true;
-            Walk w(run);
+            Walk w(p, run);
             while (ok && w.next(p)) {
                 const Segment &g = w.g;
                 if (g.n == 0) continue;
@@ -414,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const unsigned long long c2 = f2_pack(c, c);
         uint32_t ns = 0, no = 0, nwg = 0, nhalf = 0, filled = 0;
         bool ok = true;
-        Walk w(run);
+        Walk w(p, run);
         while (ok && w.next(p)) {
             const AttendUnit &a = w.a;
             const Segment &g = w.g;

@@ -26,7 +26,8 @@
 // to the rows that see them.
 //
 // Roles: warps 0-3 and 4-7 softmax of t = 0 and 1, a thread per row; warp 8
-// loads; warp 9 issues the MMAs.  TMEM: S_0 | S_1 | O_0 | O_1, 128 columns each.
+// loads; warps 9 and 10 issue the MMAs of t = 0 and 1 (one issuing thread spent
+// 4,300 clocks on the waits and MMAs of a step whose MMAs take 2,048).  TMEM: S_0 | S_1 | O_0 | O_1, 128 columns each.
 // Shared memory: two Q tiles and a ring of 5 (D = 128: 64 + 160 KB) or 12 tiles that
 // K and V pass through in the order the MMAs use them.  Every wait is
 // bounded and nothing waits on a barrier without a limit, so a wait that runs
@@ -61,7 +62,7 @@ struct Bars {
     uint64_t full[STAGES], empty[STAGES];
     uint64_t q_full, q_empty;
     uint64_t s_full[2], p_full[2], o_full[2];
-    uint64_t half_full, wg[2], drain;
+    uint64_t half_full, half_empty, wg[2], drain[2];
     uint32_t tmem;
     volatile int abort_flag;
     int dirty;            // some value taken out of V
@@ -114,6 +115,14 @@ __device__ __forceinline__ void regs_inc() {
 template <int N>
 __device__ __forceinline__ void regs_dec() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// One thread of a converged warp, known to the compiler as such: the MMAs it
+// issues take half as many clocks as those of a thread picked by its index.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t is;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(is));
+    return is != 0;
 }
 
 // The bounded wait, its outcome the same for the whole warp (what follows is
@@ -170,7 +179,11 @@ __device__ __forceinline__ void load_at(const Segment &g, int l, bool *is_v, int
         *tile = m - (g.n - lead);
     }
 }
-// Place in it of V of the segment's tile i.
+// Place in it of K and V of the segment's tile i.
+__device__ __forceinline__ int k_at(const Segment &g, int i) {
+    const int lead = min(2, g.n);
+    return !g.split ? 2 * i : i < lead ? i : lead + 2 * (i - 2) + 1;
+}
 __device__ __forceinline__ int v_at(const Segment &g, int i) {
     return g.split ? min(2, g.n) + i + min(i, max(g.n - 2, 0)) : 2 * i + 1;
 }
@@ -223,18 +236,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&b.full[i], 1);
-            mbar_init(&b.empty[i], 1);
+            mbar_init(&b.empty[i], 2);
         }
         mbar_init(&b.q_full, 1);
-        mbar_init(&b.q_empty, 1);
+        mbar_init(&b.q_empty, 2);
         for (int t = 0; t < 2; ++t) {
             mbar_init(&b.s_full[t], 1);
             mbar_init(&b.p_full[t], 4);
             mbar_init(&b.o_full[t], 1);
             mbar_init(&b.wg[t], 4);
+            mbar_init(&b.drain[t], 1);
         }
         mbar_init(&b.half_full, 4);
-        mbar_init(&b.drain, 1);
+        mbar_init(&b.half_empty, 4);
         b.abort_flag = 0;
         b.dirty = 0;
         fence_barrier_init();
@@ -326,32 +340,39 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_drain(&b.full[f % kStages], (f / kStages) & 1);
             if (segs) mbar_drain(&b.q_full, (segs - 1) & 1);
         }
-    } else if (warp == kMmaWarp) {
-        // ------------------------------------------------ MMA issue
-        if (lane == 0) {
+    } else if (warp >= kMmaWarp && warp < kMmaWarp + 2) {
+        // ------------------------------------------------ MMA issue, a warp per half
+        if (elect_one()) {
             constexpr uint32_t kIdS = idesc_bf16_f32(kTile, kTile);
             constexpr uint32_t kIdO = idesc_bf16_f32(kTile, D) | (1u << 16);   // B MN-major
-            uint32_t use = 0, segs = 0, np[2] = {0, 0};   // ring stages used, P tiles seen
-            const uint64_t qd = desc_sw128(smem_u32(sq), 16, 1024);
+            const int t = warp - kMmaWarp;
+            const uint32_t col_s = tmem + kColS + t * 128, col_o = tmem + kColO + t * 128;
+            uint32_t use = 0, segs = 0, np = 0;   // ring stages passed, segments, P tiles seen
             auto stage_full = [&](uint32_t f) {
                 return mbar_wait(&b.full[f % kStages], (f / kStages) & 1, stop, p.status);
             };
-            auto issue_s = [&](int t, bool split, uint32_t f) {
-                const uint64_t a = qd + (split ? 0 : (uint64_t)((t * kStageBytes) >> 4));
-                const uint64_t k = desc_sw128(smem_u32(ring + (f % kStages) * kStageBytes), 16, 1024);
+            // a stage is free after two arrivals: this half's commit, and the
+            // other's or, of a tile that only this half uses, a plain one
+            auto stage_used = [&](uint32_t f, bool alone) {
+                if (alone) mbar_arrive(&b.empty[f % kStages]);
+                tc_commit(&b.empty[f % kStages]);
+            };
+            auto issue_s = [&](bool split, uint32_t f) {
+                const uint64_t a = desc_sw128(smem_u32(sq) + (split ? 0 : t * kStageBytes), 16, 1024);
+                const uint64_t k = desc_sw128(smem_u32(ring) + (f % kStages) * kStageBytes, 16, 1024);
 #pragma unroll
                 for (int ks = 0; ks < 4 * KH; ++ks) {
                     const uint64_t off = (uint64_t)(((ks >> 2) * kBox + (ks & 3) * 32) >> 4);
-                    tc_mma_bf16(tmem + kColS + t * 128, a + off, k + off, kIdS, ks > 0);
+                    tc_mma_bf16(col_s, a + off, k + off, kIdS, ks > 0);
                 }
                 tc_commit(&b.s_full[t]);
             };
-            auto issue_o = [&](int t, uint32_t f, bool add) {
-                const uint64_t v = desc_sw128(smem_u32(ring + (f % kStages) * kStageBytes), kBox, 1024);
+            auto issue_o = [&](uint32_t f, bool add) {
+                const uint64_t v = desc_sw128(smem_u32(ring) + (f % kStages) * kStageBytes, kBox, 1024);
 #pragma unroll
                 for (int ks = 0; ks < kTile / 16; ++ks)
-                    tc_mma_bf16_tmem_a(tmem + kColO + t * 128, tmem + kColS + t * 128 + ks * 8,
-                                       v + (uint64_t)(ks * (16 * 128 >> 4)), kIdO, add || ks > 0);
+                    tc_mma_bf16_tmem_a(col_o, col_s + ks * 8, v + (uint64_t)(ks * (16 * 128 >> 4)), kIdO,
+                                       add || ks > 0);
             };
             bool ok = true;
             Walk w(p, run);
@@ -361,67 +382,42 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!(ok = mbar_wait(&b.q_full, segs & 1, stop, p.status))) break;
                 ++segs;
                 tc_fence_after();
-                if (!g.split) {
-                    for (int i = -1; ok && i < g.n; ++i) {
-                        // ring: V i at use, K i+1 behind it
-                        const uint32_t fv = use, fk = use + (i >= 0 ? 1 : 0);
-                        const bool more = i + 1 < g.n;
-                        if (i >= 0 && !(ok = stage_full(fv))) break;
-                        for (int t = 0; ok && t < 2; ++t) {
-                            if (i >= 0 && i < g.cnt[t]) {
-                                if (!(ok = mbar_wait(&b.p_full[t], np[t] & 1, stop, p.status))) break;
-                                ++np[t];
-                                tc_fence_after();
-                                issue_o(t, fv, i > 0);
-                                if (i + 1 == g.cnt[t]) tc_commit(&b.o_full[t]);
-                            }
-                            if (t == 1 && i >= 0) tc_commit(&b.empty[fv % kStages]);
-                            if (i + 1 < g.cnt[t]) {
-                                if (!(ok = stage_full(fk))) break;
-                                tc_fence_after();
-                                issue_s(t, false, fk);
-                            }
-                        }
-                        if (!ok) break;
-                        if (more) {
-                            tc_commit(&b.empty[fk % kStages]);
-                            if (i + 2 == g.n) tc_commit(&b.q_empty);
-                        }
-                        use = fk + (more ? 1 : 0);
-                    }
-                } else {
-                    const int lead = min(2, g.n);
-                    for (int i = 0; ok && i < lead; ++i, ++use) {
-                        if (!(ok = stage_full(use))) break;
+                const int cnt = g.cnt[t];
+                if (cnt == 0) mbar_arrive(&b.q_empty);
+                for (int i = 0; i < cnt; ++i) {
+                    const int ti = g.split ? 2 * i + t : i;
+                    const bool alone = g.split || i >= g.cnt[t ^ 1];
+                    if (i == 0) {
+                        const uint32_t f = use + k_at(g, ti);
+                        if (!(ok = stage_full(f))) break;
                         tc_fence_after();
-                        issue_s(i, true, use);
-                        tc_commit(&b.empty[use % kStages]);
-                        if (i + 1 == g.n) tc_commit(&b.q_empty);
+                        issue_s(g.split, f);
+                        stage_used(f, alone);
+                        if (cnt == 1) tc_commit(&b.q_empty);
                     }
-                    for (int i = 0; ok && i < g.n; ++i) {
-                        const int t = i & 1;
-                        if (!(ok = stage_full(use))) break;
-                        if (!(ok = mbar_wait(&b.p_full[t], np[t] & 1, stop, p.status))) break;
-                        ++np[t];
-                        tc_fence_after();
-                        issue_o(t, use, i >= 2);
-                        tc_commit(&b.empty[use % kStages]);
-                        ++use;
-                        if (i + 2 < g.n) {
-                            if (!(ok = stage_full(use))) break;
-                            tc_fence_after();
-                            issue_s(t, true, use);
-                            tc_commit(&b.empty[use % kStages]);
-                            ++use;
-                            if (i + 3 == g.n) tc_commit(&b.q_empty);
-                        } else {
-                            tc_commit(&b.o_full[t]);
-                        }
+                    const uint32_t fv = use + v_at(g, ti);
+                    const bool more = i + 1 < cnt;
+                    if (!(ok = stage_full(fv))) break;
+                    const uint32_t fk = more ? use + k_at(g, g.split ? ti + 2 : ti + 1) : 0;
+                    if (more && !(ok = stage_full(fk))) break;
+                    if (!(ok = mbar_wait(&b.p_full[t], np & 1, stop, p.status))) break;
+                    ++np;
+                    tc_fence_after();
+                    issue_o(fv, i > 0);
+                    if (more) {
+                        issue_s(g.split, fk);
+                        stage_used(fv, alone);
+                        stage_used(fk, g.split || i + 1 >= g.cnt[t ^ 1]);
+                        if (i + 2 == cnt) tc_commit(&b.q_empty);
+                    } else {
+                        tc_commit(&b.o_full[t]);
+                        stage_used(fv, alone);
                     }
                 }
+                use += 2 * g.n;
             }
-            tc_commit(&b.drain);
-            mbar_drain(&b.drain, 0);
+            tc_commit(&b.drain[t]);
+            mbar_drain(&b.drain[t], 0);
         }
     }
     } else {
@@ -445,6 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool any = __any_sync(0xffffffffu, real);
             const int sees = real ? attend_sees(p, a, rt) : 0;
             const int sees0 = attend_sees(p, a, g.split ? 0 : t * R);   // the tile's first row's
+            const int from = attend_sees(p, a, 0);                      // the unit's
             float m = -INFINITY, l = 0.f;
             const int cnt = g.cnt[t];
             for (int i = 0; i < cnt; ++i) {
@@ -534,35 +531,39 @@ __global__ void __launch_bounds__(kThreads, 1)
                     l += s0 + s1;
                     tmem_st_wait();
                 }
-                if (edge) {
-                    // V's rows from the first that some row of the tile does not see
+                if (k0 + kTile > from) {
+                    // V's rows from the first that some row of the unit does
+                    // not see.  Both halves go over the same rows, so each
+                    // product finds them clean whatever the other half is at;
+                    // the note that something was taken out comes first.
                     const uint32_t f = filled + v_at(g, ti);
                     if (!(ok = warp_wait(&b.full[f % kStages], (f / kStages) & 1, stop, p.status))) break;
-                    if (k0 + r >= sees0) {
+                    if (k0 + r >= from) {
                         uint8_t *row = ring + (f % kStages) * kStageBytes + r * 128;
                         const bool inside = k0 + r < a.len;
-                        bool found = false;
                         for (int kh = 0; kh < KH; ++kh)
                             for (int ch = 0; ch < 8; ++ch) {
                                 uint4 *at = reinterpret_cast<uint4 *>(row + kh * kBox + ch * 16);
                                 uint4 x = *at;
-                                uint32_t *xs = &x.x;
-                                bool put = false;
+                                bool found = false;
 #pragma unroll
                                 for (int e = 0; e < 4; ++e) {
-                                    if ((xs[e] & 0x7f80u) == 0x7f80u) {
-                                        xs[e] &= 0xffff0000u;
-                                        put = true;
+                                    uint32_t &xe = e == 0 ? x.x : e == 1 ? x.y : e == 2 ? x.z : x.w;
+                                    if ((xe & 0x7f80u) == 0x7f80u) {
+                                        xe &= 0xffff0000u;
+                                        found = true;
                                     }
-                                    if ((xs[e] & 0x7f800000u) == 0x7f800000u) {
-                                        xs[e] &= 0xffffu;
-                                        put = true;
+                                    if ((xe & 0x7f800000u) == 0x7f800000u) {
+                                        xe &= 0xffffu;
+                                        found = true;
                                     }
                                 }
-                                if (put) *at = x;
-                                found |= put;
+                                if (found) {
+                                    if (inside) *static_cast<volatile int *>(&b.dirty) = 1;
+                                    __threadfence_block();
+                                    *at = x;
+                                }
                             }
-                        if (found && inside) *static_cast<volatile int *>(&b.dirty) = 1;
                     }
                     fence_async_shared();
                 }
@@ -582,10 +583,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool hand = g.whole && g.split && t == 1;
             const bool keep = g.whole && g.split && t == 0;
             const int slot_of_cta = g.whole ? kSlotExchange : g.begins ? kSlotLast : kSlotFirst;
-            const int half = slot_of_cta == kSlotExchange ? (int)(nhalf & 1) : t;
-            const int64_t slot = ((int64_t)blockIdx.x * kSlotsTc + slot_of_cta) * p.slot_rows + half * kTile + r;
+            const int64_t slot = ((int64_t)blockIdx.x * kSlotsTc + slot_of_cta) * p.slot_rows +
+                                 (slot_of_cta == kSlotExchange ? 0 : t * kTile) + r;
             if (keep && g.cnt[1] > 0) {   // the other half's rows of this unit
                 if (!(ok = warp_wait(&b.half_full, nhalf & 1, stop, p.status))) break;
+            }
+            if (hand && cnt > 0 && nhalf > 0) {   // those of the unit before have been read
+                if (!(ok = warp_wait(&b.half_empty, (nhalf - 1) & 1, stop, p.status))) break;
             }
             if (any && !(hand && cnt == 0)) {
                 float other_w = 0.f, mine_w = 1.f;
@@ -599,7 +603,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const float inv = sees > 0 ? 1.f / l : 0.f;
                 const int64_t out_row = real ? attend_out_row(p, a, rt) : 0;
-                const int from = attend_sees(p, a, 0);   // first key taken out of V
                 const bool dirty = *static_cast<volatile int *>(&b.dirty);
 #pragma unroll 1
                 for (int d = 0; d < D; d += 32) {
@@ -672,10 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_before();   // O is read: the next unit's products may overwrite it
             if (g.whole && g.split) {
                 if (g.cnt[1] > 0) {
-                    if (hand) {
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&b.half_full);
-                    }
+                    if (lane == 0) mbar_arrive(hand ? &b.half_full : &b.half_empty);
                     ++nhalf;
                 }
             } else if (!g.whole) {

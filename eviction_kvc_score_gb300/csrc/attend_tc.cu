@@ -33,6 +33,8 @@
 // bounded and nothing waits on a barrier without a limit, so a wait that runs
 // out ends the kernel with KVC_DEV_TIMEOUT (the workspace then has to be
 // initialised again).
+#include <type_traits>
+
 #include "attend.cuh"
 
 namespace kvc {
@@ -62,7 +64,7 @@ struct Bars {
     uint64_t full[STAGES], empty[STAGES];
     uint64_t q_full, q_empty;
     uint64_t s_full[2], p_full[2], o_full[2];
-    uint64_t half_full, half_empty, wg[2], drain[2];
+    uint64_t half_full, half_empty, wg[2], drain[2], issued[2];
     uint32_t tmem;
     volatile int abort_flag;
     int dirty;            // some value taken out of V
@@ -246,6 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&b.o_full[t], 1);
             mbar_init(&b.wg[t], 4);
             mbar_init(&b.drain[t], 1);
+            mbar_init(&b.issued[t], 1);
         }
         mbar_init(&b.half_full, 4);
         mbar_init(&b.half_empty, 4);
@@ -348,6 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int t = warp - kMmaWarp;
             const uint32_t col_s = tmem + kColS + t * 128, col_o = tmem + kColO + t * 128;
             uint32_t use = 0, segs = 0, np = 0;   // ring stages passed, segments, P tiles seen
+            uint32_t turns = 0;                   // groups of MMAs that both halves issue in turn
             auto stage_full = [&](uint32_t f) {
                 return mbar_wait(&b.full[f % kStages], (f / kStages) & 1, stop, p.status);
             };
@@ -374,6 +378,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_mma_bf16_tmem_a(col_o, col_s + ks * 8, v + (uint64_t)(ks * (16 * 128 >> 4)), kIdO,
                                        add || ks > 0);
             };
+            // The halves' groups (O of a tile, S of the next) go to the tensor
+            // cores whole and in turn.  Mixed, both softmaxes would get their S
+            // at the same time and the tensor cores would wait for both
+            // (measured: a step of 4,930 clocks).
+            auto my_turn = [&]() {
+                return t == 0 ? turns == 0 || mbar_wait(&b.issued[1], (turns - 1) & 1, stop, p.status)
+                              : mbar_wait(&b.issued[0], turns & 1, stop, p.status);
+            };
+            auto turn_over = [&]() {
+                mbar_arrive(&b.issued[t]);
+                ++turns;
+            };
             bool ok = true;
             Walk w(p, run);
             while (ok && w.next(p)) {
@@ -382,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!(ok = mbar_wait(&b.q_full, segs & 1, stop, p.status))) break;
                 ++segs;
                 tc_fence_after();
-                const int cnt = g.cnt[t];
+                const int cnt = g.cnt[t], both = min(g.cnt[0], g.cnt[1]);
                 if (cnt == 0) mbar_arrive(&b.q_empty);
                 for (int i = 0; i < cnt; ++i) {
                     const int ti = g.split ? 2 * i + t : i;
@@ -390,8 +406,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (i == 0) {
                         const uint32_t f = use + k_at(g, ti);
                         if (!(ok = stage_full(f))) break;
+                        if (both > 0 && !(ok = my_turn())) break;
                         tc_fence_after();
                         issue_s(g.split, f);
+                        if (both > 0) turn_over();
                         stage_used(f, alone);
                         if (cnt == 1) tc_commit(&b.q_empty);
                     }
@@ -402,10 +420,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (more && !(ok = stage_full(fk))) break;
                     if (!(ok = mbar_wait(&b.p_full[t], np & 1, stop, p.status))) break;
                     ++np;
+                    if (i < both && !(ok = my_turn())) break;
                     tc_fence_after();
                     issue_o(fv, i > 0);
+                    if (more) issue_s(g.split, fk);
+                    if (i < both) turn_over();
                     if (more) {
-                        issue_s(g.split, fk);
                         stage_used(fv, alone);
                         stage_used(fk, g.split || i + 1 >= g.cnt[t ^ 1]);
                         if (i + 2 == cnt) tc_commit(&b.q_empty);
@@ -451,7 +471,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++ns;
                 tc_fence_after();
                 const bool edge = k0 + kTile > sees0;
-                if (any) {
+                // slow: some row of the tile sees only part of it, or maxima are
+                // minima; two copies, because a select per logit costs as much
+                // as the rest
+                auto soften = [&](auto slow) {
+                    constexpr bool kSlow = decltype(slow)::value;
                     float v[4][32];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) tmem_ld32(cs + q * 32, v[q]);
@@ -459,13 +483,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int q = 0; q < 4; ++q) reg_fence(v[q]);
                     const int lim = sees - k0;   // keys of the tile the row sees
-                    if (flip) {
+                    if (kSlow && flip) {
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
 #pragma unroll
                             for (int j = 0; j < 32; ++j) v[q][j] = -v[q][j];
                     }
-                    if (edge) {
+                    if (kSlow) {
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
 #pragma unroll
@@ -517,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             float y0, y1;
                             f2_unpack(f2_fma(f2_pack(v[q][e], v[q][e + 1]), c2, nm2), y0, y1);
                             float p0 = ex2(y0), p1 = ex2(y1);
-                            if (edge) {   // -inf * 0 is no number: mask again
+                            if (kSlow) {   // -inf * 0 is no number: mask again
                                 if (64 * h + 2 * j >= lim) p0 = 0.f;
                                 if (64 * h + 2 * j + 1 >= lim) p1 = 0.f;
                             }
@@ -530,6 +554,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     f2_unpack(f2_add(sum2[0], sum2[1]), s0, s1);
                     l += s0 + s1;
                     tmem_st_wait();
+                };
+                if (any) {
+                    if (edge || flip)
+                        soften(std::true_type{});
+                    else
+                        soften(std::false_type{});
                 }
                 if (k0 + kTile > from) {
                     // V's rows from the first that some row of the unit does

@@ -25,8 +25,8 @@
 // before the product (p = 0 would not cancel them) and given back at the end
 // to the rows that see them.
 //
-// Roles: warps 0-3 and 4-7 softmax of t = 0 and 1, a thread per row; warp 8
-// loads; warps 9 and 10 issue the MMAs of t = 0 and 1 (one issuing thread spent
+// Roles: warps 0-3 and 4-7 softmax of t = 0 and 1, a thread per row; warps 8
+// and 11 load; warps 9 and 10 issue the MMAs of t = 0 and 1 (one issuing thread spent
 // 4,300 clocks on the waits and MMAs of a step whose MMAs take 2,048).  TMEM: S_0 | S_1 | O_0 | O_1, 128 columns each.
 // Shared memory: two Q tiles and a ring of 5 (D = 128: 64 + 160 KB) or 12 tiles that
 // K and V pass through in the order the MMAs use them.  Every wait is
@@ -44,12 +44,12 @@ namespace {
 constexpr int kThreads = 384;
 // Registers per thread: 168 at launch (64,512 of the SM's 65,536), moved from
 // the loading and issuing warpgroup to the two that hold a row of 128 logits
-// per thread.  256 x 216 + 128 x 72 = 384 x 168: the launch checks the 168,
+// per thread.  256 x 208 + 128 x 88 = 384 x 168: the launch checks the 168,
 // because an increase beyond what the block was launched with never returns.
-constexpr int kRegsLaunch = 168, kRegsSoftmax = 216, kRegsOther = 72;
+constexpr int kRegsLaunch = 168, kRegsSoftmax = 208, kRegsOther = 88;
 static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreads * kRegsLaunch, "register split");
 constexpr int kTile = 128;              // rows of Q, keys of K and V
-constexpr int kLoadWarp = 8, kMmaWarp = 9;
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kLoadWarp2 = 11;
 constexpr int kBox = kTile * 128;       // bytes of 128 rows x 64 bf16
 constexpr uint32_t kColS = 0, kColO = 256;
 constexpr float kGrow = 8.f;            // log2 units m may lag behind
@@ -63,7 +63,7 @@ template <int STAGES>
 struct Bars {
     uint64_t full[STAGES], empty[STAGES];
     uint64_t q_full, q_empty;
-    uint64_t s_full[2], p_full[2], o_full[2];
+    uint64_t s_full[2], p_full[2][2], o_full[2];   // p_full: [half][keys 0-63, 64-127]
     uint64_t half_full, half_empty, wg[2], drain[2], issued[2];
     uint32_t tmem;
     volatile int abort_flag;
@@ -244,7 +244,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&b.q_empty, 2);
         for (int t = 0; t < 2; ++t) {
             mbar_init(&b.s_full[t], 1);
-            mbar_init(&b.p_full[t], 4);
+            mbar_init(&b.p_full[t][0], 4);
+            mbar_init(&b.p_full[t][1], 4);
             mbar_init(&b.o_full[t], 1);
             mbar_init(&b.wg[t], 4);
             mbar_init(&b.drain[t], 1);
@@ -270,32 +271,34 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp >= kLoadWarp) {
     regs_dec<kRegsOther>();
-    if (warp == kLoadWarp) {
-        // ------------------------------------------------ loads
+    if (warp == kLoadWarp || warp == kLoadWarp2) {
+        // ------------------------------------------------ loads, every other one a warp
+        const uint32_t side = warp == kLoadWarp ? 0 : 1;
         if (lane == 0) {
             tma_prefetch_desc(&tq);
             tma_prefetch_desc(&tk);
             tma_prefetch_desc(&tv);
         }
-        uint32_t fill = 0, segs = 0;   // ring stages filled, segments
+        uint32_t base_fill = 0, segs = 0, done = 0;   // loads before this segment, segments, loads of this side
         bool ok = true;
         const int tile_shift = 7 - p.shift, per_tile = 1 << tile_shift, ps = 1 << p.shift;
         Walk w(p, run);
         while (ok && w.next(p)) {
             const Segment &g = w.g;
             if (g.n == 0) continue;
-            // Q once the segment before has used it
-            ok = segs == 0 || warp_wait(&b.q_empty, (segs - 1) & 1, stop, p.status);
-            if (!ok) break;
-            if (lane == 0) {
-                const int tiles = g.split ? 1 : 2;
-                mbar_arrive_expect_tx(&b.q_full, (uint32_t)(tiles * KH * R * 128));
-                for (int t = 0; t < tiles; ++t)
-                    for (int kh = 0; kh < KH; ++kh)
-                        tma_load_4d(&tq, &b.q_full, sq + t * kStageBytes + kh * kBox, kh * 64, 0, w.a.h,
-                                    w.a.q0 + (w.a.row0 + t * R) / p.group);
+            if (side == 0) {   // Q once the segment before has used it
+                ok = segs == 0 || warp_wait(&b.q_empty, (segs - 1) & 1, stop, p.status);
+                if (!ok) break;
+                if (lane == 0) {
+                    const int tiles = g.split ? 1 : 2;
+                    mbar_arrive_expect_tx(&b.q_full, (uint32_t)(tiles * KH * R * 128));
+                    for (int t = 0; t < tiles; ++t)
+                        for (int kh = 0; kh < KH; ++kh)
+                            tma_load_4d(&tq, &b.q_full, sq + t * kStageBytes + kh * kBox, kh * 64, 0, w.a.h,
+                                        w.a.q0 + (w.a.row0 + t * R) / p.group);
+                }
+                ++segs;
             }
-            ++segs;
             // page numbers 32 at a time, a lane each: the batch in use, the
             // one before (V is up to two tiles behind K) and the next, asked
             // for while the one in use lasts
@@ -306,8 +309,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return j < page1 ? p.table[(int64_t)w.a.list * p.max_pages + j] : 0;
             };
             int batch = 0, before = 0, now = look_up(0), ahead = look_up(1);
-            const int loads = 2 * g.n;
-            for (int l = 0; l < loads; ++l, ++fill) {
+            // a segment makes an even number of loads: the sides keep their parity
+            for (int l = (int)side; l < 2 * g.n; l += 2) {
                 bool is_v;
                 int tile;
                 load_at(g, l, &is_v, &tile);
@@ -325,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     set_status(p.status, KVC_DEV_BAD_PAGE);
                     page = p.n_pages;   // outside the tensor: zeros
                 }
-                const uint32_t st = fill % kStages;
+                const uint32_t fill = base_fill + l, st = fill % kStages;
                 ok = fill < kStages || warp_wait(&b.empty[st], (fill / kStages - 1) & 1, stop, p.status);
                 if (!ok) break;
                 if (lane == 0) mbar_arrive_expect_tx(&b.full[st], (uint32_t)(pages * ps * D * 2));
@@ -336,11 +339,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int kh = 0; kh < KH; ++kh)
                         tma_load_3d(is_v ? &tv : &tk, &b.full[st], dst + kh * kBox, kh * 64, 0, page);
                 }
+                ++done;
             }
+            base_fill += 2 * g.n;
         }
         if (*stop) {   // unwind: every copy started must land
-            for (uint32_t f = fill > kStages ? fill - kStages : 0; f < fill; ++f)
+            for (uint32_t i = done > (kStages + 1) / 2 ? done - (kStages + 1) / 2 : 0; i < done; ++i) {
+                const uint32_t f = 2 * i + side;
                 mbar_drain(&b.full[f % kStages], (f / kStages) & 1);
+            }
             if (segs) mbar_drain(&b.q_full, (segs - 1) & 1);
         }
     } else if (warp >= kMmaWarp && warp < kMmaWarp + 2) {
@@ -371,10 +378,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tc_commit(&b.s_full[t]);
             };
-            auto issue_o = [&](uint32_t f, bool add) {
+            // keys 0-63 or 64-127 of the tile
+            auto issue_o = [&](uint32_t f, auto upper, bool add) {
+                constexpr int k0 = decltype(upper)::value ? 4 : 0;
                 const uint64_t v = desc_sw128(smem_u32(ring) + (f % kStages) * kStageBytes, kBox, 1024);
 #pragma unroll
-                for (int ks = 0; ks < kTile / 16; ++ks)
+                for (int ks = k0; ks < k0 + 4; ++ks)
                     tc_mma_bf16_tmem_a(col_o, col_s + ks * 8, v + (uint64_t)(ks * (16 * 128 >> 4)), kIdO,
                                        add || ks > 0);
             };
@@ -418,11 +427,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!(ok = stage_full(fv))) break;
                     const uint32_t fk = more ? use + k_at(g, g.split ? ti + 2 : ti + 1) : 0;
                     if (more && !(ok = stage_full(fk))) break;
-                    if (!(ok = mbar_wait(&b.p_full[t], np & 1, stop, p.status))) break;
-                    ++np;
+                    if (!(ok = mbar_wait(&b.p_full[t][0], np & 1, stop, p.status))) break;
                     if (i < both && !(ok = my_turn())) break;
                     tc_fence_after();
-                    issue_o(fv, i > 0);
+                    issue_o(fv, std::false_type{}, i > 0);
+                    if (!(ok = mbar_wait(&b.p_full[t][1], np & 1, stop, p.status))) break;
+                    ++np;
+                    tc_fence_after();
+                    issue_o(fv, std::true_type{}, true);
                     if (more) issue_s(g.split, fk);
                     if (i < both) turn_over();
                     if (more) {
@@ -471,6 +483,42 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++ns;
                 tc_fence_after();
                 const bool edge = k0 + kTile > sees0;
+                if (k0 + kTile > from) {
+                    // V's rows from the first that some row of the unit does
+                    // not see.  Both halves go over the same rows, so each
+                    // product finds them clean whatever the other half is at;
+                    // the note that something was taken out comes first.
+                    const uint32_t f = filled + v_at(g, ti);
+                    if (!(ok = warp_wait(&b.full[f % kStages], (f / kStages) & 1, stop, p.status))) break;
+                    if (k0 + r >= from) {
+                        uint8_t *row = ring + (f % kStages) * kStageBytes + r * 128;
+                        const bool inside = k0 + r < a.len;
+                        for (int kh = 0; kh < KH; ++kh)
+                            for (int ch = 0; ch < 8; ++ch) {
+                                uint4 *at = reinterpret_cast<uint4 *>(row + kh * kBox + ch * 16);
+                                uint4 x = *at;
+                                bool found = false;
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    uint32_t &xe = e == 0 ? x.x : e == 1 ? x.y : e == 2 ? x.z : x.w;
+                                    if ((xe & 0x7f80u) == 0x7f80u) {
+                                        xe &= 0xffff0000u;
+                                        found = true;
+                                    }
+                                    if ((xe & 0x7f800000u) == 0x7f800000u) {
+                                        xe &= 0xffffu;
+                                        found = true;
+                                    }
+                                }
+                                if (found) {
+                                    if (inside) *static_cast<volatile int *>(&b.dirty) = 1;
+                                    __threadfence_block();
+                                    *at = x;
+                                }
+                            }
+                    }
+                    fence_async_shared();
+                }
                 // slow: some row of the tile sees only part of it, or maxima are
                 // minima; two copies, because a select per logit costs as much
                 // as the rest
@@ -549,57 +597,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                             asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(pw[j]) : "f"(p1), "f"(p0));
                         }
                         tmem_st32(cs + h * 32, pw);
+                        // half of P is enough for half of the product to start
+                        tmem_st_wait();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&b.p_full[t][h]);
                     }
                     float s0, s1;
                     f2_unpack(f2_add(sum2[0], sum2[1]), s0, s1);
                     l += s0 + s1;
-                    tmem_st_wait();
                 };
                 if (any) {
                     if (edge || flip)
                         soften(std::true_type{});
                     else
                         soften(std::false_type{});
+                } else if (lane == 0) {
+                    mbar_arrive(&b.p_full[t][0]);
+                    mbar_arrive(&b.p_full[t][1]);
                 }
-                if (k0 + kTile > from) {
-                    // V's rows from the first that some row of the unit does
-                    // not see.  Both halves go over the same rows, so each
-                    // product finds them clean whatever the other half is at;
-                    // the note that something was taken out comes first.
-                    const uint32_t f = filled + v_at(g, ti);
-                    if (!(ok = warp_wait(&b.full[f % kStages], (f / kStages) & 1, stop, p.status))) break;
-                    if (k0 + r >= from) {
-                        uint8_t *row = ring + (f % kStages) * kStageBytes + r * 128;
-                        const bool inside = k0 + r < a.len;
-                        for (int kh = 0; kh < KH; ++kh)
-                            for (int ch = 0; ch < 8; ++ch) {
-                                uint4 *at = reinterpret_cast<uint4 *>(row + kh * kBox + ch * 16);
-                                uint4 x = *at;
-                                bool found = false;
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    uint32_t &xe = e == 0 ? x.x : e == 1 ? x.y : e == 2 ? x.z : x.w;
-                                    if ((xe & 0x7f80u) == 0x7f80u) {
-                                        xe &= 0xffff0000u;
-                                        found = true;
-                                    }
-                                    if ((xe & 0x7f800000u) == 0x7f800000u) {
-                                        xe &= 0xffffu;
-                                        found = true;
-                                    }
-                                }
-                                if (found) {
-                                    if (inside) *static_cast<volatile int *>(&b.dirty) = 1;
-                                    __threadfence_block();
-                                    *at = x;
-                                }
-                            }
-                    }
-                    fence_async_shared();
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&b.p_full[t]);
             }
             if (!ok) break;
             if (cnt > 0) {

@@ -19,14 +19,30 @@
 
 namespace kvc {
 
+// n / d for n < 2^31 by a multiplication and a shift (the round-up method of
+// Granlund and Montgomery, "Division by invariant integers using
+// multiplication", 1994): the walk over units divides a lot.
+struct Divider {
+    uint32_t d, mul, shift;
+    __host__ __device__ Divider() {}
+    explicit Divider(uint32_t by) : d(by), shift(0) {
+        while (((uint64_t)1 << shift) < by) ++shift;
+        mul = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << shift) - by)) / by + 1);
+    }
+    __device__ __forceinline__ int operator()(int n) const {
+        return (int)((__umulhi((uint32_t)n, mul) + (uint32_t)n) >> shift);
+    }
+};
+
 struct AttendParams {
     int n_seqs, n_q_heads, n_kv_heads, group, dim;
+    Divider by_group, by_heads, by_blocks;
     int n_pages, max_pages, shift;
     int64_t n_tokens;
     int max_new;
     int unit_rows;       // rows of a unit
     int blocks;          // units per list
-    int64_t n_units;
+    int n_units;
     int step_keys;       // keys per step ...
     int split_rows;      // ... twice as many for units of at most so many rows
     int slots;           // slots per CTA
@@ -56,17 +72,17 @@ struct AttendUnit {
 struct AttendRaw {
     int q0, q1, len;
 };
-__device__ __forceinline__ AttendRaw attend_raw(const AttendParams &p, int64_t u) {
+__device__ __forceinline__ AttendRaw attend_raw(const AttendParams &p, int u) {
     if (u >= p.n_units) return AttendRaw{0, 0, 0};
-    const int list = (int)(u / p.blocks), b = list / p.n_kv_heads;
+    const int list = p.by_blocks(u), b = p.by_heads(list);
     return AttendRaw{p.q_start[b], p.q_start[b + 1], p.len[list]};
 }
 
-__device__ __forceinline__ AttendUnit attend_unit(const AttendParams &p, int64_t u, const AttendRaw &raw) {
+__device__ __forceinline__ AttendUnit attend_unit(const AttendParams &p, int u, const AttendRaw &raw) {
     AttendUnit a;
-    a.list = (int)(u / p.blocks);
-    const int block = (int)(u - (int64_t)a.list * p.blocks);
-    a.b = a.list / p.n_kv_heads;
+    a.list = p.by_blocks(u);
+    const int block = u - a.list * p.blocks;
+    a.b = p.by_heads(a.list);
     a.h = a.list - a.b * p.n_kv_heads;
     int q0 = raw.q0, q1 = raw.q1;
     a.len = raw.len;
@@ -81,23 +97,23 @@ __device__ __forceinline__ AttendUnit attend_unit(const AttendParams &p, int64_t
     a.n = max(0, q1 - q0);
     a.row0 = block * p.unit_rows;
     a.rows = min(p.unit_rows, a.n * p.group - a.row0);
-    a.hi = a.rows <= 0 ? 0 : max(0, a.len - a.n + (a.row0 + a.rows - 1) / p.group + 1);
+    a.hi = a.rows <= 0 ? 0 : max(0, a.len - a.n + p.by_group(a.row0 + a.rows - 1) + 1);
     const int keys = a.rows <= p.split_rows ? 2 * p.step_keys : p.step_keys;
     a.steps = a.rows <= 0 ? 0 : max(1, (a.hi + keys - 1) / keys);
     return a;
 }
 
-__device__ __forceinline__ AttendUnit attend_unit(const AttendParams &p, int64_t u) {
+__device__ __forceinline__ AttendUnit attend_unit(const AttendParams &p, int u) {
     return attend_unit(p, u, attend_raw(p, u));
 }
 
 // Cached rows that row r of the unit sees.
 __device__ __forceinline__ int attend_sees(const AttendParams &p, const AttendUnit &a, int r) {
-    return max(0, a.len - a.n + (a.row0 + r) / p.group + 1);
+    return max(0, a.len - a.n + p.by_group(a.row0 + r) + 1);
 }
 // Its row of out [n_tokens][n_q_heads].
 __device__ __forceinline__ int64_t attend_out_row(const AttendParams &p, const AttendUnit &a, int r) {
-    const int token = (a.row0 + r) / p.group;
+    const int token = p.by_group(a.row0 + r);
     return (int64_t)(a.q0 + token) * p.n_q_heads + a.h * p.group + (a.row0 + r - token * p.group);
 }
 
@@ -115,7 +131,8 @@ __device__ __forceinline__ int attend_page(const AttendParams &p, int list, int 
 struct AttendRun {
     int64_t total, lo, hi;   // steps in all; this CTA's
     int grid;                // CTAs with work
-    int64_t unit, unit_lo;   // first unit and its first step
+    int unit;                // first unit ...
+    int64_t unit_lo;         // ... and its first step
 };
 
 __device__ __forceinline__ int64_t attend_cut(int64_t total, int grid, int64_t c) {
@@ -130,10 +147,10 @@ __device__ __forceinline__ int attend_cta_of(int64_t total, int grid, int64_t x)
 template <int NT>
 __device__ AttendRun attend_plan(const AttendParams &p, int64_t *scratch) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t per = (p.n_units + NT - 1) / NT;
-    const int64_t u0 = min(p.n_units, per * threadIdx.x), u1 = min(p.n_units, u0 + per);
+    const int per = p.n_units / NT + 1;
+    const int u0 = (int)min((int64_t)p.n_units, (int64_t)per * threadIdx.x), u1 = min(p.n_units - u0, per) + u0;
     int64_t mine = 0;
-    for (int64_t u = u0; u < u1; ++u) mine += attend_unit(p, u).steps;
+    for (int u = u0; u < u1; ++u) mine += attend_unit(p, u).steps;
     int64_t x = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -157,7 +174,7 @@ __device__ AttendRun attend_plan(const AttendParams &p, int64_t *scratch) {
     r.hi = works ? attend_cut(total, r.grid, blockIdx.x + 1) : 0;
     int64_t at = before + x - mine;
     if (works && r.lo >= at && r.lo < at + mine) {
-        for (int64_t u = u0; u < u1; ++u) {
+        for (int u = u0; u < u1; ++u) {
             const int s = attend_unit(p, u).steps;
             if (r.lo < at + s) {
                 found[0] = u;
@@ -168,14 +185,14 @@ __device__ AttendRun attend_plan(const AttendParams &p, int64_t *scratch) {
         }
     }
     __syncthreads();
-    r.unit = works ? found[0] : 0;
+    r.unit = works ? (int)found[0] : 0;
     r.unit_lo = works ? found[1] : 0;
     return r;
 }
 
 // The unit behind u; blocks behind a sequence's last row are passed over.
-__device__ __forceinline__ int64_t attend_next(const AttendParams &p, const AttendUnit &a, int64_t u) {
-    return a.steps == 0 || a.row0 + a.rows >= a.n * p.group ? ((int64_t)a.list + 1) * p.blocks : u + 1;
+__device__ __forceinline__ int attend_next(const AttendParams &p, const AttendUnit &a, int u) {
+    return a.steps == 0 || a.row0 + a.rows >= a.n * p.group ? (a.list + 1) * p.blocks : u + 1;
 }
 
 // ln of the row's sum = ln 2 (m + log2 l).
@@ -194,7 +211,18 @@ struct AttendNeeds {
 AttendNeeds attend_simt_needs(int sms);
 AttendNeeds attend_tc_needs(int sms);
 bool attend_tc_takes(int dtype, int dim, int group);
-// Both fill the units' shape in.
+// The units' shape: blocks of unit_rows rows.  False if there are too many.
+inline bool attend_units(AttendParams &p, int unit_rows) {
+    p.unit_rows = unit_rows;
+    p.blocks = (p.max_new * p.group + unit_rows - 1) / unit_rows;
+    const int64_t n = (int64_t)p.n_seqs * p.n_kv_heads * p.blocks;
+    p.n_units = (int)n;
+    p.by_group = Divider((uint32_t)p.group);
+    p.by_heads = Divider((uint32_t)p.n_kv_heads);
+    p.by_blocks = Divider((uint32_t)p.blocks);
+    return n < INT_MAX;
+}
+// Both set the units' shape.
 int launch_attend_simt(AttendParams &p, bool f32, int grid, cudaStream_t st);
 int launch_attend_tc(AttendParams &p, int grid, cudaStream_t st);
 

@@ -91,7 +91,8 @@ __global__ void __launch_bounds__(kThreads) attend_simt_kernel(const AttendParam
 
     const AttendRun run = attend_plan<kThreads>(p, plan);
     if (run.lo >= run.hi) return;
-    int64_t u = run.unit, u_lo = run.unit_lo;
+    int u = run.unit;
+    int64_t u_lo = run.unit_lo;
     for (int64_t pos = run.lo; pos < run.hi;) {
         const AttendUnit a = attend_unit(p, u);
         if (a.steps == 0) {
@@ -130,7 +131,7 @@ __global__ void __launch_bounds__(kThreads) attend_simt_kernel(const AttendParam
             const int r = i / (D / 4), c = (i - r * (D / 4)) * 4;
             Quad x{0, 0};
             if (r < a.rows) {
-                const int token = (a.row0 + r) / p.group, g = a.row0 + r - token * p.group;
+                const int token = p.by_group(a.row0 + r), g = a.row0 + r - token * p.group;
                 x = quad(static_cast<const T *>(p.q) + (a.q0 + token) * p.q_stride +
                          (int64_t)(a.h * p.group + g) * D + c);
             }
@@ -374,9 +375,10 @@ AttendNeeds attend_simt_needs(int sms) { return {kBlocksPerSm * sms, 2, kSlotRow
 int launch_attend_simt(AttendParams &p, bool f32, int grid, cudaStream_t st) {
     // 16 rows per block where a list's tokens fill no more
     const int rows = p.max_new * p.group <= 16 ? 16 : 64;
-    p.unit_rows = rows;
-    p.blocks = (p.max_new * p.group + rows - 1) / rows;
-    p.n_units = (int64_t)p.n_seqs * p.n_kv_heads * p.blocks;
+    if (!attend_units(p, rows)) {
+        set_error("kvc_attend: n_seqs * n_kv_heads * max_new is too large");
+        return KVC_ERR_UNSUPPORTED;
+    }
     p.step_keys = kKeys;
     p.split_rows = 0;
     const int sms = grid / kBlocksPerSm;

@@ -53,8 +53,7 @@ constexpr int kLoadWarp = 8, kMmaWarp = 9, kLoadWarp2 = 11;
 constexpr int kBox = kTile * 128;       // bytes of 128 rows x 64 bf16
 constexpr uint32_t kColS = 0, kColO = 256;
 constexpr float kGrow = 8.f;            // log2 units m may lag behind
-constexpr int kSlotsTc = 3;             // first, last, exchange of the halves
-constexpr int kSlotExchange = 2;
+constexpr int kSlotsTc = 2;
 
 // Ring stages: what shared memory holds beside Q.
 constexpr int stages_of(int kh) { return kh == 2 ? 5 : 12; }
@@ -69,6 +68,7 @@ struct Bars {
     volatile int abort_flag;
     int dirty;            // some value taken out of V
     int last[2];
+    float2 other[kTile];  // half 1's (max, sum) of a split unit
     int64_t plan[kThreads / 32 + 4];
 };
 
@@ -193,12 +193,13 @@ __device__ __forceinline__ int v_at(const Segment &g, int i) {
 // Walks the units of the CTA's run.
 struct Walk {
     AttendRun run;
-    int64_t pos, u, u_lo;
+    int64_t pos, u_lo;
+    int u;
     AttendUnit a;
     Segment g;
     AttendRaw raw;   // of unit u, asked for while the unit before is worked on
     __device__ Walk(const AttendParams &p, const AttendRun &r)
-        : run(r), pos(r.lo), u(r.unit), u_lo(r.unit_lo), raw(attend_raw(p, r.unit)) {}
+        : run(r), pos(r.lo), u_lo(r.unit_lo), u(r.unit), raw(attend_raw(p, r.unit)) {}
     __device__ bool next(const AttendParams &p) {
         while (pos < run.hi) {
             a = attend_unit(p, u, raw);
@@ -221,10 +222,81 @@ struct Walk {
     int64_t lo;   // the unit's first step
 };
 
+// Adds up the slots of CTAs c0..c1 for rows first.. of the unit and writes them
+// out; 128 threads, `me` their index.  Four chunks of four columns times four
+// slots are asked for at a time: with one load after the other the joining of
+// 19 CTAs' slots took longer than their products.
+template <int D>
+__device__ __noinline__ void join_slots(const AttendParams &p, const AttendUnit &a, int first, int rows,
+                                        int slot_row, int c0, int c1, int me) {
+    constexpr int U = 4, S = 4, kVec = D / 4;
+    for (int x0 = me; x0 < rows * kVec; x0 += kTile * U) {
+        float top[U], sum[U];
+        float4 acc[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            top[u] = -INFINITY;
+            sum[u] = 0.f;
+            acc[u] = make_float4(0, 0, 0, 0);
+        }
+        for (int c = c0; c <= c1; c += S) {
+            float2 st[U][S];
+            float4 y[U][S];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int k = 0; k < S; ++k) {
+                    const int x = x0 + u * kTile, row = x / kVec, d = (x - row * kVec) * 4;
+                    st[u][k] = make_float2(-INFINITY, 0.f);
+                    y[u][k] = make_float4(0, 0, 0, 0);
+                    if (row < rows && c + k <= c1) {
+                        const int64_t at = ((int64_t)(c + k) * kSlotsTc + (c + k == c0 ? kSlotLast : kSlotFirst)) * p.slot_rows + slot_row + row;
+                        st[u][k] = __ldcg(&p.stat[at]);
+                        y[u][k] = __ldcg(reinterpret_cast<const float4 *>(p.part + at * D + d));
+                    }
+                }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float t = top[u];
+#pragma unroll
+                for (int k = 0; k < S; ++k) t = fmaxf(t, st[u][k].x);
+                const float ref = t == -INFINITY ? 0.f : t, down = ex2(top[u] - ref);
+                top[u] = t;
+                sum[u] *= down;
+                acc[u] = make_float4(acc[u].x * down, acc[u].y * down, acc[u].z * down, acc[u].w * down);
+#pragma unroll
+                for (int k = 0; k < S; ++k) {
+                    const float w = ex2(st[u][k].x - ref);
+                    sum[u] = fmaf(st[u][k].y, w, sum[u]);
+                    acc[u].x = fmaf(y[u][k].x, w, acc[u].x);
+                    acc[u].y = fmaf(y[u][k].y, w, acc[u].y);
+                    acc[u].z = fmaf(y[u][k].z, w, acc[u].z);
+                    acc[u].w = fmaf(y[u][k].w, w, acc[u].w);
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int x = x0 + u * kTile, row = x / kVec, d = (x - row * kVec) * 4;
+            if (row >= rows) continue;
+            const bool see = attend_sees(p, a, first + row) > 0;
+            const float inv = 1.f / sum[u];
+            const int64_t out_row = attend_out_row(p, a, first + row);
+            uint32_t q0, q1;
+            const float y0 = see ? acc[u].x * inv : 0.f, y1 = see ? acc[u].y * inv : 0.f;
+            const float y2 = see ? acc[u].z * inv : 0.f, y3 = see ? acc[u].w * inv : 0.f;
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(q0) : "f"(y1), "f"(y0));
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(q1) : "f"(y3), "f"(y2));
+            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + out_row * D + d) = make_uint2(q0, q1);
+            if (d == 0) attend_store_lse(p, out_row, top[u], sum[u], see);
+        }
+    }
+}
+
 template <int KH>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
-                     const __grid_constant__ CUtensorMap tv, const AttendParams p) {
+                     const __grid_constant__ CUtensorMap tv, const __grid_constant__ AttendParams p) {
     constexpr int D = 64 * KH;
     constexpr int kStageBytes = KH * kBox, kStages = stages_of(KH);
     extern __shared__ uint8_t raw[];
@@ -295,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int t = 0; t < tiles; ++t)
                         for (int kh = 0; kh < KH; ++kh)
                             tma_load_4d(&tq, &b.q_full, sq + t * kStageBytes + kh * kBox, kh * 64, 0, w.a.h,
-                                        w.a.q0 + (w.a.row0 + t * R) / p.group);
+                                        w.a.q0 + p.by_group(w.a.row0 + t * R));
                 }
                 ++segs;
             }
@@ -459,10 +531,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r = quarter * 32 + lane;   // row of the tile
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         const uint32_t cs = tmem + lanes + kColS + t * 128, co = tmem + lanes + kColO + t * 128;
-        const bool flip = p.scale_log2 < 0.f;   // maxima are taken of S itself
-        const float c = fabsf(p.scale_log2);
+        // whole tiles take maxima of S itself: only for a positive factor
+        const bool plain = p.scale_log2 > 0.f;
+        const float c = p.scale_log2;
         const unsigned long long c2 = f2_pack(c, c);
-        uint32_t ns = 0, no = 0, nwg = 0, nhalf = 0, filled = 0;
+        uint32_t ns = 0, no = 0, nwg = 0, handed = 0, filled = 0;
+        bool owed = false;   // half 1: O is still being read by half 0
         bool ok = true;
         Walk w(p, run);
         while (ok && w.next(p)) {
@@ -483,6 +557,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++ns;
                 tc_fence_after();
                 const bool edge = k0 + kTile > sees0;
+                if (owed) {
+                    if (!(ok = warp_wait(&b.half_empty, (handed - 1) & 1, stop, p.status))) break;
+                    owed = false;
+                }
                 if (k0 + kTile > from) {
                     // V's rows from the first that some row of the unit does
                     // not see.  Both halves go over the same rows, so each
@@ -492,38 +570,36 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!(ok = warp_wait(&b.full[f % kStages], (f / kStages) & 1, stop, p.status))) break;
                     if (k0 + r >= from) {
                         uint8_t *row = ring + (f % kStages) * kStageBytes + r * 128;
-                        const bool inside = k0 + r < a.len;
-                        for (int kh = 0; kh < KH; ++kh)
-                            for (int ch = 0; ch < 8; ++ch) {
-                                uint4 *at = reinterpret_cast<uint4 *>(row + kh * kBox + ch * 16);
-                                uint4 x = *at;
-                                bool found = false;
+                        // a halfword of ~x & 0x7f80 is 0 where x is not finite;
+                        // lanes start at chunks of their own: no bank conflicts
+                        uint32_t low = 0xffffffffu;
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    uint32_t &xe = e == 0 ? x.x : e == 1 ? x.y : e == 2 ? x.z : x.w;
-                                    if ((xe & 0x7f80u) == 0x7f80u) {
-                                        xe &= 0xffff0000u;
-                                        found = true;
-                                    }
-                                    if ((xe & 0x7f800000u) == 0x7f800000u) {
-                                        xe &= 0xffffu;
-                                        found = true;
-                                    }
-                                }
-                                if (found) {
-                                    if (inside) *static_cast<volatile int *>(&b.dirty) = 1;
-                                    __threadfence_block();
-                                    *at = x;
-                                }
+                        for (int ch = 0; ch < 8 * KH; ++ch) {
+                            const uint4 x = *reinterpret_cast<const uint4 *>(row + (ch >> 3) * kBox + ((ch + r) & 7) * 16);
+                            low = __vminu2(__vminu2(__vminu2(low, ~x.x & 0x7f807f80u), ~x.y & 0x7f807f80u),
+                                           __vminu2(~x.z & 0x7f807f80u, ~x.w & 0x7f807f80u));
+                        }
+                        if ((low & 0xffffu) == 0 || (low >> 16) == 0) {
+                            if (k0 + r < a.len) *static_cast<volatile int *>(&b.dirty) = 1;
+                            __threadfence_block();
+                            for (int e = 0; e < 32 * KH; ++e) {
+                                uint32_t *at = reinterpret_cast<uint32_t *>(row + (e >> 5) * kBox + (e & 31) * 4);
+                                uint32_t x = *at;
+                                if ((x & 0x7f80u) == 0x7f80u) x &= 0xffff0000u;
+                                if ((x & 0x7f800000u) == 0x7f800000u) x &= 0xffffu;
+                                *at = x;
                             }
+                        }
                     }
                     fence_async_shared();
                 }
-                // slow: some row of the tile sees only part of it, or maxima are
-                // minima; two copies, because a select per logit costs as much
+                // slow: some row of the tile sees only part of it, or the scale is
+                // not positive; two copies, because a select per logit costs as much
                 // as the rest
                 auto soften = [&](auto slow) {
                     constexpr bool kSlow = decltype(slow)::value;
+                    unsigned long long mul2 = c2;
+                    float mul = c;
                     float v[4][32];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) tmem_ld32(cs + q * 32, v[q]);
@@ -531,18 +607,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int q = 0; q < 4; ++q) reg_fence(v[q]);
                     const int lim = sees - k0;   // keys of the tile the row sees
-                    if (kSlow && flip) {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) v[q][j] = -v[q][j];
-                    }
                     if (kSlow) {
+                        // scaled here: -infinity for what is not seen may not
+                        // meet a factor of 0 or below later
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
 #pragma unroll
                             for (int j = 0; j < 32; ++j)
-                                if (q * 32 + j >= lim) v[q][j] = -INFINITY;
+                                v[q][j] = q * 32 + j < lim ? v[q][j] * p.scale_log2 : -INFINITY;
+                        mul = 1.f;
+                        mul2 = f2_pack(1.f, 1.f);
                     }
                     float x[4];
 #pragma unroll
@@ -553,8 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         x[q] = fmaxf(x[q], v[q][31]);
                     }
                     const float s_top = fmaxf(fmax3(x[0], x[1], x[2]), x[3]);
-                    // -inf where the row sees nothing yet, also at c = 0
-                    const float top = s_top == -INFINITY ? -INFINITY : s_top * c;
+                    const float top = s_top * mul;
                     if (i == 0) {
                         m = top;
                     } else {
@@ -587,12 +660,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int j = 0; j < 32; ++j) {
                             const int q = 2 * h + (j >> 4), e = 2 * (j & 15);
                             float y0, y1;
-                            f2_unpack(f2_fma(f2_pack(v[q][e], v[q][e + 1]), c2, nm2), y0, y1);
-                            float p0 = ex2(y0), p1 = ex2(y1);
-                            if (kSlow) {   // -inf * 0 is no number: mask again
-                                if (64 * h + 2 * j >= lim) p0 = 0.f;
-                                if (64 * h + 2 * j + 1 >= lim) p1 = 0.f;
-                            }
+                            f2_unpack(f2_fma(f2_pack(v[q][e], v[q][e + 1]), mul2, nm2), y0, y1);
+                            const float p0 = ex2(y0), p1 = ex2(y1);
                             sum2[j & 1] = f2_add(sum2[j & 1], f2_pack(p0, p1));
                             asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(pw[j]) : "f"(p1), "f"(p0));
                         }
@@ -608,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     l += s0 + s1;
                 };
                 if (any) {
-                    if (edge || flip)
+                    if (edge || !plain)
                         soften(std::true_type{});
                     else
                         soften(std::false_type{});
@@ -619,35 +688,38 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!ok) break;
             if (cnt > 0) {
-                if (!(ok = warp_wait(&b.o_full[t], no & 1, stop, p.status))) break;
-                ++no;
+                if (!(ok = warp_wait(&b.o_full[t], no++ & 1, stop, p.status))) break;
                 tc_fence_after();
             }
             filled += 2 * g.n;
-            // where this half's rows go: straight out, to the other half, or to a slot
-            const bool direct = g.whole && !g.split;
-            const bool hand = g.whole && g.split && t == 1;
-            const bool keep = g.whole && g.split && t == 0;
-            const int slot_of_cta = g.whole ? kSlotExchange : g.begins ? kSlotLast : kSlotFirst;
-            const int64_t slot = ((int64_t)blockIdx.x * kSlotsTc + slot_of_cta) * p.slot_rows +
-                                 (slot_of_cta == kSlotExchange ? 0 : t * kTile) + r;
-            if (keep && g.cnt[1] > 0) {   // the other half's rows of this unit
-                if (!(ok = warp_wait(&b.half_full, nhalf & 1, stop, p.status))) break;
-            }
-            if (hand && cnt > 0 && nhalf > 0) {   // those of the unit before have been read
-                if (!(ok = warp_wait(&b.half_empty, (nhalf - 1) & 1, stop, p.status))) break;
-            }
-            if (any && !(hand && cnt == 0)) {
-                float other_w = 0.f, mine_w = 1.f;
-                if (keep && g.cnt[1] > 0 && real) {
-                    const float2 st = __ldcg(&p.stat[slot]);
-                    const float top = fmaxf(m, st.x), ref = top == -INFINITY ? 0.f : top;
-                    mine_w = ex2(m - ref);
-                    other_w = ex2(st.x - ref);
-                    l = l * mine_w + st.y * other_w;
-                    m = top;
+            if (g.split && t == 1) {
+                // the other half takes these rows over, O straight from TMEM
+                if (cnt > 0) {
+                    b.other[r] = make_float2(m, l);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&b.half_full);
+                    ++handed;
+                    owed = true;
                 }
-                const float inv = sees > 0 ? 1.f / l : 0.f;
+                continue;
+            }
+            const bool take = g.split && g.cnt[1] > 0;
+            float w_mine = 1.f, w_other = 0.f;
+            if (take) {
+                if (!(ok = warp_wait(&b.half_full, handed++ & 1, stop, p.status))) break;
+                tc_fence_after();
+                const float2 st = b.other[r];
+                const float top = fmaxf(m, st.x), ref = top == -INFINITY ? 0.f : top;
+                w_mine = ex2(m - ref);
+                w_other = ex2(st.x - ref);
+                l = l * w_mine + st.y * w_other;
+                m = top;
+            }
+            const int64_t slot = ((int64_t)blockIdx.x * kSlotsTc + (g.begins ? kSlotLast : kSlotFirst)) * p.slot_rows +
+                                 t * kTile + r;
+            if (any) {
+                const float inv = 1.f / l;
                 const int64_t out_row = real ? attend_out_row(p, a, rt) : 0;
                 const bool dirty = *static_cast<volatile int *>(&b.dirty);
 #pragma unroll 1
@@ -656,16 +728,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float o[32];
                     if (cnt > 0) {
                         tmem_ld32(co + d, o);
-                        tmem_ld_wait();
-                        reg_fence(o);
+                        if (take) {
+                            float y[32];
+                            tmem_ld32(co + 128 + d, y);
+                            tmem_ld_wait();
+                            reg_fence(o);
+                            reg_fence(y);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) o[j] = fmaf(o[j], w_mine, y[j] * w_other);
+                        } else {
+                            tmem_ld_wait();
+                            reg_fence(o);
+                        }
                     } else {
 #pragma unroll
                         for (int j = 0; j < 32; ++j) o[j] = 0.f;
                     }
-                    if (dirty && real) {   // what was taken out, for rows that see it
+                    if (!real) continue;
+                    if (dirty) {   // what was taken out of V, for rows that see it
                         const int k1 = min(sees, (g.first + g.n) * kTile);
                         for (int k = max(from, g.first * kTile); k < k1; ++k) {
-                            if (g.split && ((k / kTile - g.first) & 1) != t) continue;
                             const int page = p.table[(int64_t)a.list * p.max_pages + (k >> p.shift)];
                             if (page < 0 || page >= p.n_pages) continue;
                             const uint16_t *vr = static_cast<const uint16_t *>(p.v_pool) +
@@ -677,19 +759,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         }
                     }
-                    if (!real) continue;
-                    if (direct || keep) {
-                        if (keep && g.cnt[1] > 0) {
-                            const float4 *src = reinterpret_cast<const float4 *>(p.part + slot * D + d);
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                const float4 y = __ldcg(src + j);
-                                o[4 * j] = o[4 * j] * mine_w + y.x * other_w;
-                                o[4 * j + 1] = o[4 * j + 1] * mine_w + y.y * other_w;
-                                o[4 * j + 2] = o[4 * j + 2] * mine_w + y.z * other_w;
-                                o[4 * j + 3] = o[4 * j + 3] * mine_w + y.w * other_w;
-                            }
-                        }
+                    if (g.whole) {
                         uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + out_row * D + d);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
@@ -711,7 +781,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (real) {
-                    if (direct || keep)
+                    if (g.whole)
                         attend_store_lse(p, out_row, m, l, sees > 0);
                     else
                         p.stat[slot] = make_float2(m, l);
@@ -719,13 +789,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
             tc_fence_before();   // O is read: the next unit's products may overwrite it
-            if (g.whole && g.split) {
-                if (g.cnt[1] > 0) {
-                    if (lane == 0) mbar_arrive(hand ? &b.half_full : &b.half_empty);
-                    ++nhalf;
-                }
-            } else if (!g.whole) {
-                // the last of the CTAs (and, where both halves hold the same rows, halves) joins
+            if (take && lane == 0) mbar_arrive(&b.half_empty);
+            if (!g.whole) {
+                // the CTA that finishes last joins the unit's slots
                 const int c0 = attend_cta_of(run.total, run.grid, w.lo);
                 const int c1 = attend_cta_of(run.total, run.grid, w.lo + a.steps - 1);
                 __threadfence();
@@ -733,9 +799,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive(&b.wg[t]);
                 if (!(ok = warp_wait(&b.wg[t], nwg++ & 1, stop, p.status))) break;
                 if (quarter == 0 && lane == 0) {
-                    uint32_t *count = &p.arrived[2 * c0 + (g.split ? 0 : t)];
-                    const uint32_t all = (uint32_t)(c1 - c0 + 1) * (g.split ? 2u : 1u);
-                    const bool last = atomicAdd(count, 1u) == all - 1;
+                    uint32_t *count = &p.arrived[2 * c0 + t];
+                    const bool last = atomicAdd(count, 1u) == (uint32_t)(c1 - c0);
                     if (last) *count = 0;
                     __threadfence();
                     b.last[t] = last;
@@ -745,45 +810,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!(ok = warp_wait(&b.wg[t], nwg++ & 1, stop, p.status))) break;
                 if (*static_cast<volatile int *>(&b.last[t])) {
                     __threadfence();
-                    const int first_row = g.split ? 0 : t * R;
-                    const int rows = min(a.rows - first_row, R);
-                    const int halves = g.split ? 2 : 1;
-                    constexpr int kVec = D / 4;
-                    for (int x = r; x < rows * kVec; x += kTile) {
-                        const int rr = x / kVec, d = (x - rr * kVec) * 4;
-                        auto at = [&](int cta, int h) {
-                            return ((int64_t)cta * kSlotsTc + (cta == c0 ? kSlotLast : kSlotFirst)) * p.slot_rows +
-                                   (g.split ? h : t) * kTile + rr;
-                        };
-                        float top = -INFINITY;
-                        for (int cta = c0; cta <= c1; ++cta)
-                            for (int h = 0; h < halves; ++h) top = fmaxf(top, __ldcg(&p.stat[at(cta, h)]).x);
-                        const float ref = top == -INFINITY ? 0.f : top;
-                        float sum = 0.f;
-                        float4 acc = make_float4(0, 0, 0, 0);
-                        for (int cta = c0; cta <= c1; ++cta)
-                            for (int h = 0; h < halves; ++h) {
-                                const int64_t s = at(cta, h);
-                                const float2 st = __ldcg(&p.stat[s]);
-                                const float4 y = __ldcg(reinterpret_cast<const float4 *>(p.part + s * D + d));
-                                const float wgt = ex2(st.x - ref);
-                                sum = fmaf(st.y, wgt, sum);
-                                acc.x = fmaf(y.x, wgt, acc.x);
-                                acc.y = fmaf(y.y, wgt, acc.y);
-                                acc.z = fmaf(y.z, wgt, acc.z);
-                                acc.w = fmaf(y.w, wgt, acc.w);
-                            }
-                        const bool see = attend_sees(p, a, first_row + rr) > 0;
-                        const float inv = 1.f / sum;
-                        const int64_t row = attend_out_row(p, a, first_row + rr);
-                        uint32_t q0, q1;
-                        const float y0 = see ? acc.x * inv : 0.f, y1 = see ? acc.y * inv : 0.f;
-                        const float y2 = see ? acc.z * inv : 0.f, y3 = see ? acc.w * inv : 0.f;
-                        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(q0) : "f"(y1), "f"(y0));
-                        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(q1) : "f"(y3), "f"(y2));
-                        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + row * D + d) = make_uint2(q0, q1);
-                        if (d == 0) attend_store_lse(p, row, top, sum, see);
-                    }
+                    const int first_row = t * R;
+                    join_slots<D>(p, a, first_row, min(a.rows - first_row, R), t * kTile, c0, c1, r);
                 }
             }
         }
@@ -837,11 +865,12 @@ bool attend_tc_takes(int dtype, int dim, int group) {
 
 int launch_attend_tc(AttendParams &p, int grid, cudaStream_t st) {
     const int R = kTile / p.group * p.group;   // whole tokens
-    p.unit_rows = 2 * R;
     p.split_rows = R;
     p.step_keys = kTile;
-    p.blocks = (p.max_new * p.group + 2 * R - 1) / (2 * R);
-    p.n_units = (int64_t)p.n_seqs * p.n_kv_heads * p.blocks;
+    if (!attend_units(p, 2 * R)) {
+        set_error("kvc_attend: n_seqs * n_kv_heads * max_new is too large");
+        return KVC_ERR_UNSUPPORTED;
+    }
     return p.dim == 64 ? launch<1>(p, grid, st) : launch<2>(p, grid, st);
 }
 

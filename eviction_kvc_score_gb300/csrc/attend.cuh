@@ -19,21 +19,6 @@
 
 namespace kvc {
 
-// n / d for n < 2^31 by a multiplication and a shift (the round-up method of
-// Granlund and Montgomery, "Division by invariant integers using
-// multiplication", 1994): the walk over units divides a lot.
-struct Divider {
-    uint32_t d, mul, shift;
-    __host__ __device__ Divider() {}
-    explicit Divider(uint32_t by) : d(by), shift(0) {
-        while (((uint64_t)1 << shift) < by) ++shift;
-        mul = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << shift) - by)) / by + 1);
-    }
-    __device__ __forceinline__ int operator()(int n) const {
-        return (int)((__umulhi((uint32_t)n, mul) + (uint32_t)n) >> shift);
-    }
-};
-
 struct AttendParams {
     int n_seqs, n_q_heads, n_kv_heads, group, dim;
     Divider by_group, by_heads, by_blocks;

@@ -7,12 +7,12 @@
 //   m' = max(m, max_j x_j),  l' = l 2^(m - m') + sum_j 2^(x_j - m'),
 //   o' = o 2^(m - m') + sum_j 2^(x_j - m') v_j,  out = o / l.
 //
-// A block of 128 threads holds ROWS rows (tokens x query heads of one KV head)
-// and walks 64-key tiles; a thread owns 4 rows x 64/TX keys of the logits and
-// the same 4 rows x D/TX columns of o, TX = 8 for 64 rows, 32 for 16.  With 64
-// rows the work is bound by the FMA pipe: 12 16-byte shared loads feed 128 FMAs
-// (as 64 two-wide ones) of the logits, 5 feed 64 of the output at D = 128.  With
-// 16 (decode) it is bound by reading the cache.  K of the next tile is on its
+// A block holds ROWS rows (tokens x query heads of one KV head) and walks 64-key
+// tiles; a thread owns 4 rows x 64/TX keys of the logits and the same 4 rows x
+// D/TX columns of o: 256 threads, TX = 16 for 64 rows; 128 threads, TX = 32 for
+// 16 rows.  With 64 rows the work is bound by the FMA pipe, with 16 (decode) by
+// reading the cache.  (Tiles of 4 x 8 keys by 128 threads need fewer shared
+// loads but 250 registers: eight warps per SM left the FMA pipe at a third.)  K of the next tile is on its
 // way (cp.async) during the product with V, V of the next during the logits.
 // K and V stay in shared memory in their own type; a row is padded by 16 bytes,
 // which spreads 8 rows' loads over all banks for every D that is a multiple of 8.
@@ -25,7 +25,6 @@ namespace kvc {
 
 namespace {
 
-constexpr int kThreads = 128;
 constexpr int kKeys = 64;
 constexpr int kSlotRows = 64;
 constexpr int kBlocksPerSm = 4;   // at most: the workspace's slots are sized by it
@@ -34,10 +33,11 @@ template <typename T>
 constexpr int row_bytes(int dim) {
     return dim * (int)sizeof(T) + 16;
 }
+constexpr int threads_of(int rows) { return rows == 64 ? 256 : 128; }
 template <typename T, int ROWS>
 size_t smem_bytes(int dim) {
     return (size_t)ROWS * (dim + 4) * 4 + 2 * (size_t)kKeys * row_bytes<T>(dim) +
-           (size_t)kKeys * (ROWS + 4) * 4 + (kThreads / 32 + 6) * 8;
+           (size_t)kKeys * (ROWS + 4) * 4 + (threads_of(ROWS) / 32 + 6) * 8;
 }
 
 // Four elements as two pairs.
@@ -52,6 +52,32 @@ __device__ __forceinline__ Quad quad(const __nv_bfloat16 *p) {
     const uint2 w = *reinterpret_cast<const uint2 *>(p);
     return {f2_pack(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u)),
             f2_pack(__uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u))};
+}
+template <int N>
+struct Pairs {
+    unsigned long long v[N];
+};
+// 2 N elements as N pairs, N = 1 or 2.
+template <int N, typename T>
+__device__ __forceinline__ Pairs<N> pairs_at(const T *p) {
+    Pairs<N> r;
+    if constexpr (N == 2) {
+        const Quad q = quad(p);
+        r.v[0] = q.a;
+        r.v[1] = q.b;
+    } else if constexpr (sizeof(T) == 4) {
+        r.v[0] = *reinterpret_cast<const unsigned long long *>(p);
+    } else {
+        const uint32_t w = *reinterpret_cast<const uint32_t *>(p);
+        r.v[0] = f2_pack(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    }
+    return r;
+}
+__device__ __forceinline__ void store2(float *p, float x, float y) { *reinterpret_cast<float2 *>(p) = make_float2(x, y); }
+__device__ __forceinline__ void store2(__nv_bfloat16 *p, float x, float y) {
+    uint32_t a;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(a) : "f"(y), "f"(x));
+    *reinterpret_cast<uint32_t *>(p) = a;
 }
 __device__ __forceinline__ void store4(float *p, float4 x) { *reinterpret_cast<float4 *>(p) = x; }
 __device__ __forceinline__ void store4(__nv_bfloat16 *p, float4 x) {
@@ -73,10 +99,12 @@ __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// CT: 16-byte (fp32) column chunks of a thread, CT * TX * 4 >= D.
-template <typename T, int ROWS, int CT>
-__global__ void __launch_bounds__(kThreads) attend_simt_kernel(const AttendParams p) {
-    constexpr int TX = ROWS == 64 ? 8 : 32, KT = kKeys / TX;
+// A thread's columns: CT chunks of 2 N, CT * TX * 2 N >= D.
+template <typename T, int ROWS, int N, int CT>
+__global__ void __launch_bounds__(threads_of(ROWS), ROWS == 64 ? 2 : 4) attend_simt_kernel(const AttendParams p) {
+    constexpr int kThreads = threads_of(ROWS), W = 2 * N;
+    constexpr int TX = ROWS == 64 ? 16 : 32, KT = kKeys / TX;
+    constexpr int kPass = kThreads / 8, kPasses = kKeys / kPass;   // rows copied at a time
     static_assert(TX * (ROWS / 4) == kThreads, "four rows per thread");
     extern __shared__ __align__(16) uint8_t raw[];
     const int D = p.dim, rb = row_bytes<T>(D), vecs = D * (int)sizeof(T) / 16;
@@ -89,6 +117,8 @@ __global__ void __launch_bounds__(kThreads) attend_simt_kernel(const AttendParam
     const int tid = threadIdx.x, tx = tid % TX, ty = tid / TX;
     const int pr = 1 << p.shift;
 
+    let_next_start();
+    wait_for_inputs();
     const AttendRun run = attend_plan<kThreads>(p, plan);
     if (run.lo >= run.hi) return;
     int u = run.unit;
@@ -101,20 +131,20 @@ __global__ void __launch_bounds__(kThreads) attend_simt_kernel(const AttendParam
         }
         const int64_t end = min(run.hi, u_lo + a.steps);
         const int t0 = (int)(pos - u_lo), t1 = (int)(end - u_lo);
-        // eight threads copy a row, 16 rows at a time; pages are looked up
-        // ahead of the copies that use them
-        int page[4];
+        // eight threads copy a row; pages are looked up ahead of the copies
+        // that use them
+        int page[kPasses];
         auto look_up = [&](int t) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int j = t * kKeys + 16 * i + (tid >> 3);
+            for (int i = 0; i < kPasses; ++i) {
+                const int j = t * kKeys + kPass * i + (tid >> 3);
                 page[i] = j < a.hi ? attend_page(p, a.list, j >> p.shift) : -1;
             }
         };
         auto fetch = [&](uint8_t *dst, const void *pool, int t) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = 16 * i + (tid >> 3), j = t * kKeys + r;
+            for (int i = 0; i < kPasses; ++i) {
+                const int r = kPass * i + (tid >> 3), j = t * kKeys + r;
                 const bool valid = page[i] >= 0;
                 const T *src = static_cast<const T *>(pool) +
                                (((int64_t)(valid ? page[i] : 0) << p.shift) + (j & (pr - 1))) * D;
@@ -138,7 +168,7 @@ __global__ void __launch_bounds__(kThreads) attend_simt_kernel(const AttendParam
             *reinterpret_cast<ulonglong2 *>(sq + r * (D + 4) + c) = make_ulonglong2(x.a, x.b);
         }
         float m[4], l[4];
-        unsigned long long o[4][2 * CT];
+        unsigned long long o[4][N * CT];
         int sees[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -147,7 +177,7 @@ __global__ void __launch_bounds__(kThreads) attend_simt_kernel(const AttendParam
             l[i] = 0.f;
             sees[i] = r < a.rows ? attend_sees(p, a, r) : 0;
 #pragma unroll
-            for (int c = 0; c < 2 * CT; ++c) o[i][c] = 0;
+            for (int c = 0; c < N * CT; ++c) o[i][c] = 0;
         }
         const int sees0 = attend_sees(p, a, 0);
         const bool some = (tid & ~31) / TX * 4 < a.rows;   // the warp has a row
@@ -164,7 +194,7 @@ __global__ void __launch_bounds__(kThreads) attend_simt_kernel(const AttendParam
 #pragma unroll
                     for (int j = 0; j < KT; ++j) x2[i][j] = 0;
                 const float *q = sq + ty * 4 * (D + 4);
-#pragma unroll 2
+#pragma unroll 4
                 for (int c = 0; c < D; c += 4) {
                     Quad qq[4];
 #pragma unroll
@@ -208,7 +238,7 @@ __global__ void __launch_bounds__(kThreads) attend_simt_kernel(const AttendParam
                     m[i] = top;
                     const unsigned long long down2 = f2_pack(down, down);
 #pragma unroll
-                    for (int c = 0; c < 2 * CT; ++c) o[i][c] = f2_mul(o[i][c], down2);
+                    for (int c = 0; c < N * CT; ++c) o[i][c] = f2_mul(o[i][c], down2);
                 }
 #pragma unroll
                 for (int j = 0; j < KT; ++j)
@@ -225,7 +255,7 @@ __global__ void __launch_bounds__(kThreads) attend_simt_kernel(const AttendParam
             if (some) {
                 auto product = [&](auto cut) {
                     const int nk = min(kKeys, a.hi - j0);
-#pragma unroll 2
+#pragma unroll 4
                     for (int j = 0; j < nk; ++j) {
                         const float4 e = *reinterpret_cast<const float4 *>(sp + j * (ROWS + 4) + ty * 4);
                         const unsigned long long e2[4] = {f2_pack(e.x, e.x), f2_pack(e.y, e.y),
@@ -233,17 +263,16 @@ __global__ void __launch_bounds__(kThreads) attend_simt_kernel(const AttendParam
                         const T *v = reinterpret_cast<const T *>(sv + j * rb);
 #pragma unroll
                         for (int c = 0; c < CT; ++c) {
-                            const int col = (tx + TX * c) * 4;
-                            if (CT * TX * 4 == D || col < D) {
-                                const Quad vv = quad(v + col);
+                            // columns past D are read from the row's end on (still
+                            // shared memory) and never stored
+                            const Pairs<N> vv = pairs_at<N>(v + (tx + TX * c) * W);
 #pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    // a value that a row does not see may be anything
-                                    if (!decltype(cut)::value || j0 + j < sees[i]) {
-                                        o[i][2 * c] = f2_fma(e2[i], vv.a, o[i][2 * c]);
-                                        o[i][2 * c + 1] = f2_fma(e2[i], vv.b, o[i][2 * c + 1]);
-                                    }
-                            }
+                            for (int i = 0; i < 4; ++i)
+                                // a value that a row does not see may be anything
+                                if (!decltype(cut)::value || j0 + j < sees[i])
+#pragma unroll
+                                    for (int h = 0; h < N; ++h)
+                                        o[i][N * c + h] = f2_fma(e2[i], vv.v[h], o[i][N * c + h]);
                         }
                     }
                 };
@@ -268,19 +297,16 @@ __global__ void __launch_bounds__(kThreads) attend_simt_kernel(const AttendParam
             const int64_t row = attend_out_row(p, a, r);
             const float inv = sees[i] > 0 ? 1.f / l[i] : 0.f;
 #pragma unroll
-            for (int c = 0; c < CT; ++c) {
-                const int col = (tx + TX * c) * 4;
+            for (int c = 0; c < N * CT; ++c) {
+                const int col = (tx + TX * (c / N)) * W + 2 * (c % N);
                 if (col >= D) continue;
-                float4 y;
-                f2_unpack(o[i][2 * c], y.x, y.y);
-                f2_unpack(o[i][2 * c + 1], y.z, y.w);
-                if (whole) {
-                    y = sees[i] > 0 ? make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv)
-                                    : make_float4(0, 0, 0, 0);
-                    store4(static_cast<T *>(p.out) + row * D + col, y);
-                } else {
-                    *reinterpret_cast<float4 *>(p.part + (slot * p.slot_rows + r) * D + col) = y;
-                }
+                float y0, y1;
+                f2_unpack(o[i][c], y0, y1);
+                if (whole)
+                    store2(static_cast<T *>(p.out) + row * D + col, sees[i] > 0 ? y0 * inv : 0.f,
+                           sees[i] > 0 ? y1 * inv : 0.f);
+                else
+                    store2(p.part + (slot * p.slot_rows + r) * D + col, y0, y1);
             }
             if (tx == 0) {
                 if (whole)
@@ -341,31 +367,29 @@ __global__ void __launch_bounds__(kThreads) attend_simt_kernel(const AttendParam
     }
 }
 
-template <typename T, int ROWS, int CT>
+template <typename T, int ROWS, int N, int CT>
 int launch(AttendParams &p, int sms, cudaStream_t st) {
+    auto kernel = attend_simt_kernel<T, ROWS, N, CT>;
     const size_t bytes = smem_bytes<T, ROWS>(p.dim);
-    if (bytes > 48 * 1024)
-        cudaFuncSetAttribute(attend_simt_kernel<T, ROWS, CT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             232448);
+    if (bytes > 48 * 1024) cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
     // as many blocks as an SM holds at once (1 KB of shared memory is each block's own cost)
-    static const int by_regs = [] {
-        cudaFuncAttributes at{};
-        return cudaFuncGetAttributes(&at, attend_simt_kernel<T, ROWS, CT>) == cudaSuccess && at.numRegs > 0
-                   ? 65536 / (kThreads * ((at.numRegs + 7) / 8 * 8)) : 1;
-    }();
-    const int per_sm = std::max(1, std::min({kBlocksPerSm, by_regs, (int)(233472 / (bytes + 1024))}));
-    attend_simt_kernel<T, ROWS, CT><<<per_sm * sms, kThreads, bytes, st>>>(p);
+    const int per_sm = std::max(1, std::min(ROWS == 64 ? 2 : 4, (int)(233472 / (bytes + 1024))));
+    launch_early(kernel, per_sm * sms, threads_of(ROWS), bytes, st, p);
     return cache_launched("kvc_attend");
 }
 
 template <typename T>
 int launch_type(AttendParams &p, int rows, int sms, cudaStream_t st) {
     const int d = p.dim;
-    if (rows == 16) return d <= 128 ? launch<T, 16, 1>(p, sms, st) : launch<T, 16, 2>(p, sms, st);
-    return d <= 64    ? launch<T, 64, 2>(p, sms, st)
-           : d <= 96  ? launch<T, 64, 3>(p, sms, st)
-           : d <= 128 ? launch<T, 64, 4>(p, sms, st)
-                      : launch<T, 64, 8>(p, sms, st);
+    if (rows == 16)
+        return d <= 64    ? launch<T, 16, 1, 1>(p, sms, st)
+               : d <= 128 ? launch<T, 16, 2, 1>(p, sms, st)
+                          : launch<T, 16, 2, 2>(p, sms, st);
+    return d <= 64    ? launch<T, 64, 2, 1>(p, sms, st)
+           : d <= 96  ? launch<T, 64, 1, 3>(p, sms, st)
+           : d <= 128 ? launch<T, 64, 2, 2>(p, sms, st)
+           : d <= 192 ? launch<T, 64, 2, 3>(p, sms, st)
+                      : launch<T, 64, 2, 4>(p, sms, st);
 }
 
 }  // namespace

@@ -329,6 +329,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         b.dirty = 0;
         fence_barrier_init();
     }
+    let_next_start();
+    wait_for_inputs();
     const AttendRun run = attend_plan<kThreads>(p, b.plan);
     if (run.lo >= run.hi) return;   // more CTAs than steps
     if (warp == kMmaWarp) {
@@ -851,7 +853,7 @@ int launch(AttendParams &p, int grid, cudaStream_t st) {
         return KVC_ERR_UNSUPPORTED;
     }
     cudaFuncSetAttribute(attend_tc_kernel<KH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    attend_tc_kernel<KH><<<grid, kThreads, bytes, st>>>(tq, tk, tv, p);
+    launch_early(attend_tc_kernel<KH>, grid, kThreads, bytes, st, tq, tk, tv, p);
     return cache_launched("kvc_attend");
 }
 

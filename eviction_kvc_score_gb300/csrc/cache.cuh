@@ -78,6 +78,44 @@ struct RopeArgs {
     int64_t q_stride, q_out_stride, k_stride, k_out_stride;
 };
 
+// n / d for n < 2^31 by a multiplication and a shift (the round-up method of
+// Granlund and Montgomery, "Division by invariant integers using
+// multiplication", 1994): the walk over units divides a lot.
+struct Divider {
+    uint32_t d, mul, shift;
+    __host__ __device__ Divider() {}
+    explicit Divider(uint32_t by) : d(by), shift(0) {
+        while (((uint64_t)1 << shift) < by) ++shift;
+        mul = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << shift) - by)) / by + 1);
+    }
+    __device__ __forceinline__ int operator()(int n) const {
+        return (int)((__umulhi((uint32_t)n, mul) + (uint32_t)n) >> shift);
+    }
+};
+
+// Launches of these operators may begin before the kernel in front has ended
+// (programmatic dependent launch): a kernel waits with wait_for_inputs() before
+// it touches memory, which ends when everything in front is complete and
+// visible, and only its launch latency is hidden.  let_next_start() says that
+// the next kernel's blocks may be brought in.
+__device__ __forceinline__ void wait_for_inputs() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename... P, typename... A>
+void launch_early(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, A... args) {
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    cudaLaunchKernelEx(&cfg, kernel, P(args)...);   // errors stay for cache_launched
+}
+
 // KVC_OK, or KVC_ERR_CUDA with a message if the launches before failed.
 int cache_launched(const char *fn);
 

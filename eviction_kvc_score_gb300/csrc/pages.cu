@@ -90,6 +90,8 @@ __device__ void let_go(const PagesState &s, int32_t page, int32_t n_pages) {
 }
 
 __global__ void pages_init_kernel(PagesState s, int32_t n_pages) {
+    let_next_start();
+    wait_for_inputs();
     const int stride = gridDim.x * blockDim.x, me = blockIdx.x * blockDim.x + threadIdx.x;
     for (int w = me; w < s.n_words; w += stride) {
         const int left = n_pages - w * 32;
@@ -147,19 +149,42 @@ __device__ Two list_needs(const PlanParams &p, int i, uint32_t *bad) {
     return need;
 }
 
+// The n-th (from 0) set bit of x.
+__device__ __forceinline__ int nth_bit(uint32_t x, int n) {
+    int at = 0;
+#pragma unroll
+    for (int w = 16; w >= 1; w >>= 1) {
+        const int below = __popc((x >> at) & ((1u << w) - 1u));
+        if (n >= below) {
+            n -= below;
+            at += w;
+        }
+    }
+    return at;
+}
+
 __global__ void __launch_bounds__(kPlanThreads) pages_plan_kernel(PlanParams p) {
     __shared__ Two scratch[33];
-    __shared__ uint32_t s_bad;
+    __shared__ uint32_t s_bad, s_shared;
     __shared__ int32_t s_groups[kPlanThreads];
+    __shared__ uint32_t s_bits[kPlanThreads];
+    __shared__ int32_t s_rank[kPlanThreads];
     PagesHeader *head = p.s.head;
-    if (threadIdx.x == 0) s_bad = 0;
+    const int tid = threadIdx.x;
+    if (tid == 0) s_bad = s_shared = 0;
+    let_next_start();
+    wait_for_inputs();
     __syncthreads();
     uint32_t bad = 0;
     Two sum{0, 0};
+    bool shares = false;
     for (int base = 0; base < p.n_lists; base += kPlanThreads) {
-        const int i = base + threadIdx.x;
+        const int i = base + tid;
         Two need{0, 0}, all;
-        if (i < p.n_lists) need = list_needs(p, i, &bad);
+        if (i < p.n_lists) {
+            need = list_needs(p, i, &bad);
+            shares |= p.s.shared[i] >= 0;
+        }
         const Two at = block_scan(need, scratch, &all);
         if (i < p.n_lists) {
             p.s.row_begin[i] = sum.rows + at.rows;
@@ -167,16 +192,17 @@ __global__ void __launch_bounds__(kPlanThreads) pages_plan_kernel(PlanParams p) 
         }
         sum = sum + all;
         if (sum.pages > p.n_pages) {   // more than the pool holds
-            if (threadIdx.x == 0) atomicOr(&s_bad, KVC_DEV_PAGES_FULL);
+            if (tid == 0) atomicOr(&s_bad, KVC_DEV_PAGES_FULL);
             break;
         }
     }
     if (bad) atomicOr(&s_bad, bad);
+    if (shares) s_shared = 1;
     __syncthreads();
-    if (threadIdx.x == 0 && s_bad == 0 && sum.pages > head->n_free) s_bad = KVC_DEV_PAGES_FULL;
+    if (tid == 0 && s_bad == 0 && sum.pages > head->n_free) s_bad = KVC_DEV_PAGES_FULL;
     __syncthreads();
     const bool ok = s_bad == 0;
-    if (threadIdx.x == 0) {
+    if (tid == 0) {
         if (!ok) set_status(&head->status, s_bad);
         head->ok = ok;
         head->total_new = (int32_t)sum.pages;
@@ -188,48 +214,59 @@ __global__ void __launch_bounds__(kPlanThreads) pages_plan_kernel(PlanParams p) 
     }
     if (!ok) return;
 
-    // the lowest free pages, group by group, each thread a word of the bitmap
+    // the lowest free pages, group by group: each thread ranks a word of the
+    // bitmap, then each writes down pages by rank
     const int need = (int)sum.pages;
     int found = 0;
     for (int g0 = 0; g0 < p.s.n_groups && found < need; g0 += kPlanThreads) {
         __syncthreads();
-        s_groups[threadIdx.x] = g0 + threadIdx.x < p.s.n_groups ? p.s.group_free[g0 + threadIdx.x] : 0;
+        s_groups[tid] = g0 + tid < p.s.n_groups ? p.s.group_free[g0 + tid] : 0;
         __syncthreads();
         for (int j = 0; j < kPlanThreads && found < need; ++j) {
             if (s_groups[j] == 0) continue;
-            const int word = (g0 + j) * kGroupWords + threadIdx.x;
+            const int word0 = (g0 + j) * kGroupWords, word = word0 + tid;
             uint32_t bits = word < p.s.n_words ? p.s.bitmap[word] : 0;
             Two all;
-            const int at = found + (int)block_scan(Two{0, __popc(bits)}, scratch, &all).pages;
-            const int take = max(0, min(__popc(bits), need - at));
-            for (int k = 0; k < take; ++k) {
-                const int bit = __ffs(bits) - 1;
-                bits &= bits - 1;
-                p.s.fresh[at + k] = word * 32 + bit;
-                p.s.holders[word * 32 + bit] = 1;
-            }
-            if (take) p.s.bitmap[word] = bits;
+            const int rank = (int)block_scan(Two{0, __popc(bits)}, scratch, &all).pages;
             const int took = min((int)all.pages, need - found);
-            if (threadIdx.x == 0) {
+            s_bits[tid] = bits;
+            s_rank[tid] = rank;
+            __syncthreads();
+            for (int e = tid; e < took; e += kPlanThreads) {
+                int lo = 0;
+#pragma unroll
+                for (int w = kPlanThreads / 2; w >= 1; w >>= 1)
+                    if (s_rank[lo + w] <= e) lo += w;
+                const int page = (word0 + lo) * 32 + nth_bit(s_bits[lo], e - s_rank[lo]);
+                p.s.fresh[found + e] = page;
+                p.s.holders[page] = 1;
+            }
+            if (rank < took && bits) {
+                const int mine = min(__popc(bits), took - rank);
+                p.s.bitmap[word] = mine == __popc(bits) ? 0 : bits & ~((2u << nth_bit(bits, mine - 1)) - 1u);
+            }
+            if (tid == 0) {
                 p.s.group_free[g0 + j] -= took;
                 head->n_free -= took;
             }
             found += took;
+            __syncthreads();
         }
     }
     if (!p.append) return;
     // the lists' new lengths; their copied last pages lose a holder (after the
     // search, so that this call does not hand them out)
     __syncthreads();
+    const bool drop = s_shared;
     for (int base = 0; base < p.n_lists; base += kPlanThreads) {
-        const int i = base + threadIdx.x;
+        const int i = base + tid;
         int32_t page = -1;
         if (i < p.n_lists) {
             const int32_t n = p.counts[i];
             page = p.s.shared[i];
             if (n > 0) p.len[i] = p.s.old_len[i] + n;
         }
-        let_go(p.s, page, p.n_pages);
+        if (drop) let_go(p.s, page, p.n_pages);
     }
 }
 
@@ -241,49 +278,58 @@ struct MoveParams {
     const int32_t *idx;       // compact: rows of the list itself
     int32_t n_lists, n_pages, max_pages, shift, k_max;
     int vec;                  // 16-byte vectors per row
+    Divider by_vec;
     const uint4 *k_src, *v_src;
     uint4 *k_pool, *v_pool;
 };
 
-// Last i of [0, n) with begin[i] <= x.
+// Last i of [0, n) with begin[i] <= x (begin ascends from 0); the whole warp
+// asks for one x, 32 places at a time.
 template <typename T>
 __device__ __forceinline__ int owner(const T *begin, int n, T x) {
-    int lo = 0, hi = n;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (begin[mid] <= x)
-            lo = mid;
-        else
-            hi = mid;
+    const int lane = threadIdx.x & 31;
+    int lo = 0, span = n;
+    while (span > 1) {
+        const int step = (span + 31) >> 5, i = lo + lane * step;
+        const unsigned below = __ballot_sync(0xffffffffu, lane * step < span && begin[i] <= x);
+        const int k = 31 - __clz(below);
+        span = min(step, span - k * step);
+        lo += k * step;
     }
     return lo;
 }
 
 template <bool APPEND>
 __global__ void __launch_bounds__(kMoveThreads) pages_move_kernel(MoveParams p) {
+    let_next_start();
+    wait_for_inputs();
     if (!p.s.head->ok) return;
     const int64_t rows = p.s.head->total_rows;
-    const int total_new = p.s.head->total_new;
     const int ps = 1 << p.shift, lane = threadIdx.x & 31;
-    const int64_t me = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (APPEND) {   // the new pages' table entries
-        for (int64_t e = me; e < total_new; e += (int64_t)gridDim.x * blockDim.x) {
-            const int i = owner(p.s.page_begin, p.n_lists, (int32_t)e);
+    const int64_t warps = (int64_t)gridDim.x * (kMoveThreads / 32);
+    const int64_t me = ((int64_t)blockIdx.x * kMoveThreads + threadIdx.x) >> 5;
+    if (APPEND) {   // the new pages' table entries, 32 a warp
+        const int total_new = p.s.head->total_new;
+        for (int64_t e0 = me * 32; e0 < total_new; e0 += warps * 32) {
+            int i = owner(p.s.page_begin, p.n_lists, (int32_t)e0);
+            const int e = (int)e0 + lane;
+            if (e >= total_new) continue;
+            while (i + 1 < p.n_lists && p.s.page_begin[i + 1] <= e) ++i;
             const int32_t len = p.s.old_len[i];
             const int first = p.s.shared[i] >= 0 ? len >> p.shift : (len + ps - 1) >> p.shift;
-            p.table[(int64_t)i * p.max_pages + first + ((int32_t)e - p.s.page_begin[i])] = p.s.fresh[e];
+            p.table[(int64_t)i * p.max_pages + first + (e - p.s.page_begin[i])] = p.s.fresh[e];
         }
+        __syncwarp();
     }
-    const int64_t warps = (int64_t)gridDim.x * (kMoveThreads / 32);
     const int64_t per = (rows + warps - 1) / warps;
-    const int64_t r0 = (me >> 5) * per, r1 = min(rows, r0 + per);
+    const int64_t r0 = me * per, r1 = min(rows, r0 + per);
     if (r0 >= r1) return;
     int i = owner(p.s.row_begin, p.n_lists, r0);
     uint32_t bad = 0;
     const int items = (int)(r1 - r0) * p.vec;
     for (int it = lane; it < items; it += 32) {
-        const int64_t r = r0 + it / p.vec;
-        const int u = it % p.vec;
+        const int dr = p.by_vec(it), u = it - dr * p.vec;
+        const int64_t r = r0 + dr;
         while (i + 1 < p.n_lists && p.s.row_begin[i + 1] <= r) ++i;
         const int64_t *begin = p.s.row_begin;
         int32_t at = (int32_t)(r - begin[i]);   // row within the list's moved rows
@@ -336,6 +382,8 @@ __global__ void __launch_bounds__(kMoveThreads) pages_move_kernel(MoveParams p) 
 __global__ void __launch_bounds__(kListThreads)
     pages_swap_kernel(PagesState s, int32_t *table, int32_t *len, const int32_t *counts,
                       int32_t n_pages, int32_t max_pages, int shift) {
+    let_next_start();
+    wait_for_inputs();
     if (!s.head->ok) return;
     const int i = blockIdx.x;
     const int32_t n = counts[i];
@@ -361,6 +409,8 @@ __global__ void __launch_bounds__(kListThreads)
     pages_truncate_kernel(PagesState s, const int32_t *table, int32_t *len, const int32_t *new_len,
                           int32_t n_pages, int32_t max_pages, int shift) {
     const int i = blockIdx.x;
+    let_next_start();
+    wait_for_inputs();
     const int32_t want = new_len[i], now = len[i];
     const int ps = 1 << shift;
     __syncthreads();   // everyone has read len[i]
@@ -387,6 +437,8 @@ __global__ void __launch_bounds__(kListThreads)
     pages_fork_kernel(PagesState s, int32_t *table, int32_t *len, const int32_t *src,
                       int32_t n_lists, int32_t n_pages, int32_t max_pages, int shift) {
     const int i = blockIdx.x;
+    let_next_start();
+    wait_for_inputs();
     const int32_t from = src[i];
     if (from < 0) return;
     const int ps = 1 << shift;
@@ -433,10 +485,10 @@ int launch_pages_append(const kvc_cache &c, const PagesState &s, int32_t *table,
                  shift, 0, true};
     pages_plan_kernel<<<1, kPlanThreads, 0, st>>>(p);
     const int vec = c.head_dim * (c.dtype == KVC_F32 ? 4 : 2) / 16;
-    MoveParams m{s, table, src_row, src_step, nullptr, n_lists, c.n_pages, c.max_pages, shift, 0, vec,
+    MoveParams m{s, table, src_row, src_step, nullptr, n_lists, c.n_pages, c.max_pages, shift, 0, vec, Divider(vec),
                  static_cast<const uint4 *>(k_src), static_cast<const uint4 *>(v_src),
                  static_cast<uint4 *>(k_pool), static_cast<uint4 *>(v_pool)};
-    pages_move_kernel<true><<<sms * 8, kMoveThreads, 0, st>>>(m);
+    launch_early(pages_move_kernel<true>, sms * 8, kMoveThreads, 0, st, m);
     return cache_launched("kvc_pages_append");
 }
 
@@ -448,11 +500,11 @@ int launch_pages_compact(const kvc_cache &c, const PagesState &s, int32_t *table
                  false};
     pages_plan_kernel<<<1, kPlanThreads, 0, st>>>(p);
     const int vec = c.head_dim * (c.dtype == KVC_F32 ? 4 : 2) / 16;
-    MoveParams m{s, table, nullptr, 0, idx, n_lists, c.n_pages, c.max_pages, shift, k_max, vec,
+    MoveParams m{s, table, nullptr, 0, idx, n_lists, c.n_pages, c.max_pages, shift, k_max, vec, Divider(vec),
                  nullptr, nullptr, static_cast<uint4 *>(k_pool), static_cast<uint4 *>(v_pool)};
-    pages_move_kernel<false><<<sms * 8, kMoveThreads, 0, st>>>(m);
-    pages_swap_kernel<<<n_lists, kListThreads, 0, st>>>(s, table, len, counts, c.n_pages, c.max_pages,
-                                                        shift);
+    launch_early(pages_move_kernel<false>, sms * 8, kMoveThreads, 0, st, m);
+    launch_early(pages_swap_kernel, n_lists, kListThreads, 0, st, s, table, len, counts, c.n_pages,
+                 c.max_pages, shift);
     return cache_launched("kvc_pages_compact");
 }
 

@@ -90,6 +90,8 @@ __device__ __forceinline__ void turn(T &a, T &b, float2 cs) {
 template <typename T, int N, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeParams p) {
     __shared__ float2 cs[kRopePairs];
+    let_next_start();
+    wait_for_inputs();
     const int pairs = p.rot / 2;
     const int64_t t0 = (int64_t)blockIdx.x * p.per_block;
     const int nt = (int)min((int64_t)p.per_block, p.n_tokens - t0);
@@ -149,7 +151,8 @@ void launch(RopeParams &p, bool in_place, int sms, cudaStream_t st) {
     const int64_t want = (p.n_tokens + 4 * sms - 1) / (4 * sms);
     p.per_block = (int)std::min<int64_t>({std::max<int64_t>(1, want), kRopePairs / (p.rot / 2), 8});
     const dim3 block(p.units, std::max(1, kRopeThreads / p.units));
-    rope_kernel<T, N, INTER><<<(unsigned)((p.n_tokens + p.per_block - 1) / p.per_block), block, 0, st>>>(p);
+    launch_early(rope_kernel<T, N, INTER>, (unsigned)((p.n_tokens + p.per_block - 1) / p.per_block), block, 0,
+                 st, p);
 }
 
 template <typename T>

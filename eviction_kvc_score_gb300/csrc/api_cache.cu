@@ -83,7 +83,7 @@ AttendWs attend_ws(const kvc_cache &c, int group) {
     w.needs = w.tc ? attend_tc_needs(device_sms()) : attend_simt_needs(device_sms());
     const size_t rows = (size_t)w.needs.grid * w.needs.slots * w.needs.slot_rows;
     w.arrived = kWsHeader;
-    w.stat = w.arrived + cache_align((size_t)w.needs.grid * 2 * sizeof(uint32_t));
+    w.stat = w.arrived + cache_align((size_t)w.needs.grid * 8 * sizeof(uint32_t));
     w.part = w.stat + cache_align(rows * sizeof(float2));
     w.total = w.part + cache_align(rows * c.head_dim * sizeof(float));
     return w;

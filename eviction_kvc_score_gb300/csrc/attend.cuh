@@ -39,7 +39,7 @@ struct AttendParams {
     float *lse;
     float scale_log2;    // scale * log2(e)
     uint32_t *status;
-    uint32_t *arrived;   // [grid][2], zero between calls
+    uint32_t *arrived;   // [grid][8], zero between calls
     float2 *stat;        // [grid][slots][slot_rows] (max in log2 units, sum)
     float *part;         // [grid][slots][slot_rows][dim]
 };
@@ -117,14 +117,19 @@ struct AttendRun {
     int64_t total, lo, hi;   // steps in all; this CTA's
     int grid;                // CTAs with work
     int unit;                // first unit ...
-    int64_t unit_lo;         // ... and its first step
+    int64_t unit_lo;         // ... its first step
+    AttendRaw raw;           // ... and what it is made of
 };
 
-__device__ __forceinline__ int64_t attend_cut(int64_t total, int grid, int64_t c) {
+// (Where the products fit 32 bits the divisions are of 32 bits: a third of the
+// instructions.)
+__device__ __forceinline__ int64_t attend_cut(int64_t total, int grid, int c) {
+    if (total * grid <= UINT_MAX) return (uint32_t)total * (uint32_t)c / (uint32_t)grid;
     return total * c / grid;
 }
 // The CTA whose run holds step x.
 __device__ __forceinline__ int attend_cta_of(int64_t total, int grid, int64_t x) {
+    if (total * grid <= UINT_MAX) return (int)(((uint32_t)(x + 1) * (uint32_t)grid - 1) / (uint32_t)total);
     return (int)(((x + 1) * grid - 1) / total);
 }
 
@@ -160,10 +165,13 @@ __device__ AttendRun attend_plan(const AttendParams &p, int64_t *scratch) {
     int64_t at = before + x - mine;
     if (works && r.lo >= at && r.lo < at + mine) {
         for (int u = u0; u < u1; ++u) {
-            const int s = attend_unit(p, u).steps;
+            const AttendRaw raw = attend_raw(p, u);
+            const int s = attend_unit(p, u, raw).steps;
             if (r.lo < at + s) {
                 found[0] = u;
                 found[1] = at;
+                found[2] = (int64_t)((uint64_t)(uint32_t)raw.q0 << 32 | (uint32_t)raw.q1);
+                found[3] = raw.len;
                 break;
             }
             at += s;
@@ -172,6 +180,7 @@ __device__ AttendRun attend_plan(const AttendParams &p, int64_t *scratch) {
     __syncthreads();
     r.unit = works ? (int)found[0] : 0;
     r.unit_lo = works ? found[1] : 0;
+    r.raw = works ? AttendRaw{(int)(found[2] >> 32), (int)(uint32_t)found[2], (int)found[3]} : AttendRaw{0, 0, 0};
     return r;
 }
 
@@ -184,6 +193,19 @@ __device__ __forceinline__ int attend_next(const AttendParams &p, const AttendUn
 __device__ __forceinline__ void attend_store_lse(const AttendParams &p, int64_t row, float m, float l,
                                                  bool sees) {
     if (p.lse) p.lse[row] = sees ? (m + log2f(l)) * 0.693147180559945309f : -INFINITY;
+}
+
+// A warp's rows of a slot are written: count it.  True, in the whole warp, if it
+// is the last of `all`; then every other's rows are visible to it.  The counter
+// is back at zero after that.
+__device__ __forceinline__ bool attend_last(uint32_t *count, uint32_t all) {
+    __syncwarp();
+    uint32_t before = 0;
+    if ((threadIdx.x & 31) == 0) {
+        asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(count) : "memory");
+        if (before == all - 1) *count = 0;
+    }
+    return __shfl_sync(0xffffffffu, before, 0) == all - 1;
 }
 
 // Slots of a CTA: its first unit's (begun by an earlier CTA), its last unit's.

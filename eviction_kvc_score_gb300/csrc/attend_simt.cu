@@ -321,8 +321,8 @@ __global__ void __launch_bounds__(threads_of(ROWS), ROWS == 64 ? 2 : 4) attend_s
             __threadfence();
             __syncthreads();
             if (tid == 0) {
-                const bool last = atomicAdd(&p.arrived[2 * c0], 1u) == (uint32_t)(c1 - c0);
-                if (last) p.arrived[2 * c0] = 0;
+                const bool last = atomicAdd(&p.arrived[8 * c0], 1u) == (uint32_t)(c1 - c0);
+                if (last) p.arrived[8 * c0] = 0;
                 *s_last = last;
             }
             __syncthreads();

@@ -67,7 +67,7 @@ struct Bars {
     uint32_t tmem;
     volatile int abort_flag;
     int dirty;            // some value taken out of V
-    int last[2];
+    int last[2][2];
     float2 other[kTile];  // half 1's (max, sum) of a split unit
     int64_t plan[kThreads / 32 + 4];
 };
@@ -198,8 +198,8 @@ struct Walk {
     AttendUnit a;
     Segment g;
     AttendRaw raw;   // of unit u, asked for while the unit before is worked on
-    __device__ Walk(const AttendParams &p, const AttendRun &r)
-        : run(r), pos(r.lo), u_lo(r.unit_lo), u(r.unit), raw(attend_raw(p, r.unit)) {}
+    __device__ explicit Walk(const AttendRun &r)
+        : run(r), pos(r.lo), u_lo(r.unit_lo), u(r.unit), raw(r.raw) {}
     __device__ bool next(const AttendParams &p) {
         while (pos < run.hi) {
             a = attend_unit(p, u, raw);
@@ -222,15 +222,15 @@ struct Walk {
     int64_t lo;   // the unit's first step
 };
 
-// Adds up the slots of CTAs c0..c1 for rows first.. of the unit and writes them
-// out; 128 threads, `me` their index.  Four chunks of four columns times four
+// Adds up the slots of CTAs c0..c1 for `rows` rows, first.. of the unit, and
+// writes them out; `me` of `threads` threads.  Four chunks of four columns times four
 // slots are asked for at a time: with one load after the other the joining of
 // 19 CTAs' slots took longer than their products.
 template <int D>
 __device__ __noinline__ void join_slots(const AttendParams &p, const AttendUnit &a, int first, int rows,
-                                        int slot_row, int c0, int c1, int me) {
+                                        int slot_row, int c0, int c1, int me, int threads) {
     constexpr int U = 4, S = 4, kVec = D / 4;
-    for (int x0 = me; x0 < rows * kVec; x0 += kTile * U) {
+    for (int x0 = me; x0 < rows * kVec; x0 += threads * U) {
         float top[U], sum[U];
         float4 acc[U];
 #pragma unroll
@@ -246,7 +246,7 @@ __device__ __noinline__ void join_slots(const AttendParams &p, const AttendUnit 
             for (int u = 0; u < U; ++u)
 #pragma unroll
                 for (int k = 0; k < S; ++k) {
-                    const int x = x0 + u * kTile, row = x / kVec, d = (x - row * kVec) * 4;
+                    const int x = x0 + u * threads, row = x / kVec, d = (x - row * kVec) * 4;
                     st[u][k] = make_float2(-INFINITY, 0.f);
                     y[u][k] = make_float4(0, 0, 0, 0);
                     if (row < rows && c + k <= c1) {
@@ -277,7 +277,7 @@ __device__ __noinline__ void join_slots(const AttendParams &p, const AttendUnit 
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int x = x0 + u * kTile, row = x / kVec, d = (x - row * kVec) * 4;
+            const int x = x0 + u * threads, row = x / kVec, d = (x - row * kVec) * 4;
             if (row >= rows) continue;
             const bool see = attend_sees(p, a, first + row) > 0;
             const float inv = 1.f / sum[u];
@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&b.p_full[t][0], 4);
             mbar_init(&b.p_full[t][1], 4);
             mbar_init(&b.o_full[t], 1);
-            mbar_init(&b.wg[t], 4);
+            mbar_init(&b.wg[t], 1);
             mbar_init(&b.drain[t], 1);
             mbar_init(&b.issued[t], 1);
         }
@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t base_fill = 0, segs = 0, done = 0;   // loads before this segment, segments, loads of this side
         bool ok = true;
         const int tile_shift = 7 - p.shift, per_tile = 1 << tile_shift, ps = 1 << p.shift;
-        Walk w(p, run);
+        Walk w(run);
         while (ok && w.next(p)) {
             const Segment &g = w.g;
             if (g.n == 0) continue;
@@ -474,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++turns;
             };
             bool ok = true;
-            Walk w(p, run);
+            Walk w(run);
             while (ok && w.next(p)) {
                 const Segment &g = w.g;
                 if (g.n == 0) continue;
@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t ns = 0, no = 0, nwg = 0, handed = 0, filled = 0;
         bool owed = false;   // half 1: O is still being read by half 0
         bool ok = true;
-        Walk w(p, run);
+        Walk w(run);
         while (ok && w.next(p)) {
             const AttendUnit &a = w.a;
             const Segment &g = w.g;
@@ -796,24 +796,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // the CTA that finishes last joins the unit's slots
                 const int c0 = attend_cta_of(run.total, run.grid, w.lo);
                 const int c1 = attend_cta_of(run.total, run.grid, w.lo + a.steps - 1);
-                __threadfence();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&b.wg[t]);
-                if (!(ok = warp_wait(&b.wg[t], nwg++ & 1, stop, p.status))) break;
-                if (quarter == 0 && lane == 0) {
-                    uint32_t *count = &p.arrived[2 * c0 + t];
-                    const bool last = atomicAdd(count, 1u) == (uint32_t)(c1 - c0);
-                    if (last) *count = 0;
-                    __threadfence();
-                    b.last[t] = last;
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&b.wg[t]);
-                if (!(ok = warp_wait(&b.wg[t], nwg++ & 1, stop, p.status))) break;
-                if (*static_cast<volatile int *>(&b.last[t])) {
-                    __threadfence();
-                    const int first_row = t * R;
-                    join_slots<D>(p, a, first_row, min(a.rows - first_row, R), t * kTile, c0, c1, r);
+                const uint32_t all = (uint32_t)(c1 - c0 + 1);
+                const int rows = min(a.rows - t * R, R);   // of the tile
+                uint32_t *count = &p.arrived[8 * c0 + 4 * t];
+                if (rows > 32) {   // each warp its own 32 rows
+                    if (any && attend_last(count + quarter, all))
+                        join_slots<D>(p, a, t * R + 32 * quarter, min(32, rows - 32 * quarter),
+                                      t * kTile + 32 * quarter, c0, c1, lane, 32);
+                } else {           // one warp's rows: often of many slots, so all four join
+                    volatile int *last = &b.last[t][nwg & 1];
+                    if (quarter == 0) {
+                        const bool is = attend_last(count, all);
+                        if (lane == 0) {
+                            *last = is;
+                            mbar_arrive(&b.wg[t]);
+                        }
+                    }
+                    if (!(ok = warp_wait(&b.wg[t], nwg++ & 1, stop, p.status))) break;
+                    if (*last) join_slots<D>(p, a, t * R, rows, t * kTile, c0, c1, r, kTile);
                 }
             }
         }

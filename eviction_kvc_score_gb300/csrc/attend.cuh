@@ -5,9 +5,9 @@
 // token r / G, query head r % G of the group, so every key tile is read once
 // for all of them.  A unit is (list, block of unit_rows rows); its cost is
 // its number of steps over the keys its last row sees (one at least, so that
-// somebody writes the zeros of a row that sees none).  The flat sequence of all
-// units' steps is cut into equal runs, one per CTA: lists of any lengths keep
-// every SM busy to the end, and a CTA shares at most its first and its last
+// somebody writes the zeros of a row that sees none) and `extra` for what a unit
+// costs beside them.  The flat sequence of all units' costs is cut into equal
+// runs, one per CTA: lists of any lengths keep every SM busy to the end, and a CTA shares at most its first and its last
 // unit with others.  For those it leaves rows' (max, sum, unnormalised output)
 // in a slot of its own; the CTA that finishes last adds the unit's slots up in
 // CTA order, so the result does not depend on the order of finishing.
@@ -30,6 +30,7 @@ struct AttendParams {
     int n_units;
     int step_keys;       // keys per step ...
     int split_rows;      // ... twice as many for units of at most so many rows
+    int extra;           // steps' worth of a unit's beginning and end
     int slots;           // slots per CTA
     int slot_rows;       // row capacity of a slot
     int64_t q_stride;
@@ -51,6 +52,7 @@ struct AttendUnit {
     int len;          // the list's cached rows
     int hi;           // cached rows that the unit's last row sees
     int steps;        // 0: no such unit
+    int cost;         // steps + extra, or 0
 };
 
 // What a unit is made of in memory, to be asked for before it is needed.
@@ -85,6 +87,7 @@ __device__ __forceinline__ AttendUnit attend_unit(const AttendParams &p, int u, 
     a.hi = a.rows <= 0 ? 0 : max(0, a.len - a.n + p.by_group(a.row0 + a.rows - 1) + 1);
     const int keys = a.rows <= p.split_rows ? 2 * p.step_keys : p.step_keys;
     a.steps = a.rows <= 0 ? 0 : max(1, (a.hi + keys - 1) / keys);
+    a.cost = a.steps ? a.steps + p.extra : 0;
     return a;
 }
 
@@ -112,12 +115,12 @@ __device__ __forceinline__ int attend_page(const AttendParams &p, int list, int 
     return page;
 }
 
-// The CTA's run of steps and the unit it begins in.
+// The CTA's run and the unit it begins in.
 struct AttendRun {
-    int64_t total, lo, hi;   // steps in all; this CTA's
+    int64_t total, lo, hi;   // cost of all; this CTA's part
     int grid;                // CTAs with work
     int unit;                // first unit ...
-    int64_t unit_lo;         // ... its first step
+    int64_t unit_lo;         // ... where that begins
     AttendRaw raw;           // ... and what it is made of
 };
 
@@ -127,7 +130,7 @@ __device__ __forceinline__ int64_t attend_cut(int64_t total, int grid, int c) {
     if (total * grid <= UINT_MAX) return (uint32_t)total * (uint32_t)c / (uint32_t)grid;
     return total * c / grid;
 }
-// The CTA whose run holds step x.
+// The CTA whose run holds x.
 __device__ __forceinline__ int attend_cta_of(int64_t total, int grid, int64_t x) {
     if (total * grid <= UINT_MAX) return (int)(((uint32_t)(x + 1) * (uint32_t)grid - 1) / (uint32_t)total);
     return (int)(((x + 1) * grid - 1) / total);
@@ -140,7 +143,7 @@ __device__ AttendRun attend_plan(const AttendParams &p, int64_t *scratch) {
     const int per = p.n_units / NT + 1;
     const int u0 = (int)min((int64_t)p.n_units, (int64_t)per * threadIdx.x), u1 = min(p.n_units - u0, per) + u0;
     int64_t mine = 0;
-    for (int u = u0; u < u1; ++u) mine += attend_unit(p, u).steps;
+    for (int u = u0; u < u1; ++u) mine += attend_unit(p, u).cost;
     int64_t x = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -166,7 +169,7 @@ __device__ AttendRun attend_plan(const AttendParams &p, int64_t *scratch) {
     if (works && r.lo >= at && r.lo < at + mine) {
         for (int u = u0; u < u1; ++u) {
             const AttendRaw raw = attend_raw(p, u);
-            const int s = attend_unit(p, u, raw).steps;
+            const int s = attend_unit(p, u, raw).cost;
             if (r.lo < at + s) {
                 found[0] = u;
                 found[1] = at;

@@ -405,6 +405,7 @@ int launch_attend_simt(AttendParams &p, bool f32, int grid, cudaStream_t st) {
     }
     p.step_keys = kKeys;
     p.split_rows = 0;
+    p.extra = 0;
     const int sms = grid / kBlocksPerSm;
     return f32 ? launch_type<float>(p, rows, sms, st) : launch_type<__nv_bfloat16>(p, rows, sms, st);
 }

@@ -54,6 +54,23 @@ constexpr int kBox = kTile * 128;       // bytes of 128 rows x 64 bf16
 constexpr uint32_t kColS = 0, kColO = 256;
 constexpr float kGrow = 8.f;            // log2 units m may lag behind
 constexpr int kSlotsTc = 2;
+constexpr int kExtra = 4;
+constexpr int kQueue = 4;               // segments on their way from the walk to the roles
+constexpr int kReaders = 12;            // arrivals that free an entry: every warp's
+
+// What a CTA does of one unit: key tiles [first, first + n) of the list; half t
+// takes cnt[t] of them, every one (paired) or every other (split).
+struct Segment {
+    bool split, whole, begins;   // begins: the unit's first step is in it
+    int first, n, cnt[2];
+    int c0, c1;              // the CTAs that share the unit
+};
+
+struct Work {
+    AttendUnit a;
+    Segment g;
+    bool none;   // the run has ended
+};
 
 // Ring stages: what shared memory holds beside Q.
 constexpr int stages_of(int kh) { return kh == 2 ? 5 : 12; }
@@ -68,6 +85,8 @@ struct Bars {
     volatile int abort_flag;
     int dirty;            // some value taken out of V
     int last[2][2];
+    uint64_t work_full[kQueue], work_empty[kQueue];
+    Work work[kQueue];
     float2 other[kTile];  // half 1's (max, sum) of a split unit
     int64_t plan[kThreads / 32 + 4];
 };
@@ -135,13 +154,6 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, stop, status));
 }
 
-// What a CTA does of one unit: key tiles [first, first + n) of the list; half t
-// takes cnt[t] of them, every one (paired) or every other (split).
-struct Segment {
-    bool split, whole, begins;   // begins: the unit's first step is in it
-    int first, n, cnt[2];
-};
-
 __device__ __forceinline__ Segment segment_of(const AttendParams &p, const AttendUnit &a, int s0, int s1) {
     Segment g;
     g.split = a.rows <= p.split_rows;
@@ -196,31 +208,29 @@ struct Walk {
     AttendRun run;
     int64_t pos, u_lo;
     int u;
-    AttendUnit a;
-    Segment g;
     AttendRaw raw;   // of unit u, asked for while the unit before is worked on
     __device__ explicit Walk(const AttendRun &r)
         : run(r), pos(r.lo), u_lo(r.unit_lo), u(r.unit), raw(r.raw) {}
-    __device__ bool next(const AttendParams &p) {
-        while (pos < run.hi) {
-            a = attend_unit(p, u, raw);
-            if (a.steps == 0) {
-                u = attend_next(p, a, u);
-                raw = attend_raw(p, u);
-                continue;
+    __device__ void next(const AttendParams &p, Work &w) {
+        w.none = true;
+        while (w.none && pos < run.hi) {
+            w.a = attend_unit(p, u, raw);
+            if (w.a.steps > 0) {
+                const int64_t end = min(run.hi, u_lo + w.a.cost);
+                const int s0 = max(0, (int)(pos - u_lo) - p.extra), s1 = max(0, (int)(end - u_lo) - p.extra);
+                if (s1 > s0) {
+                    w.g = segment_of(p, w.a, s0, s1);
+                    w.g.c0 = attend_cta_of(run.total, run.grid, u_lo + p.extra);
+                    w.g.c1 = attend_cta_of(run.total, run.grid, u_lo + w.a.cost - 1);
+                    w.none = false;
+                }
+                pos = end;
+                u_lo += w.a.cost;
             }
-            const int64_t end = min(run.hi, u_lo + a.steps);
-            g = segment_of(p, a, (int)(pos - u_lo), (int)(end - u_lo));
-            lo = u_lo;
-            pos = end;
-            u_lo += a.steps;
-            u = attend_next(p, a, u);
+            u = attend_next(p, w.a, u);
             raw = attend_raw(p, u);
-            return true;
         }
-        return false;
     }
-    int64_t lo;   // the unit's first step
 };
 
 // Adds up the slots of CTAs c0..c1 for `rows` rows, first.. of the unit, and
@@ -324,6 +334,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&b.drain[t], 1);
             mbar_init(&b.issued[t], 1);
         }
+        for (int i = 0; i < kQueue; ++i) {
+            mbar_init(&b.work_full[i], 1);
+            mbar_init(&b.work_empty[i], kReaders);
+        }
         mbar_init(&b.half_full, 4);
         mbar_init(&b.half_empty, 4);
         b.abort_flag = 0;
@@ -343,6 +357,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = b.tmem;
     volatile int *stop = &b.abort_flag;
+    // Segment k of the run for a warp that reads the queue.  One warp walks the
+    // units: the others would each pay for its loads, some 3 us between units
+    // when memory is busy.
+    auto read_work = [&](uint32_t k, Work &w) {
+        const uint32_t e = k % kQueue;
+        if (!warp_wait(&b.work_full[e], (k / kQueue) & 1, stop, p.status)) return false;
+        w = b.work[e];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&b.work_empty[e]);
+        return !w.none;
+    };
 
     if (warp >= kLoadWarp) {
     regs_dec<kRegsOther>();
@@ -357,10 +382,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t base_fill = 0, segs = 0, done = 0;   // loads before this segment, segments, loads of this side
         bool ok = true;
         const int tile_shift = 7 - p.shift, per_tile = 1 << tile_shift, ps = 1 << p.shift;
-        Walk w(run);
-        while (ok && w.next(p)) {
+        Walk walk(run);
+        uint32_t put = 0;   // segments in the queue so far
+        auto put_work = [&]() {
+            const uint32_t e = put % kQueue;
+            Work w;
+            walk.next(p, w);
+            if (put >= kQueue && !warp_wait(&b.work_empty[e], (put / kQueue - 1) & 1, stop, p.status)) return false;
+            if (lane == 0) {
+                b.work[e] = w;
+                mbar_arrive(&b.work_full[e]);
+            }
+            ++put;
+            return true;
+        };
+        if (side == 0) ok = put_work();
+        Work w;
+        for (uint32_t k = 0; ok; ++k) {
+            if (!read_work(k, w)) break;
             const Segment &g = w.g;
-            if (g.n == 0) continue;
+            bool ahead = side != 0;   // the next segment is in the queue
+            if (g.n == 0) {
+                if (!ahead) ok = put_work();
+                continue;
+            }
             if (side == 0) {   // Q once the segment before has used it
                 ok = segs == 0 || warp_wait(&b.q_empty, (segs - 1) & 1, stop, p.status);
                 if (!ok) break;
@@ -383,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int j = page0 + batch * 32 + lane;
                 return j < page1 ? p.table[(int64_t)w.a.list * p.max_pages + j] : 0;
             };
-            int batch = 0, before = 0, now = look_up(0), ahead = look_up(1);
+            int batch = 0, before = 0, now = look_up(0), then = look_up(1);
             // a segment makes an even number of loads: the sides keep their parity
             for (int l = (int)side; l < 2 * g.n; l += 2) {
                 bool is_v;
@@ -393,8 +438,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (at >> 5 > batch) {
                     ++batch;
                     before = now;
-                    now = ahead;
-                    ahead = look_up(batch + 1);
+                    now = then;
+                    then = look_up(batch + 1);
                 }
                 int page = __shfl_sync(0xffffffffu, at >> 5 < batch ? before : now, (at + lane) & 31);
                 // those that hold visible rows
@@ -415,6 +460,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tma_load_3d(is_v ? &tv : &tk, &b.full[st], dst + kh * kBox, kh * 64, 0, page);
                 }
                 ++done;
+                // the ring is full or the segment done: time for the next one
+                if (!ahead && (l + 2 >= kStages || l + 2 >= 2 * g.n)) {
+                    ahead = true;
+                    if (!(ok = put_work())) break;
+                }
             }
             base_fill += 2 * g.n;
         }
@@ -475,8 +525,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++turns;
             };
             bool ok = true;
-            Walk w(run);
-            while (ok && w.next(p)) {
+            Work w;
+            for (uint32_t k = 0; ok; ++k) {
+                if (!(ok = mbar_wait(&b.work_full[k % kQueue], (k / kQueue) & 1, stop, p.status))) break;
+                w = b.work[k % kQueue];
+                mbar_arrive(&b.work_empty[k % kQueue]);
+                if (w.none) break;
                 const Segment &g = w.g;
                 if (g.n == 0) continue;
                 if (!(ok = mbar_wait(&b.q_full, segs & 1, stop, p.status))) break;
@@ -541,8 +595,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t ns = 0, no = 0, nwg = 0, handed = 0, filled = 0;
         bool owed = false;   // half 1: O is still being read by half 0
         bool ok = true;
-        Walk w(run);
-        while (ok && w.next(p)) {
+        Work w;
+        for (uint32_t k = 0; ok; ++k) {
+            if (!read_work(k, w)) break;
             const AttendUnit &a = w.a;
             const Segment &g = w.g;
             const int rt = g.split ? r : t * R + r;
@@ -807,8 +862,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (take && lane == 0) mbar_arrive(&b.half_empty);
             if (!g.whole) {
                 // the CTA that finishes last joins the unit's slots
-                const int c0 = attend_cta_of(run.total, run.grid, w.lo);
-                const int c1 = attend_cta_of(run.total, run.grid, w.lo + a.steps - 1);
+                const int c0 = g.c0, c1 = g.c1;
                 const uint32_t all = (uint32_t)(c1 - c0 + 1);
                 const int rows = min(a.rows - t * R, R);   // of the tile
                 uint32_t *count = &p.arrived[8 * c0 + 4 * t];
@@ -882,6 +936,7 @@ int launch_attend_tc(AttendParams &p, int grid, cudaStream_t st) {
     const int R = kTile / p.group * p.group;   // whole tokens
     p.split_rows = R;
     p.step_keys = kTile;
+    p.extra = kExtra;
     if (!attend_units(p, 2 * R)) {
         set_error("kvc_attend: n_seqs * n_kv_heads * max_new is too large");
         return KVC_ERR_UNSUPPORTED;

@@ -105,13 +105,18 @@ __global__ void pages_init_kernel(PagesState s, int32_t n_pages) {
     }
 }
 
+// What the plan knows of a list.
+struct ListPlan {
+    int32_t n, len, shared;   // rows to move, length, last page to copy from (or -1)
+};
+
 // Pages and rows of list i, and what stands against the call.
-__device__ Two list_needs(const PlanParams &p, int i, uint32_t *bad) {
+__device__ Two list_needs(const PlanParams &p, int i, uint32_t *bad, ListPlan *list) {
     const int32_t n = p.counts[i], len = p.len[i], ps = 1 << p.shift;
+    const int64_t row = p.append ? p.src_row[i] : 0;
     const int64_t most = (int64_t)p.max_pages << p.shift;
     Two need{0, 0};
-    p.s.shared[i] = -1;
-    p.s.old_len[i] = len;
+    *list = ListPlan{n, len, -1};
     if (p.append ? n <= 0 : n < 0) return need;
     if (len < 0 || len > most) {
         *bad |= KVC_DEV_BAD_LIST;
@@ -124,7 +129,7 @@ __device__ Two list_needs(const PlanParams &p, int i, uint32_t *bad) {
         need.pages = (n + ps - 1) >> p.shift;
         return need;
     }
-    const int64_t now = (int64_t)len + n, row = p.src_row[i];
+    const int64_t now = (int64_t)len + n;
     if (now > most) {
         *bad |= KVC_DEV_PAGES_FULL;
         return need;
@@ -141,7 +146,7 @@ __device__ Two list_needs(const PlanParams &p, int i, uint32_t *bad) {
         if (last < 0 || last >= p.n_pages) {
             *bad |= KVC_DEV_BAD_PAGE;
         } else if (p.s.holders[last] > 1) {
-            p.s.shared[i] = last;
+            list->shared = last;
             need.pages += 1;
             need.rows += len & (ps - 1);
         }
@@ -174,16 +179,24 @@ __global__ void __launch_bounds__(kPlanThreads) pages_plan_kernel(PlanParams p) 
     if (tid == 0) s_bad = s_shared = 0;
     let_next_start();
     wait_for_inputs();
+    // asked for now, needed after the lists are counted: the free counts and
+    // the first group's words (a plan is a chain of memory latencies)
+    const int32_t n_free = head->n_free;
+    int32_t groups = tid < p.s.n_groups ? p.s.group_free[tid] : 0;
+    const uint32_t bits0 = tid < p.s.n_words ? p.s.bitmap[tid] : 0;
     __syncthreads();
     uint32_t bad = 0;
     Two sum{0, 0};
     bool shares = false;
+    ListPlan list{0, 0, -1};
     for (int base = 0; base < p.n_lists; base += kPlanThreads) {
         const int i = base + tid;
         Two need{0, 0}, all;
         if (i < p.n_lists) {
-            need = list_needs(p, i, &bad);
-            shares |= p.s.shared[i] >= 0;
+            need = list_needs(p, i, &bad, &list);
+            shares |= list.shared >= 0;
+            p.s.shared[i] = list.shared;
+            p.s.old_len[i] = list.len;
         }
         const Two at = block_scan(need, scratch, &all);
         if (i < p.n_lists) {
@@ -199,11 +212,10 @@ __global__ void __launch_bounds__(kPlanThreads) pages_plan_kernel(PlanParams p) 
     if (bad) atomicOr(&s_bad, bad);
     if (shares) s_shared = 1;
     __syncthreads();
-    if (tid == 0 && s_bad == 0 && sum.pages > head->n_free) s_bad = KVC_DEV_PAGES_FULL;
-    __syncthreads();
-    const bool ok = s_bad == 0;
+    const uint32_t against = s_bad ? s_bad : sum.pages > n_free ? KVC_DEV_PAGES_FULL : 0;
+    const bool ok = against == 0;
     if (tid == 0) {
-        if (!ok) set_status(&head->status, s_bad);
+        if (!ok) set_status(&head->status, against);
         head->ok = ok;
         head->total_new = (int32_t)sum.pages;
         head->total_rows = sum.rows;
@@ -220,12 +232,13 @@ __global__ void __launch_bounds__(kPlanThreads) pages_plan_kernel(PlanParams p) 
     int found = 0;
     for (int g0 = 0; g0 < p.s.n_groups && found < need; g0 += kPlanThreads) {
         __syncthreads();
-        s_groups[tid] = g0 + tid < p.s.n_groups ? p.s.group_free[g0 + tid] : 0;
+        if (g0 > 0) groups = g0 + tid < p.s.n_groups ? p.s.group_free[g0 + tid] : 0;
+        s_groups[tid] = groups;
         __syncthreads();
         for (int j = 0; j < kPlanThreads && found < need; ++j) {
             if (s_groups[j] == 0) continue;
             const int word0 = (g0 + j) * kGroupWords, word = word0 + tid;
-            uint32_t bits = word < p.s.n_words ? p.s.bitmap[word] : 0;
+            const uint32_t bits = g0 + j == 0 ? bits0 : word < p.s.n_words ? p.s.bitmap[word] : 0;
             Two all;
             const int rank = (int)block_scan(Two{0, __popc(bits)}, scratch, &all).pages;
             const int took = min((int)all.pages, need - found);
@@ -246,8 +259,8 @@ __global__ void __launch_bounds__(kPlanThreads) pages_plan_kernel(PlanParams p) 
                 p.s.bitmap[word] = mine == __popc(bits) ? 0 : bits & ~((2u << nth_bit(bits, mine - 1)) - 1u);
             }
             if (tid == 0) {
-                p.s.group_free[g0 + j] -= took;
-                head->n_free -= took;
+                p.s.group_free[g0 + j] = s_groups[j] - took;
+                head->n_free = n_free - found - took;
             }
             found += took;
             __syncthreads();
@@ -262,9 +275,9 @@ __global__ void __launch_bounds__(kPlanThreads) pages_plan_kernel(PlanParams p) 
         const int i = base + tid;
         int32_t page = -1;
         if (i < p.n_lists) {
-            const int32_t n = p.counts[i];
-            page = p.s.shared[i];
-            if (n > 0) p.len[i] = p.s.old_len[i] + n;
+            if (p.n_lists > kPlanThreads) list = ListPlan{p.counts[i], p.s.old_len[i], p.s.shared[i]};
+            page = list.shared;
+            if (list.n > 0) p.len[i] = list.len + list.n;
         }
         if (drop) let_go(p.s, page, p.n_pages);
     }
@@ -483,7 +496,7 @@ int launch_pages_append(const kvc_cache &c, const PagesState &s, int32_t *table,
     const int shift = log2_of(c.page_rows);
     PlanParams p{s, table, len, counts, src_row, src_step, src_rows, n_lists, c.n_pages, c.max_pages,
                  shift, 0, true};
-    pages_plan_kernel<<<1, kPlanThreads, 0, st>>>(p);
+    launch_early(pages_plan_kernel, 1, kPlanThreads, 0, st, p);
     const int vec = c.head_dim * (c.dtype == KVC_F32 ? 4 : 2) / 16;
     MoveParams m{s, table, src_row, src_step, nullptr, n_lists, c.n_pages, c.max_pages, shift, 0, vec, Divider(vec),
                  static_cast<const uint4 *>(k_src), static_cast<const uint4 *>(v_src),
@@ -498,7 +511,7 @@ int launch_pages_compact(const kvc_cache &c, const PagesState &s, int32_t *table
     const int shift = log2_of(c.page_rows);
     PlanParams p{s, table, len, counts, nullptr, 0, 0, n_lists, c.n_pages, c.max_pages, shift, k_max,
                  false};
-    pages_plan_kernel<<<1, kPlanThreads, 0, st>>>(p);
+    launch_early(pages_plan_kernel, 1, kPlanThreads, 0, st, p);
     const int vec = c.head_dim * (c.dtype == KVC_F32 ? 4 : 2) / 16;
     MoveParams m{s, table, nullptr, 0, idx, n_lists, c.n_pages, c.max_pages, shift, k_max, vec, Divider(vec),
                  nullptr, nullptr, static_cast<uint4 *>(k_pool), static_cast<uint4 *>(v_pool)};
@@ -510,15 +523,15 @@ int launch_pages_compact(const kvc_cache &c, const PagesState &s, int32_t *table
 
 int launch_pages_fork(const kvc_cache &c, const PagesState &s, int32_t *table, int32_t *len,
                       int32_t n_lists, const int32_t *src, cudaStream_t st) {
-    pages_fork_kernel<<<n_lists, kListThreads, 0, st>>>(s, table, len, src, n_lists, c.n_pages,
-                                                        c.max_pages, log2_of(c.page_rows));
+    launch_early(pages_fork_kernel, n_lists, kListThreads, 0, st, s, table, len, src, n_lists, c.n_pages,
+                 c.max_pages, log2_of(c.page_rows));
     return cache_launched("kvc_pages_fork");
 }
 
 int launch_pages_truncate(const kvc_cache &c, const PagesState &s, int32_t *table, int32_t *len,
                           int32_t n_lists, const int32_t *new_len, cudaStream_t st) {
-    pages_truncate_kernel<<<n_lists, kListThreads, 0, st>>>(s, table, len, new_len, c.n_pages,
-                                                            c.max_pages, log2_of(c.page_rows));
+    launch_early(pages_truncate_kernel, n_lists, kListThreads, 0, st, s, table, len, new_len, c.n_pages,
+                 c.max_pages, log2_of(c.page_rows));
     return cache_launched("kvc_pages_truncate");
 }
 

@@ -87,6 +87,18 @@ __device__ __forceinline__ void store4(__nv_bfloat16 *p, float4 x) {
     *reinterpret_cast<uint2 *>(p) = make_uint2(a, b);
 }
 
+// Whether the 16 bytes at p hold numbers only.
+__device__ __forceinline__ bool all_finite(const float *p) {
+    const float4 x = *reinterpret_cast<const float4 *>(p);
+    return isfinite(x.x) && isfinite(x.y) && isfinite(x.z) && isfinite(x.w);
+}
+__device__ __forceinline__ bool all_finite(const __nv_bfloat16 *p) {
+    const uint4 x = *reinterpret_cast<const uint4 *>(p);
+    const uint32_t low = __vminu2(__vminu2(~x.x & 0x7f807f80u, ~x.y & 0x7f807f80u),
+                                  __vminu2(~x.z & 0x7f807f80u, ~x.w & 0x7f807f80u));
+    return (low & 0xffffu) != 0 && (low >> 16) != 0;
+}
+
 // 16 bytes global -> shared, zeros where !valid (src is then not read).
 __device__ __forceinline__ void copy16(void *dst, const void *src, bool valid) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
@@ -94,6 +106,7 @@ __device__ __forceinline__ void copy16(void *dst, const void *src, bool valid) {
                  : "memory");
 }
 __device__ __forceinline__ void copies_done() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the last N groups.
 template <int N>
 __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
@@ -180,12 +193,12 @@ __global__ void __launch_bounds__(threads_of(ROWS), ROWS == 64 ? 2 : 4) attend_s
             for (int c = 0; c < N * CT; ++c) o[i][c] = 0;
         }
         const int sees0 = attend_sees(p, a, 0);
+        copies_wait<1>();
+        __syncthreads();   // the first K and q are here
         const bool some = (tid & ~31) / TX * 4 < a.rows;   // the warp has a row
         for (int t = t0; t < t1; ++t) {
             const int j0 = t * kKeys;
             const bool more = t + 1 < t1, edge = j0 + kKeys > sees0;
-            copies_wait<1>();
-            __syncthreads();   // K and q are here
             if (more) look_up(t + 1);
             if (some) {
                 unsigned long long x2[4][KT];
@@ -245,16 +258,22 @@ __global__ void __launch_bounds__(threads_of(ROWS), ROWS == 64 ? 2 : 4) attend_s
                     *reinterpret_cast<float4 *>(sp + (tx + TX * j) * (ROWS + 4) + ty * 4) =
                         make_float4(x[0][j], x[1][j], x[2][j], x[3][j]);
             }
-            __syncthreads();   // K is read, p is here
-            if (more)
-                fetch(sk, p.k_pool, t + 1);
-            else
-                copies_done();   // an empty group keeps the count
-            copies_wait<1>();
-            __syncthreads();   // V is here
+            copies_wait<0>();
+            __syncthreads();   // K is read, p and V are here
+            if (more) fetch(sk, p.k_pool, t + 1);
+            const int nk = min(kKeys, a.hi - j0);
+            // where some row sees only part of the tile, p is 0 for the rest,
+            // but 0 times an infinite or NaN value is not
+            bool strict = false;
+            if (edge) {
+                bool odd = false;
+                for (int r = max(0, sees0 - j0) + (tid >> 3); r < nk; r += kPass)
+                    for (int v = tid & 7; v < vecs; v += 8)
+                        odd |= !all_finite(reinterpret_cast<const T *>(sv + r * rb + v * 16));
+                strict = __syncthreads_or(odd);
+            }
             if (some) {
                 auto product = [&](auto cut) {
-                    const int nk = min(kKeys, a.hi - j0);
 #pragma unroll 4
                     for (int j = 0; j < nk; ++j) {
                         const float4 e = *reinterpret_cast<const float4 *>(sp + j * (ROWS + 4) + ty * 4);
@@ -276,16 +295,16 @@ __global__ void __launch_bounds__(threads_of(ROWS), ROWS == 64 ? 2 : 4) attend_s
                         }
                     }
                 };
-                if (edge)
+                if (strict)
                     product(std::true_type{});
                 else
                     product(std::false_type{});
             }
-            __syncthreads();   // V and p are read
-            if (more)
+            if (more) {
+                copies_wait<0>();
+                __syncthreads();   // V and p are read, the next K is here
                 fetch(sv, p.v_pool, t + 1);
-            else
-                copies_done();
+            }
         }
         // whole units go straight out, shared ones through the slots
         const bool whole = t0 == 0 && t1 == a.steps;

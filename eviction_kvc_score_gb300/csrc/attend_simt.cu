@@ -112,9 +112,88 @@ __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// After the block has written its slot of a unit that it shares: the block that
+// finishes last adds the slots up, two chunks of columns times four slots at a
+// time.  Every thread of the block calls it.
+template <typename T, int THREADS>
+__device__ __noinline__ void join_blocks(const AttendParams &p, const AttendUnit &a, int c0, int c1,
+                                         uint32_t *s_last) {
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        const bool last = atomicAdd(&p.arrived[8 * c0], 1u) == (uint32_t)(c1 - c0);
+        if (last) p.arrived[8 * c0] = 0;
+        *s_last = last;
+    }
+    __syncthreads();
+    if (!*s_last) return;
+    __threadfence();
+    constexpr int U = 2, S = 4;
+    const int D = p.dim, chunks = D / 4;
+    for (int x0 = threadIdx.x; x0 < a.rows * chunks; x0 += THREADS * U) {
+        float top[U], sum[U];
+        float4 acc[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            top[u] = -INFINITY;
+            sum[u] = 0.f;
+            acc[u] = make_float4(0, 0, 0, 0);
+        }
+        for (int c = c0; c <= c1; c += S) {
+            float2 st[U][S];
+            float4 y[U][S];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int x = x0 + u * THREADS, row = x / chunks, col = (x - row * chunks) * 4;
+#pragma unroll
+                for (int k = 0; k < S; ++k) {
+                    st[u][k] = make_float2(-INFINITY, 0.f);
+                    y[u][k] = make_float4(0, 0, 0, 0);
+                    if (row < a.rows && c + k <= c1) {
+                        const int64_t at = ((int64_t)(c + k) * p.slots + (c + k == c0 ? kSlotLast : kSlotFirst)) * p.slot_rows + row;
+                        st[u][k] = __ldcg(&p.stat[at]);
+                        y[u][k] = __ldcg(reinterpret_cast<const float4 *>(p.part + at * D + col));
+                    }
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float t = top[u];
+#pragma unroll
+                for (int k = 0; k < S; ++k) t = fmaxf(t, st[u][k].x);
+                const float ref = t == -INFINITY ? 0.f : t, down = ex2(top[u] - ref);
+                top[u] = t;
+                sum[u] *= down;
+                acc[u] = make_float4(acc[u].x * down, acc[u].y * down, acc[u].z * down, acc[u].w * down);
+#pragma unroll
+                for (int k = 0; k < S; ++k) {
+                    const float w = ex2(st[u][k].x - ref);
+                    sum[u] = fmaf(st[u][k].y, w, sum[u]);
+                    acc[u].x = fmaf(y[u][k].x, w, acc[u].x);
+                    acc[u].y = fmaf(y[u][k].y, w, acc[u].y);
+                    acc[u].z = fmaf(y[u][k].z, w, acc[u].z);
+                    acc[u].w = fmaf(y[u][k].w, w, acc[u].w);
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int x = x0 + u * THREADS, row = x / chunks, col = (x - row * chunks) * 4;
+            if (row >= a.rows) continue;
+            const bool see = attend_sees(p, a, row) > 0;
+            const int64_t out_row = attend_out_row(p, a, row);
+            const float inv = 1.f / sum[u];
+            const float4 r = see ? make_float4(acc[u].x * inv, acc[u].y * inv, acc[u].z * inv, acc[u].w * inv)
+                                 : make_float4(0, 0, 0, 0);
+            store4(static_cast<T *>(p.out) + out_row * D + col, r);
+            if (col == 0) attend_store_lse(p, out_row, top[u], sum[u], see);
+        }
+    }
+}
+
 // A thread's columns: CT chunks of 2 N, CT * TX * 2 N >= D.
 template <typename T, int ROWS, int N, int CT>
-__global__ void __launch_bounds__(threads_of(ROWS), ROWS == 64 ? 2 : 4) attend_simt_kernel(const AttendParams p) {
+__global__ void __launch_bounds__(threads_of(ROWS), ROWS == 64 ? 2 : 4) attend_simt_kernel(const __grid_constant__ AttendParams p) {
     constexpr int kThreads = threads_of(ROWS), W = 2 * N;
     constexpr int TX = ROWS == 64 ? 16 : 32, KT = kKeys / TX;
     constexpr int kPass = kThreads / 8, kPasses = kKeys / kPass;   // rows copied at a time
@@ -337,48 +416,7 @@ __global__ void __launch_bounds__(threads_of(ROWS), ROWS == 64 ? 2 : 4) attend_s
         if (!whole) {
             const int c0 = attend_cta_of(run.total, run.grid, u_lo);
             const int c1 = attend_cta_of(run.total, run.grid, u_lo + a.steps - 1);
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) {
-                const bool last = atomicAdd(&p.arrived[8 * c0], 1u) == (uint32_t)(c1 - c0);
-                if (last) p.arrived[8 * c0] = 0;
-                *s_last = last;
-            }
-            __syncthreads();
-            if (*s_last) {
-                __threadfence();
-                const int chunks = D / 4;
-                for (int x = tid; x < a.rows * chunks; x += kThreads) {
-                    const int r = x / chunks, col = (x - r * chunks) * 4;
-                    auto at = [&](int c) {
-                        return ((int64_t)c * p.slots + (c == c0 ? kSlotLast : kSlotFirst)) * p.slot_rows + r;
-                    };
-                    float top = -INFINITY;
-                    for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(&p.stat[at(c)]).x);
-                    const float ref = top == -INFINITY ? 0.f : top;
-                    float sum = 0.f;
-                    float4 acc = make_float4(0, 0, 0, 0);
-                    for (int c = c0; c <= c1; ++c) {
-                        const float2 st = __ldcg(&p.stat[at(c)]);
-                        const float4 y = __ldcg(reinterpret_cast<const float4 *>(p.part + at(c) * D + col));
-                        const float w = ex2(st.x - ref);
-                        sum = fmaf(st.y, w, sum);
-                        acc.x = fmaf(y.x, w, acc.x);
-                        acc.y = fmaf(y.y, w, acc.y);
-                        acc.z = fmaf(y.z, w, acc.z);
-                        acc.w = fmaf(y.w, w, acc.w);
-                    }
-                    const bool any = attend_sees(p, a, r) > 0;
-                    const int64_t row = attend_out_row(p, a, r);
-                    const float inv = 1.f / sum;
-                    if (any)
-                        acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-                    else
-                        acc = make_float4(0, 0, 0, 0);
-                    store4(static_cast<T *>(p.out) + row * D + col, acc);
-                    if (col == 0) attend_store_lse(p, row, top, sum, any);
-                }
-            }
+            join_blocks<T, kThreads>(p, a, c0, c1, s_last);
         }
         pos = end;
         u_lo += a.steps;

@@ -70,11 +70,11 @@ int state_of(const kvc_cache &c, int32_t n_lists, void *state, size_t bytes, con
 }
 
 // The kernel that takes a call, and its workspace: header | arrival counters |
-// slots' (max, sum) | slots' rows.
+// slots' (max, sum) | groups' (max, sum) | slots' rows.
 struct AttendWs {
     bool tc;
     AttendNeeds needs;
-    size_t arrived, stat, part, total;
+    size_t arrived, stat, group_stat, part, total;
 };
 
 AttendWs attend_ws(const kvc_cache &c, int group) {
@@ -83,8 +83,9 @@ AttendWs attend_ws(const kvc_cache &c, int group) {
     w.needs = w.tc ? attend_tc_needs(device_sms()) : attend_simt_needs(device_sms());
     const size_t rows = (size_t)w.needs.grid * w.needs.slots * w.needs.slot_rows;
     w.arrived = kWsHeader;
-    w.stat = w.arrived + cache_align((size_t)w.needs.grid * 8 * sizeof(uint32_t));
-    w.part = w.stat + cache_align(rows * sizeof(float2));
+    w.stat = w.arrived + cache_align((size_t)w.needs.grid * 16 * sizeof(uint32_t));
+    w.group_stat = w.stat + cache_align(rows * sizeof(float2));
+    w.part = w.group_stat + cache_align(rows * sizeof(float2));
     w.total = w.part + cache_align(rows * c.head_dim * sizeof(float));
     return w;
 }
@@ -335,6 +336,7 @@ int kvc_attend(const kvc_cache *cache, int32_t n_q_heads, int32_t n_kv_heads, in
     p.status = static_cast<uint32_t *>(ws);
     p.arrived = reinterpret_cast<uint32_t *>(base + w.arrived);
     p.stat = reinterpret_cast<float2 *>(base + w.stat);
+    p.group_stat = reinterpret_cast<float2 *>(base + w.group_stat);
     p.part = reinterpret_cast<float *>(base + w.part);
     return w.tc ? launch_attend_tc(p, w.needs.grid, stream)
                 : launch_attend_simt(p, c.dtype == KVC_F32, w.needs.grid, stream);

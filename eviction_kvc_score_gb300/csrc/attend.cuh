@@ -10,7 +10,8 @@
 // runs, one per CTA: lists of any lengths keep every SM busy to the end, and a CTA shares at most its first and its last
 // unit with others.  For those it leaves rows' (max, sum, unnormalised output)
 // in a slot of its own; the CTA that finishes last adds the unit's slots up in
-// CTA order, so the result does not depend on the order of finishing.
+// CTA order (of many slots, neighbours first), so the result does not depend on
+// the order of finishing.
 #pragma once
 
 #include <climits>
@@ -40,8 +41,10 @@ struct AttendParams {
     float *lse;
     float scale_log2;    // scale * log2(e)
     uint32_t *status;
-    uint32_t *arrived;   // [grid][8], zero between calls
+    Divider by_quads;    // dim / 4
+    uint32_t *arrived;   // [grid][2][8], zero between calls: of a unit, of a group
     float2 *stat;        // [grid][slots][slot_rows] (max in log2 units, sum)
+    float2 *group_stat;  // the same of joined groups
     float *part;         // [grid][slots][slot_rows][dim]
 };
 
@@ -214,6 +217,122 @@ __device__ __forceinline__ bool attend_last(uint32_t *count, uint32_t all) {
 // Slots of a CTA: its first unit's (begun by an earlier CTA), its last unit's.
 constexpr int kSlotFirst = 0, kSlotLast = 1;
 
+__device__ __forceinline__ void attend_store4(float *p, float4 x) { *reinterpret_cast<float4 *>(p) = x; }
+__device__ __forceinline__ void attend_store4(__nv_bfloat16 *p, float4 x) {
+    uint32_t a, b;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(a) : "f"(x.y), "f"(x.x));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(b) : "f"(x.w), "f"(x.z));
+    *reinterpret_cast<uint2 *>(p) = make_uint2(a, b);
+}
+
+// Joining: a unit shared by few CTAs is joined by the one that finishes last.  Of
+// many, every kJoinGroup neighbours' slots are joined first, into the first
+// one's, by the last of those: one SM reading 150 slots would take longer than
+// all SMs took for their steps.
+constexpr int kJoinAtOnce = 24, kJoinGroup = 12;
+__device__ __forceinline__ int attend_groups(int ctas) {
+    return ctas <= kJoinAtOnce ? 1 : (ctas + kJoinGroup - 1) / kJoinGroup;
+}
+
+struct AttendSpan {
+    int c0;         // the unit's first CTA
+    int from, step, n;   // slots of CTAs from, from + step, ..
+    bool groups;    // they are joined groups
+    bool out;       // the result is the output, else a group's
+};
+
+// Rows first.. of the unit; their places in the slots begin at slot_row.  `me`
+// of `threads` threads; U chunks of four columns times S slots are asked for at a
+// time.
+template <typename T, int U, int S>
+__device__ __noinline__ void attend_join(const AttendParams &p, const AttendUnit &a, const AttendSpan &s,
+                                         int first, int rows, int slot_row, int me, int threads) {
+    const int D = p.dim, quads = D / 4;
+    // slot k of the span is slot0 + k * stride - (k > 0 and it begins with the
+    // unit's first CTA): one 64-bit offset per slot, one addition per load
+    const bool whole = s.from == s.c0;
+    const int64_t slot0 = (int64_t)s.from * p.slots + (whole ? kSlotLast : kSlotFirst);
+    const int64_t stride = (int64_t)s.step * p.slots, back = whole ? kSlotLast - kSlotFirst : 0;
+    const int64_t slot_floats = (int64_t)p.slot_rows * D;
+    const float2 *stat = (s.groups ? p.group_stat : p.stat) + slot_row;
+    float *part = p.part + (int64_t)slot_row * D;
+    for (int x0 = me; x0 < rows * quads; x0 += threads * U) {
+        float top[U], sum[U];
+        float4 acc[U];
+        const float2 *stat_at[U];
+        const float *part_at[U];
+        bool real[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int x = x0 + u * threads, row = p.by_quads(x), col = (x - row * quads) * 4;
+            real[u] = row < rows;
+            stat_at[u] = stat + (real[u] ? row : 0);
+            part_at[u] = part + (real[u] ? row * D + col : 0);
+            top[u] = -INFINITY;
+            sum[u] = 0.f;
+            acc[u] = make_float4(0, 0, 0, 0);
+        }
+        for (int k0 = 0; k0 < s.n; k0 += S) {
+            float2 st[U][S];
+            float4 y[U][S];
+#pragma unroll
+            for (int k = 0; k < S; ++k) {
+                const bool is = k0 + k < s.n;
+                const int64_t slot = slot0 + (is ? (k0 + k) * stride - (k0 + k > 0 ? back : 0) : 0);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    st[u][k] = __ldcg(stat_at[u] + slot * p.slot_rows);
+                    y[u][k] = __ldcg(reinterpret_cast<const float4 *>(part_at[u] + slot * slot_floats));
+                }
+                if (!is) {   // the span's first slot once more, with no weight
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        st[u][k] = make_float2(-INFINITY, 0.f);
+                        y[u][k] = make_float4(0, 0, 0, 0);
+                    }
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float t = top[u];
+#pragma unroll
+                for (int k = 0; k < S; ++k) t = fmaxf(t, st[u][k].x);
+                const float ref = t == -INFINITY ? 0.f : t, down = ex2(top[u] - ref);
+                top[u] = t;
+                sum[u] *= down;
+                acc[u] = make_float4(acc[u].x * down, acc[u].y * down, acc[u].z * down, acc[u].w * down);
+#pragma unroll
+                for (int k = 0; k < S; ++k) {
+                    const float w = ex2(st[u][k].x - ref);
+                    sum[u] = fmaf(st[u][k].y, w, sum[u]);
+                    acc[u].x = fmaf(y[u][k].x, w, acc[u].x);
+                    acc[u].y = fmaf(y[u][k].y, w, acc[u].y);
+                    acc[u].z = fmaf(y[u][k].z, w, acc[u].z);
+                    acc[u].w = fmaf(y[u][k].w, w, acc[u].w);
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (!real[u]) continue;
+            const int x = x0 + u * threads, row = p.by_quads(x), col = (x - row * quads) * 4;
+            if (!s.out) {   // this thread alone has read this chunk of the slot
+                *reinterpret_cast<float4 *>(part + slot0 * slot_floats + row * D + col) = acc[u];
+                if (col == 0) p.group_stat[slot0 * p.slot_rows + slot_row + row] = make_float2(top[u], sum[u]);
+                continue;
+            }
+            const bool see = attend_sees(p, a, first + row) > 0;
+            const int64_t out_row = attend_out_row(p, a, first + row);
+            const float inv = 1.f / sum[u];
+            const float4 r = see ? make_float4(acc[u].x * inv, acc[u].y * inv, acc[u].z * inv, acc[u].w * inv)
+                                 : make_float4(0, 0, 0, 0);
+            attend_store4(static_cast<T *>(p.out) + out_row * D + col, r);
+            if (col == 0) attend_store_lse(p, out_row, top[u], sum[u], see);
+        }
+    }
+}
+
+
 // What a launch needs of the workspace.
 struct AttendNeeds {
     int grid, slots, slot_rows;
@@ -230,6 +349,7 @@ inline bool attend_units(AttendParams &p, int unit_rows) {
     p.by_group = Divider((uint32_t)p.group);
     p.by_heads = Divider((uint32_t)p.n_kv_heads);
     p.by_blocks = Divider((uint32_t)p.blocks);
+    p.by_quads = Divider((uint32_t)p.dim / 4);
     return n < INT_MAX;
 }
 // Both set the units' shape.

@@ -79,14 +79,6 @@ __device__ __forceinline__ void store2(__nv_bfloat16 *p, float x, float y) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(a) : "f"(y), "f"(x));
     *reinterpret_cast<uint32_t *>(p) = a;
 }
-__device__ __forceinline__ void store4(float *p, float4 x) { *reinterpret_cast<float4 *>(p) = x; }
-__device__ __forceinline__ void store4(__nv_bfloat16 *p, float4 x) {
-    uint32_t a, b;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(a) : "f"(x.y), "f"(x.x));
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(b) : "f"(x.w), "f"(x.z));
-    *reinterpret_cast<uint2 *>(p) = make_uint2(a, b);
-}
-
 // Whether the 16 bytes at p hold numbers only.
 __device__ __forceinline__ bool all_finite(const float *p) {
     const float4 x = *reinterpret_cast<const float4 *>(p);
@@ -112,83 +104,20 @@ __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// After the block has written its slot of a unit that it shares: the block that
-// finishes last adds the slots up, two chunks of columns times four slots at a
-// time.  Every thread of the block calls it.
-template <typename T, int THREADS>
-__device__ __noinline__ void join_blocks(const AttendParams &p, const AttendUnit &a, int c0, int c1,
-                                         uint32_t *s_last) {
+// The block's rows of a slot are written: count it; true in the whole block if it
+// is the last of `all`.
+__device__ __forceinline__ bool block_last(uint32_t *count, uint32_t all, uint32_t *s_last) {
     __threadfence();
     __syncthreads();
     if (threadIdx.x == 0) {
-        const bool last = atomicAdd(&p.arrived[8 * c0], 1u) == (uint32_t)(c1 - c0);
-        if (last) p.arrived[8 * c0] = 0;
+        const bool last = atomicAdd(count, 1u) == all - 1;
+        if (last) *count = 0;
         *s_last = last;
     }
     __syncthreads();
-    if (!*s_last) return;
+    const bool last = *s_last;
     __threadfence();
-    constexpr int U = 2, S = 4;
-    const int D = p.dim, chunks = D / 4;
-    for (int x0 = threadIdx.x; x0 < a.rows * chunks; x0 += THREADS * U) {
-        float top[U], sum[U];
-        float4 acc[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            top[u] = -INFINITY;
-            sum[u] = 0.f;
-            acc[u] = make_float4(0, 0, 0, 0);
-        }
-        for (int c = c0; c <= c1; c += S) {
-            float2 st[U][S];
-            float4 y[U][S];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int x = x0 + u * THREADS, row = x / chunks, col = (x - row * chunks) * 4;
-#pragma unroll
-                for (int k = 0; k < S; ++k) {
-                    st[u][k] = make_float2(-INFINITY, 0.f);
-                    y[u][k] = make_float4(0, 0, 0, 0);
-                    if (row < a.rows && c + k <= c1) {
-                        const int64_t at = ((int64_t)(c + k) * p.slots + (c + k == c0 ? kSlotLast : kSlotFirst)) * p.slot_rows + row;
-                        st[u][k] = __ldcg(&p.stat[at]);
-                        y[u][k] = __ldcg(reinterpret_cast<const float4 *>(p.part + at * D + col));
-                    }
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                float t = top[u];
-#pragma unroll
-                for (int k = 0; k < S; ++k) t = fmaxf(t, st[u][k].x);
-                const float ref = t == -INFINITY ? 0.f : t, down = ex2(top[u] - ref);
-                top[u] = t;
-                sum[u] *= down;
-                acc[u] = make_float4(acc[u].x * down, acc[u].y * down, acc[u].z * down, acc[u].w * down);
-#pragma unroll
-                for (int k = 0; k < S; ++k) {
-                    const float w = ex2(st[u][k].x - ref);
-                    sum[u] = fmaf(st[u][k].y, w, sum[u]);
-                    acc[u].x = fmaf(y[u][k].x, w, acc[u].x);
-                    acc[u].y = fmaf(y[u][k].y, w, acc[u].y);
-                    acc[u].z = fmaf(y[u][k].z, w, acc[u].z);
-                    acc[u].w = fmaf(y[u][k].w, w, acc[u].w);
-                }
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int x = x0 + u * THREADS, row = x / chunks, col = (x - row * chunks) * 4;
-            if (row >= a.rows) continue;
-            const bool see = attend_sees(p, a, row) > 0;
-            const int64_t out_row = attend_out_row(p, a, row);
-            const float inv = 1.f / sum[u];
-            const float4 r = see ? make_float4(acc[u].x * inv, acc[u].y * inv, acc[u].z * inv, acc[u].w * inv)
-                                 : make_float4(0, 0, 0, 0);
-            store4(static_cast<T *>(p.out) + out_row * D + col, r);
-            if (col == 0) attend_store_lse(p, out_row, top[u], sum[u], see);
-        }
-    }
+    return last;
 }
 
 // A thread's columns: CT chunks of 2 N, CT * TX * 2 N >= D.
@@ -416,7 +345,16 @@ __global__ void __launch_bounds__(threads_of(ROWS), ROWS == 64 ? 2 : 4) attend_s
         if (!whole) {
             const int c0 = attend_cta_of(run.total, run.grid, u_lo);
             const int c1 = attend_cta_of(run.total, run.grid, u_lo + a.steps - 1);
-            join_blocks<T, kThreads>(p, a, c0, c1, s_last);
+            const int me = blockIdx.x, n = c1 - c0 + 1, groups = attend_groups(n);
+            bool last = true;
+            if (groups > 1) {
+                const int g0 = c0 + (me - c0) / kJoinGroup * kJoinGroup, gn = min(kJoinGroup, c1 - g0 + 1);
+                last = block_last(&p.arrived[16 * g0 + 8], gn, s_last);
+                if (last) attend_join<T, 2, 4>(p, a, AttendSpan{c0, g0, 1, gn, false, false}, 0, a.rows, 0, tid, kThreads);
+            }
+            if (last && block_last(&p.arrived[16 * c0], groups > 1 ? groups : n, s_last))
+                attend_join<T, 2, 4>(p, a, AttendSpan{c0, c0, groups > 1 ? kJoinGroup : 1, groups > 1 ? groups : n, groups > 1, true},
+                                     0, a.rows, 0, tid, kThreads);
         }
         pos = end;
         u_lo += a.steps;

@@ -80,7 +80,7 @@ struct Bars {
     uint64_t full[STAGES], empty[STAGES];
     uint64_t q_full, q_empty;
     uint64_t s_full[2], p_full[2][2], o_full[2];   // p_full: [half][keys 0-63, 64-127]
-    uint64_t half_full, half_empty, wg[2], drain[2], issued[2];
+    uint64_t half_full, half_empty, wg[2], joined[2], drain[2], issued[2];
     uint32_t tmem;
     volatile int abort_flag;
     int dirty;            // some value taken out of V
@@ -233,77 +233,6 @@ struct Walk {
     }
 };
 
-// Adds up the slots of CTAs c0..c1 for `rows` rows, first.. of the unit, and
-// writes them out; `me` of `threads` threads.  Four chunks of four columns times four
-// slots are asked for at a time: with one load after the other the joining of
-// 19 CTAs' slots took longer than their products.
-template <int D>
-__device__ __noinline__ void join_slots(const AttendParams &p, const AttendUnit &a, int first, int rows,
-                                        int slot_row, int c0, int c1, int me, int threads) {
-    constexpr int U = 4, S = 4, kVec = D / 4;
-    for (int x0 = me; x0 < rows * kVec; x0 += threads * U) {
-        float top[U], sum[U];
-        float4 acc[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            top[u] = -INFINITY;
-            sum[u] = 0.f;
-            acc[u] = make_float4(0, 0, 0, 0);
-        }
-        for (int c = c0; c <= c1; c += S) {
-            float2 st[U][S];
-            float4 y[U][S];
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int k = 0; k < S; ++k) {
-                    const int x = x0 + u * threads, row = x / kVec, d = (x - row * kVec) * 4;
-                    st[u][k] = make_float2(-INFINITY, 0.f);
-                    y[u][k] = make_float4(0, 0, 0, 0);
-                    if (row < rows && c + k <= c1) {
-                        const int64_t at = ((int64_t)(c + k) * kSlotsTc + (c + k == c0 ? kSlotLast : kSlotFirst)) * p.slot_rows + slot_row + row;
-                        st[u][k] = __ldcg(&p.stat[at]);
-                        y[u][k] = __ldcg(reinterpret_cast<const float4 *>(p.part + at * D + d));
-                    }
-                }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                float t = top[u];
-#pragma unroll
-                for (int k = 0; k < S; ++k) t = fmaxf(t, st[u][k].x);
-                const float ref = t == -INFINITY ? 0.f : t, down = ex2(top[u] - ref);
-                top[u] = t;
-                sum[u] *= down;
-                acc[u] = make_float4(acc[u].x * down, acc[u].y * down, acc[u].z * down, acc[u].w * down);
-#pragma unroll
-                for (int k = 0; k < S; ++k) {
-                    const float w = ex2(st[u][k].x - ref);
-                    sum[u] = fmaf(st[u][k].y, w, sum[u]);
-                    acc[u].x = fmaf(y[u][k].x, w, acc[u].x);
-                    acc[u].y = fmaf(y[u][k].y, w, acc[u].y);
-                    acc[u].z = fmaf(y[u][k].z, w, acc[u].z);
-                    acc[u].w = fmaf(y[u][k].w, w, acc[u].w);
-                }
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int x = x0 + u * threads, row = x / kVec, d = (x - row * kVec) * 4;
-            if (row >= rows) continue;
-            const bool see = attend_sees(p, a, first + row) > 0;
-            const float inv = 1.f / sum[u];
-            const int64_t out_row = attend_out_row(p, a, first + row);
-            uint32_t q0, q1;
-            const float y0 = see ? acc[u].x * inv : 0.f, y1 = see ? acc[u].y * inv : 0.f;
-            const float y2 = see ? acc[u].z * inv : 0.f, y3 = see ? acc[u].w * inv : 0.f;
-            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(q0) : "f"(y1), "f"(y0));
-            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(q1) : "f"(y3), "f"(y2));
-            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + out_row * D + d) = make_uint2(q0, q1);
-            if (d == 0) attend_store_lse(p, out_row, top[u], sum[u], see);
-        }
-    }
-}
-
 template <int KH>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
@@ -331,6 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&b.p_full[t][1], 4);
             mbar_init(&b.o_full[t], 1);
             mbar_init(&b.wg[t], 1);
+            mbar_init(&b.joined[t], 4);
             mbar_init(&b.drain[t], 1);
             mbar_init(&b.issued[t], 1);
         }
@@ -592,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool plain = p.scale_log2 > 0.f;
         const float c = p.scale_log2;
         const unsigned long long c2 = f2_pack(c, c);
-        uint32_t ns = 0, no = 0, nwg = 0, handed = 0, filled = 0;
+        uint32_t ns = 0, no = 0, nwg = 0, njoined = 0, handed = 0, filled = 0;
         bool owed = false;   // half 1: O is still being read by half 0
         bool ok = true;
         Work w;
@@ -863,24 +793,52 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!g.whole) {
                 // the CTA that finishes last joins the unit's slots
                 const int c0 = g.c0, c1 = g.c1;
-                const uint32_t all = (uint32_t)(c1 - c0 + 1);
+                const int n = c1 - c0 + 1, groups = attend_groups(n);
+                const int g0 = c0 + ((int)blockIdx.x - c0) / kJoinGroup * kJoinGroup, gn = min(kJoinGroup, c1 - g0 + 1);
+                const AttendSpan group{c0, g0, 1, gn, false, false};
+                const AttendSpan unit{c0, c0, groups > 1 ? kJoinGroup : 1, groups > 1 ? groups : n, groups > 1, true};
                 const int rows = min(a.rows - t * R, R);   // of the tile
-                uint32_t *count = &p.arrived[8 * c0 + 4 * t];
+                uint32_t *of_group = &p.arrived[16 * g0 + 8 + 4 * t], *of_unit = &p.arrived[16 * c0 + 4 * t];
                 if (rows > 32) {   // each warp its own 32 rows
-                    if (any && attend_last(count + quarter, all))
-                        join_slots<D>(p, a, t * R + 32 * quarter, min(32, rows - 32 * quarter),
-                                      t * kTile + 32 * quarter, c0, c1, lane, 32);
+                    const int row0 = 32 * quarter, mine = min(32, rows - row0);
+                    bool last = any;
+                    if (last && groups > 1) {
+                        last = attend_last(of_group + quarter, gn);
+                        if (last)
+                            attend_join<__nv_bfloat16, 4, 4>(p, a, group, t * R + row0, mine, t * kTile + row0, lane, 32);
+                    }
+                    if (last && attend_last(of_unit + quarter, unit.n))
+                        attend_join<__nv_bfloat16, 4, 4>(p, a, unit, t * R + row0, mine, t * kTile + row0, lane, 32);
                 } else {           // one warp's rows: often of many slots, so all four join
-                    volatile int *last = &b.last[t][nwg & 1];
-                    if (quarter == 0) {
-                        const bool is = attend_last(count, all);
-                        if (lane == 0) {
-                            *last = is;
-                            mbar_arrive(&b.wg[t]);
+                    // the first warp counts and tells the others
+                    auto all_last = [&](uint32_t *count, int of, bool *is) {
+                        volatile int *last = &b.last[t][nwg & 1];
+                        if (quarter == 0) {
+                            const bool x = attend_last(count, of);
+                            if (lane == 0) {
+                                *last = x;
+                                mbar_arrive(&b.wg[t]);
+                            }
+                        }
+                        if (!warp_wait(&b.wg[t], nwg++ & 1, stop, p.status)) return false;
+                        *is = *last;
+                        return true;
+                    };
+                    bool last = true;
+                    if (groups > 1) {
+                        if (!(ok = all_last(of_group, gn, &last))) break;
+                        if (last) {
+                            attend_join<__nv_bfloat16, 2, 4>(p, a, group, t * R, rows, t * kTile, r, kTile);
+                            __threadfence();   // before the first warp counts for all four
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&b.joined[t]);
+                            if (!(ok = warp_wait(&b.joined[t], njoined++ & 1, stop, p.status))) break;
                         }
                     }
-                    if (!(ok = warp_wait(&b.wg[t], nwg++ & 1, stop, p.status))) break;
-                    if (*last) join_slots<D>(p, a, t * R, rows, t * kTile, c0, c1, r, kTile);
+                    if (last) {
+                        if (!(ok = all_last(of_unit, unit.n, &last))) break;
+                        if (last) attend_join<__nv_bfloat16, 2, 4>(p, a, unit, t * R, rows, t * kTile, r, kTile);
+                    }
                 }
             }
         }

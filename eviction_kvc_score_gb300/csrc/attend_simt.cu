@@ -364,9 +364,9 @@ __global__ void __launch_bounds__(threads_of(ROWS), ROWS == 64 ? 2 : 4) attend_s
 
 template <typename T, int ROWS, int N, int CT>
 int launch(AttendParams &p, int sms, cudaStream_t st) {
-    auto kernel = attend_simt_kernel<T, ROWS, N, CT>;
+    constexpr auto kernel = attend_simt_kernel<T, ROWS, N, CT>;
     const size_t bytes = smem_bytes<T, ROWS>(p.dim);
-    if (bytes > 48 * 1024) cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
+    if (bytes > 48 * 1024) allow_shared<kernel>(232448);
     // as many blocks as an SM holds at once (1 KB of shared memory is each block's own cost)
     const int per_sm = std::max(1, std::min(ROWS == 64 ? 2 : 4, (int)(233472 / (bytes + 1024))));
     launch_early(kernel, per_sm * sms, threads_of(ROWS), bytes, st, p);

@@ -877,7 +877,7 @@ int launch(AttendParams &p, int grid, cudaStream_t st) {
                   kRegsLaunch);
         return KVC_ERR_UNSUPPORTED;
     }
-    cudaFuncSetAttribute(attend_tc_kernel<KH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    allow_shared<attend_tc_kernel<KH>>((int)bytes);
     launch_early(attend_tc_kernel<KH>, grid, kThreads, bytes, st, tq, tk, tv, p);
     return cache_launched("kvc_attend");
 }

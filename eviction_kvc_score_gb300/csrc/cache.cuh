@@ -3,6 +3,8 @@
 // page table without trusting it.
 #pragma once
 
+#include <atomic>
+
 #include "kvc_internal.cuh"
 
 namespace kvc {
@@ -100,6 +102,19 @@ struct Divider {
 // the next kernel's blocks may be brought in.
 __device__ __forceinline__ void wait_for_inputs() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// Lets a kernel use up to `bytes` of shared memory per block; asked of the driver
+// once per kernel and device.
+template <auto kKernel>
+void allow_shared(int bytes) {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return;   // the launch will say so
+    const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return;
+    if (cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess)
+        done.fetch_or(bit, std::memory_order_relaxed);
+}
 
 template <typename... P, typename... A>
 void launch_early(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, A... args) {

@@ -344,15 +344,16 @@ def _at(t, name, dtype, dev, numel=0):
     elements at least."""
     if t is None:
         return None
+    if (t.get_device() == dev and t.dtype is dtype and t.is_contiguous()
+            and (not numel or t.numel() >= numel)):
+        return t.data_ptr()
     if t.get_device() != dev:
         raise ValueError(f"{name} must be a tensor on cuda:{dev}, the current device")
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.numel() < numel:
-        raise ValueError(f"{name} has {t.numel()} elements, needs {numel}")
-    return t.data_ptr()
+    raise ValueError(f"{name} has {t.numel()} elements, needs {numel}")
 
 
 def _lists(c: KvcCache, table, lens):

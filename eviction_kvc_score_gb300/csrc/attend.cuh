@@ -214,6 +214,14 @@ __device__ __forceinline__ bool attend_last(uint32_t *count, uint32_t all) {
     return __shfl_sync(0xffffffffu, before, 0) == all - 1;
 }
 
+// How many warps have been counted; what they wrote before is visible after it.
+__device__ __forceinline__ uint32_t attend_peek(const uint32_t *count) {
+    uint32_t is = 0;
+    if ((threadIdx.x & 31) == 0)
+        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(is) : "l"(count) : "memory");
+    return __shfl_sync(0xffffffffu, is, 0);
+}
+
 // Slots of a CTA: its first unit's (begun by an earlier CTA), its last unit's.
 constexpr int kSlotFirst = 0, kSlotLast = 1;
 

@@ -55,6 +55,7 @@ constexpr uint32_t kColS = 0, kColO = 256;
 constexpr float kGrow = 8.f;            // log2 units m may lag behind
 constexpr int kSlotsTc = 2;
 constexpr int kExtra = 4;
+constexpr int kDirect = 4;              // shares that are joined from registers
 constexpr int kQueue = 4;               // segments on their way from the walk to the roles
 constexpr int kReaders = 12;            // arrivals that free an entry: every warp's
 
@@ -152,6 +153,24 @@ __device__ __forceinline__ bool elect_one() {
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *stop,
                                           uint32_t *status) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, stop, status));
+}
+
+// Slot of the k-th of the CTAs that share the segment's unit.
+__device__ __forceinline__ int64_t share_at(const Segment &g, int k) {
+    return (int64_t)(g.c0 + k) * kSlotsTc + (k == 0 ? kSlotLast : kSlotFirst);
+}
+
+// Eight floats at a 32-byte boundary, a whole sector, past L1.
+__device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
+    asm volatile("ld.global.cg.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+                 : "l"(p)
+                 : "memory");
+}
+__device__ __forceinline__ void store8(float *p, const float *v) {
+    asm volatile("st.global.v8.f32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"f"(v[0]), "f"(v[1]), "f"(v[2]),
+                 "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "l"(p)
+                 : "memory");
 }
 
 __device__ __forceinline__ Segment segment_of(const AttendParams &p, const AttendUnit &a, int s0, int s1) {
@@ -718,6 +737,39 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const int64_t slot = ((int64_t)blockIdx.x * kSlotsTc + (g.begins ? kSlotLast : kSlotFirst)) * p.slot_rows +
                                  t * kTile + r;
+            const int n = g.whole ? 1 : g.c1 - g.c0 + 1, me = (int)blockIdx.x;
+            const int rows = min(a.rows - t * R, R);   // of the tile
+            uint32_t *of_unit = &p.arrived[16 * g.c0 + 4 * t + (rows > 32 ? quarter : 0)];
+            // The others of a few are all done (mostly: the CTA that begins a
+            // unit ends with it, long after the others did their share): join
+            // from the registers, without writing this share down.  The sums
+            // are attend_join's, term by term.  (Tiles of few rows, where the
+            // look costs more than the writing, do without.)
+            bool direct = false;
+            float weight[kDirect];
+            if (!g.whole && n <= kDirect && rows > 32 && any) {
+                direct = attend_peek(of_unit) == (uint32_t)(n - 1);
+                if (direct) {
+                    float2 st[kDirect];
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int k = 0; k < kDirect; ++k) {
+                        st[k] = make_float2(-INFINITY, 0.f);
+                        if (k < n) st[k] = g.c0 + k == me ? make_float2(m, l) : __ldcg(&p.stat[share_at(g, k) * p.slot_rows + t * kTile + r]);
+                        top = fmaxf(top, st[k].x);
+                    }
+                    const float ref = top == -INFINITY ? 0.f : top;
+                    float sum = 0.f;
+#pragma unroll
+                    for (int k = 0; k < kDirect; ++k) {
+                        weight[k] = ex2(st[k].x - ref);
+                        sum = fmaf(st[k].y, weight[k], sum);
+                    }
+                    m = top;
+                    l = sum;
+                    if (lane == 0) *of_unit = 0;
+                }
+            }
             if (any) {
                 const float inv = 1.f / l;
                 const int64_t out_row = real ? attend_out_row(p, a, rt) : 0;
@@ -759,7 +811,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         }
                     }
-                    if (g.whole) {
+                    if (direct) {
+                        float sum[32];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) sum[j] = 0.f;
+#pragma unroll
+                        for (int k = 0; k < kDirect; ++k) {
+                            if (k >= n) break;
+                            if (g.c0 + k == me) {
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) sum[j] = fmaf(o[j], weight[k], sum[j]);
+                            } else {
+                                const float *src = p.part + (share_at(g, k) * p.slot_rows + t * kTile + r) * D + d;
+#pragma unroll
+                                for (int j = 0; j < 32; j += 8) {
+                                    float y[8];
+                                    load8(src + j, y);
+#pragma unroll
+                                    for (int e = 0; e < 8; ++e) sum[j + e] = fmaf(y[e], weight[k], sum[j + e]);
+                                }
+                            }
+                        }
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) o[j] = sum[j];
+                    }
+                    if (g.whole || direct) {
                         uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + out_row * D + d);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
@@ -774,14 +850,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                             dst[j] = make_uint4(q[0], q[1], q[2], q[3]);
                         }
                     } else {
-                        float4 *dst = reinterpret_cast<float4 *>(p.part + slot * D + d);
+                        float *dst = p.part + slot * D + d;
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            dst[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                        for (int j = 0; j < 32; j += 8) store8(dst + j, o + j);
                     }
                 }
                 if (real) {
-                    if (g.whole)
+                    if (g.whole || direct)
                         attend_store_lse(p, out_row, m, l, sees > 0);
                     else
                         p.stat[slot] = make_float2(m, l);
@@ -793,21 +868,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!g.whole) {
                 // the CTA that finishes last joins the unit's slots
                 const int c0 = g.c0, c1 = g.c1;
-                const int n = c1 - c0 + 1, groups = attend_groups(n);
-                const int g0 = c0 + ((int)blockIdx.x - c0) / kJoinGroup * kJoinGroup, gn = min(kJoinGroup, c1 - g0 + 1);
+                const int groups = attend_groups(n);
+                const int g0 = c0 + (me - c0) / kJoinGroup * kJoinGroup, gn = min(kJoinGroup, c1 - g0 + 1);
                 const AttendSpan group{c0, g0, 1, gn, false, false};
                 const AttendSpan unit{c0, c0, groups > 1 ? kJoinGroup : 1, groups > 1 ? groups : n, groups > 1, true};
-                const int rows = min(a.rows - t * R, R);   // of the tile
-                uint32_t *of_group = &p.arrived[16 * g0 + 8 + 4 * t], *of_unit = &p.arrived[16 * c0 + 4 * t];
+                uint32_t *of_group = &p.arrived[16 * g0 + 8 + 4 * t + (rows > 32 ? quarter : 0)];
                 if (rows > 32) {   // each warp its own 32 rows
                     const int row0 = 32 * quarter, mine = min(32, rows - row0);
-                    bool last = any;
+                    bool last = any && !direct;
                     if (last && groups > 1) {
-                        last = attend_last(of_group + quarter, gn);
+                        last = attend_last(of_group, gn);
                         if (last)
                             attend_join<__nv_bfloat16, 4, 4>(p, a, group, t * R + row0, mine, t * kTile + row0, lane, 32);
                     }
-                    if (last && attend_last(of_unit + quarter, unit.n))
+                    if (last && attend_last(of_unit, unit.n))
                         attend_join<__nv_bfloat16, 4, 4>(p, a, unit, t * R + row0, mine, t * kTile + row0, lane, 32);
                 } else {           // one warp's rows: often of many slots, so all four join
                     // the first warp counts and tells the others

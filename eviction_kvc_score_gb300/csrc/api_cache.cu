@@ -2,6 +2,7 @@
 // validation, the layout of the pages' state and of the attention's workspace,
 // and dispatch to the kernels.  As in api.cu, nothing here allocates device
 // memory and every launch goes to the caller's stream.
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -83,7 +84,10 @@ AttendWs attend_ws(const kvc_cache &c, int group) {
     w.needs = w.tc ? attend_tc_needs(device_sms()) : attend_simt_needs(device_sms());
     const size_t rows = (size_t)w.needs.grid * w.needs.slots * w.needs.slot_rows;
     w.arrived = kWsHeader;
-    w.stat = w.arrived + cache_align((size_t)w.needs.grid * 16 * sizeof(uint32_t));
+    // as many counters for either kernel: one's scratch is never the other's
+    // counters, so a workspace may serve caches of several kinds
+    const int counters = 16 * std::max(attend_tc_needs(device_sms()).grid, attend_simt_needs(device_sms()).grid);
+    w.stat = w.arrived + cache_align((size_t)counters * sizeof(uint32_t));
     w.group_stat = w.stat + cache_align(rows * sizeof(float2));
     w.part = w.group_stat + cache_align(rows * sizeof(float2));
     w.total = w.part + cache_align(rows * c.head_dim * sizeof(float));

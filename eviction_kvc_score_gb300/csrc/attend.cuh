@@ -40,6 +40,7 @@ struct AttendParams {
     void *out;
     float *lse;
     float scale_log2;    // scale * log2(e)
+    int skip_load;       // tests: every CTA's first load is left out
     uint32_t *status;
     Divider by_quads;    // dim / 4
     uint32_t *arrived;   // [grid][2][8], zero between calls: of a unit, of a group

@@ -517,7 +517,9 @@ int kvc_rope(int32_t dtype, int64_t n_tokens, int32_t n_q_heads, int32_t n_k_hea
 
 /* Bytes of workspace kvc_attend needs on the CURRENT device (0 if an argument
  * is invalid).  Initialise it once with kvc_workspace_init; read its status
- * word with kvc_workspace_status. */
+ * word with kvc_workspace_status.  The workspace is kvc_attend's alone (the
+ * scoring calls' scratch would overwrite its counters); one that is large
+ * enough serves calls of several caches and shapes, one after the other. */
 size_t kvc_attend_workspace_size(const kvc_cache *cache, int32_t n_q_heads, int32_t n_kv_heads,
                                  int32_t n_seqs, int32_t max_new);
 
@@ -540,7 +542,10 @@ size_t kvc_attend_workspace_size(const kvc_cache *cache, int32_t n_q_heads, int3
  * (KVC_DEV_BAD_LIST); a page outside the pool counts as rows of zeros
  * (KVC_DEV_BAD_PAGE).  Long lists are split over the GPU and joined in a fixed
  * order, so results do not vary from run to run.  q, out and the pools are
- * 16-byte aligned, q_stride a multiple of 8. */
+ * 16-byte aligned, q_stride a multiple of 8.  Device waits are bounded as in
+ * kvc_score; after KVC_DEV_TIMEOUT the workspace has to be initialised again
+ * (its counters of finished blocks are not at rest).  KVC_TEST_SKIP_ARRIVE=1
+ * (tests only) leaves loads out to exercise that. */
 int kvc_attend(const kvc_cache *cache, int32_t n_q_heads, int32_t n_kv_heads, int32_t n_seqs,
                int32_t max_new, int64_t n_tokens, const void *q, int64_t q_stride,
                const int32_t *q_start, const int32_t *table, const int32_t *len,

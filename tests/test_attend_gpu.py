@@ -243,6 +243,28 @@ def test_two_streams_with_workspaces_of_their_own():
     b.check()
 
 
+def test_one_workspace_serves_caches_of_several_kinds():
+    cases = [Case(ns=[5, 3], lens=[20000, 9000], hq=8, h=2, d=128, ps=64, dtype="bf16", seed=20),
+             Case(ns=[1, 2], lens=[9000, 700], hq=8, h=2, d=64, ps=64, dtype="f32", seed=21),
+             Case(ns=[40], lens=[3000], hq=8, h=1, d=80, ps=16, dtype="bf16", seed=22),
+             Case(ns=[300], lens=[3000], hq=8, h=1, d=64, ps=16, dtype="bf16", seed=23)]
+    ws = max((c.ws for c in cases), key=lambda w: w.numel())
+    for _ in range(2):
+        for c in cases:
+            c.ws = ws
+            c.run().check()
+
+
+def test_lists_that_share_pages():
+    """Forked lists: the same pages in several rows of the table."""
+    c = Case(ns=[1, 1, 1], lens=[500, 500, 500], hq=4, h=2, d=128, ps=64, dtype="bf16", seed=24)
+    c.table[2:4] = c.table[0:2]
+    c.table[4:6] = c.table[0:2]
+    c.q[1:] = c.q[0]
+    c.run().check()
+    assert torch.equal(c.out[1], c.out[0]) and torch.equal(c.out[2], c.out[0])
+
+
 def test_bad_pages_count_as_rows_of_zeros():
     for d, dtype in ((128, "bf16"), (64, "f32")):
         c = Case(ns=[1, 20], lens=[200, 100], hq=2, h=1, d=d, ps=16, dtype=dtype, seed=12)

@@ -26,13 +26,26 @@
 // to the rows that see them.
 //
 // Roles: warps 0-3 and 4-7 softmax of t = 0 and 1, a thread per row; warps 8
-// and 11 load; warps 9 and 10 issue the MMAs of t = 0 and 1 (one issuing thread spent
-// 4,300 clocks on the waits and MMAs of a step whose MMAs take 2,048).  TMEM: S_0 | S_1 | O_0 | O_1, 128 columns each.
-// Shared memory: two Q tiles and a ring of 5 (D = 128: 64 + 160 KB) or 12 tiles that
-// K and V pass through in the order the MMAs use them.  Every wait is
-// bounded and nothing waits on a barrier without a limit, so a wait that runs
-// out ends the kernel with KVC_DEV_TIMEOUT (the workspace then has to be
-// initialised again).
+// and 11 load, every other tile each (one warp takes 1,200 clocks to issue the
+// 16 boxes of a tile of 16-row pages); warps 9 and 10 issue the MMAs of t = 0
+// and 1 (one thread spent 4,300 clocks on the waits and MMAs of a step whose
+// MMAs take 2,048).  Warp 8 also walks the units and puts segments of them into
+// a queue for the others.  TMEM: S_0 | S_1 | O_0 | O_1, 128 columns each.  Shared
+// memory: two Q tiles and a ring of 5 (D = 128: 64 + 160 KB) or 12 tiles that K
+// and V pass through in the order the MMAs use them.  Every wait is bounded and
+// nothing waits on a barrier without a limit, so a wait that runs out ends the
+// kernel with KVC_DEV_TIMEOUT (the workspace then has to be initialised again).
+//
+// What bounds it, measured on one GB300:
+// - chunks: the chain S -> softmax -> P V of a half, 3,000 clocks for a step of two
+//   halves whose MMAs take 2,048 (128 x 128 x 16 in 64 clocks).  4,096 tokens x 32
+//   heads behind 28,672 cached rows: 1.25 ms on a cool GPU (1,650 TFLOP/s, 87% of
+//   the measured burst rate), 1.43-1.47 ms back to back, where the power limit
+//   holds the clock at about 1.7 GHz.
+// - decode: reading the cache.  64 sequences x 8 KV heads of 500-6,000 rows in
+//   16-row pages, 853 MB: 151 us, 5.6 TB/s or 83% of the measured copy rate.
+// - short calls: latency.  One sequence of 1,000 rows: 13.9 us, of which about 5
+//   up to the first MMA and 5 from the last to the joined output.
 #include <cstdlib>
 #include <type_traits>
 
@@ -55,6 +68,8 @@ constexpr int kBox = kTile * 128;       // bytes of 128 rows x 64 bf16
 constexpr uint32_t kColS = 0, kColO = 256;
 constexpr float kGrow = 8.f;            // log2 units m may lag behind
 constexpr int kSlotsTc = 2;
+// A unit costs about 4 steps beside its steps (12 lists of 60,000-130,000 rows: 68
+// us without, 63 with 4, 62 with 8; 512 short lists: 148, 150 and 152 us).
 constexpr int kExtra = 4;
 constexpr int kDirect = 4;              // shares that are joined from registers
 constexpr int kQueue = 4;               // segments on their way from the walk to the roles

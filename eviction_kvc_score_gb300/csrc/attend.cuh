@@ -204,9 +204,12 @@ __device__ __forceinline__ void attend_store_lse(const AttendParams &p, int64_t 
 
 // A warp's rows of a slot are written: count it.  True, in the whole warp, if it
 // is the last of `all`; then every other's rows are visible to it.  The counter
-// is back at zero after that.
+// is back at zero after that.  One alone is not counted: a group of one CTA,
+// its unit's last, shares its counter with the group that the next unit may begin
+// in that CTA, and the others of that one may have counted already.
 __device__ __forceinline__ bool attend_last(uint32_t *count, uint32_t all) {
     __syncwarp();
+    if (all == 1) return true;
     uint32_t before = 0;
     if ((threadIdx.x & 31) == 0) {
         asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(count) : "memory");

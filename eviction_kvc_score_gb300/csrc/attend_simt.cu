@@ -108,10 +108,11 @@ __device__ __forceinline__ void copies_wait() {
 }
 
 // The block's rows of a slot are written: count it; true in the whole block if it
-// is the last of `all`.
+// is the last of `all` (one alone is not counted, as in attend_last).
 __device__ __forceinline__ bool block_last(uint32_t *count, uint32_t all, uint32_t *s_last) {
     __threadfence();
     __syncthreads();
+    if (all == 1) return true;
     if (threadIdx.x == 0) {
         const bool last = atomicAdd(count, 1u) == all - 1;
         if (last) *count = 0;

@@ -231,6 +231,22 @@ def test_same_bits_again_and_from_a_graph(dtype, case):
     c.check()
 
 
+@pytest.mark.parametrize("dtype,d,hq", [("f32", 64, 2), ("bf16", 64, 2), ("bf16", 128, 40), ("bf16", 96, 2)])
+def test_neighbouring_lists_that_fill_the_gpu(dtype, d, hq):
+    """Two long lists share one block of the launch, at every place of its work: the joins of
+    the first list's end and of the second one's beginning do not meet."""
+    c = Case(ns=[1, 1], lens=[40000, 40000], hq=hq, h=1, d=d, ps=128, dtype=dtype, seed=8)
+    for cut in range(0, 12000, 192):
+        c.lens = [40000 - cut, 40000]
+        c.len.copy_(torch.tensor(c.lens, dtype=torch.int32))
+        for again in range(4):
+            c.out.fill_(7)
+            c.run()
+            out = c.out.clone() if again == 0 else out
+            assert torch.equal(c.out, out), (cut, again)
+        c.check()
+
+
 def test_two_streams_with_workspaces_of_their_own():
     a = Case(ns=[5, 3], lens=[20000, 9000], hq=8, h=2, d=128, ps=64, dtype="bf16", seed=10)
     b = Case(ns=[200], lens=[3000], hq=8, h=2, d=64, ps=16, dtype="bf16", seed=11)

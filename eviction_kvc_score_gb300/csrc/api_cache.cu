@@ -47,8 +47,9 @@ bool cache_ok(const kvc_cache *c, const char *fn) {
         return fail(0, "%s: head_dim must be a multiple of 8 in 8..256", fn), false;
     if (c->dtype != KVC_F32 && c->dtype != KVC_BF16)
         return fail(0, "%s: unknown dtype %d", fn, c->dtype), false;
-    if (c->max_pages < 1 || (int64_t)c->max_pages * c->page_rows >= ((int64_t)1 << 31))
-        return fail(0, "%s: max_pages must be >= 1 and max_pages * page_rows < 2^31", fn), false;
+    // 256 short of 2^31, so that the end of a list's last step is still an int
+    if (c->max_pages < 1 || (int64_t)c->max_pages * c->page_rows > ((int64_t)1 << 31) - 256)
+        return fail(0, "%s: max_pages must be >= 1 and max_pages * page_rows <= 2^31 - 256", fn), false;
     return true;
 }
 
@@ -168,8 +169,10 @@ int kvc_pages_append(const kvc_cache *cache, int32_t *table, int32_t *len, int32
     PagesState s;
     const int rc = state_of(*cache, n_lists, state, state_bytes, "kvc_pages_append", &s);
     if (rc) return rc;
+    const int sms = device_sms();
+    if (sms == 0) return fail(KVC_ERR_CUDA, "kvc_pages_append: no usable CUDA device");
     return launch_pages_append(*cache, s, table, len, n_lists, counts, src_row, src_step, k_src, v_src,
-                               src_rows, k_pool, v_pool, device_sms(), stream);
+                               src_rows, k_pool, v_pool, sms, stream);
 }
 
 int kvc_pages_fork(const kvc_cache *cache, int32_t *table, int32_t *len, int32_t n_lists,
@@ -199,8 +202,10 @@ int kvc_pages_compact(const kvc_cache *cache, int32_t *table, int32_t *len, int3
     PagesState s;
     const int rc = state_of(*cache, n_lists, state, state_bytes, "kvc_pages_compact", &s);
     if (rc) return rc;
-    return launch_pages_compact(*cache, s, table, len, n_lists, idx, k_max, counts, k_pool, v_pool,
-                                device_sms(), stream);
+    const int sms = device_sms();
+    if (sms == 0) return fail(KVC_ERR_CUDA, "kvc_pages_compact: no usable CUDA device");
+    return launch_pages_compact(*cache, s, table, len, n_lists, idx, k_max, counts, k_pool, v_pool, sms,
+                                stream);
 }
 
 int kvc_pages_truncate(const kvc_cache *cache, int32_t *table, int32_t *len, int32_t n_lists,
@@ -275,7 +280,9 @@ int kvc_rope(int32_t dtype, int64_t n_tokens, int32_t n_q_heads, int32_t n_k_hea
     }
     const RopeArgs a{dtype, n_tokens, n_q_heads, n_k_heads, head_dim, rot_dim, flags, amplitude, positions,
                      table, q, k, q_out, k_out, q_stride, q_out_stride, k_stride, k_out_stride};
-    return launch_rope(a, device_sms(), stream);
+    const int sms = device_sms();
+    if (sms == 0) return fail(KVC_ERR_CUDA, "kvc_rope: no usable CUDA device");
+    return launch_rope(a, sms, stream);
 }
 
 size_t kvc_attend_workspace_size(const kvc_cache *cache, int32_t n_q_heads, int32_t n_kv_heads,
@@ -305,7 +312,8 @@ int kvc_attend(const kvc_cache *cache, int32_t n_q_heads, int32_t n_kv_heads, in
     if (q_stride < (int64_t)n_q_heads * c.head_dim || q_stride % 8 || q_stride > ((int64_t)1 << 38))
         return fail(KVC_ERR_INVALID_ARG,
                     "kvc_attend: q_stride must be a multiple of 8 and >= n_q_heads * head_dim");
-    if (!std::isfinite(scale)) return fail(KVC_ERR_INVALID_ARG, "kvc_attend: scale must be finite");
+    if (!std::isfinite((float)(scale * kLog2e)))
+        return fail(KVC_ERR_INVALID_ARG, "kvc_attend: scale must be finite (times log2 e, too)");
     const AttendWs w = attend_ws(c, n_q_heads / n_kv_heads);
     if (w.needs.grid == 0) return fail(KVC_ERR_CUDA, "kvc_attend: no usable CUDA device");
     if (!ws) return fail(KVC_ERR_WORKSPACE, "kvc_attend: workspace is NULL");

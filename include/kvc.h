@@ -424,7 +424,7 @@ typedef struct {
     int32_t head_dim;   /* D: a multiple of 8, 8..256 */
     int32_t dtype;      /* kvc_dtype of the rows */
     int32_t max_pages;  /* entries of one page-table row, >= 1; max_pages *
-                           page_rows < 2^31 */
+                           page_rows <= 2^31 - 256 */
 } kvc_cache;
 
 /* Bytes of state for `cache` and calls of up to n_lists lists (0 if either is
@@ -541,8 +541,10 @@ size_t kvc_attend_workspace_size(const kvc_cache *cache, int32_t n_q_heads, int3
  * in fp32.  Lengths and q_start out of range are cut to it
  * (KVC_DEV_BAD_LIST); a page outside the pool counts as rows of zeros
  * (KVC_DEV_BAD_PAGE).  Long lists are split over the GPU and joined in a fixed
- * order, so results do not vary from run to run.  q, out and the pools are
- * 16-byte aligned, q_stride a multiple of 8.  Device waits are bounded as in
+ * order, so results do not vary from run to run.  Sequences without tokens and
+ * lists without rows may stand anywhere.  q, out and the pools are 16-byte
+ * aligned, q_stride a multiple of 8; out and lse overlap no input; scale and
+ * scale log2 e are finite (scale may be 0 or negative).  Device waits are bounded as in
  * kvc_score; after KVC_DEV_TIMEOUT the workspace has to be initialised again
  * (its counters of finished blocks are not at rest).  KVC_TEST_SKIP_ARRIVE=1
  * (tests only) leaves loads out to exercise that. */

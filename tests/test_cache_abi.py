@@ -19,7 +19,8 @@ def kvc():
 
 GOOD = dict(n_pages=64, page_rows=16, head_dim=64, max_pages=8, dtype="bf16")
 BAD = [dict(n_pages=0), dict(n_pages=(1 << 30) + 1), dict(page_rows=8), dict(page_rows=48), dict(head_dim=4),
-       dict(head_dim=68), dict(head_dim=264), dict(max_pages=0), dict(max_pages=1 << 27), dict(dtype=7)]
+       dict(head_dim=68), dict(head_dim=264), dict(max_pages=0), dict(max_pages=1 << 27),
+       dict(max_pages=(1 << 27) - 15), dict(dtype=7)]
 
 
 def make(kvc, **kw):
@@ -94,10 +95,27 @@ def test_attend_arguments(kvc):
         return L.kvc_attend(p, hq, h, b, m, n, q, qs, start, FAKE, FAKE, k, FAKE, scale, out, NUL, ws, size, NUL)
     for bad in (dict(hq=7), dict(h=0), dict(hq=0), dict(b=0), dict(b=1 << 20), dict(m=0), dict(m=1 << 29), dict(n=-1), dict(n=1 << 31),
                 dict(q=NUL), dict(q=ODD), dict(qs=504), dict(qs=513), dict(start=NUL), dict(k=ODD), dict(out=NUL),
-                dict(scale=math.inf), dict(scale=math.nan)):
+                dict(scale=math.inf), dict(scale=math.nan), dict(scale=3e38)):
         assert attend(**bad) == -1, bad
     assert L.kvc_attend_workspace_size(p, 8, 3, 1, 1) == 0
     assert L.kvc_attend_workspace_size(p, 8, 2, 0, 1) == 0
+
+
+def test_without_a_device_calls_end_with_an_error(kvc):
+    if torch.cuda.is_available():
+        pytest.skip("needs a machine without a GPU")
+    L, c = kvc._lib, make(kvc, max_pages=(1 << 27) - 16)
+    p, st = C.byref(c), 1 << 40
+    assert L.kvc_rope_table(64, 1e4, 1.0, 1.0, 4.0, 100.0, FAKE, NUL) == -3
+    assert L.kvc_rope(1, 4, 2, 1, 64, 64, 0, 1.0, FAKE, FAKE, FAKE, 128, FAKE, 128, FAKE, 64, FAKE, 64, NUL) == -3
+    assert L.kvc_pages_init(p, FAKE, st, NUL) == -3
+    assert L.kvc_pages_status(p, FAKE, st, None, None, NUL) == -3
+    assert L.kvc_pages_append(p, FAKE, FAKE, 4, FAKE, FAKE, 1, FAKE, FAKE, 9, FAKE, FAKE, FAKE, st, NUL) == -3
+    assert L.kvc_pages_fork(p, FAKE, FAKE, 4, FAKE, FAKE, st, NUL) == -3
+    assert L.kvc_pages_compact(p, FAKE, FAKE, 4, FAKE, 3, FAKE, FAKE, FAKE, FAKE, st, NUL) == -3
+    assert L.kvc_pages_truncate(p, FAKE, FAKE, 4, FAKE, FAKE, st, NUL) == -3
+    assert L.kvc_attend(p, 8, 2, 1, 1, 1, FAKE, 512, FAKE, FAKE, FAKE, FAKE, FAKE, 1.0, FAKE, NUL, FAKE, st, NUL) == -3
+    assert "kvc_attend" in kvc.kvc_last_error()
 
 
 def test_binding_refuses_wrong_tensors(kvc):

@@ -14,6 +14,7 @@
 // the order of finishing.
 #pragma once
 
+#include <algorithm>
 #include <climits>
 
 #include "cache.cuh"
@@ -31,6 +32,7 @@ struct AttendParams {
     int n_units;
     int step_keys;       // keys per step ...
     int split_rows;      // ... twice as many for units of at most so many rows
+    int rows_above, rows_upto;   // lists of so many rows are this launch's
     int extra;           // steps' worth of a unit's beginning and end
     int slots;           // slots per CTA
     int slot_rows;       // row capacity of a slot
@@ -69,6 +71,8 @@ __device__ __forceinline__ AttendRaw attend_raw(const AttendParams &p, int u) {
     return AttendRaw{p.q_start[b], p.q_start[b + 1], p.len[list]};
 }
 
+// kSome: the launch has only lists of so many rows.
+template <bool kSome>
 __device__ __forceinline__ AttendUnit attend_unit(const AttendParams &p, int u, const AttendRaw &raw) {
     AttendUnit a;
     a.list = p.by_blocks(u);
@@ -86,6 +90,7 @@ __device__ __forceinline__ AttendUnit attend_unit(const AttendParams &p, int u, 
     }
     a.q0 = q0;
     a.n = max(0, q1 - q0);
+    if (kSome && (a.n * p.group <= p.rows_above || a.n * p.group > p.rows_upto)) a.n = 0;
     a.row0 = block * p.unit_rows;
     a.rows = min(p.unit_rows, a.n * p.group - a.row0);
     a.hi = a.rows <= 0 ? 0 : max(0, a.len - a.n + p.by_group(a.row0 + a.rows - 1) + 1);
@@ -95,8 +100,28 @@ __device__ __forceinline__ AttendUnit attend_unit(const AttendParams &p, int u, 
     return a;
 }
 
+template <bool kSome>
 __device__ __forceinline__ AttendUnit attend_unit(const AttendParams &p, int u) {
-    return attend_unit(p, u, attend_raw(p, u));
+    return attend_unit<kSome>(p, u, attend_raw(p, u));
+}
+
+// The unit behind u; blocks behind a sequence's last row are passed over.
+__device__ __forceinline__ int attend_next(const AttendParams &p, const AttendUnit &a, int u) {
+    return a.steps == 0 || a.row0 + a.rows >= a.n * p.group ? (a.list + 1) * p.blocks : u + 1;
+}
+
+// The first unit behind sequence b that somebody has to work on, or n_units: 32
+// sequences are looked at together, so that a batch whose places are mostly empty
+// is not walked one latency after the other.  The whole warp asks for one b.
+template <bool kSome>
+__device__ __noinline__ int attend_next_seq(const AttendParams &p, int b) {
+    const int lists = p.n_kv_heads * p.blocks;
+    for (++b; b < p.n_seqs; b += 32) {
+        const int i = b + (threadIdx.x & 31);
+        const unsigned has = __ballot_sync(0xffffffffu, i < p.n_seqs && attend_unit<kSome>(p, i * lists).steps > 0);
+        if (has) return (b + __ffs(has) - 1) * lists;
+    }
+    return p.n_units;
 }
 
 // Cached rows that row r of the unit sees.
@@ -141,13 +166,17 @@ __device__ __forceinline__ int attend_cta_of(int64_t total, int grid, int64_t x)
 }
 
 // Every thread of a block of NT threads calls it; scratch: NT / 32 + 4 int64.
-template <int NT>
+template <int NT, bool kSome>
 __device__ AttendRun attend_plan(const AttendParams &p, int64_t *scratch) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int per = p.n_units / NT + 1;
     const int u0 = (int)min((int64_t)p.n_units, (int64_t)per * threadIdx.x), u1 = min(p.n_units - u0, per) + u0;
     int64_t mine = 0;
-    for (int u = u0; u < u1; ++u) mine += attend_unit(p, u).cost;
+    for (int u = u0; u < u1;) {
+        const AttendUnit a = attend_unit<kSome>(p, u);
+        mine += a.cost;
+        u = attend_next(p, a, u);
+    }
     int64_t x = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -171,17 +200,18 @@ __device__ AttendRun attend_plan(const AttendParams &p, int64_t *scratch) {
     r.hi = works ? attend_cut(total, r.grid, blockIdx.x + 1) : 0;
     int64_t at = before + x - mine;
     if (works && r.lo >= at && r.lo < at + mine) {
-        for (int u = u0; u < u1; ++u) {
+        for (int u = u0; u < u1;) {
             const AttendRaw raw = attend_raw(p, u);
-            const int s = attend_unit(p, u, raw).cost;
-            if (r.lo < at + s) {
+            const AttendUnit a = attend_unit<kSome>(p, u, raw);
+            if (r.lo < at + a.cost) {
                 found[0] = u;
                 found[1] = at;
                 found[2] = (int64_t)((uint64_t)(uint32_t)raw.q0 << 32 | (uint32_t)raw.q1);
                 found[3] = raw.len;
                 break;
             }
-            at += s;
+            at += a.cost;
+            u = attend_next(p, a, u);
         }
     }
     __syncthreads();
@@ -189,11 +219,6 @@ __device__ AttendRun attend_plan(const AttendParams &p, int64_t *scratch) {
     r.unit_lo = works ? found[1] : 0;
     r.raw = works ? AttendRaw{(int)(found[2] >> 32), (int)(uint32_t)found[2], (int)found[3]} : AttendRaw{0, 0, 0};
     return r;
-}
-
-// The unit behind u; blocks behind a sequence's last row are passed over.
-__device__ __forceinline__ int attend_next(const AttendParams &p, const AttendUnit &a, int u) {
-    return a.steps == 0 || a.row0 + a.rows >= a.n * p.group ? (a.list + 1) * p.blocks : u + 1;
 }
 
 // ln of the row's sum = ln 2 (m + log2 l).
@@ -352,10 +377,13 @@ struct AttendNeeds {
 AttendNeeds attend_simt_needs(int sms);
 AttendNeeds attend_tc_needs(int sms);
 bool attend_tc_takes(int dtype, int dim, int group);
-// The units' shape: blocks of unit_rows rows.  False if there are too many.
-inline bool attend_units(AttendParams &p, int unit_rows) {
+// The units' shape: blocks of unit_rows rows, of lists that have more than
+// rows_above and at most rows_upto.  False if there are too many.
+inline bool attend_units(AttendParams &p, int unit_rows, int rows_above, int rows_upto) {
     p.unit_rows = unit_rows;
-    p.blocks = (p.max_new * p.group + unit_rows - 1) / unit_rows;
+    p.rows_above = rows_above;
+    p.rows_upto = rows_upto;
+    p.blocks = (std::min(p.max_new * p.group, rows_upto) + unit_rows - 1) / unit_rows;
     const int64_t n = (int64_t)p.n_seqs * p.n_kv_heads * p.blocks;
     p.n_units = (int)n;
     p.by_group = Divider((uint32_t)p.group);

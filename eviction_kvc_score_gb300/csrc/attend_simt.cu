@@ -144,14 +144,14 @@ __global__ void __launch_bounds__(threads_of(ROWS), ROWS == 64 ? 2 : 4) attend_s
 
     let_next_start();
     wait_for_inputs();
-    const AttendRun run = attend_plan<kThreads>(p, plan);
+    const AttendRun run = attend_plan<kThreads, true>(p, plan);
     if (run.lo >= run.hi) return;
     int u = run.unit;
     int64_t u_lo = run.unit_lo;
     for (int64_t pos = run.lo; pos < run.hi;) {
-        const AttendUnit a = attend_unit(p, u);
+        const AttendUnit a = attend_unit<true>(p, u);
         if (a.steps == 0) {
-            u = attend_next(p, a, u);
+            u = attend_next_seq<true>(p, a.b);
             continue;
         }
         const int64_t end = min(run.hi, u_lo + a.steps);
@@ -396,17 +396,28 @@ int launch_type(AttendParams &p, int rows, int sms, cudaStream_t st) {
 AttendNeeds attend_simt_needs(int sms) { return {kBlocksPerSm * sms, 2, kSlotRows}; }
 
 int launch_attend_simt(AttendParams &p, bool f32, int grid, cudaStream_t st) {
-    // 16 rows per block where a list's tokens fill no more
-    const int rows = p.max_new * p.group <= 16 ? 16 : 64;
-    if (!attend_units(p, rows)) {
-        set_error("kvc_attend: n_seqs * n_kv_heads * max_new is too large");
-        return KVC_ERR_UNSUPPORTED;
-    }
     p.step_keys = kKeys;
     p.split_rows = 0;
     p.extra = 0;
     const int sms = grid / kBlocksPerSm;
-    return f32 ? launch_type<float>(p, rows, sms, st) : launch_type<__nv_bfloat16>(p, rows, sms, st);
+    // Blocks of 64 rows, of 16 where no list has more.  Lists of both kinds take a
+    // launch each: in a block of 64 rows one warp of eight would work on a token's
+    // (a chunk of 256 tokens and 255 decoding sequences of 1,000 rows, fp32, 8 KV
+    // heads of 128: 2,512 us in one launch, 1,097 in two).  A launch that finds no
+    // list costs 6 us, so one does where the lists have more than 128 rows on
+    // average: the short ones are then at most a third of the blocks.
+    const int64_t most = (int64_t)p.max_new * p.group;
+    const bool both = most > 16 && p.group <= 16 && p.n_tokens * p.group <= 128 * (int64_t)p.n_seqs;
+    for (int rows = most > 16 ? 64 : 16; rows >= 16; rows -= both ? 48 : rows) {
+        const bool large = rows == 64;
+        if (!attend_units(p, rows, large && both ? 16 : 0, large ? INT_MAX : 16)) {
+            set_error("kvc_attend: n_seqs * n_kv_heads * max_new is too large");
+            return KVC_ERR_UNSUPPORTED;
+        }
+        const int rc = f32 ? launch_type<float>(p, rows, sms, st) : launch_type<__nv_bfloat16>(p, rows, sms, st);
+        if (rc) return rc;
+    }
+    return KVC_OK;
 }
 
 }  // namespace kvc

@@ -249,7 +249,7 @@ struct Walk {
     __device__ void next(const AttendParams &p, Work &w) {
         w.none = true;
         while (w.none && pos < run.hi) {
-            w.a = attend_unit(p, u, raw);
+            w.a = attend_unit<false>(p, u, raw);
             if (w.a.steps > 0) {
                 const int64_t end = min(run.hi, u_lo + w.a.cost);
                 const int s0 = max(0, (int)(pos - u_lo) - p.extra), s1 = max(0, (int)(end - u_lo) - p.extra);
@@ -262,7 +262,7 @@ struct Walk {
                 pos = end;
                 u_lo += w.a.cost;
             }
-            u = attend_next(p, w.a, u);
+            u = w.a.steps > 0 ? attend_next(p, w.a, u) : attend_next_seq<false>(p, w.a.b);
             raw = attend_raw(p, u);
         }
     }
@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     let_next_start();
     wait_for_inputs();
-    const AttendRun run = attend_plan<kThreads>(p, b.plan);
+    const AttendRun run = attend_plan<kThreads, false>(p, b.plan);
     if (run.lo >= run.hi) return;   // more CTAs than steps
     if (warp == kMmaWarp) {
         tmem_alloc(&b.tmem, 512);
@@ -991,7 +991,7 @@ int launch_attend_tc(AttendParams &p, int grid, cudaStream_t st) {
     p.split_rows = R;
     p.step_keys = kTile;
     p.extra = kExtra;
-    if (!attend_units(p, 2 * R)) {
+    if (!attend_units(p, 2 * R, 0, INT_MAX)) {
         set_error("kvc_attend: n_seqs * n_kv_heads * max_new is too large");
         return KVC_ERR_UNSUPPORTED;
     }

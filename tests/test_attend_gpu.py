@@ -147,6 +147,24 @@ def test_matches_the_definition(i, dtype):
     Case(**c, dtype=dtype, seed=i, gap=8 * (i % 3), behind=i % 2 * 3).run().check()
 
 
+@pytest.mark.parametrize("dtype,d,hq,h", [("f32", 64, 8, 2), ("f32", 80, 17, 1), ("bf16", 64, 8, 2), ("bf16", 128, 8, 2),
+                                          ("bf16", 96, 6, 2)])
+@pytest.mark.parametrize("ns", [[40, 1, 0, 3, 1, 17], [1, 1, 130, 5, 1], [4, 0, 5, 300]])
+def test_chunks_and_single_tokens_in_one_call(dtype, d, hq, h, ns):
+    lens = [900, 333, 60, 77, 1, 450][:len(ns)]
+    Case(ns=ns, lens=lens, hq=hq, h=h, d=d, ps=32, dtype=dtype, seed=len(ns)).run().check()
+
+
+@pytest.mark.parametrize("dtype,d", [("f32", 64), ("bf16", 64), ("bf16", 128)])
+@pytest.mark.parametrize("places,n", [(33, 1), (700, 1), (700, 20)])
+def test_batches_whose_places_are_mostly_empty(dtype, d, places, n):
+    """Few sequences have tokens; the others' lists are empty or keep their rows."""
+    ns, lens = [0] * places, [(0, 40)[i % 2] for i in range(places)]
+    for i in (1, places // 2, places - 1):
+        ns[i], lens[i] = n, 300 + i % 7
+    Case(ns=ns, lens=lens, hq=4, h=2, d=d, ps=16, dtype=dtype, seed=places).run().check()
+
+
 @pytest.mark.parametrize("dtype,d", [("f32", 64), ("bf16", 64), ("bf16", 128), ("bf16", 80)])
 @pytest.mark.parametrize("junk", [math.nan, math.inf, -math.inf])
 def test_rows_that_a_token_does_not_see_may_hold_anything(dtype, d, junk):

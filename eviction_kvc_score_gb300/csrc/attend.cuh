@@ -165,53 +165,168 @@ __device__ __forceinline__ int attend_cta_of(int64_t total, int grid, int64_t x)
     return (int)(((x + 1) * grid - 1) / total);
 }
 
-// Every thread of a block of NT threads calls it; scratch: NT / 32 + 4 int64.
-template <int NT, bool kSome>
-__device__ AttendRun attend_plan(const AttendParams &p, int64_t *scratch) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int per = p.n_units / NT + 1;
-    const int u0 = (int)min((int64_t)p.n_units, (int64_t)per * threadIdx.x), u1 = min(p.n_units - u0, per) + u0;
-    int64_t mine = 0;
-    for (int u = u0; u < u1;) {
-        const AttendUnit a = attend_unit<kSome>(p, u);
-        mine += a.cost;
-        u = attend_next(p, a, u);
-    }
-    int64_t x = mine;
+// The sum over a warp, in every lane.
+__device__ __forceinline__ int64_t attend_warp_sum(int64_t x) {
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+    return x;
+}
+// The sum over a warp's lanes up to this one.
+__device__ __forceinline__ int64_t attend_warp_scan(int64_t x) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
         const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
         if (lane >= d) x += y;
     }
-    if (lane == 31) scratch[warp] = x;
+    return x;
+}
+__device__ __forceinline__ AttendRaw attend_raw_of(const AttendRaw &raw, int lane) {
+    return AttendRaw{__shfl_sync(0xffffffffu, raw.q0, lane), __shfl_sync(0xffffffffu, raw.q1, lane),
+                     __shfl_sync(0xffffffffu, raw.len, lane)};
+}
+
+// The cost of the lane's list (0 where !real); a list of several units is added
+// up by the whole warp.
+template <bool kSome>
+__device__ __forceinline__ int64_t attend_list_cost(const AttendParams &p, int list, bool real, AttendRaw *raw) {
+    const int lane = threadIdx.x & 31;
+    *raw = attend_raw(p, real ? list * p.blocks : p.n_units);
+    int64_t cost = 0;
+    int rows = 0;
+    if (real) {
+        const AttendUnit a = attend_unit<kSome>(p, list * p.blocks, *raw);
+        cost = a.cost;
+        rows = a.n * p.group;
+    }
+    for (unsigned left = __ballot_sync(0xffffffffu, rows > p.unit_rows); left; left &= left - 1) {
+        const int of = __ffs(left) - 1, u0 = __shfl_sync(0xffffffffu, list, of) * p.blocks;
+        const int all = __shfl_sync(0xffffffffu, rows, of);
+        const AttendRaw r = attend_raw_of(*raw, of);
+        int64_t sum = 0;
+        for (int i = lane; i < p.blocks && (int64_t)i * p.unit_rows < all; i += 32)
+            sum += attend_unit<kSome>(p, u0 + i, r).cost;
+        sum = attend_warp_sum(sum);
+        if (lane == of) cost = sum;
+    }
+    return cost;
+}
+
+// The run without its unit.
+__device__ __forceinline__ bool attend_run(int64_t total, AttendRun *r) {
+    r->total = total;
+    r->grid = (int)min((int64_t)gridDim.x, total);
+    const bool works = (int)blockIdx.x < r->grid;
+    r->lo = works ? attend_cut(total, r->grid, blockIdx.x) : 0;
+    r->hi = works ? attend_cut(total, r->grid, blockIdx.x + 1) : 0;
+    return works;
+}
+
+// The plan by lists: each warp adds up a stretch of them; the one whose stretch the
+// CTA's run begins in looks for the unit, 32 lists and then 32 units at a time.  The total.
+template <int NT, bool kSome>
+__device__ __noinline__ int64_t attend_plan_lists(const AttendParams &p, int64_t *scratch) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lists = p.n_seqs * p.n_kv_heads, per = (lists + NT / 32 - 1) / (NT / 32);
+    const int l0 = min(lists, warp * per), l1 = min(lists, l0 + per);
+    AttendRaw raw;
+    int64_t mine = 0;
+    for (int l = l0; l < l1; l += 32) mine += attend_list_cost<kSome>(p, l + lane, l + lane < l1, &raw);
+    mine = attend_warp_sum(mine);
+    if (lane == 0) scratch[warp] = mine;
     __syncthreads();
-    int64_t before = 0, total = 0;
+    int64_t at = 0, total = 0;
 #pragma unroll
     for (int w = 0; w < NT / 32; ++w) {
-        if (w < warp) before += scratch[w];
+        if (w < warp) at += scratch[w];
         total += scratch[w];
     }
     int64_t *found = scratch + NT / 32;
     AttendRun r;
-    r.total = total;
-    r.grid = (int)min((int64_t)gridDim.x, total);
-    const bool works = (int)blockIdx.x < r.grid;
-    r.lo = works ? attend_cut(total, r.grid, blockIdx.x) : 0;
-    r.hi = works ? attend_cut(total, r.grid, blockIdx.x + 1) : 0;
-    int64_t at = before + x - mine;
+    const bool works = attend_run(total, &r);
     if (works && r.lo >= at && r.lo < at + mine) {
-        for (int u = u0; u < u1;) {
-            const AttendRaw raw = attend_raw(p, u);
-            const AttendUnit a = attend_unit<kSome>(p, u, raw);
-            if (r.lo < at + a.cost) {
-                found[0] = u;
-                found[1] = at;
-                found[2] = (int64_t)((uint64_t)(uint32_t)raw.q0 << 32 | (uint32_t)raw.q1);
-                found[3] = raw.len;
+        for (int l = l0; l < l1; l += 32) {
+            const int64_t cost = attend_list_cost<kSome>(p, l + lane, l + lane < l1, &raw);
+            const int64_t end = at + attend_warp_scan(cost);
+            const unsigned past = __ballot_sync(0xffffffffu, r.lo < end);
+            if (past == 0) {
+                at = __shfl_sync(0xffffffffu, end, 31);
+                continue;
+            }
+            const int of = __ffs(past) - 1;
+            at = __shfl_sync(0xffffffffu, end - cost, of);
+            raw = attend_raw_of(raw, of);
+            for (int i = 0; i < p.blocks; i += 32) {
+                const int u = (l + of) * p.blocks + i + lane;
+                const int64_t c = i + lane < p.blocks ? attend_unit<kSome>(p, u, raw).cost : 0;
+                const int64_t until = at + attend_warp_scan(c);
+                const unsigned beyond = __ballot_sync(0xffffffffu, r.lo < until);
+                if (beyond == 0) {
+                    at = __shfl_sync(0xffffffffu, until, 31);
+                    continue;
+                }
+                if (lane == __ffs(beyond) - 1) {
+                    found[0] = u;
+                    found[1] = until - c;
+                    found[2] = (int64_t)((uint64_t)(uint32_t)raw.q0 << 32 | (uint32_t)raw.q1);
+                    found[3] = raw.len;
+                }
                 break;
             }
-            at += a.cost;
+            break;
+        }
+    }
+    return total;
+}
+
+// Every thread of a block of NT threads calls it; scratch: NT / 32 + 4 int64.
+// By units: each thread adds up a stretch of them.  Where lists of several units
+// make more than four per thread, by lists: a chunk's units would be one thread's
+// (2,048 tokens and 255 decoding sequences, 64K units of which 2,300 have work:
+// 362 us by units, 294 by lists; with one unit a list or few units the plan by
+// lists takes 1 us longer).
+template <int NT, bool kSome>
+__device__ AttendRun attend_plan(const AttendParams &p, int64_t *scratch) {
+    int64_t *found = scratch + NT / 32;
+    AttendRun r;
+    bool works;
+    if (p.blocks > 1 && p.n_units > 4 * NT) {
+        works = attend_run(attend_plan_lists<NT, kSome>(p, scratch), &r);
+    } else {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        const int per = p.n_units / NT + 1;
+        const int u0 = (int)min((int64_t)p.n_units, (int64_t)per * threadIdx.x), u1 = min(p.n_units - u0, per) + u0;
+        int64_t mine = 0;
+        for (int u = u0; u < u1;) {
+            const AttendUnit a = attend_unit<kSome>(p, u);
+            mine += a.cost;
             u = attend_next(p, a, u);
+        }
+        const int64_t x = attend_warp_scan(mine);
+        if (lane == 31) scratch[warp] = x;
+        __syncthreads();
+        int64_t before = 0, total = 0;
+#pragma unroll
+        for (int w = 0; w < NT / 32; ++w) {
+            if (w < warp) before += scratch[w];
+            total += scratch[w];
+        }
+        works = attend_run(total, &r);
+        int64_t at = before + x - mine;
+        if (works && r.lo >= at && r.lo < at + mine) {
+            for (int u = u0; u < u1;) {
+                const AttendRaw raw = attend_raw(p, u);
+                const AttendUnit a = attend_unit<kSome>(p, u, raw);
+                if (r.lo < at + a.cost) {
+                    found[0] = u;
+                    found[1] = at;
+                    found[2] = (int64_t)((uint64_t)(uint32_t)raw.q0 << 32 | (uint32_t)raw.q1);
+                    found[3] = raw.len;
+                    break;
+                }
+                at += a.cost;
+                u = attend_next(p, a, u);
+            }
         }
     }
     __syncthreads();

@@ -155,6 +155,13 @@ def test_chunks_and_single_tokens_in_one_call(dtype, d, hq, h, ns):
     Case(ns=ns, lens=lens, hq=hq, h=h, d=d, ps=32, dtype=dtype, seed=len(ns)).run().check()
 
 
+@pytest.mark.parametrize("dtype,d", [("f32", 64), ("bf16", 64), ("bf16", 128), ("bf16", 80)])
+@pytest.mark.parametrize("ns", [[300] + [1] * 200 + [0] * 40 + [70, 2], [1, 0] * 60 + [1100] + [130, 0, 3] * 20])
+def test_large_batches_of_chunks_and_single_tokens(dtype, d, ns):
+    lens = [n + (37 * i % 700) * (n > 0 or i % 3 == 0) for i, n in enumerate(ns)]
+    Case(ns=ns, lens=lens, hq=8, h=2, d=d, ps=32, dtype=dtype, seed=3).run().check()
+
+
 @pytest.mark.parametrize("dtype,d", [("f32", 64), ("bf16", 64), ("bf16", 128)])
 @pytest.mark.parametrize("places,n", [(33, 1), (700, 1), (700, 20)])
 def test_batches_whose_places_are_mostly_empty(dtype, d, places, n):

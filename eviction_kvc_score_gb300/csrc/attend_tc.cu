@@ -44,7 +44,7 @@
 //   holds the clock at about 1.7 GHz.
 // - decode: reading the cache.  64 sequences x 8 KV heads of 500-6,000 rows in
 //   16-row pages, 853 MB: 151 us, 5.6 TB/s or 83% of the measured copy rate.
-// - short calls: latency.  One sequence of 1,000 rows: 13.9 us, of which about 5
+// - short calls: latency.  One sequence of 1,000 rows: 14.5 us, of which about 5
 //   up to the first MMA and 5 from the last to the joined output.
 #include <cstdlib>
 #include <type_traits>

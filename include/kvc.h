@@ -544,10 +544,10 @@ size_t kvc_attend_workspace_size(const kvc_cache *cache, int32_t n_q_heads, int3
  * order, so results do not vary from run to run.  Sequences without tokens and
  * lists without rows may stand anywhere.  q, out and the pools are 16-byte
  * aligned, q_stride a multiple of 8; out and lse overlap no input; scale and
- * scale log2 e are finite (scale may be 0 or negative).  Device waits are bounded as in
- * kvc_score; after KVC_DEV_TIMEOUT the workspace has to be initialised again
- * (its counters of finished blocks are not at rest).  KVC_TEST_SKIP_ARRIVE=1
- * (tests only) leaves loads out to exercise that. */
+ * scale log2 e are finite (scale may be 0 or negative).  Device waits are
+ * bounded as in kvc_score; after KVC_DEV_TIMEOUT the workspace has to be
+ * initialised again (its counters of finished blocks are not at rest).
+ * KVC_TEST_SKIP_ARRIVE=1 (tests only) leaves loads out to exercise that. */
 int kvc_attend(const kvc_cache *cache, int32_t n_q_heads, int32_t n_kv_heads, int32_t n_seqs,
                int32_t max_new, int64_t n_tokens, const void *q, int64_t q_stride,
                const int32_t *q_start, const int32_t *table, const int32_t *len,

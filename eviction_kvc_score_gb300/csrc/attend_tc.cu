@@ -619,6 +619,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     fence_async_shared();
+                    // lane 0 says for all 32 rows that they are clean
+                    __syncwarp();
                 }
                 // slow: some row of the tile sees only part of it, or the scale is
                 // not positive; two copies, because a select per logit costs as much

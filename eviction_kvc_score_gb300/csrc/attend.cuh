@@ -355,7 +355,9 @@ __device__ __forceinline__ bool attend_last(uint32_t *count, uint32_t all) {
         asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(count) : "memory");
         if (before == all - 1) *count = 0;
     }
-    return __shfl_sync(0xffffffffu, before, 0) == all - 1;
+    before = __shfl_sync(0xffffffffu, before, 0);
+    __syncwarp();   // lane 0's acquire is the warp's: a shuffle alone orders no memory
+    return before == all - 1;
 }
 
 // How many warps have been counted; what they wrote before is visible after it.
@@ -363,7 +365,9 @@ __device__ __forceinline__ uint32_t attend_peek(const uint32_t *count) {
     uint32_t is = 0;
     if ((threadIdx.x & 31) == 0)
         asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(is) : "l"(count) : "memory");
-    return __shfl_sync(0xffffffffu, is, 0);
+    is = __shfl_sync(0xffffffffu, is, 0);
+    __syncwarp();   // as in attend_last
+    return is;
 }
 
 // Slots of a CTA: its first unit's (begun by an earlier CTA), its last unit's.

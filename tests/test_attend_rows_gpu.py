@@ -34,3 +34,19 @@ def test_warps_without_rows_wait_for_their_clean_values(d, hq, ps):
         c.out.fill_(7)
         c.run()
         assert torch.equal(c.out, out) and torch.equal(c.lse, lse), again
+
+
+@pytest.mark.parametrize("dtype,d,hq,n", [("bf16", 128, 8, 1), ("bf16", 64, 2, 5), ("bf16", 128, 64, 3), ("f32", 64, 8, 1)])
+def test_joins_read_only_what_this_call_wrote(dtype, d, hq, n):
+    """Lists shared by few and by many blocks: what the slots held before is NaN, so a lane that
+    reads another block's slot before it may gives NaN."""
+    c = Case(ns=[n] * 3, lens=[40000, 9000, 70000], hq=hq, h=1, d=d, ps=64, dtype=dtype, seed=hq)
+    c.run().check()
+    out, lse = c.out.clone(), c.lse.clone()
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    slots = 256 + 16 * 4 * sms * 4      # behind the header and the counters
+    for again in range(20):
+        c.ws[slots:] = 255
+        c.out.fill_(7)
+        c.run()
+        assert torch.equal(c.out, out) and torch.equal(c.lse, lse), again

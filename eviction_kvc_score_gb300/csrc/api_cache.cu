@@ -297,8 +297,18 @@ int kvc_attend(const kvc_cache *cache, int32_t n_q_heads, int32_t n_kv_heads, in
                const int32_t *q_start, const int32_t *table, const int32_t *len,
                const void *k_pool, const void *v_pool, float scale, void *out, float *lse,
                void *ws, size_t ws_bytes, cudaStream_t stream) {
+    return kvc_attend_ex(cache, n_q_heads, n_kv_heads, n_seqs, max_new, n_tokens, q, q_stride, q_start, table,
+                         len, k_pool, v_pool, scale, out, lse, 0, ws, ws_bytes, stream);
+}
+
+int kvc_attend_ex(const kvc_cache *cache, int32_t n_q_heads, int32_t n_kv_heads, int32_t n_seqs,
+                  int32_t max_new, int64_t n_tokens, const void *q, int64_t q_stride,
+                  const int32_t *q_start, const int32_t *table, const int32_t *len,
+                  const void *k_pool, const void *v_pool, float scale, void *out, float *lse,
+                  uint32_t flags, void *ws, size_t ws_bytes, cudaStream_t stream) {
     NvtxRange nvtx_range("kvc_attend");
     set_error("%s", "");
+    if (flags & ~KVC_ATTEND_BF16_P) return fail(KVC_ERR_INVALID_ARG, "kvc_attend: unknown flags %#x", flags);
     if (!attend_shape_ok(cache, n_q_heads, n_kv_heads, n_seqs, max_new, "kvc_attend"))
         return KVC_ERR_INVALID_ARG;
     const kvc_cache &c = *cache;
@@ -345,6 +355,7 @@ int kvc_attend(const kvc_cache *cache, int32_t n_q_heads, int32_t n_kv_heads, in
     p.out = out;
     p.lse = lse;
     p.scale_log2 = (float)(scale * kLog2e);
+    p.one_term = flags & KVC_ATTEND_BF16_P;
     p.status = static_cast<uint32_t *>(ws);
     p.arrived = reinterpret_cast<uint32_t *>(base + w.arrived);
     p.stat = reinterpret_cast<float2 *>(base + w.stat);

@@ -43,6 +43,7 @@ struct AttendParams {
     float *lse;
     float scale_log2;    // scale * log2(e)
     int skip_load;       // tests: every CTA's first load is left out
+    bool one_term;       // tensor cores: probabilities in one bf16 term, not two
     uint32_t *status;
     Divider by_quads;    // dim / 4
     uint32_t *arrived;   // [grid][2][8], zero between calls: of a unit, of a group

@@ -4,10 +4,17 @@
 // A CTA walks its run of steps (attend.cuh).  Per 128-key tile of a list and
 // per tile t of up to 128 rows (tokens x the KV head's query heads):
 //   MMA   S_t = Q_t K^T        128 x 128, D deep, both operands in shared memory
-//   soft  p = 2^(S c - m), c = scale log2 e, rounded to bf16 and written over
-//         S_t in TMEM; l += sum of the unrounded p
-//   MMA   O_t += P_t V         128 x D, P straight from TMEM, V as TMA left it
-//                              (channel-contiguous: the MN-major layout)
+//   soft  p = 2^(S c - m), c = scale log2 e, as two bf16 terms written over S_t
+//         in TMEM: the upper 16 bits of p, and the rest rounded to bf16 (2^-16 p
+//         is lost); l += sum of the unrounded p
+//   MMA   O_t += P_t V         128 x D, both terms of P straight from TMEM, V as
+//                              TMA left it (channel-contiguous: the MN-major layout)
+// One term (KVC_ATTEND_BF16_P, the caller's choice) rounds p to 8 bits: the
+// outputs' error against 64 bits is then 1.3 to 1.4 times that of an fp32 softmax
+// rounded once; with two it is the same.  The second term costs four instructions
+// per pair of probabilities in a chain that one warp walks alone, and half as many
+// products again: 16.6 us against 14.5 for one sequence of 1,000 rows, 172 against
+// 152 for the batch below, 2.01 ms against 1.46 for the chunk.
 // The reference m only follows the running maximum when that has grown by more
 // than 8 (p then stays below 2^8, far from any limit of bf16 or fp32); O and l
 // are rescaled then, which after the first tiles hardly ever happens.
@@ -23,7 +30,8 @@
 // Nothing a row does not see reaches it: its S is masked, and in tiles that
 // some row sees only part of, V's elements that are not finite are taken out
 // before the product (p = 0 would not cancel them) and given back at the end
-// to the rows that see them.
+// to the rows that see them.  Elsewhere an infinite value goes through the
+// product: neither term of a p above 2^-110 is 0 or negative.
 //
 // Roles: warps 0-3 and 4-7 softmax of t = 0 and 1, a thread per row; warps 8
 // and 11 load, every other tile each (one warp takes 1,200 clocks to issue the
@@ -37,15 +45,14 @@
 // kernel with KVC_DEV_TIMEOUT (the workspace then has to be initialised again).
 //
 // What bounds it, measured on one GB300:
-// - chunks: the chain S -> softmax -> P V of a half, 3,000 clocks for a step of two
-//   halves whose MMAs take 2,048 (128 x 128 x 16 in 64 clocks).  4,096 tokens x 32
-//   heads behind 28,672 cached rows: 1.25 ms on a cool GPU (1,650 TFLOP/s, 87% of
-//   the measured burst rate), 1.43-1.47 ms back to back, where the power limit
-//   holds the clock at about 1.7 GHz.
-// - decode: reading the cache.  64 sequences x 8 KV heads of 500-6,000 rows in
-//   16-row pages, 853 MB: 151 us, 5.6 TB/s or 83% of the measured copy rate.
-// - short calls: latency.  One sequence of 1,000 rows: 14.5 us, of which about 5
-//   up to the first MMA and 5 from the last to the joined output.
+// - chunks: the MMAs of a step of two halves take 3,072 clocks (128 x 128 x 16 in
+//   64 clocks; one term: 2,048), the chain S -> softmax -> P V the rest.  4,096
+//   tokens x 32 heads behind 28,672 cached rows: 2.00-2.02 ms back to back, one
+//   term 1.45-1.47.
+// - decode: reading the cache, and the softmax of one warp between K and V.  64
+//   sequences x 8 KV heads of 500-6,000 rows in 16-row pages, 853 MB: 172 us, 5.0
+//   TB/s or 73% of the measured copy rate; one term 152 us, 83%.
+// - short calls: latency.  One sequence of 1,000 rows: 16.6 us; one term 14.5.
 #include <cstdlib>
 #include <type_traits>
 
@@ -268,7 +275,7 @@ struct Walk {
     }
 };
 
-template <int KH>
+template <int KH, bool TWO>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                      const __grid_constant__ CUtensorMap tv, const __grid_constant__ AttendParams p) {
@@ -477,9 +484,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 constexpr int k0 = decltype(upper)::value ? 4 : 0;
                 const uint64_t v = desc_sw128(smem_u32(ring) + (f % kStages) * kStageBytes, kBox, 1024);
 #pragma unroll
-                for (int ks = k0; ks < k0 + 4; ++ks)
-                    tc_mma_bf16_tmem_a(col_o, col_s + ks * 8, v + (uint64_t)(ks * (16 * 128 >> 4)), kIdO,
-                                       add || ks > 0);
+                for (int ks = k0; ks < k0 + 4; ++ks) {
+                    const uint64_t at = v + (uint64_t)(ks * (16 * 128 >> 4));
+                    tc_mma_bf16_tmem_a(col_o, col_s + ks * 8, at, kIdO, add || ks > 0);
+                    if (TWO) tc_mma_bf16_tmem_a(col_o, col_s + 64 + ks * 8, at, kIdO, 1);
+                }
             };
             // The halves' groups (O of a tile, S of the next) go to the tensor
             // cores whole and in turn.  Mixed, both softmaxes would get their S
@@ -561,6 +570,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool plain = p.scale_log2 > 0.f;
         const float c = p.scale_log2;
         const unsigned long long c2 = f2_pack(c, c);
+        // p (1 + 2^-23): the second term of a p > 0 is never 0, which an infinite value of V may not meet
+        const unsigned long long above1 = f2_pack(1.f + 0x1p-23f, 1.f + 0x1p-23f);
         uint32_t ns = 0, no = 0, nwg = 0, njoined = 0, handed = 0, filled = 0;
         bool owed = false;   // half 1: O is still being read by half 0
         bool ok = true;
@@ -692,17 +703,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                     unsigned long long sum2[2] = {0, 0};
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        uint32_t pw[32];
+                        uint32_t pw[32], lo[TWO ? 32 : 1];
 #pragma unroll
                         for (int j = 0; j < 32; ++j) {
                             const int q = 2 * h + (j >> 4), e = 2 * (j & 15);
                             float y0, y1;
                             f2_unpack(f2_fma(f2_pack(v[q][e], v[q][e + 1]), mul2, nm2), y0, y1);
                             const float p0 = ex2(y0), p1 = ex2(y1);
-                            sum2[j & 1] = f2_add(sum2[j & 1], f2_pack(p0, p1));
-                            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(pw[j]) : "f"(p1), "f"(p0));
+                            const unsigned long long pp = f2_pack(p0, p1);
+                            sum2[j & 1] = f2_add(sum2[j & 1], pp);
+                            if constexpr (TWO) {
+                                // the upper 16 bits, and what is left of the rest
+                                const uint32_t b0 = __float_as_uint(p0), b1 = __float_as_uint(p1);
+                                pw[j] = __byte_perm(b0, b1, 0x7632);
+                                float r0, r1;
+                                f2_unpack(f2_fma(pp, above1, f2_pack(-__uint_as_float(b0 & 0xffff0000u),
+                                                                     -__uint_as_float(b1 & 0xffff0000u))),
+                                          r0, r1);
+                                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(lo[j]) : "f"(r1), "f"(r0));
+                            } else {
+                                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(pw[j]) : "f"(p1), "f"(p0));
+                            }
                         }
                         tmem_st32(cs + h * 32, pw);
+                        if constexpr (TWO) tmem_st32(cs + 64 + h * 32, lo);   // S is in registers by now
                         // half of P is enough for half of the product to start
                         tmem_st_wait();
                         tc_fence_before();
@@ -947,7 +971,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int KH>
+template <int KH, bool TWO>
 int launch(AttendParams &p, int grid, cudaStream_t st) {
     const uint64_t D = 64 * KH, G = p.group;
     const uint32_t tokens = kTile / p.group;
@@ -966,15 +990,15 @@ int launch(AttendParams &p, int grid, cudaStream_t st) {
     static_assert(bytes <= 232448, "shared memory of one block");
     static const int regs = [] {
         cudaFuncAttributes at{};
-        return cudaFuncGetAttributes(&at, attend_tc_kernel<KH>) == cudaSuccess ? at.numRegs : 0;
+        return cudaFuncGetAttributes(&at, attend_tc_kernel<KH, TWO>) == cudaSuccess ? at.numRegs : 0;
     }();
     if (regs != kRegsLaunch) {
         set_error("kvc_attend: the tensor-core kernel has %d registers per thread, its split needs %d", regs,
                   kRegsLaunch);
         return KVC_ERR_UNSUPPORTED;
     }
-    allow_shared<attend_tc_kernel<KH>>((int)bytes);
-    launch_early(attend_tc_kernel<KH>, grid, kThreads, bytes, st, tq, tk, tv, p);
+    allow_shared<attend_tc_kernel<KH, TWO>>((int)bytes);
+    launch_early(attend_tc_kernel<KH, TWO>, grid, kThreads, bytes, st, tq, tk, tv, p);
     return cache_launched("kvc_attend");
 }
 
@@ -997,7 +1021,8 @@ int launch_attend_tc(AttendParams &p, int grid, cudaStream_t st) {
         set_error("kvc_attend: n_seqs * n_kv_heads * max_new is too large");
         return KVC_ERR_UNSUPPORTED;
     }
-    return p.dim == 64 ? launch<1>(p, grid, st) : launch<2>(p, grid, st);
+    if (p.one_term) return p.dim == 64 ? launch<1, false>(p, grid, st) : launch<2, false>(p, grid, st);
+    return p.dim == 64 ? launch<1, true>(p, grid, st) : launch<2, true>(p, grid, st);
 }
 
 }  // namespace kvc

@@ -36,6 +36,7 @@ VALUE_REUSE_SCORE_STATS = 0x1   # kvc_channel_prune_value_ex flag
 DEV_INVARIANT = 0x10   # bounds-checking builds only
 DEV_BAD_LIST, DEV_BAD_PAGE, DEV_PAGES_FULL = 0x20, 0x40, 0x80   # paged cache
 ROPE_INTERLEAVED, ROPE_INVERSE = 0x1, 0x2
+ATTEND_BF16_P = 0x1   # kvc_attend_ex flag
 
 
 class KvcError(RuntimeError):
@@ -95,6 +96,8 @@ _SIGS = {
     "kvc_attend_workspace_size": (_sz, [_cp, _i32, _i32, _i32, _i32]),
     "kvc_attend": (C.c_int, [_cp, _i32, _i32, _i32, _i32, _i64, _p, _i64, _p, _p, _p, _p, _p, _f, _p,
                              _p, _p, _sz, _p]),
+    "kvc_attend_ex": (C.c_int, [_cp, _i32, _i32, _i32, _i32, _i64, _p, _i64, _p, _p, _p, _p, _p, _f, _p,
+                                _p, _u32, _p, _sz, _p]),
     "kvc_keep_channels": (_i32, [_d, _i32]),
     "kvc_status_string": (C.c_char_p, [C.c_int]),
     "kvc_last_error": (C.c_char_p, []),
@@ -512,18 +515,24 @@ def kvc_attend(c: KvcCache, q, q_start, table, lens, k_pool, v_pool, max_new: in
                lse=None, scale: Optional[float] = None, stream=None) -> None:
     """Attention of new tokens q [n_tokens][H_q][D] over the paged lists of one
     layer, table [n_seqs * H_kv][max_pages]; scale defaults to 1 / sqrt(D)."""
+    kvc_attend_ex(c, q, q_start, table, lens, k_pool, v_pool, max_new, out, 0, ws, lse, scale, stream)
+
+
+def kvc_attend_ex(c: KvcCache, q, q_start, table, lens, k_pool, v_pool, max_new: int, out, flags: int,
+                  ws, lse=None, scale: Optional[float] = None, stream=None) -> None:
+    """kvc_attend with flags (ATTEND_BF16_P; see kvc.h)."""
     dev, t, n_len, n_lists = _lists(c, table, lens)
     n_seqs = q_start.numel() - 1
     if n_seqs < 1 or n_lists % n_seqs:
         raise ValueError("table must hold the same number of lists for every sequence of q_start")
     dt, n, dim = _DTYPES[c.dtype], q.shape[0], c.head_dim
     hq, qp, qs = _heads(q, "q", dt, dev, n, dim)
-    _check("kvc_attend", _lib.kvc_attend(
+    _check("kvc_attend", _lib.kvc_attend_ex(
         C.byref(c), hq, n_lists // n_seqs, n_seqs, max_new, n, qp, qs,
         _at(q_start, "q_start", torch.int32, dev), t, n_len, *_pools(c, k_pool, v_pool, dev),
         dim ** -0.5 if scale is None else scale, _at(out, "out", dt, dev, n * hq * dim),
-        _at(lse, "lse", torch.float32, dev, n * hq), *_bytes(ws, "workspace", dev),
-        _handle(stream, dev)))
+        _at(lse, "lse", torch.float32, dev, n * hq), flags,
+        *_bytes(ws, "workspace", dev), _handle(stream, dev)))
 
 
 def kvc_status_string(code: int) -> str:

@@ -536,9 +536,9 @@ size_t kvc_attend_workspace_size(const kvc_cache *cache, int32_t n_q_heads, int3
  * n = 1 is a decode step.  q_stride counts elements from token to token; out
  * is [n_tokens][n_q_heads][D] contiguous, lse [n_tokens][n_q_heads] fp32 or
  * NULL.  Logits, softmax and sums are fp32.  bf16 with D 64 or 128 and at most
- * 128 query heads per KV head runs on the tensor cores (the probabilities
- * rounded to bf16 for the product with V); everything else on the CUDA cores
- * in fp32.  Lengths and q_start out of range are cut to it
+ * 128 query heads per KV head runs on the tensor cores, the probabilities as
+ * the sum of two bf16 numbers (16 bits) for the product with V; everything else
+ * on the CUDA cores in fp32.  Lengths and q_start out of range are cut to it
  * (KVC_DEV_BAD_LIST); a page outside the pool counts as rows of zeros
  * (KVC_DEV_BAD_PAGE).  Long lists are split over the GPU and joined in a fixed
  * order, so results do not vary from run to run.  Sequences without tokens and
@@ -553,6 +553,17 @@ int kvc_attend(const kvc_cache *cache, int32_t n_q_heads, int32_t n_kv_heads, in
                const int32_t *q_start, const int32_t *table, const int32_t *len,
                const void *k_pool, const void *v_pool, float scale, void *out, float *lse,
                void *ws, size_t ws_bytes, cudaStream_t stream);
+
+/* kvc_attend with flags.  KVC_ATTEND_BF16_P: on the tensor cores the
+ * probabilities are rounded to one bf16 number (8 bits) for the product with
+ * V, which is faster; the CUDA cores' calls are the same with it.  Other flags
+ * are refused. */
+#define KVC_ATTEND_BF16_P 0x1u
+int kvc_attend_ex(const kvc_cache *cache, int32_t n_q_heads, int32_t n_kv_heads, int32_t n_seqs,
+                  int32_t max_new, int64_t n_tokens, const void *q, int64_t q_stride,
+                  const int32_t *q_start, const int32_t *table, const int32_t *len,
+                  const void *k_pool, const void *v_pool, float scale, void *out, float *lse,
+                  uint32_t flags, void *ws, size_t ws_bytes, cudaStream_t stream);
 
 const char *kvc_status_string(int status);
 

@@ -53,6 +53,9 @@
 //   sequences x 8 KV heads of 500-6,000 rows in 16-row pages, 853 MB: 172 us, 5.0
 //   TB/s or 73% of the measured copy rate; one term 152 us, 83%.
 // - short calls: latency.  One sequence of 1,000 rows: 16.6 us; one term 14.5.
+#include <cudaTypedefs.h>
+
+#include <atomic>
 #include <cstdlib>
 #include <type_traits>
 
@@ -971,6 +974,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
+// bf16 q as [token][KV head][query head][D] in 128-byte swizzled boxes of 64 x box
+// elements (make_tma_map has three dimensions, of contiguous rows).
+bool make_q_map(CUtensorMap *m, const void *q, const uint64_t (&dims)[4], const uint64_t (&strides)[3],
+                const uint32_t (&box)[4]) {
+    static std::atomic<void *> entry{nullptr};
+    void *fn = entry.load(std::memory_order_relaxed);
+    if (!fn) {
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) !=
+                cudaSuccess || found != cudaDriverEntryPointSuccess)
+            return false;
+        entry.store(fn, std::memory_order_relaxed);
+    }
+    const cuuint32_t steps[4] = {1, 1, 1, 1};
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn)(
+               m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(q), dims, strides, box, steps,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int KH, bool TWO>
 int launch(AttendParams &p, int grid, cudaStream_t st) {
     const uint64_t D = 64 * KH, G = p.group;
@@ -980,7 +1003,7 @@ int launch(AttendParams &p, int grid, cudaStream_t st) {
     const uint64_t strides[3] = {D * 2, G * D * 2, (uint64_t)p.q_stride * 2};
     const uint32_t box[4] = {64, (uint32_t)G, 1, tokens};
     const uint64_t ps = (uint64_t)1 << p.shift;
-    if (!make_tma_map_nd(&tq, p.q, 4, dims, strides, box) ||
+    if (!make_q_map(&tq, p.q, dims, strides, box) ||
         !make_tma_map(&tk, p.k_pool, D, ps, (uint64_t)p.n_pages, (uint32_t)ps) ||
         !make_tma_map(&tv, p.v_pool, D, ps, (uint64_t)p.n_pages, (uint32_t)ps)) {
         set_error("kvc_attend: cuTensorMapEncodeTiled failed (alignment or driver)");

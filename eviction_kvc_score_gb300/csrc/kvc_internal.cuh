@@ -547,10 +547,6 @@ int score_tc_pairs(int sms);
 // entry point is missing or the encoding is refused.
 bool make_tma_map(CUtensorMap *m, const void *base, uint64_t inner, uint64_t mid, uint64_t outer,
                   uint32_t box_rows);
-// The same for 2 to 5 dimensions: sizes, byte strides of dimensions 1.. and box,
-// innermost first.
-bool make_tma_map_nd(CUtensorMap *m, const void *base, int rank, const uint64_t *dims,
-                     const uint64_t *strides, const uint32_t *box);
 int launch_score_tc(const kvc_shape &s, const ScoreSplit &sp, const ScoreArgs &a, cudaStream_t st);
 int launch_score_tc_keyformer(const kvc_shape &s, const ScoreSplit &sp, const ScoreArgs &a,
                               uint64_t seed, double tau, cudaStream_t st);

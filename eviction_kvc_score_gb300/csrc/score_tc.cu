@@ -889,30 +889,18 @@ PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
 
 }  // namespace
 
-bool make_tma_map_nd(CUtensorMap *m, const void *base, int rank, const uint64_t *dims,
-                     const uint64_t *strides, const uint32_t *box) {
-    auto enc = get_encode();
-    if (!enc || rank < 2 || rank > 5) return false;
-    cuuint64_t d[5], st[4];
-    cuuint32_t b[5], estr[5];
-    for (int i = 0; i < rank; ++i) {
-        d[i] = dims[i];
-        b[i] = box[i];
-        estr[i] = 1;
-        if (i) st[i - 1] = strides[i - 1];
-    }
-    CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), d, st, b,
-                     estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS;
-}
-
 bool make_tma_map(CUtensorMap *m, const void *base, uint64_t inner, uint64_t mid, uint64_t outer,
                   uint32_t box_rows) {
-    const uint64_t dims[3] = {inner, mid, outer};
-    const uint64_t strides[2] = {inner * 2, inner * mid * 2};
-    const uint32_t box[3] = {64, box_rows, 1};
-    return make_tma_map_nd(m, base, 3, dims, strides, box);
+    auto enc = get_encode();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {inner, mid, outer};
+    cuuint64_t strides[2] = {inner * 2, inner * mid * 2};
+    cuuint32_t box[3] = {64, box_rows, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides,
+                     box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
 }
 
 namespace {

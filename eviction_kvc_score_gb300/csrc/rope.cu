@@ -21,26 +21,90 @@ namespace kvc {
 namespace {
 
 constexpr int kRopeThreads = 256;
+constexpr int kTableThreads = 32;  // a warp per SM: fp64 instructions are issued rarely
 constexpr int kRopePairs = 512;   // (token, pair) angles of a block
+
+// A number as the unevaluated sum h + l, |l| <= ulp(h) / 2: about 106 bits
+// (Dekker, "A floating-point technique for extending the available precision",
+// 1971).  A double's 53 bits would leave the last 11 of the table's 64 empty,
+// 2.6e-7 rad at position 2^31.
+struct Twice {
+    double h, l;
+};
+__device__ Twice exact_sum(double a, double b) {
+    const double s = __dadd_rn(a, b), t = __dsub_rn(s, a);
+    return {s, __dadd_rn(__dsub_rn(a, __dsub_rn(s, t)), __dsub_rn(b, t))};
+}
+__device__ Twice exact_product(double a, double b) {
+    const double p = __dmul_rn(a, b);
+    return {p, __fma_rn(a, b, -p)};
+}
+__device__ Twice operator+(Twice a, Twice b) {
+    const Twice s = exact_sum(a.h, b.h);
+    return exact_sum(s.h, __dadd_rn(s.l, __dadd_rn(a.l, b.l)));
+}
+__device__ Twice operator*(Twice a, Twice b) {
+    const Twice p = exact_product(a.h, b.h);
+    return exact_sum(p.h, __dadd_rn(p.l, __fma_rn(a.h, b.l, __dmul_rn(a.l, b.h))));
+}
+__device__ Twice operator-(Twice a) { return {-a.h, -a.l}; }
+__device__ Twice operator/(Twice a, Twice b) {   // long division, a quotient's double at a time
+    const double q0 = a.h / b.h;
+    const Twice r = a + -(Twice{q0, 0} * b);
+    const double q1 = r.h / b.h;
+    const Twice left = r + -(Twice{q1, 0} * b);
+    return exact_sum(q0, q1) + Twice{left.h / b.h, 0};
+}
+__device__ Twice scaled(Twice a, int by) { return {ldexp(a.h, by), ldexp(a.l, by)}; }
+
+__device__ Twice ln2() { return {0x1.62e42fefa39efp-1, 0x1.abc9e3b39803fp-56}; }
+__device__ Twice half_over_pi() { return {0x1.45f306dc9c883p-3, -0x1.6b01ec5417056p-57}; }
+// 1 / n, for the compiler to work out.
+__device__ __forceinline__ Twice inverse(int n) {
+    const double h = 1.0 / n;
+    return {h, fma(-(double)n, h, 1.0) / n};
+}
+
+// e^x, |x| < 710: x = k ln 2 + 256 t, |t| < 0.0014, the series of e^t - 1 up to
+// t^7 (t^8 / 8! is 2^-91) and 2^k (1 + it)^256 by doubling, (1 + y)^2 = 1 + (2 y + y^2).
+__device__ Twice exponential(Twice x) {
+    const double k = rint(x.h / ln2().h);
+    const Twice t = scaled(x + -(Twice{k, 0} * ln2()), -8);
+    Twice y = t * inverse(7);
+#pragma unroll
+    for (int n = 6; n >= 1; --n) y = t * (Twice{1, 0} + y) * inverse(n);
+#pragma unroll
+    for (int n = 0; n < 8; ++n) y = scaled(y, 1) + y * y;
+    return scaled(Twice{1, 0} + y, (int)k);
+}
+// The root of e^y = m near log(m): y + (m e^-y - 1).
+__device__ Twice logarithm(double x) {
+    int e;
+    const double m = frexp(x, &e);
+    const Twice y{log(m), 0};
+    return Twice{(double)e, 0} * ln2() + y + (Twice{m, 0} * exponential(-y) + Twice{-1, 0});
+}
 
 __global__ void rope_table_kernel(int rot, double theta, double factor, double alpha, double beta,
                                   double context, uint64_t *table) {
-    const int i = threadIdx.x;
+    const int i = blockIdx.x * kTableThreads + threadIdx.x;
     if (i >= rot / 2) return;
-    constexpr double kTwoPi = 6.283185307179586476925286766559;
-    double f = pow(theta, -2.0 * i / rot);
+    const Twice power = Twice{-2.0 * i, 0} / Twice{(double)rot, 0};
+    Twice f = exponential(power * logarithm(theta)) * half_over_pi();   // turns per position
     if (factor > 1.0) {
-        const double turns = context * f / kTwoPi;
-        double g;
-        if (turns >= beta)
-            g = 1.0;
-        else if (turns <= alpha)
-            g = 0.0;
+        const Twice turns = f * Twice{context, 0};
+        Twice g;
+        if (turns.h > beta || (turns.h == beta && turns.l >= 0.0))
+            g = {1, 0};
+        else if (turns.h < alpha || (turns.h == alpha && turns.l <= 0.0) || isinf(beta))
+            g = {0, 0};
         else
-            g = (turns - alpha) / (beta - alpha);
-        f *= g + (1.0 - g) / factor;
+            g = (turns + Twice{-alpha, 0}) / exact_sum(beta, -alpha);
+        f = f * (g + (Twice{1, 0} + -g) / Twice{factor, 0});
     }
-    table[i] = __double2ull_rn(f / kTwoPi * 18446744073709551616.0);
+    // to the nearest 2^-64: what h has of whole units, then the rest
+    const double units = f.h * 0x1p64, whole = floor(units);
+    table[i] = (uint64_t)whole + (uint64_t)(int64_t)rint((units - whole) + f.l * 0x1p64);
 }
 
 struct RopeSide {
@@ -171,7 +235,7 @@ void launch_type(RopeParams &p, bool inter, bool in_place, bool wide, int sms, c
 
 int launch_rope_table(int32_t rot, double theta, double factor, double alpha, double beta,
                       double context, uint64_t *table, cudaStream_t st) {
-    rope_table_kernel<<<1, 128, 0, st>>>(rot, theta, factor, alpha, beta, context, table);
+    rope_table_kernel<<<(rot / 2 + kTableThreads - 1) / kTableThreads, kTableThreads, 0, st>>>(rot, theta, factor, alpha, beta, context, table);
     return cache_launched("kvc_rope_table");
 }
 

@@ -483,8 +483,8 @@ int kvc_pages_truncate(const kvc_cache *cache, int32_t *table, int32_t *len, int
                        cudaStream_t stream);
 
 /* Rotary frequencies of the rot_dim / 2 pairs, as turns per position in units
- * of 2^-64 (device array of rot_dim / 2 uint64): pair i makes f_i / (2 pi)
- * turns per position, f_i = theta^(-2 i / rot_dim).  With factor > 1, for
+ * of 2^-64, to the nearest (device array of rot_dim / 2 uint64): pair i makes
+ * f_i / (2 pi) turns per position, f_i = theta^(-2 i / rot_dim).  With factor > 1, for
  * contexts longer than the `context` positions the model was trained on, pairs
  * that make fewer than alpha turns in `context` positions are slowed down by
  * factor, those that make beta or more are kept, and between the two
@@ -501,8 +501,8 @@ int kvc_rope_table(int32_t rot_dim, double theta, double factor, double alpha, d
  * t = positions[token] * f_i of the table; the pair (a, b) is elements
  * (i, i + rot_dim / 2), or (2i, 2i + 1) with KVC_ROPE_INTERLEAVED.
  * KVC_ROPE_INVERSE turns by -t (which is also the gradient's way back).  The
- * angle is reduced exactly in 64-bit fixed point, so far positions (any int32,
- * negative ones too) lose nothing.  Elements from rot_dim on are copied.
+ * angle is reduced exactly in 64-bit fixed point, so the table's half a unit is
+ * all that far positions lose: 2^-34 turns at 2^31 (any int32, negative too).  Elements from rot_dim on are copied.
  * Arithmetic is fp32, rounded once.  q_stride and the others count elements
  * from token to token (>= heads * D); heads are contiguous.  q_out may be q
  * (then with the same stride), k_out may be k; other overlaps are not

@@ -4,8 +4,9 @@
 // A pair (a, b) of a head at position p turns by the angle 2 pi p u, u turns
 // per position.  u is held as a 64-bit fraction, and the product with the
 // integer p modulo 2^64 IS the angle modulo a full turn, exactly: no position
-// is too far and the reduction is one integer multiply.  What is left is one
-// sincospi of a 32-bit fraction of half a turn, within 2^-24.
+// is too far and the reduction is one integer multiply.  What is left is a
+// quarter turn and one sincospi of at most an eighth of a turn either way, whose
+// rounding to fp32 moves the angle by pi 2^-27 at most.
 //
 // Each block takes a few tokens, computes every (token, pair) angle once into
 // shared memory and turns all their heads with 16-byte loads and stores.  Bound
@@ -166,8 +167,20 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeParams p) {
     for (int i = tid; i < nt * pairs; i += nthr) {
         const int t = i / pairs, j = i - t * pairs;
         const uint64_t turns = (uint64_t)(int64_t)p.pos[t0 + t] * p.table[j];
+        // the nearest quarter turn comes off as an integer: what fp32 then rounds
+        // is an eighth of a turn at most
+        const uint64_t quarter = (turns + (1ull << 61)) >> 62;
         float s, c;
-        sincospif((float)(int64_t)turns * 0x1p-63f, &s, &c);
+        sincospif((float)(int64_t)(turns - (quarter << 62)) * 0x1p-63f, &s, &c);
+        if (quarter & 1) {
+            const float x = c;
+            c = -s;
+            s = x;
+        }
+        if (quarter & 2) {
+            c = -c;
+            s = -s;
+        }
         cs[i] = make_float2(p.amplitude * c, p.amplitude * (p.inverse ? -s : s));
     }
     __syncthreads();

@@ -47,3 +47,19 @@ def test_every_frequency_is_the_nearest_unit(rot, theta, kw):
     """The kernel's error of 2^-80 is 2^-16 of a unit at most: 0.51 for the nearest."""
     for got, u in zip(table_of(rot, theta, **kw).tolist(), turns_of(rot, theta, **kw)):
         assert abs(got % UNIT - u * UNIT) <= Decimal("0.51"), (got, u * UNIT)
+
+
+@pytest.mark.parametrize("far", [1, 1 << 15, 1 << 31])
+def test_cosines_and_sines_of_every_angle(far):
+    """Unit vectors turned.  The angle's fraction of half a turn is at most 1/4, rounded by 2^-27: pi 2^-27 = 0.4 2^-24
+    of the outputs; sincospif is within one step below 1, 2^-24; the table's half unit is 2^-34 turns at 2^31."""
+    rot = 128
+    pos = torch.randint(-far, far, (1500,), generator=torch.Generator().manual_seed(far)).int()
+    x = torch.zeros((1500, 1, rot), device="cuda")
+    x[..., :rot // 2] = 1
+    y = torch.empty_like(x)
+    K().kvc_rope(table_of(rot), pos.cuda(), None, x, None, y, rot)
+    turns = list(turns_of(rot, 10000.0))
+    angle = torch.tensor([[float(p * u % 1) * 2 * math.pi for u in turns] for p in pos.tolist()], dtype=torch.float64)
+    want = torch.cat((torch.cos(angle), torch.sin(angle)), -1)
+    assert (y[:, 0].double().cpu() - want).abs().max().item() <= 1.4 * 2.0 ** -24 + 2 * math.pi * 2.0 ** -34

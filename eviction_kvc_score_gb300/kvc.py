@@ -128,12 +128,20 @@ def _stream(stream=None):
     return C.c_void_p(s.cuda_stream)
 
 
+def _dtype_code(dtype) -> int:
+    """kvc_dtype of a torch type or its name; a number is the code itself, which
+    the library's calls check."""
+    if type(dtype) is int:
+        return dtype
+    for code, names in ((KVC_F32, (torch.float32, "f32", "float32")),
+                        (KVC_BF16, (torch.bfloat16, "bf16", "bfloat16"))):
+        if dtype in names:
+            return code
+    raise ValueError(f"the library takes float32 and bfloat16, not {dtype!r}")
+
+
 def shape(n_layers, n_q_heads, n_kv_heads, head_dim, seq_len, window, dtype) -> KvcShape:
-    if isinstance(dtype, torch.dtype):
-        dt = KVC_F32 if dtype == torch.float32 else KVC_BF16
-    else:
-        dt = KVC_F32 if dtype in ("f32", KVC_F32) else KVC_BF16
-    return KvcShape(n_layers, n_q_heads, n_kv_heads, head_dim, seq_len, window, dt)
+    return KvcShape(n_layers, n_q_heads, n_kv_heads, head_dim, seq_len, window, _dtype_code(dtype))
 
 
 def shape_of(wl) -> KvcShape:
@@ -312,13 +320,10 @@ _DTYPES = {KVC_F32: torch.float32, KVC_BF16: torch.bfloat16}
 
 def cache(n_pages, page_rows, head_dim, max_pages, dtype) -> KvcCache:
     """Description of a page pool and its tables (kvc_cache in kvc.h)."""
-    if isinstance(dtype, torch.dtype):
-        if dtype not in _DTYPES.values():
-            raise ValueError(f"pages hold float32 or bfloat16 rows, not {dtype}")
-        dt = KVC_F32 if dtype == torch.float32 else KVC_BF16
-    else:
-        dt = KVC_F32 if dtype in ("f32", KVC_F32) else KVC_BF16
-    return KvcCache(int(n_pages), int(page_rows), int(head_dim), dt, int(max_pages))
+    code = _dtype_code(dtype)
+    if code not in _DTYPES:
+        raise ValueError(f"unknown dtype {code}")
+    return KvcCache(int(n_pages), int(page_rows), int(head_dim), code, int(max_pages))
 
 
 # The checks of these calls cost more than their launches if written freely

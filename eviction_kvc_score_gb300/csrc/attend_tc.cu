@@ -59,6 +59,7 @@
 #include <cstdlib>
 #include <type_traits>
 
+#include "asked.cuh"
 #include "attend.cuh"
 
 namespace kvc {
@@ -1011,10 +1012,19 @@ int launch(AttendParams &p, int grid, cudaStream_t st) {
     }
     constexpr size_t bytes = smem_bytes<KH>();
     static_assert(bytes <= 232448, "shared memory of one block");
-    static const int regs = [] {
+    static AskedOnce asked;
+    cudaError_t err = cudaSuccess;
+    const int regs = asked.get([&] {
         cudaFuncAttributes at{};
-        return cudaFuncGetAttributes(&at, attend_tc_kernel<KH, TWO>) == cudaSuccess ? at.numRegs : 0;
-    }();
+        err = cudaFuncGetAttributes(&at, attend_tc_kernel<KH, TWO>);
+        return err == cudaSuccess ? at.numRegs : 0;
+    });
+    if (err != cudaSuccess) {
+        cudaGetLastError();
+        set_error("kvc_attend: the tensor-core kernel's attributes: %s", cudaGetErrorString(err));
+        return KVC_ERR_CUDA;
+    }
+    // (of a library built by the compiler it was measured with, these are 168)
     if (regs != kRegsLaunch) {
         set_error("kvc_attend: the tensor-core kernel has %d registers per thread, its split needs %d", regs,
                   kRegsLaunch);

@@ -539,8 +539,9 @@ size_t kvc_attend_workspace_size(const kvc_cache *cache, int32_t n_q_heads, int3
  * 128 query heads per KV head runs on the tensor cores, the probabilities as
  * the sum of two bf16 numbers (16 bits) for the product with V; everything else
  * on the CUDA cores in fp32.  Lengths and q_start out of range are cut to it
- * (KVC_DEV_BAD_LIST); a page outside the pool counts as rows of zeros
- * (KVC_DEV_BAD_PAGE).  Long lists are split over the GPU and joined in a fixed
+ * (KVC_DEV_BAD_LIST; where q_start goes backwards, the outputs of tokens that
+ * two sequences then claim are undefined); a page outside the pool counts as
+ * rows of zeros (KVC_DEV_BAD_PAGE).  Long lists are split over the GPU and joined in a fixed
  * order, so results do not vary from run to run.  Sequences without tokens and
  * lists without rows may stand anywhere.  q, out and the pools are 16-byte
  * aligned, q_stride a multiple of 8; out and lse overlap no input; scale and

@@ -284,7 +284,7 @@ __device__ __noinline__ int64_t attend_plan_lists(const AttendParams &p, int64_t
 // By units: each thread adds up a stretch of them.  Where lists of several units
 // make more than four per thread, by lists: a chunk's units would be one thread's
 // (2,048 tokens and 255 decoding sequences, 64K units of which 2,300 have work:
-// 362 us by units, 294 by lists; with one unit a list or few units the plan by
+// 362 us by units, 294 by lists, in one bf16 term; with one unit a list or few units the plan by
 // lists takes 1 us longer).
 template <int NT, bool kSome>
 __device__ AttendRun attend_plan(const AttendParams &p, int64_t *scratch) {

@@ -15,7 +15,7 @@
 // loads but 250 registers: eight warps per SM left the FMA pipe at a third, 179 us
 // for five chunks of up to 293 tokens x 8 heads of 80 over up to 2,757 rows; now 120
 // us, 24 TFLOP/s, FMA pipe and shared loads each half busy.  Decode of 2 x 4 lists
-// of 60,000 rows: 124 us, 4.0 TB/s.)  K of the next tile is on its
+// of 60,000 rows: 120 us, 4.1 TB/s.)  K of the next tile is on its
 // way (cp.async) during the product with V, V of the next during the logits.
 // K and V stay in shared memory in their own type; a row is padded by 16 bytes,
 // which spreads 8 rows' loads over all banks for every D that is a multiple of 8.
@@ -403,7 +403,7 @@ int launch_attend_simt(AttendParams &p, bool f32, int grid, cudaStream_t st) {
     // Blocks of 64 rows, of 16 where no list has more.  Lists of both kinds take a
     // launch each: in a block of 64 rows one warp of eight would work on a token's
     // (a chunk of 256 tokens and 255 decoding sequences of 1,000 rows, fp32, 8 KV
-    // heads of 128: 2,512 us in one launch, 1,033 in two).  A launch that finds no
+    // heads of 128: 2,512 us in one launch, 1,035 in two).  A launch that finds no
     // list costs 6 us, so one does where the lists have more than 128 rows on
     // average: the short ones are then at most a third of the blocks.
     const int64_t most = (int64_t)p.max_new * p.group;

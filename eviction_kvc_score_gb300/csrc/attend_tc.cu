@@ -11,10 +11,11 @@
 //                              TMA left it (channel-contiguous: the MN-major layout)
 // One term (KVC_ATTEND_BF16_P, the caller's choice) rounds p to 8 bits: the
 // outputs' error against 64 bits is then 1.3 to 1.4 times that of an fp32 softmax
-// rounded once; with two it is the same.  The second term costs four instructions
-// per pair of probabilities in a chain that one warp walks alone, and half as many
-// products again: 16.6 us against 14.5 for one sequence of 1,000 rows, 172 against
-// 152 for the batch below, 2.01 ms against 1.46 for the chunk.
+// rounded once; with two it is the same.  The second term costs half as many
+// products again, and four instructions per pair of probabilities, which in a
+// decode step one scheduler of four issues for both halves (their rows lie in the
+// same quarter of TMEM): 16.7 us against 14.5 for one sequence of 1,000 rows, 172
+// against 152 for the batch below, 2.01 ms against 1.46 for the chunk.
 // The reference m only follows the running maximum when that has grown by more
 // than 8 (p then stays below 2^8, far from any limit of bf16 or fp32); O and l
 // are rescaled then, which after the first tiles hardly ever happens.
@@ -47,12 +48,12 @@
 // What bounds it, measured on one GB300:
 // - chunks: the MMAs of a step of two halves take 3,072 clocks (128 x 128 x 16 in
 //   64 clocks; one term: 2,048), the chain S -> softmax -> P V the rest.  4,096
-//   tokens x 32 heads behind 28,672 cached rows: 2.00-2.02 ms back to back, one
-//   term 1.45-1.47.
+//   tokens x 32 heads behind 28,672 cached rows: 2.01 ms back to back, 1,540
+//   TFLOP/s of products or 91% of the measured sustained rate; one term 1.46.
 // - decode: reading the cache, and the softmax of one warp between K and V.  64
 //   sequences x 8 KV heads of 500-6,000 rows in 16-row pages, 853 MB: 172 us, 5.0
 //   TB/s or 73% of the measured copy rate; one term 152 us, 83%.
-// - short calls: latency.  One sequence of 1,000 rows: 16.6 us; one term 14.5.
+// - short calls: latency.  One sequence of 1,000 rows: 16.7 us; one term 14.5.
 #include <cudaTypedefs.h>
 
 #include <atomic>
@@ -79,8 +80,8 @@ constexpr int kBox = kTile * 128;       // bytes of 128 rows x 64 bf16
 constexpr uint32_t kColS = 0, kColO = 256;
 constexpr float kGrow = 8.f;            // log2 units m may lag behind
 constexpr int kSlotsTc = 2;
-// A unit costs about 4 steps beside its steps (12 lists of 60,000-130,000 rows: 68
-// us without, 63 with 4, 62 with 8; 512 short lists: 148, 150 and 152 us).
+// A unit costs about 4 steps beside its steps (one term, 12 lists of 60,000-130,000
+// rows: 68 us without, 63 with 4, 62 with 8; 512 short lists: 148, 150 and 152 us).
 constexpr int kExtra = 4;
 constexpr int kDirect = 4;              // shares that are joined from registers
 constexpr int kQueue = 4;               // segments on their way from the walk to the roles

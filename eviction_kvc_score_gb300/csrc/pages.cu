@@ -12,10 +12,10 @@
 // zero gets its bit, which commute.
 //
 // The moves are bound by HBM: 560,000 rows of 128 bf16 (K and V, read and
-// written: 573 MB) in 88 us, 6.5 TB/s or 96% of the measured copy rate.  The plan
-// is a chain of memory latencies, 5 us for a few pages and 13 us for 9,000 with
-// cold caches; while each thread wrote down the pages of its own word it took
-// 17 us.
+// written: 573 MB) in 90 us with cold caches, 6.3 TB/s or 93% of the measured copy
+// rate.  The plan is a chain of memory latencies, 7 us for a few pages and 12 us
+// for 9,000 with cold caches; while each thread wrote down the pages of its own word
+// it took 4 us more.
 #include "cache.cuh"
 
 namespace kvc {

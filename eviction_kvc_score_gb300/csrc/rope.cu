@@ -11,7 +11,7 @@
 // Each block takes a few tokens, computes every (token, pair) angle once into
 // shared memory and turns all their heads with 16-byte loads and stores.  Bound
 // by HBM: 32,768 tokens of 32 + 8 heads of 128 (bf16, out of place, 671 MB) take
-// 106 us, 6.3 TB/s or 93% of the measured copy rate; 64 tokens 2.7 us, mostly
+// 106-107 us, 6.3 TB/s or 93% of the measured copy rate; 64 tokens 2.7 us, mostly
 // launch.
 #include <algorithm>
 

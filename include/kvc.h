@@ -535,7 +535,8 @@ size_t kvc_attend_workspace_size(const kvc_cache *cache, int32_t n_q_heads, int3
  * hold.  Tokens outside [q_start[0], q_start[n_seqs]) are left as they were.
  * n = 1 is a decode step.  q_stride counts elements from token to token; out
  * is [n_tokens][n_q_heads][D] contiguous, lse [n_tokens][n_q_heads] fp32 or
- * NULL.  Logits, softmax and sums are fp32.  bf16 with D 64 or 128 and at most
+ * NULL.  Logits, softmax and sums are fp32, the sums divided at the end (elements
+ * of V above 2^100 may overflow them).  bf16 with D 64 or 128 and at most
  * 128 query heads per KV head runs on the tensor cores, the probabilities as
  * the sum of two bf16 numbers (16 bits) for the product with V; everything else
  * on the CUDA cores in fp32.  Lengths and q_start out of range are cut to it

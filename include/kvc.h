@@ -535,20 +535,21 @@ size_t kvc_attend_workspace_size(const kvc_cache *cache, int32_t n_q_heads, int3
  * hold.  Tokens outside [q_start[0], q_start[n_seqs]) are left as they were.
  * n = 1 is a decode step.  q_stride counts elements from token to token; out
  * is [n_tokens][n_q_heads][D] contiguous, lse [n_tokens][n_q_heads] fp32 or
- * NULL.  Logits, softmax and sums are fp32, the sums divided at the end (elements
- * of V above 2^100 may overflow them).  bf16 with D 64 or 128 and at most
- * 128 query heads per KV head runs on the tensor cores, the probabilities as
- * the sum of two bf16 numbers (16 bits) for the product with V; everything else
- * on the CUDA cores in fp32.  Lengths and q_start out of range are cut to it
- * (KVC_DEV_BAD_LIST; where q_start goes backwards, the outputs of tokens that
- * two sequences then claim are undefined); a page outside the pool counts as
- * rows of zeros (KVC_DEV_BAD_PAGE).  Long lists are split over the GPU and joined in a fixed
- * order, so results do not vary from run to run.  Sequences without tokens and
- * lists without rows may stand anywhere.  q, out and the pools are 16-byte
- * aligned, q_stride a multiple of 8; out and lse overlap no input; scale and
- * scale log2 e are finite (scale may be 0 or negative).  Device waits are
- * bounded as in kvc_score; after KVC_DEV_TIMEOUT the workspace has to be
- * initialised again (its counters of finished blocks are not at rest).
+ * NULL.  Logits, softmax and sums are fp32, the sums divided at the end
+ * (elements of V above 2^100 may overflow them). bf16 with D 64 or 128 and at
+ * most 128 query heads per KV head runs on the tensor cores, the probabilities
+ * as the sum of two bf16 numbers (16 bits) for the product with V; everything
+ * else on the CUDA cores in fp32.  Lengths and q_start out of range are cut to
+ * it (KVC_DEV_BAD_LIST; where q_start goes backwards, the outputs of tokens
+ * that two sequences then claim are undefined); a page outside the pool counts
+ * as rows of zeros (KVC_DEV_BAD_PAGE).  Long lists are split over the GPU and
+ * joined in a fixed order, so results do not vary from run to run.  Sequences
+ * without tokens and lists without rows may stand anywhere. q, out and the
+ * pools are 16-byte aligned, q_stride a multiple of 8; out and lse overlap no
+ * input; scale and scale log2 e are finite (scale may be 0 or negative).
+ * Device waits are bounded as in kvc_score; after KVC_DEV_TIMEOUT the workspace
+ * has to be initialised again (its counters of finished blocks are not at
+ * rest).
  * KVC_TEST_SKIP_ARRIVE=1 (tests only) leaves loads out to exercise that. */
 int kvc_attend(const kvc_cache *cache, int32_t n_q_heads, int32_t n_kv_heads, int32_t n_seqs,
                int32_t max_new, int64_t n_tokens, const void *q, int64_t q_stride,

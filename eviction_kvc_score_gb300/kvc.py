@@ -11,6 +11,7 @@ streams only).
 from __future__ import annotations
 
 import ctypes as C
+import numbers
 import os
 from dataclasses import dataclass
 from typing import Optional
@@ -131,8 +132,8 @@ def _stream(stream=None):
 def _dtype_code(dtype) -> int:
     """kvc_dtype of a torch type or its name; a number is the code itself, which
     the library's calls check."""
-    if type(dtype) is int:
-        return dtype
+    if isinstance(dtype, numbers.Integral) and not isinstance(dtype, bool):
+        return int(dtype)
     for code, names in ((KVC_F32, (torch.float32, "f32", "float32")),
                         (KVC_BF16, (torch.bfloat16, "bf16", "bfloat16"))):
         if dtype in names:

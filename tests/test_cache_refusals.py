@@ -1,6 +1,7 @@
 """CPU checks of what the paged cache's calls refuse."""
 import ctypes as C
 
+import numpy as np
 import pytest
 import torch
 
@@ -39,7 +40,7 @@ def test_unknown_codes_are_refused(kvc, code):
         kvc.kvc_workspace_size(kvc.shape(1, 2, 1, 64, 100, 4, code))
 
 
-@pytest.mark.parametrize("code,names", [(0, ["f32", "float32", torch.float32, 0]), (1, ["bf16", "bfloat16", torch.bfloat16, 1])])
+@pytest.mark.parametrize("code,names", [(0, ["f32", "float32", torch.float32, 0, np.int32(0)]), (1, ["bf16", "bfloat16", torch.bfloat16, 1, np.int64(1)])])
 def test_types_by_every_name(kvc, code, names):
     for name in names:
         assert kvc.cache(64, 16, 64, 8, name).dtype == code

@@ -9,6 +9,7 @@
 #include <mutex>
 
 #include "attend.cuh"
+#include "quant.cuh"
 
 namespace kvc {
 
@@ -53,6 +54,11 @@ bool cache_ok(const kvc_cache *c, const char *fn) {
     return true;
 }
 
+bool bits_ok(int32_t bits, const char *fn) {
+    if (bits != 4 && bits != 8) return fail(0, "%s: bits must be 4 or 8", fn), false;
+    return true;
+}
+
 bool lists_ok(int32_t n_lists, const char *fn) {
     if (n_lists < 1 || n_lists > kMaxLists)
         return fail(0, "%s: n_lists must be in 1..2^20", fn), false;
@@ -79,9 +85,9 @@ struct AttendWs {
     size_t arrived, stat, group_stat, part, total;
 };
 
-AttendWs attend_ws(const kvc_cache &c, int group) {
+AttendWs attend_ws(const kvc_cache &c, int bits, int group) {
     AttendWs w;
-    w.tc = attend_tc_takes(c.dtype, c.head_dim, group);
+    w.tc = bits == 0 && attend_tc_takes(c.dtype, c.head_dim, group);
     w.needs = w.tc ? attend_tc_needs(device_sms()) : attend_simt_needs(device_sms());
     const size_t rows = (size_t)w.needs.grid * w.needs.slots * w.needs.slot_rows;
     w.arrived = kWsHeader;
@@ -105,6 +111,74 @@ bool attend_shape_ok(const kvc_cache *c, int32_t n_q_heads, int32_t n_kv_heads, 
     if (max_new < 1 || (int64_t)max_new * (n_q_heads / n_kv_heads) > (1 << 30))
         return fail(0, "%s: max_new must be >= 1 and max_new * query heads per KV head <= 2^30", fn), false;
     return true;
+}
+
+// kvc_attend and kvc_attend_quant; bits 0: rows of the cache's own type.
+int attend_call(const char *fn, int bits, const kvc_cache *cache, int32_t n_q_heads, int32_t n_kv_heads,
+                int32_t n_seqs, int32_t max_new, int64_t n_tokens, const void *q, int64_t q_stride,
+                const int32_t *q_start, const int32_t *table, const int32_t *len, const void *k_pool,
+                const void *v_pool, float scale, void *out, float *lse, uint32_t flags, void *ws, size_t ws_bytes,
+                cudaStream_t stream) {
+    set_error("%s", "");
+    if (flags & ~KVC_ATTEND_BF16_P) return fail(KVC_ERR_INVALID_ARG, "%s: unknown flags %#x", fn, flags);
+    if (!attend_shape_ok(cache, n_q_heads, n_kv_heads, n_seqs, max_new, fn))
+        return KVC_ERR_INVALID_ARG;
+    const kvc_cache &c = *cache;
+    if (n_tokens < 0 || n_tokens >= ((int64_t)1 << 31))
+        return fail(KVC_ERR_INVALID_ARG, "%s: n_tokens must be in 0..2^31-1", fn);
+    if (n_tokens == 0) return KVC_OK;   // empty tensors have no address
+    if (!q || !q_start || !table || !len || !k_pool || !v_pool || !out)
+        return fail(KVC_ERR_INVALID_ARG, "%s: NULL tensor", fn);
+    if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out))
+        return fail(KVC_ERR_INVALID_ARG, "%s: q, out and pools must be 16-byte aligned", fn);
+    if (q_stride < (int64_t)n_q_heads * c.head_dim || q_stride % 8 || q_stride > ((int64_t)1 << 38))
+        return fail(KVC_ERR_INVALID_ARG,
+                    "%s: q_stride must be a multiple of 8 and >= n_q_heads * head_dim", fn);
+    if (!std::isfinite((float)(scale * kLog2e)))
+        return fail(KVC_ERR_INVALID_ARG, "%s: scale must be finite (times log2 e, too)", fn);
+    const AttendWs w = attend_ws(c, bits, n_q_heads / n_kv_heads);
+    if (w.needs.grid == 0) return fail(KVC_ERR_CUDA, "%s: no usable CUDA device", fn);
+    if (!ws) return fail(KVC_ERR_WORKSPACE, "%s: workspace is NULL", fn);
+    if (reinterpret_cast<uintptr_t>(ws) % 256)
+        return fail(KVC_ERR_WORKSPACE, "%s: workspace must be 256-byte aligned", fn);
+    if (ws_bytes < w.total)
+        return fail(KVC_ERR_WORKSPACE, "%s: workspace has %zu bytes, needs %zu", fn, ws_bytes, w.total);
+    char *base = static_cast<char *>(ws);
+    AttendParams p{};
+    p.n_seqs = n_seqs;
+    p.n_q_heads = n_q_heads;
+    p.n_kv_heads = n_kv_heads;
+    p.group = n_q_heads / n_kv_heads;
+    p.dim = c.head_dim;
+    p.bits = bits;
+    p.n_pages = c.n_pages;
+    p.max_pages = c.max_pages;
+    while ((1 << p.shift) < c.page_rows) ++p.shift;
+    p.n_tokens = n_tokens;
+    p.max_new = max_new;
+    p.slots = w.needs.slots;
+    p.slot_rows = w.needs.slot_rows;
+    p.q_stride = q_stride;
+    p.q = q;
+    p.k_pool = k_pool;
+    p.v_pool = v_pool;
+    p.q_start = q_start;
+    p.table = table;
+    p.len = len;
+    p.out = out;
+    p.lse = lse;
+    p.scale_log2 = (float)(scale * kLog2e);
+    p.one_term = flags & KVC_ATTEND_BF16_P;
+    p.status = static_cast<uint32_t *>(ws);
+    p.arrived = reinterpret_cast<uint32_t *>(base + w.arrived);
+    p.stat = reinterpret_cast<float2 *>(base + w.stat);
+    p.group_stat = reinterpret_cast<float2 *>(base + w.group_stat);
+    p.part = reinterpret_cast<float *>(base + w.part);
+    const bool f32 = c.dtype == KVC_F32;
+    if (bits != 0)
+        return bits == 4 ? launch_attend_simt_quant4(p, f32, w.needs.grid, stream)
+                         : launch_attend_simt_quant8(p, f32, w.needs.grid, stream);
+    return w.tc ? launch_attend_tc(p, w.needs.grid, stream) : launch_attend_simt(p, f32, w.needs.grid, stream);
 }
 
 }  // namespace
@@ -289,7 +363,7 @@ size_t kvc_attend_workspace_size(const kvc_cache *cache, int32_t n_q_heads, int3
                                  int32_t n_seqs, int32_t max_new) {
     if (!attend_shape_ok(cache, n_q_heads, n_kv_heads, n_seqs, max_new, "kvc_attend_workspace_size"))
         return 0;
-    return attend_ws(*cache, n_q_heads / n_kv_heads).total;
+    return attend_ws(*cache, 0, n_q_heads / n_kv_heads).total;
 }
 
 int kvc_attend(const kvc_cache *cache, int32_t n_q_heads, int32_t n_kv_heads, int32_t n_seqs,
@@ -307,62 +381,100 @@ int kvc_attend_ex(const kvc_cache *cache, int32_t n_q_heads, int32_t n_kv_heads,
                   const void *k_pool, const void *v_pool, float scale, void *out, float *lse,
                   uint32_t flags, void *ws, size_t ws_bytes, cudaStream_t stream) {
     NvtxRange nvtx_range("kvc_attend");
+    return attend_call("kvc_attend", 0, cache, n_q_heads, n_kv_heads, n_seqs, max_new, n_tokens, q, q_stride, q_start,
+                       table, len, k_pool, v_pool, scale, out, lse, flags, ws, ws_bytes, stream);
+}
+
+size_t kvc_quant_page_size(const kvc_cache *cache, int32_t bits) {
     set_error("%s", "");
-    if (flags & ~KVC_ATTEND_BF16_P) return fail(KVC_ERR_INVALID_ARG, "kvc_attend: unknown flags %#x", flags);
-    if (!attend_shape_ok(cache, n_q_heads, n_kv_heads, n_seqs, max_new, "kvc_attend"))
-        return KVC_ERR_INVALID_ARG;
-    const kvc_cache &c = *cache;
-    if (n_tokens < 0 || n_tokens >= ((int64_t)1 << 31))
-        return fail(KVC_ERR_INVALID_ARG, "kvc_attend: n_tokens must be in 0..2^31-1");
-    if (n_tokens == 0) return KVC_OK;   // empty tensors have no address
-    if (!q || !q_start || !table || !len || !k_pool || !v_pool || !out)
-        return fail(KVC_ERR_INVALID_ARG, "kvc_attend: NULL tensor");
-    if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out))
-        return fail(KVC_ERR_INVALID_ARG, "kvc_attend: q, out and pools must be 16-byte aligned");
-    if (q_stride < (int64_t)n_q_heads * c.head_dim || q_stride % 8 || q_stride > ((int64_t)1 << 38))
-        return fail(KVC_ERR_INVALID_ARG,
-                    "kvc_attend: q_stride must be a multiple of 8 and >= n_q_heads * head_dim");
-    if (!std::isfinite((float)(scale * kLog2e)))
-        return fail(KVC_ERR_INVALID_ARG, "kvc_attend: scale must be finite (times log2 e, too)");
-    const AttendWs w = attend_ws(c, n_q_heads / n_kv_heads);
-    if (w.needs.grid == 0) return fail(KVC_ERR_CUDA, "kvc_attend: no usable CUDA device");
-    if (!ws) return fail(KVC_ERR_WORKSPACE, "kvc_attend: workspace is NULL");
-    if (reinterpret_cast<uintptr_t>(ws) % 256)
-        return fail(KVC_ERR_WORKSPACE, "kvc_attend: workspace must be 256-byte aligned");
-    if (ws_bytes < w.total)
-        return fail(KVC_ERR_WORKSPACE, "kvc_attend: workspace has %zu bytes, needs %zu", ws_bytes, w.total);
-    char *base = static_cast<char *>(ws);
-    AttendParams p{};
-    p.n_seqs = n_seqs;
-    p.n_q_heads = n_q_heads;
-    p.n_kv_heads = n_kv_heads;
-    p.group = n_q_heads / n_kv_heads;
-    p.dim = c.head_dim;
-    p.n_pages = c.n_pages;
-    p.max_pages = c.max_pages;
-    while ((1 << p.shift) < c.page_rows) ++p.shift;
-    p.n_tokens = n_tokens;
-    p.max_new = max_new;
-    p.slots = w.needs.slots;
-    p.slot_rows = w.needs.slot_rows;
-    p.q_stride = q_stride;
-    p.q = q;
-    p.k_pool = k_pool;
-    p.v_pool = v_pool;
-    p.q_start = q_start;
-    p.table = table;
-    p.len = len;
-    p.out = out;
-    p.lse = lse;
-    p.scale_log2 = (float)(scale * kLog2e);
-    p.one_term = flags & KVC_ATTEND_BF16_P;
-    p.status = static_cast<uint32_t *>(ws);
-    p.arrived = reinterpret_cast<uint32_t *>(base + w.arrived);
-    p.stat = reinterpret_cast<float2 *>(base + w.stat);
-    p.group_stat = reinterpret_cast<float2 *>(base + w.group_stat);
-    p.part = reinterpret_cast<float *>(base + w.part);
-    return w.tc ? launch_attend_tc(p, w.needs.grid, stream)
-                : launch_attend_simt(p, c.dtype == KVC_F32, w.needs.grid, stream);
+    if (!cache_ok(cache, "kvc_quant_page_size") || !bits_ok(bits, "kvc_quant_page_size")) return 0;
+    return (size_t)(cache->page_rows / kQuantRows) * quant_block(bits, quant_groups(cache->head_dim));
+}
+
+int kvc_pages_append_quant(const kvc_cache *cache, int32_t bits, int32_t *table, int32_t *len, int32_t n_lists,
+                           const int32_t *counts, const int64_t *src_row, int64_t src_step, const void *k_src,
+                           const void *v_src, int64_t src_rows, void *k_pool, void *v_pool, void *state,
+                           size_t state_bytes, cudaStream_t stream) {
+    const char *fn = "kvc_pages_append_quant";
+    NvtxRange nvtx_range(fn);
+    set_error("%s", "");
+    if (!cache_ok(cache, fn) || !bits_ok(bits, fn) || !lists_ok(n_lists, fn)) return KVC_ERR_INVALID_ARG;
+    if (!table || !len || !counts || !src_row || (src_rows != 0 && (!k_src || !v_src)) || !k_pool || !v_pool)
+        return fail(KVC_ERR_INVALID_ARG, "%s: NULL tensor", fn);
+    if (!aligned16(k_src) || !aligned16(v_src) || !aligned16(k_pool) || !aligned16(v_pool))
+        return fail(KVC_ERR_INVALID_ARG, "%s: rows and pools must be 16-byte aligned", fn);
+    if (src_step < 0 || src_rows < 0)
+        return fail(KVC_ERR_INVALID_ARG, "%s: src_step and src_rows must be >= 0", fn);
+    PagesState s;
+    const int rc = state_of(*cache, n_lists, state, state_bytes, fn, &s);
+    if (rc) return rc;
+    const int sms = device_sms();
+    if (sms == 0) return fail(KVC_ERR_CUDA, "%s: no usable CUDA device", fn);
+    return launch_pages_append_quant(*cache, bits, s, table, len, n_lists, counts, src_row, src_step, k_src, v_src,
+                                     src_rows, k_pool, v_pool, sms, stream);
+}
+
+int kvc_pages_compact_quant(const kvc_cache *cache, int32_t bits, int32_t *table, int32_t *len, int32_t n_lists,
+                            const int32_t *idx, int32_t k_max, const int32_t *counts, void *k_pool, void *v_pool,
+                            void *state, size_t state_bytes, cudaStream_t stream) {
+    const char *fn = "kvc_pages_compact_quant";
+    NvtxRange nvtx_range(fn);
+    set_error("%s", "");
+    if (!cache_ok(cache, fn) || !bits_ok(bits, fn) || !lists_ok(n_lists, fn)) return KVC_ERR_INVALID_ARG;
+    if (!table || !len || !idx || !counts || !k_pool || !v_pool)
+        return fail(KVC_ERR_INVALID_ARG, "%s: NULL tensor", fn);
+    if (k_max < 1) return fail(KVC_ERR_INVALID_ARG, "%s: k_max must be >= 1", fn);
+    if (!aligned16(k_pool) || !aligned16(v_pool))
+        return fail(KVC_ERR_INVALID_ARG, "%s: pools must be 16-byte aligned", fn);
+    PagesState s;
+    const int rc = state_of(*cache, n_lists, state, state_bytes, fn, &s);
+    if (rc) return rc;
+    const int sms = device_sms();
+    if (sms == 0) return fail(KVC_ERR_CUDA, "%s: no usable CUDA device", fn);
+    return launch_pages_compact_quant(*cache, bits, s, table, len, n_lists, idx, k_max, counts, k_pool, v_pool, sms,
+                                      stream);
+}
+
+int kvc_pages_read_quant(const kvc_cache *cache, int32_t bits, const int32_t *table, const int32_t *len,
+                         int32_t n_lists, const int32_t *first, const int32_t *counts, const int64_t *dst_row,
+                         int64_t dst_step, const void *k_pool, const void *v_pool, void *k_dst, void *v_dst,
+                         int64_t dst_rows, void *state, size_t state_bytes, cudaStream_t stream) {
+    const char *fn = "kvc_pages_read_quant";
+    NvtxRange nvtx_range(fn);
+    set_error("%s", "");
+    if (!cache_ok(cache, fn) || !bits_ok(bits, fn) || !lists_ok(n_lists, fn)) return KVC_ERR_INVALID_ARG;
+    if (!table || !len || !counts || !dst_row || (k_dst && !k_pool) || (v_dst && !v_pool) ||
+        (dst_rows != 0 && !k_dst && !v_dst))
+        return fail(KVC_ERR_INVALID_ARG, "%s: NULL tensor", fn);
+    if (!aligned16(k_dst) || !aligned16(v_dst) || !aligned16(k_pool) || !aligned16(v_pool))
+        return fail(KVC_ERR_INVALID_ARG, "%s: rows and pools must be 16-byte aligned", fn);
+    if (dst_step < 0 || dst_rows < 0)
+        return fail(KVC_ERR_INVALID_ARG, "%s: dst_step and dst_rows must be >= 0", fn);
+    PagesState s;
+    const int rc = state_of(*cache, n_lists, state, state_bytes, fn, &s);
+    if (rc) return rc;
+    const int sms = device_sms();
+    if (sms == 0) return fail(KVC_ERR_CUDA, "%s: no usable CUDA device", fn);
+    return launch_pages_read_quant(*cache, bits, s, table, len, n_lists, first, counts, dst_row, dst_step, k_pool,
+                                   v_pool, k_dst, v_dst, dst_rows, sms, stream);
+}
+
+size_t kvc_attend_quant_workspace_size(const kvc_cache *cache, int32_t bits, int32_t n_q_heads, int32_t n_kv_heads,
+                                       int32_t n_seqs, int32_t max_new) {
+    const char *fn = "kvc_attend_quant_workspace_size";
+    if (!attend_shape_ok(cache, n_q_heads, n_kv_heads, n_seqs, max_new, fn) || !bits_ok(bits, fn)) return 0;
+    return attend_ws(*cache, bits, n_q_heads / n_kv_heads).total;
+}
+
+int kvc_attend_quant(const kvc_cache *cache, int32_t bits, int32_t n_q_heads, int32_t n_kv_heads, int32_t n_seqs,
+                     int32_t max_new, int64_t n_tokens, const void *q, int64_t q_stride, const int32_t *q_start,
+                     const int32_t *table, const int32_t *len, const void *k_pool, const void *v_pool, float scale,
+                     void *out, float *lse, uint32_t flags, void *ws, size_t ws_bytes, cudaStream_t stream) {
+    const char *fn = "kvc_attend_quant";
+    NvtxRange nvtx_range(fn);
+    if (!bits_ok(bits, fn)) return KVC_ERR_INVALID_ARG;
+    return attend_call(fn, bits, cache, n_q_heads, n_kv_heads, n_seqs, max_new, n_tokens, q, q_stride, q_start, table,
+                       len, k_pool, v_pool, scale, out, lse, flags, ws, ws_bytes, stream);
 }
 
 }  // extern "C"

@@ -1,5 +1,5 @@
 // attend.cuh -- the work split and the joining of partial results that both
-// attention kernels (attend_simt.cu, attend_tc.cu) share.
+// attention kernels (attend_simt.cuh, attend_tc.cu) share.
 //
 // Rows: the G query heads of a KV head stand side by side, row r of a list =
 // token r / G, query head r % G of the group, so every key tile is read once
@@ -23,6 +23,7 @@ namespace kvc {
 
 struct AttendParams {
     int n_seqs, n_q_heads, n_kv_heads, group, dim;
+    int bits;            // of the pools' rows (quant.cuh); 0: rows of the outputs' type
     Divider by_group, by_heads, by_blocks;
     int n_pages, max_pages, shift;
     int64_t n_tokens;
@@ -512,8 +513,10 @@ inline bool attend_units(AttendParams &p, int unit_rows, int rows_above, int row
     p.by_quads = Divider((uint32_t)p.dim / 4);
     return n < INT_MAX;
 }
-// Both set the units' shape.
+// All set the units' shape.
 int launch_attend_simt(AttendParams &p, bool f32, int grid, cudaStream_t st);
+int launch_attend_simt_quant4(AttendParams &p, bool f32, int grid, cudaStream_t st);
+int launch_attend_simt_quant8(AttendParams &p, bool f32, int grid, cudaStream_t st);
 int launch_attend_tc(AttendParams &p, int grid, cudaStream_t st);
 
 }  // namespace kvc

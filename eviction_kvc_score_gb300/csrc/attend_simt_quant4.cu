@@ -1,0 +1,10 @@
+// attend_simt_quant4.cu -- the CUDA cores' attention over rows held in 4 bits.
+#include "attend_simt.cuh"
+
+namespace kvc {
+
+int launch_attend_simt_quant4(AttendParams &p, bool f32, int grid, cudaStream_t st) {
+    return launch_all<4>(p, f32, grid, st);
+}
+
+}  // namespace kvc

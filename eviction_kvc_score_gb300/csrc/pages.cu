@@ -16,60 +16,13 @@
 // rate.  The plan is a chain of memory latencies, 7 us for a few pages and 12 us
 // for 9,000 with cold caches; while each thread wrote down the pages of its own word
 // it took 4 us more.
-#include "cache.cuh"
+#include "pages.cuh"
 
 namespace kvc {
 
 namespace {
 
-constexpr int kPlanThreads = 1024;
-constexpr int kMoveThreads = 256;
 constexpr int kListThreads = 128;
-
-struct PlanParams {
-    PagesState s;
-    int32_t *table, *len;
-    const int32_t *counts;
-    const int64_t *src_row;   // append only
-    int64_t src_step, src_rows;
-    int32_t n_lists, n_pages, max_pages, shift, k_max;
-    bool append;
-};
-
-struct Two {
-    int64_t rows, pages;
-};
-
-__device__ __forceinline__ Two operator+(Two a, Two b) { return {a.rows + b.rows, a.pages + b.pages}; }
-
-// Exclusive scan over the block; *total receives the sum.  scratch: 33 entries.
-__device__ Two block_scan(Two v, Two *scratch, Two *total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    Two x = v;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const Two y{__shfl_up_sync(0xffffffffu, x.rows, d), __shfl_up_sync(0xffffffffu, x.pages, d)};
-        if (lane >= d) x = x + y;
-    }
-    if (lane == 31) scratch[warp] = x;
-    __syncthreads();
-    if (warp == 0) {
-        Two w = lane < (int)(blockDim.x >> 5) ? scratch[lane] : Two{0, 0};
-        const Two own = w;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const Two y{__shfl_up_sync(0xffffffffu, w.rows, d), __shfl_up_sync(0xffffffffu, w.pages, d)};
-            if (lane >= d) w = w + y;
-        }
-        if (lane == 31) scratch[32] = w;
-        scratch[lane] = {w.rows - own.rows, w.pages - own.pages};
-    }
-    __syncthreads();
-    const Two r{scratch[warp].rows + x.rows - v.rows, scratch[warp].pages + x.pages - v.pages};
-    *total = scratch[32];
-    __syncthreads();
-    return r;
-}
 
 // Count a page's holder away; pages nobody holds become free.  Every thread of
 // the warp calls it (page < 0: nothing to let go of).
@@ -289,57 +242,12 @@ __global__ void __launch_bounds__(kPlanThreads) pages_plan_kernel(PlanParams p) 
     }
 }
 
-struct MoveParams {
-    PagesState s;
-    int32_t *table;
-    const int64_t *src_row;   // append: rows of the source
-    int64_t src_step;
-    const int32_t *idx;       // compact: rows of the list itself
-    int32_t n_lists, n_pages, max_pages, shift, k_max;
+struct MoveParams : MoveLists {
     int vec;                  // 16-byte vectors per row
     Divider by_vec;
     const uint4 *k_src, *v_src;
     uint4 *k_pool, *v_pool;
 };
-
-// Last i of [0, n) with begin[i] <= x (begin ascends from 0); the whole warp
-// asks for one x, 32 places at a time.
-template <typename T>
-__device__ __forceinline__ int owner(const T *begin, int n, T x) {
-    const int lane = threadIdx.x & 31;
-    int lo = 0, span = n;
-    while (span > 1) {
-        const int step = (span + 31) >> 5, i = lo + lane * step;
-        const unsigned below = __ballot_sync(0xffffffffu, lane * step < span && begin[i] <= x);
-        const int k = 31 - __clz(below);
-        span = min(step, span - k * step);
-        lo += k * step;
-    }
-    return lo;
-}
-
-// The same for one lane that knows an i with begin[i] <= x: the next list's where x
-// is past it, further on by doubled steps and halving, because lists without rows
-// (all but one sequence's, when that sequence's prompt is appended) may stand
-// between by the hundred thousand (2 x 12,000 rows in 262,144 lists: 15.5 ms one
-// list after the other, 0.43 so).
-template <typename T>
-__device__ __forceinline__ int owner_from(const T *begin, int n, T x, int i) {
-    if (i + 1 >= n || begin[i + 1] > x) return i;
-    int lo = i + 1, step = 1;
-    while (lo + step < n && begin[lo + step] <= x) {
-        lo += step;
-        step = min(2 * step, n);
-    }
-    for (int hi = min(n, lo + step); hi - lo > 1;) {
-        const int mid = lo + (hi - lo) / 2;
-        if (begin[mid] <= x)
-            lo = mid;
-        else
-            hi = mid;
-    }
-    return lo;
-}
 
 template <bool APPEND>
 __global__ void __launch_bounds__(kMoveThreads) pages_move_kernel(MoveParams p) {
@@ -347,22 +255,10 @@ __global__ void __launch_bounds__(kMoveThreads) pages_move_kernel(MoveParams p) 
     wait_for_inputs();
     if (!p.s.head->ok) return;
     const int64_t rows = p.s.head->total_rows;
-    const int ps = 1 << p.shift, lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31;
     const int64_t warps = (int64_t)gridDim.x * (kMoveThreads / 32);
     const int64_t me = ((int64_t)blockIdx.x * kMoveThreads + threadIdx.x) >> 5;
-    if (APPEND) {   // the new pages' table entries, 32 a warp
-        const int total_new = p.s.head->total_new;
-        for (int64_t e0 = me * 32; e0 < total_new; e0 += warps * 32) {
-            int i = owner(p.s.page_begin, p.n_lists, (int32_t)e0);
-            const int e = (int)e0 + lane;
-            if (e >= total_new) continue;
-            i = owner_from(p.s.page_begin, p.n_lists, (int32_t)e, i);
-            const int32_t len = p.s.old_len[i];
-            const int first = p.s.shared[i] >= 0 ? len >> p.shift : (len + ps - 1) >> p.shift;
-            p.table[(int64_t)i * p.max_pages + first + (e - p.s.page_begin[i])] = p.s.fresh[e];
-        }
-        __syncwarp();
-    }
+    if (APPEND) enter_pages(p, me, warps);
     const int64_t per = (rows + warps - 1) / warps;
     const int64_t r0 = me * per, r1 = min(rows, r0 + per);
     if (r0 >= r1) return;
@@ -373,48 +269,14 @@ __global__ void __launch_bounds__(kMoveThreads) pages_move_kernel(MoveParams p) 
         const int dr = p.by_vec(it), u = it - dr * p.vec;
         const int64_t r = r0 + dr;
         i = owner_from(p.s.row_begin, p.n_lists, r, i);
-        const int64_t *begin = p.s.row_begin;
-        int32_t at = (int32_t)(r - begin[i]);   // row within the list's moved rows
-        const int32_t *fresh = p.s.fresh + p.s.page_begin[i];
-        const int32_t *entry = p.table + (int64_t)i * p.max_pages;
-        int64_t from = -1, to;
-        bool own_pool = true;
-        if (APPEND) {
-            const int32_t len = p.s.old_len[i], shared = p.s.shared[i], fill = len & (ps - 1);
-            const int first = shared >= 0 ? len >> p.shift : (len + ps - 1) >> p.shift;
-            int32_t pos;
-            if (shared >= 0 && at < fill) {
-                from = ((int64_t)shared << p.shift) + at;
-                pos = (len - fill) + at;
-            } else {
-                if (shared >= 0) at -= fill;
-                from = p.src_row[i] + at * p.src_step;
-                own_pool = false;
-                pos = len + at;
-            }
-            const int slot = pos >> p.shift;
-            const int32_t page = slot >= first ? fresh[slot - first] : entry[slot];
-            to = ((int64_t)page << p.shift) + (pos & (ps - 1));
-        } else {
-            const int32_t src = p.idx[(int64_t)i * p.k_max + at];
-            if (src >= 0 && src < p.s.old_len[i]) {
-                const int32_t page = entry[src >> p.shift];
-                if (page >= 0 && page < p.n_pages)
-                    from = ((int64_t)page << p.shift) + (src & (ps - 1));
-                else
-                    bad |= KVC_DEV_BAD_PAGE;
-            } else {
-                bad |= KVC_DEV_BAD_LIST;
-            }
-            to = ((int64_t)fresh[at >> p.shift] << p.shift) + (at & (ps - 1));
-        }
+        const MovedRow m = moved_row<APPEND>(p, i, r, &bad);
         uint4 kk = make_uint4(0, 0, 0, 0), vv = kk;
-        if (from >= 0) {
-            kk = (own_pool ? p.k_pool : p.k_src)[from * p.vec + u];
-            vv = (own_pool ? p.v_pool : p.v_src)[from * p.vec + u];
+        if (m.from >= 0) {
+            kk = (m.own_pool ? p.k_pool : p.k_src)[m.from * p.vec + u];
+            vv = (m.own_pool ? p.v_pool : p.v_src)[m.from * p.vec + u];
         }
-        p.k_pool[to * p.vec + u] = kk;
-        p.v_pool[to * p.vec + u] = vv;
+        p.k_pool[m.to * p.vec + u] = kk;
+        p.v_pool[m.to * p.vec + u] = vv;
     }
     if (!APPEND && bad) set_status(&p.s.head->status, bad);
 }
@@ -505,17 +367,21 @@ __global__ void __launch_bounds__(kListThreads)
     if (threadIdx.x == 0) len[i] = n;
 }
 
-int log2_of(int x) {
-    int s = 0;
-    while ((1 << s) < x) ++s;
-    return s;
-}
-
 }  // namespace
 
 int launch_pages_init(const kvc_cache &c, const PagesState &s, cudaStream_t st) {
     pages_init_kernel<<<256, 256, 0, st>>>(s, c.n_pages);
     return cache_launched("kvc_pages_init");
+}
+
+void launch_pages_plan(const PlanParams &p, cudaStream_t st) {
+    launch_early(pages_plan_kernel, 1, kPlanThreads, 0, st, p);
+}
+
+void launch_pages_swap(const kvc_cache &c, const PagesState &s, int32_t *table, int32_t *len, int32_t n_lists,
+                       const int32_t *counts, cudaStream_t st) {
+    launch_early(pages_swap_kernel, n_lists, kListThreads, 0, st, s, table, len, counts, c.n_pages, c.max_pages,
+                 log2_of(c.page_rows));
 }
 
 int launch_pages_append(const kvc_cache &c, const PagesState &s, int32_t *table, int32_t *len,
@@ -525,9 +391,9 @@ int launch_pages_append(const kvc_cache &c, const PagesState &s, int32_t *table,
     const int shift = log2_of(c.page_rows);
     PlanParams p{s, table, len, counts, src_row, src_step, src_rows, n_lists, c.n_pages, c.max_pages,
                  shift, 0, true};
-    launch_early(pages_plan_kernel, 1, kPlanThreads, 0, st, p);
+    launch_pages_plan(p, st);
     const int vec = c.head_dim * (c.dtype == KVC_F32 ? 4 : 2) / 16;
-    MoveParams m{s, table, src_row, src_step, nullptr, n_lists, c.n_pages, c.max_pages, shift, 0, vec, Divider(vec),
+    MoveParams m{{s, table, src_row, src_step, nullptr, n_lists, c.n_pages, c.max_pages, shift, 0}, vec, Divider(vec),
                  static_cast<const uint4 *>(k_src), static_cast<const uint4 *>(v_src),
                  static_cast<uint4 *>(k_pool), static_cast<uint4 *>(v_pool)};
     launch_early(pages_move_kernel<true>, sms * 8, kMoveThreads, 0, st, m);
@@ -540,13 +406,12 @@ int launch_pages_compact(const kvc_cache &c, const PagesState &s, int32_t *table
     const int shift = log2_of(c.page_rows);
     PlanParams p{s, table, len, counts, nullptr, 0, 0, n_lists, c.n_pages, c.max_pages, shift, k_max,
                  false};
-    launch_early(pages_plan_kernel, 1, kPlanThreads, 0, st, p);
+    launch_pages_plan(p, st);
     const int vec = c.head_dim * (c.dtype == KVC_F32 ? 4 : 2) / 16;
-    MoveParams m{s, table, nullptr, 0, idx, n_lists, c.n_pages, c.max_pages, shift, k_max, vec, Divider(vec),
+    MoveParams m{{s, table, nullptr, 0, idx, n_lists, c.n_pages, c.max_pages, shift, k_max}, vec, Divider(vec),
                  nullptr, nullptr, static_cast<uint4 *>(k_pool), static_cast<uint4 *>(v_pool)};
     launch_early(pages_move_kernel<false>, sms * 8, kMoveThreads, 0, st, m);
-    launch_early(pages_swap_kernel, n_lists, kListThreads, 0, st, s, table, len, counts, c.n_pages,
-                 c.max_pages, shift);
+    launch_pages_swap(c, s, table, len, n_lists, counts, st);
     return cache_launched("kvc_pages_compact");
 }
 

@@ -99,6 +99,14 @@ _SIGS = {
                              _p, _p, _sz, _p]),
     "kvc_attend_ex": (C.c_int, [_cp, _i32, _i32, _i32, _i32, _i64, _p, _i64, _p, _p, _p, _p, _p, _f, _p,
                                 _p, _u32, _p, _sz, _p]),
+    "kvc_quant_page_size": (_sz, [_cp, _i32]),
+    "kvc_pages_append_quant": (C.c_int, [_cp, _i32, _p, _p, _i32, _p, _p, _i64, _p, _p, _i64, _p, _p, _p, _sz, _p]),
+    "kvc_pages_compact_quant": (C.c_int, [_cp, _i32, _p, _p, _i32, _p, _i32, _p, _p, _p, _p, _sz, _p]),
+    "kvc_pages_read_quant": (C.c_int, [_cp, _i32, _p, _p, _i32, _p, _p, _p, _i64, _p, _p, _p, _p, _i64, _p, _sz,
+                                       _p]),
+    "kvc_attend_quant_workspace_size": (_sz, [_cp, _i32, _i32, _i32, _i32, _i32]),
+    "kvc_attend_quant": (C.c_int, [_cp, _i32, _i32, _i32, _i32, _i32, _i64, _p, _i64, _p, _p, _p, _p, _p, _f,
+                                   _p, _p, _u32, _p, _sz, _p]),
     "kvc_keep_channels": (_i32, [_d, _i32]),
     "kvc_status_string": (C.c_char_p, [C.c_int]),
     "kvc_last_error": (C.c_char_p, []),
@@ -536,6 +544,89 @@ def kvc_attend_ex(c: KvcCache, q, q_start, table, lens, k_pool, v_pool, max_new:
     _check("kvc_attend", _lib.kvc_attend_ex(
         C.byref(c), hq, n_lists // n_seqs, n_seqs, max_new, n, qp, qs,
         _at(q_start, "q_start", torch.int32, dev), t, n_len, *_pools(c, k_pool, v_pool, dev),
+        dim ** -0.5 if scale is None else scale, _at(out, "out", dt, dev, n * hq * dim),
+        _at(lse, "lse", torch.float32, dev, n * hq), flags,
+        *_bytes(ws, "workspace", dev), _handle(stream, dev)))
+
+
+# --- the paged cache in 4 or 8 bits -----------------------------------------
+
+def kvc_quant_page_size(c: KvcCache, bits: int) -> int:
+    """Bytes of one page of a pool held in so many bits: pools are uint8 tensors
+    of c.n_pages times as many."""
+    n = _lib.kvc_quant_page_size(C.byref(c), int(bits))
+    if n == 0:
+        raise KvcError("kvc_quant_page_size", -1, _lib.kvc_last_error().decode())
+    return n
+
+
+def _quant_pools(c: KvcCache, bits, k_pool, v_pool, dev):
+    n = c.n_pages * _lib.kvc_quant_page_size(C.byref(c), bits)   # 0: the call itself refuses
+    return _at(k_pool, "k_pool", torch.uint8, dev, n), _at(v_pool, "v_pool", torch.uint8, dev, n)
+
+
+def kvc_pages_append_quant(c: KvcCache, bits: int, table, lens, counts, src_row, src_step: int, k_src, v_src,
+                           k_pool, v_pool, state, stream=None) -> None:
+    """kvc_pages_append into pools held in 4 or 8 bits (uint8 tensors)."""
+    dev, t, n_len, n = _lists(c, table, lens)
+    dt = _DTYPES[c.dtype]
+    rows = min(k_src.numel(), v_src.numel()) // c.head_dim
+    _check("kvc_pages_append_quant", _lib.kvc_pages_append_quant(
+        C.byref(c), bits, t, n_len, n, _at(counts, "counts", torch.int32, dev, n),
+        _at(src_row, "src_row", torch.int64, dev, n), src_step, _at(k_src, "k_src", dt, dev),
+        _at(v_src, "v_src", dt, dev), rows, *_quant_pools(c, bits, k_pool, v_pool, dev),
+        *_bytes(state, "state", dev), _handle(stream, dev)))
+
+
+def kvc_pages_compact_quant(c: KvcCache, bits: int, table, lens, idx, counts, k_pool, v_pool, state,
+                            stream=None) -> None:
+    """kvc_pages_compact of pools held in 4 or 8 bits: rows are moved as they are."""
+    dev, t, n_len, n = _lists(c, table, lens)
+    k_max = idx.shape[-1]
+    _check("kvc_pages_compact_quant", _lib.kvc_pages_compact_quant(
+        C.byref(c), bits, t, n_len, n, _at(idx, "idx", torch.int32, dev, n * k_max), k_max,
+        _at(counts, "counts", torch.int32, dev, n), *_quant_pools(c, bits, k_pool, v_pool, dev),
+        *_bytes(state, "state", dev), _handle(stream, dev)))
+
+
+def kvc_pages_read_quant(c: KvcCache, bits: int, table, lens, first, counts, dst_row, dst_step: int, k_pool, v_pool,
+                         k_dst, v_dst, state, stream=None) -> None:
+    """What rows first[i] .. first[i] + counts[i] - 1 of every list i stand for, to
+    rows dst_row[i] + r * dst_step of k_dst and v_dst (rows of head_dim elements of
+    the cache's type); first None: from row 0; either pool and its k_dst or v_dst
+    may be None."""
+    dev, t, n_len, n = _lists(c, table, lens)
+    dt = _DTYPES[c.dtype]
+    rows = min(x.numel() for x in (k_dst, v_dst) if x is not None) // c.head_dim if (
+        k_dst is not None or v_dst is not None) else 0
+    _check("kvc_pages_read_quant", _lib.kvc_pages_read_quant(
+        C.byref(c), bits, t, n_len, n, _at(first, "first", torch.int32, dev, n),
+        _at(counts, "counts", torch.int32, dev, n), _at(dst_row, "dst_row", torch.int64, dev, n), dst_step,
+        *_quant_pools(c, bits, k_pool, v_pool, dev), _at(k_dst, "k_dst", dt, dev), _at(v_dst, "v_dst", dt, dev), rows,
+        *_bytes(state, "state", dev), _handle(stream, dev)))
+
+
+def kvc_attend_quant_workspace_size(c: KvcCache, bits: int, n_q_heads: int, n_kv_heads: int, n_seqs: int,
+                                    max_new: int) -> int:
+    n = _lib.kvc_attend_quant_workspace_size(C.byref(c), int(bits), int(n_q_heads), int(n_kv_heads), int(n_seqs),
+                                             int(max_new))
+    if n == 0:
+        raise KvcError("kvc_attend_quant_workspace_size", -1, _lib.kvc_last_error().decode())
+    return n
+
+
+def kvc_attend_quant(c: KvcCache, bits: int, q, q_start, table, lens, k_pool, v_pool, max_new: int, out, ws,
+                     lse=None, scale: Optional[float] = None, flags: int = 0, stream=None) -> None:
+    """kvc_attend_ex over pools held in 4 or 8 bits (uint8 tensors)."""
+    dev, t, n_len, n_lists = _lists(c, table, lens)
+    n_seqs = q_start.numel() - 1
+    if n_seqs < 1 or n_lists % n_seqs:
+        raise ValueError("table must hold the same number of lists for every sequence of q_start")
+    dt, n, dim = _DTYPES[c.dtype], q.shape[0], c.head_dim
+    hq, qp, qs = _heads(q, "q", dt, dev, n, dim)
+    _check("kvc_attend_quant", _lib.kvc_attend_quant(
+        C.byref(c), bits, hq, n_lists // n_seqs, n_seqs, max_new, n, qp, qs,
+        _at(q_start, "q_start", torch.int32, dev), t, n_len, *_quant_pools(c, bits, k_pool, v_pool, dev),
         dim ** -0.5 if scale is None else scale, _at(out, "out", dt, dev, n * hq * dim),
         _at(lse, "lse", torch.float32, dev, n * hq), flags,
         *_bytes(ws, "workspace", dev), _handle(stream, dev)))

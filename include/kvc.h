@@ -568,6 +568,67 @@ int kvc_attend_ex(const kvc_cache *cache, int32_t n_q_heads, int32_t n_kv_heads,
                   const void *k_pool, const void *v_pool, float scale, void *out, float *lse,
                   uint32_t flags, void *ws, size_t ws_bytes, cudaStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * The paged cache in 4 or 8 bits.
+ *
+ * Lists, tables, lengths, pages and the pages' state are those above, and so are
+ * kvc_pages_init, _status, _fork and _truncate, which touch no rows; only what a
+ * row of the pools is made of differs.  cache->dtype is the type of the rows as
+ * they are written and read back and of q and out; `bits`, 4 or 8, is the same in
+ * every call on a pool.  A pool is n_pages * kvc_quant_page_size() bytes, 16-byte
+ * aligned; a page's bytes hang on nothing outside the page, so pages may be copied.
+ *
+ * A row is cut into groups of 32 channels (the last one filled up with zeros).
+ * A group of values x has codes n of `bits` bits, a step s and a zero code z, and
+ * stands for (n - z) s.  With N = 2^bits - 1, lo = min(0, min x), hi = max(0, max x)
+ * and fl() the rounding to fp32:
+ *   s = fl((hi/2 - lo/2) / (N/2)), rounded up to four significant bits (4 bits) or
+ *       to a power of two (8 bits), and at least 2^-126;
+ *   z = rint(fl(-lo fl(1/s))), n = min(max(rint(fl(x fl(1/s))) + z, 0), N).
+ * (n - z) s is exact in bf16.  It is within half a step of x, one where n was cut to
+ * N; a group's step is at most 1.125 (4 bits) or 2 times (hi - lo) / N.  A value that
+ * is 0 stays 0.  A group with a value of 2^126 or more in size, an infinity or a NaN
+ * stands for NaN throughout.  A row takes 4.5 or 8.5 bits per channel.
+ * ------------------------------------------------------------------------ */
+
+/* Bytes of one page of either pool (0 if an argument is invalid). */
+size_t kvc_quant_page_size(const kvc_cache *cache, int32_t bits);
+
+/* kvc_pages_append into such pools: the rows of k_src and v_src (of cache->dtype)
+ * are quantised as they are written.  Everything else is as there. */
+int kvc_pages_append_quant(const kvc_cache *cache, int32_t bits, int32_t *table, int32_t *len, int32_t n_lists,
+                           const int32_t *counts, const int64_t *src_row, int64_t src_step, const void *k_src,
+                           const void *v_src, int64_t src_rows, void *k_pool, void *v_pool, void *state,
+                           size_t state_bytes, cudaStream_t stream);
+
+/* kvc_pages_compact of such pools: rows are moved as they are, never quantised
+ * again. */
+int kvc_pages_compact_quant(const kvc_cache *cache, int32_t bits, int32_t *table, int32_t *len, int32_t n_lists,
+                            const int32_t *idx, int32_t k_max, const int32_t *counts, void *k_pool, void *v_pool,
+                            void *state, size_t state_bytes, cudaStream_t stream);
+
+/* What the rows stand for: rows first[i] .. first[i] + counts[i] - 1 (none where
+ * counts[i] <= 0; first NULL: 0) of every list i go to rows dst_row[i] + r * dst_step
+ * of k_dst and v_dst, [dst_rows][D] of cache->dtype.  Either may be NULL (with its
+ * pool): K or V alone.  Rows outside a list or outside dst (KVC_DEV_BAD_LIST) leave
+ * everything unread; a page outside the pool gives rows of zeros
+ * (KVC_DEV_BAD_PAGE).  Two destinations of one row are written in no order.  The
+ * state lends the call its scratch and takes the status; dst overlaps no input,
+ * dst_step >= 0. */
+int kvc_pages_read_quant(const kvc_cache *cache, int32_t bits, const int32_t *table, const int32_t *len,
+                         int32_t n_lists, const int32_t *first, const int32_t *counts, const int64_t *dst_row,
+                         int64_t dst_step, const void *k_pool, const void *v_pool, void *k_dst, void *v_dst,
+                         int64_t dst_rows, void *state, size_t state_bytes, cudaStream_t stream);
+
+/* kvc_attend_ex over what the rows of such pools stand for, with its arguments,
+ * flags and guarantees; a row's NaN reaches the tokens that see it, and no others. */
+size_t kvc_attend_quant_workspace_size(const kvc_cache *cache, int32_t bits, int32_t n_q_heads, int32_t n_kv_heads,
+                                       int32_t n_seqs, int32_t max_new);
+int kvc_attend_quant(const kvc_cache *cache, int32_t bits, int32_t n_q_heads, int32_t n_kv_heads, int32_t n_seqs,
+                     int32_t max_new, int64_t n_tokens, const void *q, int64_t q_stride, const int32_t *q_start,
+                     const int32_t *table, const int32_t *len, const void *k_pool, const void *v_pool, float scale,
+                     void *out, float *lse, uint32_t flags, void *ws, size_t ws_bytes, cudaStream_t stream);
+
 const char *kvc_status_string(int status);
 
 /* Message for the last error returned on the calling thread ("" if none). */

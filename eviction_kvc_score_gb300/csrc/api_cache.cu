@@ -85,9 +85,9 @@ struct AttendWs {
     size_t arrived, stat, group_stat, part, total;
 };
 
-AttendWs attend_ws(const kvc_cache &c, int bits, int group) {
+AttendWs attend_ws(const kvc_cache &c, int group) {
     AttendWs w;
-    w.tc = bits == 0 && attend_tc_takes(c.dtype, c.head_dim, group);
+    w.tc = attend_tc_takes(c.dtype, c.head_dim, group);
     w.needs = w.tc ? attend_tc_needs(device_sms()) : attend_simt_needs(device_sms());
     const size_t rows = (size_t)w.needs.grid * w.needs.slots * w.needs.slot_rows;
     w.arrived = kWsHeader;
@@ -136,7 +136,7 @@ int attend_call(const char *fn, int bits, const kvc_cache *cache, int32_t n_q_he
                     "%s: q_stride must be a multiple of 8 and >= n_q_heads * head_dim", fn);
     if (!std::isfinite((float)(scale * kLog2e)))
         return fail(KVC_ERR_INVALID_ARG, "%s: scale must be finite (times log2 e, too)", fn);
-    const AttendWs w = attend_ws(c, bits, n_q_heads / n_kv_heads);
+    const AttendWs w = attend_ws(c, n_q_heads / n_kv_heads);
     if (w.needs.grid == 0) return fail(KVC_ERR_CUDA, "%s: no usable CUDA device", fn);
     if (!ws) return fail(KVC_ERR_WORKSPACE, "%s: workspace is NULL", fn);
     if (reinterpret_cast<uintptr_t>(ws) % 256)
@@ -175,6 +175,7 @@ int attend_call(const char *fn, int bits, const kvc_cache *cache, int32_t n_q_he
     p.group_stat = reinterpret_cast<float2 *>(base + w.group_stat);
     p.part = reinterpret_cast<float *>(base + w.part);
     const bool f32 = c.dtype == KVC_F32;
+    if (bits != 0 && w.tc) return launch_attend_tc_quant(p, 0, w.needs.grid, stream);
     if (bits != 0)
         return bits == 4 ? launch_attend_simt_quant4(p, f32, w.needs.grid, stream)
                          : launch_attend_simt_quant8(p, f32, w.needs.grid, stream);
@@ -363,7 +364,7 @@ size_t kvc_attend_workspace_size(const kvc_cache *cache, int32_t n_q_heads, int3
                                  int32_t n_seqs, int32_t max_new) {
     if (!attend_shape_ok(cache, n_q_heads, n_kv_heads, n_seqs, max_new, "kvc_attend_workspace_size"))
         return 0;
-    return attend_ws(*cache, 0, n_q_heads / n_kv_heads).total;
+    return attend_ws(*cache, n_q_heads / n_kv_heads).total;
 }
 
 int kvc_attend(const kvc_cache *cache, int32_t n_q_heads, int32_t n_kv_heads, int32_t n_seqs,
@@ -463,18 +464,18 @@ size_t kvc_attend_quant_workspace_size(const kvc_cache *cache, int32_t bits, int
                                        int32_t n_seqs, int32_t max_new) {
     const char *fn = "kvc_attend_quant_workspace_size";
     if (!attend_shape_ok(cache, n_q_heads, n_kv_heads, n_seqs, max_new, fn) || !bits_ok(bits, fn)) return 0;
-    return attend_ws(*cache, bits, n_q_heads / n_kv_heads).total;
+    return attend_ws(*cache, n_q_heads / n_kv_heads).total;
 }
 
 int kvc_attend_quant(const kvc_cache *cache, int32_t bits, int32_t n_q_heads, int32_t n_kv_heads, int32_t n_seqs,
                      int32_t max_new, int64_t n_tokens, const void *q, int64_t q_stride, const int32_t *q_start,
                      const int32_t *table, const int32_t *len, const void *k_pool, const void *v_pool, float scale,
-                     void *out, float *lse, uint32_t flags, void *ws, size_t ws_bytes, cudaStream_t stream) {
+                     void *out, float *lse, void *ws, size_t ws_bytes, cudaStream_t stream) {
     const char *fn = "kvc_attend_quant";
     NvtxRange nvtx_range(fn);
     if (!bits_ok(bits, fn)) return KVC_ERR_INVALID_ARG;
     return attend_call(fn, bits, cache, n_q_heads, n_kv_heads, n_seqs, max_new, n_tokens, q, q_stride, q_start, table,
-                       len, k_pool, v_pool, scale, out, lse, flags, ws, ws_bytes, stream);
+                       len, k_pool, v_pool, scale, out, lse, 0, ws, ws_bytes, stream);
 }
 
 }  // extern "C"

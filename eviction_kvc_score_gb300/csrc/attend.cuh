@@ -1,5 +1,5 @@
 // attend.cuh -- the work split and the joining of partial results that both
-// attention kernels (attend_simt.cuh, attend_tc.cu) share.
+// attention kernels (attend_simt.cuh, attend_tc.cuh) share.
 //
 // Rows: the G query heads of a KV head stand side by side, row r of a list =
 // token r / G, query head r % G of the group, so every key tile is read once
@@ -518,5 +518,7 @@ int launch_attend_simt(AttendParams &p, bool f32, int grid, cudaStream_t st);
 int launch_attend_simt_quant4(AttendParams &p, bool f32, int grid, cudaStream_t st);
 int launch_attend_simt_quant8(AttendParams &p, bool f32, int grid, cudaStream_t st);
 int launch_attend_tc(AttendParams &p, int grid, cudaStream_t st);
+// Lists of more than rows_above rows.
+int launch_attend_tc_quant(AttendParams &p, int rows_above, int grid, cudaStream_t st);
 
 }  // namespace kvc

@@ -106,7 +106,7 @@ _SIGS = {
                                        _p]),
     "kvc_attend_quant_workspace_size": (_sz, [_cp, _i32, _i32, _i32, _i32, _i32]),
     "kvc_attend_quant": (C.c_int, [_cp, _i32, _i32, _i32, _i32, _i32, _i64, _p, _i64, _p, _p, _p, _p, _p, _f,
-                                   _p, _p, _u32, _p, _sz, _p]),
+                                   _p, _p, _p, _sz, _p]),
     "kvc_keep_channels": (_i32, [_d, _i32]),
     "kvc_status_string": (C.c_char_p, [C.c_int]),
     "kvc_last_error": (C.c_char_p, []),
@@ -616,8 +616,8 @@ def kvc_attend_quant_workspace_size(c: KvcCache, bits: int, n_q_heads: int, n_kv
 
 
 def kvc_attend_quant(c: KvcCache, bits: int, q, q_start, table, lens, k_pool, v_pool, max_new: int, out, ws,
-                     lse=None, scale: Optional[float] = None, flags: int = 0, stream=None) -> None:
-    """kvc_attend_ex over pools held in 4 or 8 bits (uint8 tensors)."""
+                     lse=None, scale: Optional[float] = None, stream=None) -> None:
+    """kvc_attend over pools held in 4 or 8 bits (uint8 tensors)."""
     dev, t, n_len, n_lists = _lists(c, table, lens)
     n_seqs = q_start.numel() - 1
     if n_seqs < 1 or n_lists % n_seqs:
@@ -628,7 +628,7 @@ def kvc_attend_quant(c: KvcCache, bits: int, q, q_start, table, lens, k_pool, v_
         C.byref(c), bits, hq, n_lists // n_seqs, n_seqs, max_new, n, qp, qs,
         _at(q_start, "q_start", torch.int32, dev), t, n_len, *_quant_pools(c, bits, k_pool, v_pool, dev),
         dim ** -0.5 if scale is None else scale, _at(out, "out", dt, dev, n * hq * dim),
-        _at(lse, "lse", torch.float32, dev, n * hq), flags,
+        _at(lse, "lse", torch.float32, dev, n * hq),
         *_bytes(ws, "workspace", dev), _handle(stream, dev)))
 
 

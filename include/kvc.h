@@ -620,14 +620,19 @@ int kvc_pages_read_quant(const kvc_cache *cache, int32_t bits, const int32_t *ta
                          int64_t dst_step, const void *k_pool, const void *v_pool, void *k_dst, void *v_dst,
                          int64_t dst_rows, void *state, size_t state_bytes, cudaStream_t stream);
 
-/* kvc_attend_ex over what the rows of such pools stand for, with its arguments,
- * flags and guarantees; a row's NaN reaches the tokens that see it, and no others. */
+/* kvc_attend over what the rows of such pools stand for, with its arguments and
+ * guarantees; a row's NaN reaches the tokens that see it, and no others.  On the
+ * tensor cores (as there: bf16, D 64 or 128) probabilities are rounded to fp16, 11
+ * bits, for the product with V, and taken times the rows' steps in fp16: what a row
+ * adds is then right to 2^-10 of (n + z) s where its step is above 2^-20 of the
+ * list's largest and its probability above 2^-20 of the row's largest, and to 2^-30
+ * of those two below. */
 size_t kvc_attend_quant_workspace_size(const kvc_cache *cache, int32_t bits, int32_t n_q_heads, int32_t n_kv_heads,
                                        int32_t n_seqs, int32_t max_new);
 int kvc_attend_quant(const kvc_cache *cache, int32_t bits, int32_t n_q_heads, int32_t n_kv_heads, int32_t n_seqs,
                      int32_t max_new, int64_t n_tokens, const void *q, int64_t q_stride, const int32_t *q_start,
                      const int32_t *table, const int32_t *len, const void *k_pool, const void *v_pool, float scale,
-                     void *out, float *lse, uint32_t flags, void *ws, size_t ws_bytes, cudaStream_t stream);
+                     void *out, float *lse, void *ws, size_t ws_bytes, cudaStream_t stream);
 
 const char *kvc_status_string(int status);
 

@@ -39,8 +39,8 @@ def read(kvc, c, bits=4, table=FAKE, n=4, first=NUL, counts=FAKE, row=FAKE, step
 
 
 def attend(kvc, c, bits=4, hq=8, h=2, b=1, m=1, n=4, q=FAKE, qs=512, start=FAKE, table=FAKE, kp=FAKE, vp=FAKE, scale=0.1, out=FAKE,
-           flags=0, ws=FAKE, size=BIG):
-    return kvc._lib.kvc_attend_quant(C.byref(c), bits, hq, h, b, m, n, q, qs, start, table, FAKE, kp, vp, scale, out, NUL, flags, ws, size, NUL)
+           ws=FAKE, size=BIG):
+    return kvc._lib.kvc_attend_quant(C.byref(c), bits, hq, h, b, m, n, q, qs, start, table, FAKE, kp, vp, scale, out, NUL, ws, size, NUL)
 
 
 CALLS = dict(kvc_pages_append_quant=append, kvc_pages_compact_quant=compact, kvc_pages_read_quant=read, kvc_attend_quant=attend)
@@ -77,7 +77,7 @@ def test_attend_arguments(kvc):
     c = cache(kvc)
     for bad in (dict(hq=7), dict(h=0), dict(b=0), dict(b=1 << 20), dict(m=0), dict(m=1 << 29), dict(n=-1), dict(n=1 << 31), dict(q=NUL),
                 dict(q=ODD), dict(qs=504), dict(qs=513), dict(start=NUL), dict(table=NUL), dict(kp=ODD), dict(vp=NUL), dict(out=NUL),
-                dict(scale=math.inf), dict(scale=math.nan), dict(flags=2), dict(flags=1 << 31)):
+                dict(scale=math.inf), dict(scale=math.nan)):
         assert attend(kvc, c, **bad) == -1, bad
         assert "kvc_attend_quant" in kvc.kvc_last_error()
     assert attend(kvc, c, n=0, q=NUL) == 0

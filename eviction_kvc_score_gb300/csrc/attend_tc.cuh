@@ -55,12 +55,12 @@
 //   TB/s or 73% of the measured copy rate; one term 152 us, 83%.
 // - short calls: latency.  One sequence of 1,000 rows: 16.7 us; one term 14.5.
 //
-// Rows held in 4 or 8 bits (BITS; quant.cuh; attend_tc_quant.cu): a fourth
-// warpgroup makes the tiles.  Each of its warps brings 32 keys of every tile, two
-// blocks of 16 rows, to shared memory with a bulk copy each and writes them out in
-// the layout that TMA would have left: K as bf16, exactly; V as fp16, (n - z) times
-// the step, the step over 2^e with e the exponent of the block's largest.  The
-// probabilities of the block's columns are multiplied by 2^(e - E), E the largest e
+// Rows held in 4 or 8 bits (BITS; quant.cuh; attend_tc_quant.cu): warps 12-19 make
+// the tiles.  Warp 11 brings blocks of 16 rows to shared memory, a bulk copy each;
+// each of the eight warps takes a block of every tile and writes it out in the layout
+// that TMA would have left: K as bf16, exactly; V as fp16, (n - z) times the step, the
+// step over 2^e with e the exponent of the block's largest.  The
+// probabilities of their columns are multiplied by 2^(e - E), E the largest e
 // so far, and rounded to one fp16 number: 11 bits where bf16 has 8, so there is no
 // second term.  O stands for sum p v / 2^E, rescaled when E grows by more than one.
 // p = 1 with e = E is held as 2^6: m's 8 and E's 1 leave it below fp16's 2^16, and
@@ -86,16 +86,14 @@ namespace {
 // the loading and issuing warpgroup to the two that hold a row of 128 logits
 // per thread.  256 x 208 + 128 x 88 = 384 x 168: the launch checks the 168,
 // because an increase beyond what the block was launched with never returns.
-// With the fourth warpgroup: 256 x 192 + 128 x 64 + 128 x 64 = 512 x 128.
+// With two warpgroups more: 256 x 128 + 128 x 64 + 256 x 80 = 640 x 96.
 template <int BITS>
 struct Shape {
-    static constexpr int kThreads = BITS == 0 ? 384 : 512;
-    static constexpr int kRegsLaunch = BITS == 0 ? 168 : 128, kRegsSoftmax = BITS == 0 ? 208 : 192;
-    static constexpr int kRegsOther = BITS == 0 ? 88 : 64, kRegsTiles = BITS == 0 ? 0 : 64;
-    static_assert(256 * kRegsSoftmax + 128 * kRegsOther + 128 * kRegsTiles <= kThreads * kRegsLaunch, "register split");
-    static constexpr int kReaders = BITS == 0 ? 12 : 15;   // warps that read the queue
-    // blocks of 16 rows, held as they are, per warp that makes tiles
-    static constexpr int kRaw = BITS == 8 ? 3 : 6;
+    static constexpr int kThreads = BITS == 0 ? 384 : 640;
+    static constexpr int kRegsLaunch = BITS == 0 ? 168 : 96, kRegsSoftmax = BITS == 0 ? 208 : 128;
+    static constexpr int kRegsOther = BITS == 0 ? 88 : 64, kRegsTiles = BITS == 0 ? 0 : 80;
+    static_assert(256 * kRegsSoftmax + 128 * kRegsOther + 256 * kRegsTiles <= kThreads * kRegsLaunch, "register split");
+    static constexpr int kReaders = BITS == 0 ? 12 : 20;   // warps that read the queue
 };
 constexpr int kTile = 128;              // rows of Q, keys of K and V
 constexpr int kLoadWarp = 8, kMmaWarp = 9, kLoadWarp2 = 11, kTileWarp = 12;
@@ -125,9 +123,14 @@ struct Work {
 
 // Ring stages: what shared memory holds beside Q.
 constexpr int stages_of(int kh, int bits) { return bits != 0 ? (kh == 2 ? 4 : 10) : kh == 2 ? 5 : 12; }
-constexpr int raw_bytes(int kh, int bits) { return bits == 0 ? 0 : 4 * (bits == 4 ? Shape<4>::kRaw : Shape<8>::kRaw) * quant_block(bits, 2 * kh); }
+// Slots for blocks of 16 rows as they are held: whole tiles of them, so that a slot
+// is always the same warp's.  (A warp that waited for a phase behind another warp's
+// of the same slot would take the one before both for it: parities repeat.)
+constexpr int raw_slots(int kh, int bits) { return bits == 0 ? 0 : bits == 4 ? 24 : kh == 2 ? 8 : 16; }
+static_assert(raw_slots(1, 4) % 8 == 0 && raw_slots(2, 8) % 8 == 0 && raw_slots(1, 8) % 8 == 0, "eight blocks a tile");
+constexpr int raw_bytes(int kh, int bits) { return bits == 0 ? 0 : raw_slots(kh, bits) * quant_block(bits, 2 * kh); }
 
-template <int STAGES, int BITS>
+template <int STAGES, int BITS, int RAW>
 struct Bars {
     uint64_t full[STAGES], empty[STAGES];
     uint64_t q_full, q_empty;
@@ -141,15 +144,16 @@ struct Bars {
     Work work[kQueue];
     float2 other[kTile];  // half 1's (max, sum) of a split unit
     int64_t plan[Shape<BITS>::kThreads / 32 + 4];
-    // held rows: a stage's blocks' exponents, those of half 1's O, blocks that have come
+    // held rows: exponents of a stage's blocks, those of half 1's O, blocks that have come and gone
     alignas(16) int exps[BITS == 0 ? 1 : STAGES][8];
     int other_exp[4];
-    uint64_t raw_full[BITS == 0 ? 1 : 4 * Shape<BITS>::kRaw];
+    uint64_t raw_full[BITS == 0 ? 1 : RAW], raw_empty[BITS == 0 ? 1 : RAW];
+    volatile int raw_there[BITS == 0 ? 1 : RAW];   // blocks that a page of the pool holds
 };
 
 template <int KH, int BITS>
 constexpr size_t smem_bytes() {
-    return 1024 + (size_t)(2 + stages_of(KH, BITS)) * KH * kBox + raw_bytes(KH, BITS) + sizeof(Bars<stages_of(KH, BITS), BITS>);
+    return 1024 + (size_t)(2 + stages_of(KH, BITS)) * KH * kBox + raw_bytes(KH, BITS) + sizeof(Bars<stages_of(KH, BITS), BITS, raw_slots(KH, BITS)>);
 }
 
 __device__ __forceinline__ void tma_load_4d(const CUtensorMap *map, uint64_t *bar, void *dst, int c0,
@@ -322,9 +326,9 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c) {
     uint32_t r;
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
     return r;
 }
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
@@ -332,9 +336,6 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-// A word of two groups (one where KH is 1 has both) as it stands in both halves.
-__device__ __forceinline__ uint32_t twice(uint32_t pair, int upper) { return __byte_perm(pair, 0, upper ? 0x3232 : 0x1010); }
-
 // Eight channels of K as bf16: codes come as 128 + n (4 bits), where bf16 counts in
 // ones, or 2^23 + n in fp32 (8 bits); the zero code comes off the same way, and times
 // the step it is exact.
@@ -357,122 +358,132 @@ __device__ __forceinline__ void tile_k(uint2 codes, uint32_t word, uint32_t (&y)
         }
     }
 }
-// Eight channels of V over 2^e as fp16, by 1024 + n, where fp16 counts in ones;
-// down = 2^-e.
+// Eight channels of V over 2^e as fp16: codes come as 16 + n or 1024 + n, where fp16
+// has room for them (n of 4 or 8 bits); off is that of the zero code times the step
+// with its sign turned, nine or eleven bits, so the fused sum is exact.
 template <int BITS>
-__device__ __forceinline__ void tile_v(uint2 codes, uint32_t word, float down, uint32_t (&y)[4]) {
-    const float f = quant_step<BITS>(word & 0xffffu) * down;
-    uint32_t s;
-    asm("cvt.rn.f16x2.f32 %0, %1, %1;" : "=r"(s) : "f"(f));
-    const uint32_t z = (word & (BITS == 4 ? 0x000f000fu : 0x00ff00ffu)) | 0x64006400u;
+__device__ __forceinline__ void tile_v(uint2 codes, uint32_t step, uint32_t off, uint32_t (&y)[4]) {
+    if (BITS == 4) {
+        y[0] = fma_f16x2((codes.x << 6 & 0x03c003c0u) | 0x4c004c00u, step, off);
+        y[1] = fma_f16x2((codes.x << 2 & 0x03c003c0u) | 0x4c004c00u, step, off);
+        y[2] = fma_f16x2((codes.x >> 2 & 0x03c003c0u) | 0x4c004c00u, step, off);
+        y[3] = fma_f16x2((codes.x >> 6 & 0x03c003c0u) | 0x4c004c00u, step, off);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t n = BITS == 4 ? ((codes.x >> 4 * i) & 0x000f000fu) | 0x64006400u
-                                     : __byte_perm(i < 2 ? codes.x : codes.y, 0x64646464u, i & 1 ? 0x4342 : 0x4140);
-        y[i] = mul_f16x2(sub_f16x2(n, z), s);
+        for (int i = 0; i < 4; ++i)
+            y[i] = fma_f16x2(__byte_perm(i < 2 ? codes.x : codes.y, 0x64646464u, i & 1 ? 0x4342 : 0x4140), step, off);
     }
 }
 
-// A block of 16 rows as it is held, at `raw`, to rows row0.. of a tile at `tile`, by
-// a warp: lane = 4 (row & 7) + c has piece c of all groups of two rows.  Rows at and
-// after `rows` are zeros.  V: groups that stand for NaN become zeros from row
-// `finite` on (*dirty is set if one of them is before `held`), and the exponent of
-// the largest step comes back (-127 if there is none).
+// A block of 16 rows as it is held, in a warp's registers: lane = 4 (row & 7) + c has
+// piece c of all groups of rows r8 and r8 + 8.
 template <int KH, int BITS>
-__device__ __forceinline__ int write_tile(const uint8_t *raw, uint32_t tile, int row0, bool is_v, int rows, int finite,
-                                          int held, volatile int *dirty) {
-    constexpr int G = 2 * KH, kCodes = quant_codes(BITS, G), kWords = quant_words(G);
-    const int lane = threadIdx.x & 31, r8 = lane >> 2, c = lane & 3;
+struct HeldRows {
+    static constexpr int G = 2 * KH, kCodes = quant_codes(BITS, G);
     uint32_t word[2][KH];
+    uint32_t code[2][kCodes / 16];
+
+    // Rows at and after `rows` are zeros.
+    __device__ __forceinline__ void load(const uint8_t *raw, int rows) {
+        const int r8 = (threadIdx.x & 31) >> 2, c = threadIdx.x & 3;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int r = r8 + 8 * i;
-        const uint32_t *w = reinterpret_cast<const uint32_t *>(raw + kQuantRows * kCodes + r * kWords);
+        for (int i = 0; i < 2; ++i) {
+            const int r = r8 + 8 * i;
+            const uint8_t *w = raw + kQuantRows * kCodes + r * quant_words(G);
+            if (KH == 2) {
+                const uint2 x = *reinterpret_cast<const uint2 *>(w);
+                word[i][0] = r < rows ? x.x : 0;
+                word[i][KH - 1] = r < rows ? x.y : 0;
+            } else {
+                word[i][0] = r < rows ? *reinterpret_cast<const uint32_t *>(w) : 0;
+            }
+            const uint8_t *at = raw + r * kCodes + c * (kCodes / 4);
+            if (kCodes == 32) {
+                const uint2 x = *reinterpret_cast<const uint2 *>(at);
+                code[i][0] = x.x;
+                code[i][1] = x.y;
+            } else {
 #pragma unroll
-        for (int k = 0; k < KH; ++k) word[i][k] = r < rows ? w[k] : 0;
+                for (int k = 0; k < kCodes / 64; ++k) {
+                    const uint4 x = reinterpret_cast<const uint4 *>(at)[k];
+                    code[i][4 * k] = x.x;
+                    code[i][4 * k + 1] = x.y;
+                    code[i][4 * k + 2] = x.z;
+                    code[i][4 * k + 3] = x.w;
+                }
+            }
+        }
     }
-    int e = 0;
-    float down = 1.f;
-    if (is_v) {
-        uint32_t top = 0;   // the largest step's exponent, biased
+    // The codes of group g of the i-th row.
+    template <bool V>
+    __device__ __forceinline__ uint2 piece(int i, int g) const {
+        if (BITS == 8) return V ? make_uint2(code[i][g], code[i][G + g]) : make_uint2(code[i][2 * g], code[i][2 * g + 1]);
+        if (!V) return make_uint2(code[i][g], 0);
+        // halves of the group from two places
+        return make_uint2(__byte_perm(code[i][g / 2], code[i][KH + g / 2], g & 1 ? 0x7632 : 0x5410), 0);
+    }
+    // V: groups that stand for NaN become zeros from row `finite` on (*dirty is set if
+    // one of them is before `held`); the exponent of the largest step, or -127.
+    __device__ __forceinline__ int exponent(int finite, int held, volatile int *dirty) {
+        const int r8 = (threadIdx.x & 31) >> 2;
+        uint32_t top = 0;
         bool odd = false;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int k = 0; k < KH; ++k) {
-                const uint32_t lo = (BITS == 4 ? word[i][k] >> 7 : word[i][k] >> 8) & 0xffu;
-                const uint32_t hi = (BITS == 4 ? word[i][k] >> 23 : word[i][k] >> 24) & 0xffu;
-                odd |= lo == 255 || hi == 255;
-                top = max(top, max(lo == 255 ? 0 : lo, hi == 255 ? 0 : hi));
-            }
-        top = __reduce_max_sync(0xffffffffu, top);
+            for (int k = 0; k < KH; ++k)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t e = word[i][k] >> (16 * h + (BITS == 4 ? 7 : 8)) & 0xffu;
+                    odd |= e == 255;
+                    top = max(top, e == 255 ? 0 : e);
+                }
         if (odd) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int r = r8 + 8 * i;
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int k = 0; k < KH; ++k)
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
-                        if (quant_is_nan<BITS>(word[i][k] >> 16 * h & 0xffffu) && r >= finite) {
+                        if (quant_is_nan<BITS>(word[i][k] >> 16 * h & 0xffffu) && r8 + 8 * i >= finite) {
                             word[i][k] &= h ? 0xffffu : 0xffff0000u;
-                            if (r < held) *dirty = 1;
+                            if (r8 + 8 * i < held) *dirty = 1;
                         }
-            }
         }
-        e = (int)top - 127;
-        down = __uint_as_float((uint32_t)(127 - e) << 23);
+        return (int)__reduce_max_sync(0xffffffffu, top) - 127;
     }
-    const bool swap = r8 & 1;   // odd rows have the groups of a pair the other way round: all banks
+    // To rows row0 .. + 15 of a tile (V: over 2^e).
+    template <bool V>
+    __device__ __forceinline__ void write(uint32_t tile, int row0, int e) const {
+        const int r8 = (threadIdx.x & 31) >> 2, c = threadIdx.x & 3;
+        const float down = V ? __uint_as_float((uint32_t)(127 - e) << 23) : 1.f;
+        const bool swap = r8 & 1;   // odd rows have the groups of a pair the other way round: all banks
+        const uint32_t at = tile + (row0 + r8) * 128 + ((c ^ r8) << 4 & 0x30) + ((c ^ r8 ^ (swap ? 4 : 0)) << 4 & 0x40);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int r = r8 + 8 * i;
-        const uint8_t *codes = raw + r * kCodes + c * (kCodes / 4);
-        const uint32_t at = tile + (row0 + r) * 128 + ((c ^ r8) << 4 & 0x30) + ((c ^ r8 ^ (swap ? 4 : 0)) << 4 & 0x40);
-        uint2 n[G];
-        if (BITS == 4 && KH == 2) {
-            const uint4 x = *reinterpret_cast<const uint4 *>(codes);
-            if (is_v) {   // halves of each group from two places
-                n[0].x = __byte_perm(x.x, x.z, 0x5410);
-                n[1].x = __byte_perm(x.x, x.z, 0x7632);
-                n[2 % G].x = __byte_perm(x.y, x.w, 0x5410);
-                n[3 % G].x = __byte_perm(x.y, x.w, 0x7632);
-            } else {
-                n[0].x = x.x;
-                n[1].x = x.y;
-                n[2 % G].x = x.z;
-                n[3 % G].x = x.w;
-            }
-        } else if (BITS == 4) {
-            const uint2 x = *reinterpret_cast<const uint2 *>(codes);
-            n[0].x = is_v ? __byte_perm(x.x, x.y, 0x5410) : x.x;
-            n[1].x = is_v ? __byte_perm(x.x, x.y, 0x7632) : x.y;
-        } else {
-            uint32_t x[2 * G];
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int k = 0; k < KH; ++k) {
-                const uint4 y = reinterpret_cast<const uint4 *>(codes)[k];
-                x[4 * k] = y.x;
-                x[4 * k + 1] = y.y;
-                x[4 * k + 2] = y.z;
-                x[4 * k + 3] = y.w;
+                const uint2 a = piece<V>(i, 2 * k), b = piece<V>(i, 2 * k + 1);
+                const uint2 n0 = swap ? b : a, n1 = swap ? a : b;
+                const uint32_t w = swap ? __byte_perm(word[i][k], 0, 0x1032) : word[i][k];
+                uint32_t y0[4], y1[4];
+                if (V) {
+                    // both groups' steps over 2^e, and the zero codes' share
+                    uint32_t s, off;
+                    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(s) : "f"(quant_step<BITS>(w >> 16) * down), "f"(quant_step<BITS>(w & 0xffffu) * down));
+                    off = mul_f16x2(BITS == 4 ? (w << 6 & 0x03c003c0u) | 0xcc00cc00u : (w & 0x00ff00ffu) | 0xe400e400u, s);
+                    tile_v<BITS>(n0, __byte_perm(s, 0, 0x1010), __byte_perm(off, 0, 0x1010), y0);
+                    tile_v<BITS>(n1, __byte_perm(s, 0, 0x3232), __byte_perm(off, 0, 0x3232), y1);
+                } else {
+                    tile_k<BITS>(n0, __byte_perm(w, 0, 0x1010), y0);
+                    tile_k<BITS>(n1, __byte_perm(w, 0, 0x3232), y1);
+                }
+                const uint32_t to = at + i * 8 * 128 + k * kBox;
+                write16(to, y0);
+                write16(to ^ 0x40, y1);
             }
-#pragma unroll
-            for (int g = 0; g < G; ++g) n[g] = is_v ? make_uint2(x[g], x[G + g]) : make_uint2(x[2 * g], x[2 * g + 1]);
-        }
-#pragma unroll
-        for (int k = 0; k < KH; ++k) {
-            const uint2 n0 = swap ? n[2 * k + 1] : n[2 * k], n1 = swap ? n[2 * k] : n[2 * k + 1];
-            const uint32_t w0 = twice(word[i][k], swap), w1 = twice(word[i][k], !swap);
-            uint32_t y[4];
-            is_v ? tile_v<BITS>(n0, w0, down, y) : tile_k<BITS>(n0, w0, y);
-            write16(at + k * kBox, y);
-            is_v ? tile_v<BITS>(n1, w1, down, y) : tile_k<BITS>(n1, w1, y);
-            write16((at ^ 0x40) + k * kBox, y);
-        }
     }
-    return e;
-}
+};
 
 // Bytes that are a multiple of 16 from global to shared memory.
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
@@ -493,13 +504,15 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1)
     uint8_t *sq = base;                              // [2][KH][128 rows][128 B]
     uint8_t *ring = base + 2 * kStageBytes;          // [stage][KH][128 keys][128 B]
     uint8_t *held = ring + kStages * kStageBytes;    // blocks as they are held
-    Bars<kStages, BITS> &b = *reinterpret_cast<Bars<kStages, BITS> *>(held + raw_bytes(KH, BITS));
+    constexpr int kRaw = raw_slots(KH, BITS);
+    using Shared = Bars<kStages, BITS, kRaw>;
+    Shared &b = *reinterpret_cast<Shared *>(held + raw_bytes(KH, BITS));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int R = p.split_rows;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&b.full[i], BITS == 0 ? 1 : 4);
+            mbar_init(&b.full[i], BITS == 0 ? 1 : 8);
             mbar_init(&b.empty[i], 2);
         }
         mbar_init(&b.q_full, 1);
@@ -519,7 +532,10 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1)
             mbar_init(&b.work_empty[i], Shape<BITS>::kReaders);
         }
         if constexpr (BITS != 0)
-            for (int i = 0; i < 4 * Shape<BITS>::kRaw; ++i) mbar_init(&b.raw_full[i], 1);
+            for (int i = 0; i < kRaw; ++i) {
+                mbar_init(&b.raw_full[i], 1);
+                mbar_init(&b.raw_empty[i], 1);
+            }
         mbar_init(&b.half_full, 4);
         mbar_init(&b.half_empty, 4);
         b.abort_flag = 0;
@@ -555,79 +571,46 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1)
         // ------------------------------------------------ tiles from rows as they are held
         if constexpr (BITS != 0) {
             regs_dec<Shape<BITS>::kRegsTiles>();
-            constexpr int kRaw = Shape<BITS>::kRaw, kBlock = quant_block(BITS, 2 * KH);
-            const int part = warp - kTileWarp;   // keys 32 part .. of every tile
-            uint8_t *mine = held + part * kRaw * kBlock;
-            uint64_t *come = b.raw_full + part * kRaw;
-            uint32_t base_fill = 0, asked = 0, used = 0;   // loads before this segment, blocks asked for and used
-            uint32_t absent = 0;                           // slots whose block is not there
+            constexpr int kBlock = quant_block(BITS, 2 * KH);
+            const int part = warp - kTileWarp;   // keys 16 part .. of every tile
+            uint32_t base_fill = 0;         // loads before this segment
+            uint32_t slot = part, round = 0;   // of the block that is next
             bool ok = true;
             Work w;
             for (uint32_t k = 0; ok; ++k) {
                 if (!read_work(k, w)) break;
                 const Segment g = w.g;
-                if (g.n == 0) continue;
                 const int hi = w.a.hi, from = attend_sees(p, w.a, 0), len = w.a.len;
-                const int32_t *entry = p.table + (int64_t)w.a.list * p.max_pages;
-                const int key0 = g.first * kTile + 32 * part;
-                // the blocks' page numbers, 16 tiles at a time: the batch in use, the one
-                // before (V is up to two tiles behind K) and the next
-                auto look_up = [&](int batch) {
-                    const int64_t key = key0 + ((int64_t)batch * 16 + (lane >> 1)) * kTile + 16 * (lane & 1);
-                    return key < hi ? entry[key >> p.shift] : 0;
-                };
-                int batch = 0, before = 0, now = look_up(0), then = look_up(1);
-                const int blocks = 4 * g.n;
-                int next = 0;   // the segment's block to be asked for
-                auto ask = [&]() {
-                    bool is_v;
-                    int tile;
-                    load_at(g, next >> 1, &is_v, &tile);
-                    const int at = 2 * tile + (next & 1);
-                    if (at >> 5 > batch) {
-                        ++batch;
-                        before = now;
-                        now = then;
-                        then = look_up(batch + 1);
-                    }
-                    const int page = __shfl_sync(0xffffffffu, at >> 5 < batch ? before : now, at & 31);
-                    const int key = key0 + tile * kTile + 16 * (next & 1);
-                    const bool seen = key < hi, there = seen && page >= 0 && page < p.n_pages;
-                    const uint32_t slot = asked % kRaw;
-                    absent = there ? absent & ~(1u << slot) : absent | 1u << slot;
-                    if (lane == 0) {
-                        if (there) {
-                            const int64_t block = (((int64_t)page << p.shift) + (key & ((1 << p.shift) - 1))) >> 4;
-                            mbar_arrive_expect_tx(&come[slot], kBlock);
-                            bulk_load(mine + slot * kBlock, static_cast<const uint8_t *>(is_v ? p.v_pool : p.k_pool) + block * kBlock,
-                                      kBlock, &come[slot]);
-                        } else {
-                            if (seen) set_status(p.status, KVC_DEV_BAD_PAGE);
-                            mbar_arrive(&come[slot]);
-                        }
-                    }
-                    ++asked;
-                    ++next;
-                };
-                while (next < min(kRaw, blocks)) ask();
-                for (int l = 0; ok && l < 2 * g.n; ++l) {
-                    bool is_v;
-                    int tile;
+                const int key0 = g.first * kTile + kQuantRows * part;
+                HeldRows<KH, BITS> rows;
+                bool is_v = false;
+                int tile = 0;
+                // load l's rows to registers; their slot is free again
+                auto read = [&](int l) {
                     load_at(g, l, &is_v, &tile);
-                    const uint32_t fill = base_fill + l, st = fill % kStages;
-                    ok = fill < kStages || warp_wait(&b.empty[st], (fill / kStages - 1) & 1, stop, p.status);
-                    for (int j = 0; ok && j < 2; ++j) {
-                        const uint32_t slot = used % kRaw;
-                        if (!(ok = warp_wait(&come[slot], (used / kRaw) & 1, stop, p.status))) break;
-                        ++used;
-                        const int key = key0 + tile * kTile + 16 * j;
-                        const int e = write_tile<KH, BITS>(mine + slot * kBlock, smem_u32(ring) + st * kStageBytes, 32 * part + 16 * j,
-                                                           is_v, absent >> slot & 1 ? 0 : hi - key, from - key, len - key, &b.dirty);
-                        if (is_v && lane == 0) b.exps[st][2 * part + j] = e;
-                        __syncwarp();   // the slot is read
-                        if (next < blocks) ask();
+                    if (!warp_wait(&b.raw_full[slot], round & 1, stop, p.status)) return false;
+                    rows.load(held + slot * kBlock, b.raw_there[slot] ? hi - (key0 + tile * kTile) : 0);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&b.raw_empty[slot]);
+                    if ((slot += 8) >= kRaw) {
+                        slot -= kRaw;
+                        ++round;
                     }
-                    if (!ok) break;
+                    return true;
+                };
+                if (g.n > 0) ok = read(0);
+                for (int l = 0; ok && l < 2 * g.n; ++l) {
+                    const uint32_t fill = base_fill + l, st = fill % kStages;
+                    if (!(ok = fill < kStages || warp_wait(&b.empty[st], (fill / kStages - 1) & 1, stop, p.status))) break;
+                    const uint32_t to = smem_u32(ring) + st * kStageBytes;
+                    if (is_v) {
+                        const int key = key0 + tile * kTile, e = rows.exponent(from - key, len - key, &b.dirty);
+                        rows.template write<true>(to, kQuantRows * part, e);
+                        if (lane == 0) b.exps[st][part] = e;
+                    } else {
+                        rows.template write<false>(to, kQuantRows * part, 0);
+                    }
+                    if (l + 1 < 2 * g.n) ok = read(l + 1);
                     __threadfence_block();   // what was taken out is noted
                     fence_async_shared();
                     __syncwarp();
@@ -635,7 +618,6 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1)
                 }
                 base_fill += 2 * g.n;
             }
-            for (; used < asked; ++used) mbar_drain(&come[used % kRaw], (used / kRaw) & 1);   // unwind: every copy must land
         }
     } else if (warp >= kLoadWarp) {
     regs_dec<Shape<BITS>::kRegsOther>();
@@ -670,6 +652,68 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1)
             ++segs;
         }
         if (*stop && segs) mbar_drain(&b.q_full, (segs - 1) & 1);
+    } else if (BITS != 0 && warp == kLoadWarp2) {
+        // ------------------------------------------------ rows as they are held, a block a lane
+        if constexpr (BITS != 0) {
+            constexpr int kBlock = quant_block(BITS, 2 * KH);
+            uint32_t asked = lane & 7;   // lanes 0-7: the tile's eight blocks
+            bool ok = true;
+            Work w;
+            for (uint32_t k = 0; ok; ++k) {
+                if (!read_work(k, w)) break;
+                const Segment &g = w.g;
+                const int hi = w.a.hi;
+                const int32_t *entry = p.table + (int64_t)w.a.list * p.max_pages;
+                // page numbers of four tiles, a lane each; those of the next four are asked
+                // for ahead, those before are kept: V is up to two tiles behind K
+                auto look_up = [&](int batch) {
+                    const int64_t key = (int64_t)(g.first + batch * 4) * kTile + 16 * lane;
+                    return key < hi ? entry[key >> p.shift] : 0;
+                };
+                int batch = 0, before = 0, now = 0, then = 0;
+                if (g.n > 0) {
+                    now = look_up(0);
+                    then = look_up(1);
+                }
+                for (int l = 0; l < 2 * g.n; ++l) {
+                    bool is_v;
+                    int tile;
+                    load_at(g, l, &is_v, &tile);
+                    if (tile >> 2 > batch) {
+                        ++batch;
+                        before = now;
+                        now = then;
+                        then = look_up(batch + 1);
+                    }
+                    const int page = __shfl_sync(0xffffffffu, tile >> 2 < batch ? before : now, (tile & 3) * 8 + (lane & 7));
+                    const int key = (g.first + tile) * kTile + 16 * (lane & 7);
+                    const bool seen = key < hi, there = seen && page >= 0 && page < p.n_pages;
+                    const uint32_t slot = asked % kRaw;
+                    const bool mine = lane < 8;
+                    bool free = true;
+                    if (mine && asked >= kRaw) free = mbar_wait(&b.raw_empty[slot], (asked / kRaw - 1) & 1, stop, p.status);
+                    if (!(ok = __all_sync(0xffffffffu, free))) break;
+                    if (mine) {
+                        b.raw_there[slot] = there;
+                        if (there) {
+                            const int64_t block = (((int64_t)page << p.shift) + (key & ((1 << p.shift) - 1))) >> 4;
+                            mbar_arrive_expect_tx(&b.raw_full[slot], kBlock);
+                            bulk_load(held + slot * kBlock, static_cast<const uint8_t *>(is_v ? p.v_pool : p.k_pool) + block * kBlock, kBlock,
+                                      &b.raw_full[slot]);
+                        } else {
+                            if (seen) set_status(p.status, KVC_DEV_BAD_PAGE);
+                            mbar_arrive(&b.raw_full[slot]);
+                        }
+                    }
+                    asked += 8;
+                }
+            }
+            if (*stop && lane < 8) {   // unwind: every copy must land
+                const uint32_t all = asked - lane, first = all > kRaw ? all - kRaw : 0;   // the last of each slot
+                for (uint32_t i = lane; i < asked; i += 8)
+                    if (i >= first) mbar_drain(&b.raw_full[i % kRaw], (i / kRaw) & 1);
+            }
+        }
     } else if (BITS == 0 && (warp == kLoadWarp || warp == kLoadWarp2)) {
         // ------------------------------------------------ loads, every other one a warp
         const uint32_t side = warp == kLoadWarp ? 0 : 1;
@@ -962,7 +1006,7 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1)
                     // lane 0 says for all 32 rows that they are clean
                     __syncwarp();
                 }
-                int exps[BITS == 0 ? 1 : 8];
+                int exps[BITS == 0 ? 1 : 8] = {};
                 if constexpr (BITS != 0) {
                     if (any) {
                         const uint32_t f = filled + v_at(g, ti);
@@ -1016,25 +1060,15 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1)
                     }
                     const float s_top = fmaxf(fmax3(x[0], x[1], x[2]), x[3]);
                     const float top = s_top * mul;
-                    int e_top = -127;
-                    if constexpr (BITS != 0) {
-#pragma unroll
-                        for (int q = 0; q < 8; ++q) e_top = max(e_top, exps[q]);
-                    }
                     if (i == 0) {
                         m = top;
-                        top_exp = e_top;
                     } else {
                         const bool grow = top > m + kGrow;
-                        if (__any_sync(0xffffffffu, grow || (BITS != 0 && e_top > top_exp + 1))) {
+                        if (__any_sync(0xffffffffu, grow)) {
                             // every product of this half up to the tile before is done: S came after it
-                            float down = grow ? ex2(m - top) : 1.f;
+                            const float down = grow ? ex2(m - top) : 1.f;
                             if (grow) m = top;
                             l *= down;
-                            if (BITS != 0 && e_top > top_exp + 1) {   // 2^(top_exp - e_top)
-                                down *= __uint_as_float((uint32_t)max(127 + top_exp - e_top, 0) << 23);
-                                top_exp = e_top;
-                            }
 #pragma unroll 1
                             for (int d = 0; d < D; d += 32) {
                                 float o[32];
@@ -1063,13 +1097,7 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1)
                             const float p0 = ex2(y0), p1 = ex2(y1);
                             const unsigned long long pp = f2_pack(p0, p1);
                             sum2[j & 1] = f2_add(sum2[j & 1], pp);
-                            if constexpr (BITS != 0) {
-                                // 2^(e - E + 6) of the block of 16 columns
-                                const float f = __uint_as_float((uint32_t)max(133 + exps[4 * h + (j >> 3)] - top_exp, 0) << 23);
-                                float r0, r1;
-                                f2_unpack(f2_mul(pp, f2_pack(f, f)), r0, r1);
-                                asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pw[j]) : "f"(r1), "f"(r0));
-                            } else if constexpr (TWO) {
+                            if constexpr (TWO) {
                                 // the upper 16 bits, and what is left of the rest
                                 const uint32_t b0 = __float_as_uint(p0), b1 = __float_as_uint(p1);
                                 pw[j] = __byte_perm(b0, b1, 0x7632);
@@ -1098,11 +1126,115 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1)
                     f2_unpack(f2_add(sum2[0], sum2[1]), s0, s1);
                     l += s0 + s1;
                 };
+                // held rows: 32 logits at a time, read from TMEM once for the maximum and
+                // once for the probabilities, for want of registers
+                auto soften_held = [&](auto slow) {
+                    constexpr bool kSlow = decltype(slow)::value;
+                    const int lim = sees - k0;
+                    auto seen = [&](int j, float s) { return j < lim ? s * c : -INFINITY; };
+                    float v[2][32], x[4];
+                    tmem_ld32(cs, v[0]);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        float(&y)[32] = v[q & 1];
+                        reg_fence(y);
+                        if (q < 3) tmem_ld32(cs + 32 * (q + 1), v[~q & 1]);
+                        if (kSlow) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) y[j] = seen(q * 32 + j, y[j]);
+                        }
+                        x[q] = fmax3(y[0], y[1], y[2]);
+#pragma unroll
+                        for (int j = 3; j < 31; j += 2) x[q] = fmax3(x[q], y[j], y[j + 1]);
+                        x[q] = fmaxf(x[q], y[31]);
+                        if (q < 3) tmem_ld_wait();
+                    }
+                    tmem_ld32(cs, v[0]);
+                    const float top = fmaxf(fmax3(x[0], x[1], x[2]), x[3]) * (kSlow ? 1.f : c);
+                    int e_top = exps[0];
+#pragma unroll
+                    for (int q = 1; q < 8; ++q) e_top = max(e_top, exps[q]);
+                    if (i == 0) {
+                        m = top;
+                        top_exp = e_top;
+                    } else {
+                        const bool grow = top > m + kGrow;
+                        if (__any_sync(0xffffffffu, grow || e_top > top_exp + 1)) {
+                            float down = grow ? ex2(m - top) : 1.f;
+                            if (grow) m = top;
+                            l *= down;
+                            if (e_top > top_exp + 1) {   // 2^(top_exp - e_top)
+                                down *= __uint_as_float((uint32_t)max(127 + top_exp - e_top, 0) << 23);
+                                top_exp = e_top;
+                            }
+                            tmem_ld_wait();
+                            reg_fence(v[0]);
+#pragma unroll 1
+                            for (int d = 0; d < D; d += 32) {
+                                float o[32];
+                                uint32_t ou[32];
+                                tmem_ld32(co + d, o);
+                                tmem_ld_wait();
+                                reg_fence(o);
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) ou[j] = __float_as_uint(o[j] * down);
+                                tmem_st32(co + d, ou);
+                            }
+                        }
+                    }
+                    const float nm = m == -INFINITY ? 0.f : -m;
+                    const unsigned long long nm2 = f2_pack(nm, nm);
+                    unsigned long long sum2[2] = {0, 0};
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        float(&y)[32] = v[q & 1];
+                        tmem_ld_wait();
+                        reg_fence(y);
+                        if (q < 3) tmem_ld32(cs + 32 * (q + 1), v[~q & 1]);
+                        uint32_t pw[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            float y0, y1;
+                            if (kSlow) {
+                                y0 = seen(q * 32 + 2 * j, y[2 * j]) + nm;
+                                y1 = seen(q * 32 + 2 * j + 1, y[2 * j + 1]) + nm;
+                            } else {
+                                f2_unpack(f2_fma(f2_pack(y[2 * j], y[2 * j + 1]), c2, nm2), y0, y1);
+                            }
+                            const unsigned long long pp = f2_pack(ex2(y0), ex2(y1));
+                            sum2[j & 1] = f2_add(sum2[j & 1], pp);
+                            // 2^(e - E + 6) of the block of 16 columns
+                            const float f = __uint_as_float((uint32_t)max(133 + exps[(2 * q + (j >> 3)) % (BITS == 0 ? 1 : 8)] - top_exp, 0) << 23);
+                            float r0, r1;
+                            f2_unpack(f2_mul(pp, f2_pack(f, f)), r0, r1);
+                            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pw[j]) : "f"(r1), "f"(r0));
+                        }
+                        // over columns of S that are read: P's 16 q are S's up to 16 q + 15
+                        tmem_st16(cs + 16 * q, pw);
+                        if (q & 1) {
+                            tmem_st_wait();
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&b.p_full[t][q >> 1]);
+                        }
+                    }
+                    float s0, s1;
+                    f2_unpack(f2_add(sum2[0], sum2[1]), s0, s1);
+                    l += s0 + s1;
+                };
                 if (any) {
-                    if (edge || !plain)
-                        soften(std::true_type{});
-                    else
-                        soften(std::false_type{});
+                    if constexpr (BITS != 0) {
+                        if (edge || !plain)
+                            soften_held(std::true_type{});
+                        else
+                            soften_held(std::false_type{});
+                    } else {
+                        if (edge || !plain)
+                            soften(std::true_type{});
+                        else
+                            soften(std::false_type{});
+                    }
                 } else if (lane == 0) {
                     mbar_arrive(&b.p_full[t][0]);
                     mbar_arrive(&b.p_full[t][1]);
@@ -1401,7 +1533,7 @@ int launch(AttendParams &p, int grid, cudaStream_t st) {
         set_error("kvc_attend: the tensor-core kernel's attributes: %s", cudaGetErrorString(err));
         return KVC_ERR_CUDA;
     }
-    // (of a library built by the compiler it was measured with, these are 168 or 128)
+    // (of a library built by the compiler it was measured with, these are 168 or 96)
     if (regs != Shape<BITS>::kRegsLaunch) {
         set_error("kvc_attend: the tensor-core kernel has %d registers per thread, its split needs %d", regs,
                   Shape<BITS>::kRegsLaunch);

@@ -375,17 +375,20 @@ __device__ __forceinline__ void tile_v(uint2 codes, uint32_t step, uint32_t off,
     }
 }
 
-// A block of 16 rows as it is held, in a warp's registers: lane = 4 (row & 7) + c has
-// piece c of all groups of rows r8 and r8 + 8.
+// A block of 16 rows as it is held, in a warp's registers: lane 4 j + c has piece c of
+// all groups of rows r8 and r8 + 8, r8 = 0, 4, 1, 5, 2, 6, 3, 7 for j = 0 .. 7: the
+// eight lanes whose 16 bytes are stored at a time hit eight places of the swizzle.
 template <int KH, int BITS>
 struct HeldRows {
     static constexpr int G = 2 * KH, kCodes = quant_codes(BITS, G);
     uint32_t word[2][KH];
     uint32_t code[2][kCodes / 16];
 
+    static __device__ __forceinline__ int row8() { return (threadIdx.x >> 3 & 3) | (threadIdx.x & 4); }
+
     // Rows at and after `rows` are zeros.
     __device__ __forceinline__ void load(const uint8_t *raw, int rows) {
-        const int r8 = (threadIdx.x & 31) >> 2, c = threadIdx.x & 3;
+        const int r8 = row8(), c = threadIdx.x & 3;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int r = r8 + 8 * i;
@@ -425,7 +428,7 @@ struct HeldRows {
     // V: groups that stand for NaN become zeros from row `finite` on (*dirty is set if
     // one of them is before `held`); the exponent of the largest step, or -127.
     __device__ __forceinline__ int exponent(int finite, int held, volatile int *dirty) {
-        const int r8 = (threadIdx.x & 31) >> 2;
+        const int r8 = row8();
         uint32_t top = 0;
         bool odd = false;
 #pragma unroll
@@ -455,28 +458,25 @@ struct HeldRows {
     // To rows row0 .. + 15 of a tile (V: over 2^e).
     template <bool V>
     __device__ __forceinline__ void write(uint32_t tile, int row0, int e) const {
-        const int r8 = (threadIdx.x & 31) >> 2, c = threadIdx.x & 3;
+        const int r8 = row8(), c = threadIdx.x & 3;
         const float down = V ? __uint_as_float((uint32_t)(127 - e) << 23) : 1.f;
-        const bool swap = r8 & 1;   // odd rows have the groups of a pair the other way round: all banks
-        const uint32_t at = tile + (row0 + r8) * 128 + ((c ^ r8) << 4 & 0x30) + ((c ^ r8 ^ (swap ? 4 : 0)) << 4 & 0x40);
+        const uint32_t at = tile + (row0 + r8) * 128 + ((c ^ r8) << 4);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int k = 0; k < KH; ++k) {
-                const uint2 a = piece<V>(i, 2 * k), b = piece<V>(i, 2 * k + 1);
-                const uint2 n0 = swap ? b : a, n1 = swap ? a : b;
-                const uint32_t w = swap ? __byte_perm(word[i][k], 0, 0x1032) : word[i][k];
+                const uint32_t w = word[i][k];
                 uint32_t y0[4], y1[4];
                 if (V) {
                     // both groups' steps over 2^e, and the zero codes' share
                     uint32_t s, off;
                     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(s) : "f"(quant_step<BITS>(w >> 16) * down), "f"(quant_step<BITS>(w & 0xffffu) * down));
                     off = mul_f16x2(BITS == 4 ? (w << 6 & 0x03c003c0u) | 0xcc00cc00u : (w & 0x00ff00ffu) | 0xe400e400u, s);
-                    tile_v<BITS>(n0, __byte_perm(s, 0, 0x1010), __byte_perm(off, 0, 0x1010), y0);
-                    tile_v<BITS>(n1, __byte_perm(s, 0, 0x3232), __byte_perm(off, 0, 0x3232), y1);
+                    tile_v<BITS>(piece<V>(i, 2 * k), __byte_perm(s, 0, 0x1010), __byte_perm(off, 0, 0x1010), y0);
+                    tile_v<BITS>(piece<V>(i, 2 * k + 1), __byte_perm(s, 0, 0x3232), __byte_perm(off, 0, 0x3232), y1);
                 } else {
-                    tile_k<BITS>(n0, __byte_perm(w, 0, 0x1010), y0);
-                    tile_k<BITS>(n1, __byte_perm(w, 0, 0x3232), y1);
+                    tile_k<BITS>(piece<V>(i, 2 * k), __byte_perm(w, 0, 0x1010), y0);
+                    tile_k<BITS>(piece<V>(i, 2 * k + 1), __byte_perm(w, 0, 0x3232), y1);
                 }
                 const uint32_t to = at + i * 8 * 128 + k * kBox;
                 write16(to, y0);
@@ -851,14 +851,16 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1)
                 }
                 tc_commit(&b.s_full[t]);
             };
-            // keys 0-63 or 64-127 of the tile
-            auto issue_o = [&](uint32_t f, auto upper, bool add) {
-                constexpr int k0 = decltype(upper)::value ? 4 : 0;
+            // keys 0-63 or 64-127 of the tile.  (Held rows: the upper ones come first, their P
+            // from S's upper columns; the first group of a unit's first tile does not add.)
+            auto issue_o = [&](uint32_t f, auto second, bool add) {
+                constexpr bool kUpper = decltype(second)::value == (BITS == 0);
+                constexpr int k0 = kUpper ? 4 : 0, kP = BITS != 0 && kUpper ? 32 : 0;
                 const uint64_t v = desc_sw128(smem_u32(ring) + (f % kStages) * kStageBytes, kBox, 1024);
 #pragma unroll
                 for (int ks = k0; ks < k0 + 4; ++ks) {
                     const uint64_t at = v + (uint64_t)(ks * (16 * 128 >> 4));
-                    tc_mma_bf16_tmem_a(col_o, col_s + ks * 8, at, kIdO, add || ks > 0);
+                    tc_mma_bf16_tmem_a(col_o, col_s + kP + ks * 8, at, kIdO, add || ks > k0);
                     if (TWO) tc_mma_bf16_tmem_a(col_o, col_s + 64 + ks * 8, at, kIdO, 1);
                 }
             };
@@ -1126,35 +1128,39 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1)
                     f2_unpack(f2_add(sum2[0], sum2[1]), s0, s1);
                     l += s0 + s1;
                 };
-                // held rows: 32 logits at a time, read from TMEM once for the maximum and
-                // once for the probabilities, for want of registers
+                // held rows: 64 logits at a time for want of registers.  The maximum of
+                // keys 0-63, that of keys 64-127, whose probabilities come first, and then
+                // keys 0-63 once more.
                 auto soften_held = [&](auto slow) {
                     constexpr bool kSlow = decltype(slow)::value;
                     const int lim = sees - k0;
                     auto seen = [&](int j, float s) { return j < lim ? s * c : -INFINITY; };
                     float v[2][32], x[4];
-                    tmem_ld32(cs, v[0]);
-                    tmem_ld_wait();
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        float(&y)[32] = v[q & 1];
-                        reg_fence(y);
-                        if (q < 3) tmem_ld32(cs + 32 * (q + 1), v[~q & 1]);
-                        if (kSlow) {
+                    for (int h = 0; h < 2; ++h) {
+                        tmem_ld32(cs + 64 * h, v[0]);
+                        tmem_ld32(cs + 64 * h + 32, v[1]);
+                        tmem_ld_wait();
+                        reg_fence(v[0]);
+                        reg_fence(v[1]);
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) y[j] = seen(q * 32 + j, y[j]);
+                        for (int q = 0; q < 2; ++q) {
+                            float(&y)[32] = v[q];
+                            if (kSlow) {
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) y[j] = seen(64 * h + 32 * q + j, y[j]);
+                            }
+                            float &top = x[2 * h + q];
+                            top = fmax3(y[0], y[1], y[2]);
+#pragma unroll
+                            for (int j = 3; j < 31; j += 2) top = fmax3(top, y[j], y[j + 1]);
+                            top = fmaxf(top, y[31]);
                         }
-                        x[q] = fmax3(y[0], y[1], y[2]);
-#pragma unroll
-                        for (int j = 3; j < 31; j += 2) x[q] = fmax3(x[q], y[j], y[j + 1]);
-                        x[q] = fmaxf(x[q], y[31]);
-                        if (q < 3) tmem_ld_wait();
                     }
-                    tmem_ld32(cs, v[0]);
                     const float top = fmaxf(fmax3(x[0], x[1], x[2]), x[3]) * (kSlow ? 1.f : c);
                     int e_top = exps[0];
 #pragma unroll
-                    for (int q = 1; q < 8; ++q) e_top = max(e_top, exps[q]);
+                    for (int q = 1; q < 8; ++q) e_top = max(e_top, exps[q % (BITS == 0 ? 1 : 8)]);
                     if (i == 0) {
                         m = top;
                         top_exp = e_top;
@@ -1168,60 +1174,77 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1)
                                 down *= __uint_as_float((uint32_t)max(127 + top_exp - e_top, 0) << 23);
                                 top_exp = e_top;
                             }
-                            tmem_ld_wait();
-                            reg_fence(v[0]);
 #pragma unroll 1
-                            for (int d = 0; d < D; d += 32) {
-                                float o[32];
-                                uint32_t ou[32];
-                                tmem_ld32(co + d, o);
+                            for (int d = 0; d < D; d += 16) {
+                                float o[16];
+                                uint32_t ou[16];
+                                tmem_ld16(co + d, o);
                                 tmem_ld_wait();
-                                reg_fence(o);
 #pragma unroll
-                                for (int j = 0; j < 32; ++j) ou[j] = __float_as_uint(o[j] * down);
-                                tmem_st32(co + d, ou);
+                                for (int j = 0; j < 16; ++j) {
+                                    asm volatile("" : "+f"(o[j]));   // read once it is there
+                                    ou[j] = __float_as_uint(o[j] * down);
+                                }
+                                tmem_st16(co + d, ou);
                             }
                         }
                     }
                     const float nm = m == -INFINITY ? 0.f : -m;
-                    const unsigned long long nm2 = f2_pack(nm, nm);
-                    unsigned long long sum2[2] = {0, 0};
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        float(&y)[32] = v[q & 1];
-                        tmem_ld_wait();
-                        reg_fence(y);
-                        if (q < 3) tmem_ld32(cs + 32 * (q + 1), v[~q & 1]);
+                    float sum = 0.f;
+                    // keys 32 q .. + 31 of the tile from y, the slow way already scaled or not
+                    auto weigh = [&](int q, float(&y)[32], auto scaled) {
                         uint32_t pw[16];
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            float y0, y1;
-                            if (kSlow) {
-                                y0 = seen(q * 32 + 2 * j, y[2 * j]) + nm;
-                                y1 = seen(q * 32 + 2 * j + 1, y[2 * j + 1]) + nm;
-                            } else {
-                                f2_unpack(f2_fma(f2_pack(y[2 * j], y[2 * j + 1]), c2, nm2), y0, y1);
+                        for (int b16 = 0; b16 < 2; ++b16) {
+                            // P is p 2^shift, shift = e - E + 6 of the block of 16 columns;
+                            // far below, where that rounds to zero, p still counts in l
+                            const int shift = max(exps[(2 * q + b16) % (BITS == 0 ? 1 : 8)] - top_exp + 6, -60);
+                            const float at = nm + (float)shift;
+                            const unsigned long long at2 = f2_pack(at, at);
+                            unsigned long long sum2 = 0;
+#pragma unroll
+                            for (int j = 8 * b16; j < 8 * b16 + 8; ++j) {
+                                float y0 = y[2 * j], y1 = y[2 * j + 1];
+                                if (kSlow) {
+                                    if (!decltype(scaled)::value) {
+                                        y0 = seen(q * 32 + 2 * j, y0);
+                                        y1 = seen(q * 32 + 2 * j + 1, y1);
+                                    }
+                                    y0 += at;
+                                    y1 += at;
+                                } else {
+                                    f2_unpack(f2_fma(f2_pack(y0, y1), c2, at2), y0, y1);
+                                }
+                                y0 = ex2(y0);
+                                y1 = ex2(y1);
+                                sum2 = j == 8 * b16 ? f2_pack(y0, y1) : f2_add(sum2, f2_pack(y0, y1));
+                                asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pw[j]) : "f"(y1), "f"(y0));
                             }
-                            const unsigned long long pp = f2_pack(ex2(y0), ex2(y1));
-                            sum2[j & 1] = f2_add(sum2[j & 1], pp);
-                            // 2^(e - E + 6) of the block of 16 columns
-                            const float f = __uint_as_float((uint32_t)max(133 + exps[(2 * q + (j >> 3)) % (BITS == 0 ? 1 : 8)] - top_exp, 0) << 23);
-                            float r0, r1;
-                            f2_unpack(f2_mul(pp, f2_pack(f, f)), r0, r1);
-                            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pw[j]) : "f"(r1), "f"(r0));
+                            float s0, s1;
+                            f2_unpack(sum2, s0, s1);
+                            sum = fmaf(s0 + s1, __uint_as_float((uint32_t)(127 - shift) << 23), sum);
                         }
-                        // over columns of S that are read: P's 16 q are S's up to 16 q + 15
-                        tmem_st16(cs + 16 * q, pw);
-                        if (q & 1) {
-                            tmem_st_wait();
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&b.p_full[t][q >> 1]);
-                        }
-                    }
-                    float s0, s1;
-                    f2_unpack(f2_add(sum2[0], sum2[1]), s0, s1);
-                    l += s0 + s1;
+                        // over logits that are in registers or read for the last time
+                        tmem_st16(cs + (q < 2 ? 0 : 32) + 16 * q, pw);
+                    };
+                    auto handed = [&](int h) {
+                        tmem_st_wait();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&b.p_full[t][h]);
+                    };
+                    weigh(2, v[0], std::true_type{});
+                    tmem_ld32(cs, v[0]);
+                    weigh(3, v[1], std::true_type{});
+                    tmem_ld32(cs + 32, v[1]);
+                    handed(0);
+                    tmem_ld_wait();
+                    reg_fence(v[0]);
+                    reg_fence(v[1]);
+                    weigh(0, v[0], std::false_type{});
+                    weigh(1, v[1], std::false_type{});
+                    handed(1);
+                    l += sum;
                 };
                 if (any) {
                     if constexpr (BITS != 0) {

@@ -175,7 +175,20 @@ int attend_call(const char *fn, int bits, const kvc_cache *cache, int32_t n_q_he
     p.group_stat = reinterpret_cast<float2 *>(base + w.group_stat);
     p.part = reinterpret_cast<float *>(base + w.part);
     const bool f32 = c.dtype == KVC_F32;
-    if (bits != 0 && w.tc) return launch_attend_tc_quant(p, 0, w.needs.grid, stream);
+    if (bits != 0 && w.tc) {
+        // Lists of few rows are attend_quant.cu's; where chunks are among them, a token's,
+        // in a launch of their own as in launch_attend_simt.
+        const int few = attend_quant_rows(c.head_dim);
+        const int64_t most = (int64_t)max_new * p.group;
+        if (most <= few) return launch_attend_quant(p, (int)most, w.needs.grid, stream);
+        const int own = p.group <= 8 ? 8 : p.group <= 16 ? 16 : 32;
+        const bool both = own <= few && n_tokens * p.group <= 128 * (int64_t)n_seqs;
+        if (both) {
+            const int rc = launch_attend_quant(p, own, w.needs.grid, stream);
+            if (rc) return rc;
+        }
+        return launch_attend_tc_quant(p, both ? own : 0, w.needs.grid, stream);
+    }
     if (bits != 0)
         return bits == 4 ? launch_attend_simt_quant4(p, f32, w.needs.grid, stream)
                          : launch_attend_simt_quant8(p, f32, w.needs.grid, stream);

@@ -362,6 +362,23 @@ __device__ __forceinline__ bool attend_last(uint32_t *count, uint32_t all) {
     return before == all - 1;
 }
 
+// The block's rows of a slot are written: count it; true in the whole block if it
+// is the last of `all` (one alone is not counted, as in attend_last).
+__device__ __forceinline__ bool attend_block_last(uint32_t *count, uint32_t all, uint32_t *s_last) {
+    __threadfence();
+    __syncthreads();
+    if (all == 1) return true;
+    if (threadIdx.x == 0) {
+        const bool last = atomicAdd(count, 1u) == all - 1;
+        if (last) *count = 0;
+        *s_last = last;
+    }
+    __syncthreads();
+    const bool last = *s_last;
+    __threadfence();
+    return last;
+}
+
 // How many warps have been counted; what they wrote before is visible after it.
 __device__ __forceinline__ uint32_t attend_peek(const uint32_t *count) {
     uint32_t is = 0;
@@ -518,6 +535,9 @@ int launch_attend_simt(AttendParams &p, bool f32, int grid, cudaStream_t st);
 int launch_attend_simt_quant4(AttendParams &p, bool f32, int grid, cudaStream_t st);
 int launch_attend_simt_quant8(AttendParams &p, bool f32, int grid, cudaStream_t st);
 int launch_attend_tc(AttendParams &p, int grid, cudaStream_t st);
+// Lists of at most `rows` rows (16; 32 where D is 64), on the warp-wide tensor instruction.
+int attend_quant_rows(int dim);
+int launch_attend_quant(AttendParams &p, int rows, int sms, cudaStream_t st);
 // Lists of more than rows_above rows.
 int launch_attend_tc_quant(AttendParams &p, int rows_above, int grid, cudaStream_t st);
 

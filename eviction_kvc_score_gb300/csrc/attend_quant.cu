@@ -1,0 +1,694 @@
+// attend_quant.cu -- attention of few rows over a cache held in 4 or 8 bits: bf16
+// queries of head size 64 or 128, up to 8 NT rows (tokens x the KV head's query heads)
+// per list.  What a decode step or a draft is made of; longer lists of rows are
+// attend_tc.cuh's.
+//
+// Reading the cache should bound it: a code may then cost three instructions, so none
+// is spent on taking it out of the packed word but the one that picks it, on its zero
+// code or on its step.  With codes n, step s and zero code z of a key's group, and
+// everything per row (query head) of the list:
+//   logit  = sum_g s_g (sum_d q_d n_d - z_g sum_d q_d)
+//   out_d  = sum_t (p_t s_tg) n_td - sum_t p_t (s_tg z_tg)
+// The sums over codes are matrix products (mma.m16n8k16) with the codes as they are:
+// a code picked out of its word by a mask is an fp16 number as it stands, n 2^-24 in
+// bits 0-3 (or 0-7) of a half and n 2^-20 in bits 4-7, exactly; the rows of Q, or of
+// the result, that meet the latter are 2^4 apart.  The groups' steps and zero codes go
+// to the products' 16 x 8 results in fp32 (K), or to the probabilities, one fp16
+// multiplication per key, row and group (V).
+//
+// Fragments: the product of K has 16 keys as its rows and 8 of the list's rows as
+// columns, a step of 16 channels picks two codes per lane out of every key's word, in
+// the order that quant.cuh lays down, so a lane loads all its codes of a key at once.
+// Its result, turned by movmatrix, is the second operand of V's product, whose rows
+// are channels.  Key i of a block stands in row pi(i) of both products: pi(2 c) = c,
+// pi(2 c + 1) = 4 + (c ^ 1), for fewer bank conflicts.
+//
+// P: fp16, 2^11 for a probability of 1 (the running maximum may lag behind by 2^4);
+// steps of V are taken over 2^E, the power of two of the largest so far, so that they
+// fit fp16 too.  Smaller numbers lose bits below 2^-35 of the largest product.
+//
+// Every warp walks 32 keys of each step of 128 by itself, with a ring of its own that
+// bulk copies fill (a block of K or V of 16 rows each); the warps' results meet in
+// shared memory at the end of a list.  Work is split as in attend.cuh.
+#include <climits>
+
+#include "attend.cuh"
+#include "quant.cuh"
+
+namespace kvc {
+
+namespace {
+
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kChunk = 32;                 // keys of a warp's step
+constexpr int kStepKeys = kWarps * kChunk;
+constexpr int kSlotRows = 32;
+// Blocks per SM by their registers: 128, 168 or 255 per thread.
+constexpr int per_sm_of(int nt) { return nt == 1 ? 4 : nt == 2 ? 3 : 2; }
+constexpr float kLag = 4.f;                // log2 units m may lag behind
+constexpr float kTop = 11.f;               // log2 of what P has for a probability of 1
+
+// Ring slots of a warp: three where four blocks of an SM have room for them.
+constexpr int slots_of(int bits, int groups) { return bits == 8 && groups == 4 ? 2 : 3; }
+constexpr int slot_bytes(int bits, int groups) { return 4 * quant_block(bits, groups); }   // K K V V
+constexpr int scratch_bytes(int groups) { return 2 * kChunk / 2 * groups * 4; }
+constexpr int out_floats(int groups) { return kWarps * 8 * (32 * groups + 1); }
+constexpr int ring_bytes(int bits, int groups) {
+    const int ring = kWarps * slots_of(bits, groups) * slot_bytes(bits, groups), out = out_floats(groups) * 4;
+    return ring > out ? ring : (out + 15) / 16 * 16;
+}
+
+template <int SLOTS>
+struct Shared {
+    uint64_t full[kWarps][SLOTS];
+    float2 stat[kWarps][8];
+    int64_t plan[kWarps + 4];
+    int stop;
+    uint32_t last;
+};
+
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// The transpose of an 8 x 8 matrix of 16-bit elements, a pair of a row per lane.
+__device__ __forceinline__ uint32_t turn(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t mul_f16(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpack_f16(uint32_t x) {
+    float2 r;
+    asm("{\n\t.reg .f16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}" : "=f"(r.x), "=f"(r.y) : "r"(x));
+    return r;
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }   // -127 .. 127
+
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+// The four pairs of codes of a piece of K (4 bits: of one word, 8 bits: of two), each
+// a pair of fp16 numbers; those of odd places 2^4 as large with 4 bits.
+template <int BITS>
+__device__ __forceinline__ void pick(uint32_t w0, uint32_t w1, uint32_t (&e)[4]) {
+    if (BITS == 4) {
+        const uint32_t up = w0 >> 8;
+        e[0] = w0 & 0x000f000fu;
+        e[1] = w0 & 0x00f000f0u;
+        e[2] = up & 0x000f000fu;
+        e[3] = up & 0x00f000f0u;
+    } else {
+        e[0] = w0 & 0x00ff00ffu;
+        e[1] = w0 >> 8 & 0x00ff00ffu;
+        e[2] = w1 & 0x00ff00ffu;
+        e[3] = w1 >> 8 & 0x00ff00ffu;
+    }
+}
+
+// Of a list's row r: channels 32 g + 8 c .. + 7.
+__device__ __forceinline__ uint4 load_q(const AttendParams &p, const AttendUnit &a, int r, int g, int c) {
+    if (r >= a.rows) return make_uint4(0, 0, 0, 0);
+    const int token = p.by_group(a.row0 + r);
+    const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) + (a.q0 + token) * p.q_stride +
+                             (int64_t)(a.h * p.group + a.row0 + r - token * p.group) * p.dim + 32 * g + 8 * c;
+    return *reinterpret_cast<const uint4 *>(q);
+}
+
+template <int G, int BITS, int NT>
+__global__ void __launch_bounds__(kThreads, per_sm_of(NT)) attend_quant_kernel(const __grid_constant__ AttendParams p) {
+    constexpr int D = 32 * G, kSlots = slots_of(BITS, G), kBlock = quant_block(BITS, G), kCodes = quant_codes(BITS, G);
+    constexpr int kRow = kCodes, kWordsAt = kQuantRows * kCodes, kOutRow = D + 1;
+    // a zero code is held as 1 + z / kZero; 16 or 256
+    constexpr float kZero = 1 << BITS;
+    extern __shared__ __align__(128) uint8_t raw[];
+    uint8_t *ring = raw;
+    float *s_out = reinterpret_cast<float *>(raw);   // the warps' results, when the ring is at rest
+    uint8_t *scratch_all = raw + ring_bytes(BITS, G);
+    Shared<kSlots> &s = *reinterpret_cast<Shared<kSlots> *>(scratch_all + kWarps * scratch_bytes(G));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r8 = lane >> 2, c = lane & 3;
+    uint8_t *mine = ring + warp * kSlots * slot_bytes(BITS, G);
+    uint32_t *steps = reinterpret_cast<uint32_t *>(scratch_all + warp * scratch_bytes(G));   // [pair of keys][G]
+    uint32_t *zeros = steps + kChunk / 2 * G;                                                // the same of s z
+    volatile int *stop = &s.stop;
+    const int key_of[2] = {(r8 & 1) ? 4 + (r8 >> 1 ^ 1) : r8 >> 1, 8 + ((r8 & 1) ? 4 + (r8 >> 1 ^ 1) : r8 >> 1)};   // of rows r8, r8 + 8
+    // the lane's own key of the 32, and its half of its pair's word
+    const int my_k = lane & 7, my_pair = (lane >> 3) * 4 + (my_k < 4 ? my_k : (my_k - 4) ^ 1), my_half = my_k >= 4;
+
+    if (tid == 0) {
+        for (int w = 0; w < kWarps; ++w)
+            for (int i = 0; i < kSlots; ++i) mbar_init(&s.full[w][i], 1);
+        s.stop = 0;
+        fence_barrier_init();
+    }
+    let_next_start();
+    wait_for_inputs();
+    const AttendRun run = attend_plan<kThreads, true>(p, s.plan);   // (its barrier is the barriers' too)
+    if (run.lo >= run.hi) return;
+    uint32_t used = 0, asked = 0;   // slots, over the whole run
+    bool ok = true;
+    int u = run.unit;
+    int64_t u_lo = run.unit_lo;
+    for (int64_t pos = run.lo; pos < run.hi;) {
+        const AttendUnit a = attend_unit<true>(p, u);
+        if (a.steps == 0) {
+            u = attend_next_seq<true>(p, a.b);
+            continue;
+        }
+        const int64_t end = min(run.hi, u_lo + a.steps);
+        const int t0 = (int)(pos - u_lo), t1 = (int)(end - u_lo);
+        // ---------------------------------------------------- loads
+        const int32_t *entry = p.table + (int64_t)a.list * p.max_pages;
+        // page numbers of the warp's blocks, 16 steps at a time
+        auto look_up = [&](int batch) {
+            const int64_t key = (int64_t)(t0 + batch * 16 + (lane >> 1)) * kStepKeys + warp * kChunk + kQuantRows * (lane & 1);
+            return key < a.hi ? entry[key >> p.shift] : 0;
+        };
+        int batch = 0, now = look_up(0), then = look_up(1), next = t0;
+        uint32_t absent = 0;   // two bits per slot: blocks that are not there
+        auto ask = [&]() {
+            const uint32_t slot = asked % kSlots;
+            const int at = 2 * (next - t0);
+            if (at >> 5 > batch) {
+                ++batch;
+                now = then;
+                then = look_up(batch + 1);
+            }
+            bool there[2];
+            int64_t block[2];
+            uint32_t bytes = 0;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int page = __shfl_sync(0xffffffffu, now, (at + j) & 31);
+                const int key = next * kStepKeys + warp * kChunk + kQuantRows * j;   // (at most 128 past a.hi)
+                there[j] = key < a.hi && page >= 0 && page < p.n_pages;
+                if (key < a.hi && !there[j] && lane == 0) set_status(p.status, KVC_DEV_BAD_PAGE);
+                block[j] = (((int64_t)page << p.shift) + (key & ((1 << p.shift) - 1))) >> 4;
+                bytes += there[j] ? 2 * kBlock : 0;
+            }
+            absent = (absent & ~(3u << 2 * slot)) | (uint32_t)(!there[0] | !there[1] << 1) << 2 * slot;
+            if (lane == 0 && !(p.skip_load && asked == 0)) {
+                uint64_t *bar = &s.full[warp][slot];
+                if (bytes)
+                    mbar_arrive_expect_tx(bar, bytes);
+                else
+                    mbar_arrive(bar);
+                uint8_t *dst = mine + slot * slot_bytes(BITS, G);
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    if (there[j]) {
+                        bulk_load(dst + j * kBlock, static_cast<const uint8_t *>(p.k_pool) + block[j] * kBlock, kBlock, bar);
+                        bulk_load(dst + (2 + j) * kBlock, static_cast<const uint8_t *>(p.v_pool) + block[j] * kBlock, kBlock, bar);
+                    }
+            }
+            ++asked;
+            ++next;
+        };
+        while (ok && next < min(t1, t0 + kSlots)) ask();
+
+        // ---------------------------------------------------- queries
+        // of row 8 nt + r8, piece c of every group, as fp16 over a power of two
+        uint32_t q[NT][G][4];
+        float qs[NT][G][2];   // of the lane's two columns: kZero times the group's sum
+        float factor[NT][2];  // logit in log2 units of a sum
+        int sees[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            uint4 x[G];
+            uint32_t top = 0;
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                x[g] = load_q(p, a, 8 * nt + r8, g, c);
+                const uint32_t w[4] = {x[g].x, x[g].y, x[g].z, x[g].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) top = max(top, max(w[i] << 16 & 0x7fffffffu, w[i] & 0x7fff0000u));
+            }
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int f = min(10 + 127 - (int)(top >> 23), 126);   // the largest becomes 2^10 and more
+            const float up = pow2(f);
+            float sum[G];
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                const uint32_t w[4] = {x[g].x, x[g].y, x[g].z, x[g].w};
+                float y[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    y[2 * i] = __uint_as_float(w[i] << 16) * up;
+                    y[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u) * up;
+                }
+                sum[g] = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    // the pairs that pick() makes; 2^4 more where the code is at 2^-24
+                    const int i0 = BITS == 4 ? 2 * i : 4 * (i >> 1) + (i & 1), i1 = BITS == 4 ? i0 + 1 : i0 + 2;
+                    const float more = BITS == 8 || i % 2 == 0 ? 16.f : 1.f;
+                    q[nt][g][i] = pack_f16(y[i0] * more, y[i1] * more);
+                    const float2 z = unpack_f16(q[nt][g][i]);
+                    sum[g] += (z.x + z.y) * (1.f / more);
+                }
+                sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
+                sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 2);
+            }
+            const float mul = p.scale_log2 * 0x1p20f * pow2(-f);   // codes times q are at 2^-20
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int from = (2 * c + e) * 4, row = 8 * nt + 2 * c + e;
+                factor[nt][e] = __shfl_sync(0xffffffffu, mul, from);
+#pragma unroll
+                for (int g = 0; g < G; ++g) qs[nt][g][e] = __shfl_sync(0xffffffffu, sum[g], from) * (0x1p-20f * kZero);
+                sees[nt][e] = row < a.rows ? attend_sees(p, a, row) : 0;
+            }
+        }
+        const int sees0 = attend_sees(p, a, 0);   // the fewest
+
+        float m[NT][2], l[NT][2], o[NT][2 * G][4], zo[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                m[nt][e] = -INFINITY;
+                l[nt][e] = 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                zo[nt][i] = 0.f;
+#pragma unroll
+                for (int mt = 0; mt < 2 * G; ++mt) o[nt][mt][i] = 0.f;
+            }
+        }
+        int top_exp = -127;   // O stands for sum p v / 2^top_exp
+
+        for (int t = t0; ok && t < t1; ++t) {
+            const uint32_t slot = used % kSlots;
+            ok = __all_sync(0xffffffffu, mbar_wait(&s.full[warp][slot], (used / kSlots) & 1, stop, p.status));
+            if (!ok) break;
+            ++used;
+            const uint8_t *k_at = mine + slot * slot_bytes(BITS, G), *v_at = k_at + 2 * kBlock;
+            const int key0 = t * kStepKeys + warp * kChunk;
+            const uint32_t gone = absent >> 2 * slot & 3;
+            // ------------------------------------------------ steps and zero codes of V, a key per lane
+            bool odd = false;
+            {
+                const uint8_t *w = v_at + (lane >> 4) * kBlock + kWordsAt + (lane & 15) * quant_words(G);
+                uint32_t word[G / 2];
+                const bool there = key0 + lane < a.hi && !(gone >> (lane >> 4) & 1);
+                if (G == 4) {
+                    const uint2 x = *reinterpret_cast<const uint2 *>(w);
+                    word[0] = there ? x.x : 0;
+                    word[G / 2 - 1] = there ? x.y : 0;
+                } else {
+                    word[0] = there ? *reinterpret_cast<const uint32_t *>(w) : 0;
+                }
+                uint32_t top = 0;
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    const uint32_t e = word[g / 2] >> (16 * (g & 1) + (BITS == 4 ? 7 : 8)) & 0xffu;
+                    odd |= e == 255;
+                    top = max(top, e == 255 ? 0 : e);
+                }
+                odd = __any_sync(0xffffffffu, odd);
+                const int e_top = (int)__reduce_max_sync(0xffffffffu, top) - 127;
+                if (e_top > top_exp) {
+                    // 2^(old - new), nothing of what was nothing
+                    const float down = pow2(max(top_exp - e_top, -127));
+                    top_exp = e_top;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            zo[nt][i] *= down;
+#pragma unroll
+                            for (int mt = 0; mt < 2 * G; ++mt) o[nt][mt][i] *= down;
+                        }
+                }
+                const float down = pow2(-top_exp);
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    const uint32_t one = g & 1 ? word[g / 2] >> 16 : word[g / 2] & 0xffffu;
+                    const bool nan = quant_is_nan<BITS>(one);
+                    const float st = nan ? 0.f : quant_step<BITS>(one) * down;
+                    const uint32_t both = pack_f16(st, nan ? 0.f : st * (float)quant_zero<BITS>(one));
+                    const int at = (my_pair * G + g) * 2 + my_half;
+                    reinterpret_cast<uint16_t *>(steps)[at] = (uint16_t)both;
+                    reinterpret_cast<uint16_t *>(zeros)[at] = (uint16_t)(both >> 16);
+                }
+            }
+            // ------------------------------------------------ logits
+            float x[2][NT][4];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                uint32_t code[2][kCodes / 16], word[2][G / 2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint8_t *at = k_at + b * kBlock + key_of[h] * kRow + c * (kCodes / 4);
+                    if (kCodes == 32) {
+                        const uint2 y = *reinterpret_cast<const uint2 *>(at);
+                        code[h][0] = y.x;
+                        code[h][1] = y.y;
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < kCodes / 64; ++i) {
+                            const uint4 y = reinterpret_cast<const uint4 *>(at)[i];
+                            code[h][4 * i] = y.x;
+                            code[h][4 * i + 1] = y.y;
+                            code[h][4 * i + 2] = y.z;
+                            code[h][4 * i + 3] = y.w;
+                        }
+                    }
+                    // (a block that is not there has steps of zero)
+                    const uint8_t *w = k_at + b * kBlock + kWordsAt + key_of[h] * quant_words(G);
+                    const uint32_t is = gone >> b & 1 ? 0 : 0xffffffffu;
+                    if (G == 4) {
+                        const uint2 y = *reinterpret_cast<const uint2 *>(w);
+                        word[h][0] = y.x & is;
+                        word[h][G / 2 - 1] = y.y & is;
+                    } else {
+                        word[h][0] = *reinterpret_cast<const uint32_t *>(w) & is;
+                    }
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[b][nt][i] = 0.f;
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    uint32_t e0[4], e1[4];   // of rows r8 and r8 + 8
+                    pick<BITS>(code[0][BITS == 4 ? g : 2 * g], code[0][BITS == 4 ? g : 2 * g + 1], e0);
+                    pick<BITS>(code[1][BITS == 4 ? g : 2 * g], code[1][BITS == 4 ? g : 2 * g + 1], e1);
+                    const uint32_t a0[4] = {e0[0], e1[0], e0[1], e1[1]}, a1[4] = {e0[2], e1[2], e0[3], e1[3]};
+                    float st[2], zf[2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t w = word[h][g / 2];
+                        if (BITS == 4) {
+                            st[h] = __uint_as_float((g & 1 ? w : w << 16) & 0xfff00000u);
+                            zf[h] = __uint_as_float(((g & 1 ? w << 3 : w << 19) & 0x00780000u) | 0x3f800000u);
+                        } else {
+                            st[h] = __uint_as_float((g & 1 ? w >> 1 : w << 15) & 0x7f800000u);
+                            zf[h] = __uint_as_float(((g & 1 ? w >> 1 : w << 15) & 0x007f8000u) | 0x3f800000u);
+                        }
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float d[4] = {qs[nt][g][0], qs[nt][g][1], qs[nt][g][0], qs[nt][g][1]};
+                        mma16816(d, a0, q[nt][g][0], q[nt][g][1]);
+                        mma16816(d, a1, q[nt][g][2], q[nt][g][3]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float y = fmaf(-zf[i >> 1], qs[nt][g][i & 1], d[i]);
+                            x[b][nt][i] = fmaf(st[i >> 1], y, x[b][nt][i]);
+                        }
+                    }
+                }
+            }
+            // ------------------------------------------------ softmax
+            const bool edge = key0 + kChunk > sees0;
+            bool grow = false;
+            float top[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float y = -INFINITY;
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            float &v = x[b][nt][2 * h + e];
+                            v *= factor[nt][e];
+                            if (edge && key0 + kQuantRows * b + key_of[h] >= sees[nt][e]) v = -INFINITY;
+                            y = fmaxf(y, v);
+                        }
+                    top[nt][e] = y;
+                    grow |= y > m[nt][e] + kLag;
+                }
+            if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float y = top[nt][e];
+#pragma unroll
+                        for (int d = 4; d <= 16; d <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
+                        y = fmaxf(y, m[nt][e]);
+                        const float down = y == -INFINITY ? 1.f : ex2(m[nt][e] - y);
+                        m[nt][e] = y;
+                        l[nt][e] *= down;
+                        zo[nt][e] *= down;
+                        zo[nt][2 + e] *= down;
+#pragma unroll
+                        for (int mt = 0; mt < 2 * G; ++mt) {
+                            o[nt][mt][e] *= down;
+                            o[nt][mt][2 + e] *= down;
+                        }
+                    }
+            }
+            uint32_t pt[2][NT][2];   // P with keys as the inner dimension: [block][..][keys 0-7, 8-15]
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const float n0 = kTop - (m[nt][0] == -INFINITY ? 0.f : m[nt][0]), n1 = kTop - (m[nt][1] == -INFINITY ? 0.f : m[nt][1]);
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float p0 = ex2(x[b][nt][2 * h] + n0), p1 = ex2(x[b][nt][2 * h + 1] + n1);
+                        l[nt][0] += p0;
+                        l[nt][1] += p1;
+                        pt[b][nt][h] = turn(pack_f16(p0, p1));
+                    }
+            }
+            __syncwarp();   // steps and zeros are written
+            // ------------------------------------------------ values
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                // keys that stand at 2 c, 2 c + 1, 2 c + 8, 2 c + 9 of the block
+                uint32_t code[4][kCodes / 32];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int key = (j & 1 ? 4 + (c ^ 1) : c) + 8 * (j >> 1);
+                    const uint8_t *at = v_at + b * kBlock + key * kRow + r8 * (kCodes / 8);
+                    if (kCodes == 32) {
+                        code[j][0] = *reinterpret_cast<const uint32_t *>(at);
+                    } else if (kCodes == 64) {
+                        const uint2 y = *reinterpret_cast<const uint2 *>(at);
+                        code[j][0] = y.x;
+                        code[j][kCodes / 32 - 1] = y.y;
+                    } else {
+                        const uint4 y = *reinterpret_cast<const uint4 *>(at);
+                        code[j][0] = y.x;
+                        code[j][1 % (kCodes / 32)] = y.y;
+                        code[j][2 % (kCodes / 32)] = y.z;
+                        code[j][3 % (kCodes / 32)] = y.w;
+                    }
+                }
+                uint32_t st[2][G];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t *at = steps + (8 * b + 4 * h + c) * G;
+                    if (G == 4) {
+                        const uint4 y = *reinterpret_cast<const uint4 *>(at);
+                        st[h][0] = y.x;
+                        st[h][1] = y.y;
+                        st[h][2 % G] = y.z;
+                        st[h][3 % G] = y.w;
+                    } else {
+                        const uint2 y = *reinterpret_cast<const uint2 *>(at);
+                        st[h][0] = y.x;
+                        st[h][1] = y.y;
+                    }
+                }
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    // codes of two keys side by side: channels e[0] .. e[3] of the lane's half
+                    uint32_t e0[4], e1[4];
+                    if (BITS == 4) {
+                        const uint32_t sel = g & 1 ? 0x7632 : 0x5410;
+                        pick<4>(__byte_perm(code[0][g / 2], code[1][g / 2], sel), 0, e0);
+                        pick<4>(__byte_perm(code[2][g / 2], code[3][g / 2], sel), 0, e1);
+                    } else {
+                        pick<8>(__byte_perm(code[0][g], code[1][g], 0x5410), __byte_perm(code[0][g], code[1][g], 0x7632), e0);
+                        pick<8>(__byte_perm(code[2][g], code[3][g], 0x5410), __byte_perm(code[2][g], code[3][g], 0x7632), e1);
+                    }
+                    const uint32_t a0[4] = {e0[0], e0[1], e1[0], e1[1]}, a1[4] = {e0[2], e0[3], e1[2], e1[3]};
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const uint32_t b0 = mul_f16(pt[b][nt][0], st[0][g]), b1 = mul_f16(pt[b][nt][1], st[1][g]);
+                        mma16816(o[nt][2 * g], a0, b0, b1);
+                        mma16816(o[nt][2 * g + 1], a1, b0, b1);
+                    }
+                }
+                // rows 0 .. G - 1 of a product of their own: the groups' s z
+                const uint32_t az[4] = {zeros[(8 * b + c) * G + r8 % G], 0, zeros[(8 * b + 4 + c) * G + r8 % G], 0};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) mma16816(zo[nt], az, pt[b][nt][0], pt[b][nt][1]);
+            }
+            if (odd) {   // groups of V that stand for NaN, for the rows that see them
+                for (int k = 0; k < kChunk; ++k) {
+                    if (key0 + k >= a.hi || (gone >> (k >> 4) & 1)) continue;
+                    const uint16_t *w = reinterpret_cast<const uint16_t *>(v_at + (k >> 4) * kBlock + kWordsAt + (k & 15) * quant_words(G));
+#pragma unroll
+                    for (int g = 0; g < G; ++g) {
+                        if (!quant_is_nan<BITS>(w[g])) continue;
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (key0 + k < sees[nt][i & 1]) o[nt][2 * g][i] = o[nt][2 * g + 1][i] = NAN;
+                    }
+                }
+            }
+            __syncwarp();   // the slot and the scratch are read
+            if (next < t1) ask();
+        }
+        for (; !ok && used < asked; ++used) mbar_drain(&s.full[warp][used % kSlots], (used / kSlots) & 1);   // every copy must land
+
+        // ---------------------------------------------------- the warps' results
+        const bool whole = t0 == 0 && t1 == a.steps;
+        const int64_t out_slot = (int64_t)blockIdx.x * p.slots + (t0 == 0 ? kSlotLast : kSlotFirst);
+        const float back = pow2(top_exp);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            __syncthreads();   // every warp's ring is at rest, the rows before are read
+            if (8 * nt >= a.rows) continue;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float sum = l[nt][e];
+#pragma unroll
+                for (int d = 4; d <= 16; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                if (r8 == 0) s.stat[warp][2 * c + e] = make_float2(m[nt][e], sum * 0x1p-11f);
+                float *dst = s_out + (warp * 8 + 2 * c + e) * kOutRow;
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    const float z = __shfl_sync(0xffffffffu, zo[nt][e], g * 4 + c);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float y = o[nt][2 * g + (i >> 1)][2 * (i & 1) + e] * (BITS == 4 && (i & 1) ? 0x1p20f : 0x1p24f) - z;
+                        const int ch = BITS == 4 ? 8 * (r8 >> 1) + 2 * i + (r8 & 1) : 4 * r8 + i;
+                        dst[32 * g + ch] = y * 0x1p-11f * back;
+                    }
+                }
+            }
+            __syncthreads();
+            const int row = tid >> 4, r = 8 * nt + row;
+            if (r >= a.rows) continue;
+            float2 st[kWarps];
+            float top = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                st[w] = s.stat[w][row];
+                top = fmaxf(top, st[w].x);
+            }
+            const float ref = top == -INFINITY ? 0.f : top;
+            float weight[kWarps], sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                weight[w] = ex2(st[w].x - ref);
+                sum = fmaf(st[w].y, weight[w], sum);
+            }
+            const bool see = attend_sees(p, a, r) > 0;
+            const int64_t out_row = attend_out_row(p, a, r);
+            const float inv = 1.f / sum;
+#pragma unroll
+            for (int j = 0; j < G; ++j) {
+                const int col = 32 * j + 2 * (tid & 15);
+                float y0 = 0.f, y1 = 0.f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const float *src = s_out + (w * 8 + row) * kOutRow + col;
+                    y0 = fmaf(src[0], weight[w], y0);
+                    y1 = fmaf(src[1], weight[w], y1);
+                }
+                if (whole) {
+                    uint32_t both;
+                    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(both) : "f"(see ? y1 * inv : 0.f), "f"(see ? y0 * inv : 0.f));
+                    *reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p.out) + out_row * D + col) = both;
+                } else {
+                    *reinterpret_cast<float2 *>(p.part + (out_slot * p.slot_rows + r) * D + col) = make_float2(y0, y1);
+                }
+            }
+            if ((tid & 15) == 0) {
+                if (whole)
+                    attend_store_lse(p, out_row, top, sum, see);
+                else
+                    p.stat[out_slot * p.slot_rows + r] = make_float2(top, sum);
+            }
+        }
+        if (!whole) {
+            const int c0 = attend_cta_of(run.total, run.grid, u_lo);
+            const int c1 = attend_cta_of(run.total, run.grid, u_lo + a.steps - 1);
+            const int me = blockIdx.x, n = c1 - c0 + 1, groups = attend_groups(n);
+            bool last = true;
+            if (groups > 1) {
+                const int g0 = c0 + (me - c0) / kJoinGroup * kJoinGroup, gn = min(kJoinGroup, c1 - g0 + 1);
+                last = attend_block_last(&p.arrived[16 * g0 + 8], gn, &s.last);
+                if (last)
+                    attend_join<__nv_bfloat16, 2, 4>(p, a, AttendSpan{c0, g0, 1, gn, false, false}, 0, a.rows, 0, tid, kThreads);
+            }
+            if (last && attend_block_last(&p.arrived[16 * c0], groups > 1 ? groups : n, &s.last))
+                attend_join<__nv_bfloat16, 2, 4>(p, a, AttendSpan{c0, c0, groups > 1 ? kJoinGroup : 1, groups > 1 ? groups : n, groups > 1, true},
+                                                 0, a.rows, 0, tid, kThreads);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // bulk copies come after what was written here
+        __syncthreads();   // the results are read: the ring may be filled again
+        pos = end;
+        u_lo += a.steps;
+        u = attend_next(p, a, u);
+    }
+}
+
+template <int G, int BITS, int NT>
+int launch(AttendParams &p, int sms, cudaStream_t st) {
+    constexpr size_t bytes = ring_bytes(BITS, G) + kWarps * scratch_bytes(G) + sizeof(Shared<slots_of(BITS, G)>);
+    static_assert(bytes <= 232448, "shared memory of one block");
+    allow_shared<attend_quant_kernel<G, BITS, NT>>((int)bytes);
+    // as many blocks as an SM holds at once (1 KB of shared memory is each block's own cost)
+    const int per_sm = std::max(1, std::min(per_sm_of(NT), (int)(233472 / (bytes + 1024))));
+    launch_early(attend_quant_kernel<G, BITS, NT>, per_sm * sms, kThreads, bytes, st, p);
+    return cache_launched("kvc_attend_quant");
+}
+
+template <int G, int BITS>
+int launch_rows(AttendParams &p, int rows, int sms, cudaStream_t st) {
+    if (rows <= 8) return launch<G, BITS, 1>(p, sms, st);
+    if constexpr (G == 2)
+        if (rows > 16) return launch<G, BITS, 4>(p, sms, st);
+    return launch<G, BITS, 2>(p, sms, st);
+}
+
+}  // namespace
+
+int attend_quant_rows(int dim) { return dim == 64 ? 32 : 16; }
+
+int launch_attend_quant(AttendParams &p, int rows, int sms, cudaStream_t st) {
+    const char *skip = getenv("KVC_TEST_SKIP_ARRIVE");
+    AttendParams own = p;
+    own.skip_load = skip && skip[0] == '1';
+    own.split_rows = 0;
+    own.step_keys = kStepKeys;
+    own.extra = 0;
+    own.slots = 2;
+    own.slot_rows = kSlotRows;
+    const int unit = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+    if (!attend_units(own, unit, 0, unit)) {
+        set_error("kvc_attend_quant: n_seqs * n_kv_heads * max_new is too large");
+        return KVC_ERR_UNSUPPORTED;
+    }
+    if (p.bits == 4) return p.dim == 64 ? launch_rows<2, 4>(own, unit, sms, st) : launch_rows<4, 4>(own, unit, sms, st);
+    return p.dim == 64 ? launch_rows<2, 8>(own, unit, sms, st) : launch_rows<4, 8>(own, unit, sms, st);
+}
+
+}  // namespace kvc

@@ -123,23 +123,6 @@ __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// The block's rows of a slot are written: count it; true in the whole block if it
-// is the last of `all` (one alone is not counted, as in attend_last).
-__device__ __forceinline__ bool block_last(uint32_t *count, uint32_t all, uint32_t *s_last) {
-    __threadfence();
-    __syncthreads();
-    if (all == 1) return true;
-    if (threadIdx.x == 0) {
-        const bool last = atomicAdd(count, 1u) == all - 1;
-        if (last) *count = 0;
-        *s_last = last;
-    }
-    __syncthreads();
-    const bool last = *s_last;
-    __threadfence();
-    return last;
-}
-
 // A thread's columns: CT chunks of 2 N, CT * TX * 2 N >= D.
 template <typename T, int ROWS, int N, int CT, int BITS>
 __global__ void __launch_bounds__(threads_of(ROWS), ROWS == 64 ? 2 : 4) attend_simt_kernel(const __grid_constant__ AttendParams p) {
@@ -414,10 +397,10 @@ __global__ void __launch_bounds__(threads_of(ROWS), ROWS == 64 ? 2 : 4) attend_s
             bool last = true;
             if (groups > 1) {
                 const int g0 = c0 + (me - c0) / kJoinGroup * kJoinGroup, gn = min(kJoinGroup, c1 - g0 + 1);
-                last = block_last(&p.arrived[16 * g0 + 8], gn, s_last);
+                last = attend_block_last(&p.arrived[16 * g0 + 8], gn, s_last);
                 if (last) attend_join<T, 2, 4>(p, a, AttendSpan{c0, g0, 1, gn, false, false}, 0, a.rows, 0, tid, kThreads);
             }
-            if (last && block_last(&p.arrived[16 * c0], groups > 1 ? groups : n, s_last))
+            if (last && attend_block_last(&p.arrived[16 * c0], groups > 1 ? groups : n, s_last))
                 attend_join<T, 2, 4>(p, a, AttendSpan{c0, c0, groups > 1 ? kJoinGroup : 1, groups > 1 ? groups : n, groups > 1, true},
                                      0, a.rows, 0, tid, kThreads);
         }

@@ -9,11 +9,11 @@ the same sum of (n + z) s, which sums over codes are made of (L_w for logits):
   largest element q_top, each is within 2^-34 q_top: 2^-34 L_top; scaled: 4 u L_w;
 - exponentials: ex2 is within 2^-22, its argument is rounded at |x| <= 2 L log2 e;
 - sums over T rows, rescaled once per tile: 2 (T + 64) u R_w;
-- on the tensor cores probabilities are rounded: to bf16, 2^-8 R, or, once alone and
-  once more times the step, to fp16 numbers, 2^-11 each of R_w, that stand at 2^15
-  for a probability of 1 and whose smallest step is 2^-24: half of that per row,
-  T 2^-40 N S with the largest step S, twice (codes and zero codes); steps below
-  2^-21 S lose bits: 2^-24 N S, twice;
+- on the tensor cores probabilities are rounded to fp16, alone and, for few rows, once
+  more times the step: 2^-11 each of R_w (2^-10 is taken).  fp16 ends at 2^-24, half of
+  which is lost per row: a probability of 1 stands at 2^6 or more, so T 2^-31 N S with
+  the largest step S, and for few rows, at 2^11, T 2^-36 N S twice (codes and zero
+  codes): together under T 2^-30 N S.  Steps below 2^-21 S lose bits: 2^-24 N S, twice;
 - the output is rounded once: eps / 2 of its value.
 lse moves by dx, the sum's T u and its own rounding."""
 import math
@@ -114,8 +114,7 @@ class Case:
         dx = 2 * (d + 18) * U * r["logit_w"] + 2.0 ** -34 * r["logit_top"] + 2.0 ** -21
         tol = 2 * dx[..., None] * r["reach"] + 2 * (t + 64) * U * r["reach_w"]
         if self.dtype == "bf16" and d in (64, 128):
-            tol = tol + 2.0 ** -8 * r["reach"] + 2.0 ** -10 * r["reach_w"]
-            tol = tol + (t * 2.0 ** -39 + 2.0 ** -23) * n * r["step"][..., None]
+            tol = tol + 2.0 ** -10 * r["reach_w"] + (t * 2.0 ** -30 + 2.0 ** -23) * n * r["step"][..., None]
         tol = tol + want.abs() * torch.finfo(self.q.dtype).eps / 2 * 1.001
         fine = want.isfinite() & real[..., None]
         assert torch.equal(self.out.isnan() & real[..., None], want.isnan() & real[..., None])

@@ -1,6 +1,7 @@
 """A wait that runs out in the tensor cores' attention over held rows.  With
 KVC_TEST_SKIP_ARRIVE=1 the warps that make tiles say nothing of their first one,
-so the bounded waits on it expire: the call records KVC_DEV_TIMEOUT, ends within
+and those that read few rows' keys leave their first load out, so the bounded waits
+on it expire: the call records KVC_DEV_TIMEOUT, ends within
 seconds and leaves the context usable -- after the workspace is initialised again,
 the next call gives what the call before gave."""
 import time
@@ -21,10 +22,11 @@ def _built():
 
 
 @pytest.mark.parametrize("bits", [4, 8])
-def test_missing_tile_times_out_and_context_recovers(monkeypatch, bits):
+@pytest.mark.parametrize("n", [1, 200])
+def test_missing_load_times_out_and_context_recovers(monkeypatch, n, bits):
     from test_quant_attend_gpu import Case, K
     kvc = K()
-    c = Case(ns=[200], lens=[900], hq=8, h=2, d=128, ps=64, dtype="bf16", bits=bits)
+    c = Case(ns=[n], lens=[900], hq=8, h=2, d=128, ps=64, dtype="bf16", bits=bits)
 
     def run():
         c.out.fill_(7), c.lse.fill_(7)

@@ -48,10 +48,11 @@ constexpr int per_sm_of(int nt) { return nt == 1 ? 4 : nt == 2 ? 3 : 2; }
 constexpr float kLag = 4.f;                // log2 units m may lag behind
 constexpr float kTop = 11.f;               // log2 of what P has for a probability of 1
 
-// Ring slots of a warp: three where four blocks of an SM have room for them.
-constexpr int slots_of(int bits, int groups) { return bits == 8 && groups == 4 ? 2 : 3; }
+// Ring slots of a warp.
+constexpr int slots_of(int bits, int groups) { return bits == 4 && groups == 2 ? 4 : 2; }
 constexpr int slot_bytes(int bits, int groups) { return 4 * quant_block(bits, groups); }   // K K V V
-constexpr int scratch_bytes(int groups) { return 2 * kChunk / 2 * groups * 4; }
+// K's steps and zero codes in fp32, V's in fp16.
+constexpr int scratch_bytes(int groups) { return kChunk * groups * 8 + 2 * kChunk / 2 * groups * 4; }
 constexpr int out_floats(int groups) { return kWarps * 8 * (32 * groups + 1); }
 constexpr int ring_bytes(int bits, int groups) {
     const int ring = kWarps * slots_of(bits, groups) * slot_bytes(bits, groups), out = out_floats(groups) * 4;
@@ -72,6 +73,11 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma16816_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 // The transpose of an 8 x 8 matrix of 16-bit elements, a pair of a row per lane.
 __device__ __forceinline__ uint32_t turn(uint32_t x) {
     uint32_t y;
@@ -86,6 +92,11 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 __device__ __forceinline__ uint32_t mul_f16(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t sub_f16(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 __device__ __forceinline__ float2 unpack_f16(uint32_t x) {
@@ -132,8 +143,6 @@ template <int G, int BITS, int NT>
 __global__ void __launch_bounds__(kThreads, per_sm_of(NT)) attend_quant_kernel(const __grid_constant__ AttendParams p) {
     constexpr int D = 32 * G, kSlots = slots_of(BITS, G), kBlock = quant_block(BITS, G), kCodes = quant_codes(BITS, G);
     constexpr int kRow = kCodes, kWordsAt = kQuantRows * kCodes, kOutRow = D + 1;
-    // a zero code is held as 1 + z / kZero; 16 or 256
-    constexpr float kZero = 1 << BITS;
     extern __shared__ __align__(128) uint8_t raw[];
     uint8_t *ring = raw;
     float *s_out = reinterpret_cast<float *>(raw);   // the warps' results, when the ring is at rest
@@ -141,7 +150,8 @@ __global__ void __launch_bounds__(kThreads, per_sm_of(NT)) attend_quant_kernel(c
     Shared<kSlots> &s = *reinterpret_cast<Shared<kSlots> *>(scratch_all + kWarps * scratch_bytes(G));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r8 = lane >> 2, c = lane & 3;
     uint8_t *mine = ring + warp * kSlots * slot_bytes(BITS, G);
-    uint32_t *steps = reinterpret_cast<uint32_t *>(scratch_all + warp * scratch_bytes(G));   // [pair of keys][G]
+    float2 *k_steps = reinterpret_cast<float2 *>(scratch_all + warp * scratch_bytes(G));   // [key][G]: s, -s z
+    uint32_t *steps = reinterpret_cast<uint32_t *>(k_steps + kChunk * G);                    // V: [pair of keys][G]
     uint32_t *zeros = steps + kChunk / 2 * G;                                                // the same of s z
     volatile int *stop = &s.stop;
     const int key_of[2] = {(r8 & 1) ? 4 + (r8 >> 1 ^ 1) : r8 >> 1, 8 + ((r8 & 1) ? 4 + (r8 >> 1 ^ 1) : r8 >> 1)};   // of rows r8, r8 + 8
@@ -158,7 +168,8 @@ __global__ void __launch_bounds__(kThreads, per_sm_of(NT)) attend_quant_kernel(c
     wait_for_inputs();
     const AttendRun run = attend_plan<kThreads, true>(p, s.plan);   // (its barrier is the barriers' too)
     if (run.lo >= run.hi) return;
-    uint32_t used = 0, asked = 0;   // slots, over the whole run
+    uint32_t slot = 0, round = 0;   // the slot that is next, and how often it has been
+    uint32_t pending = 0, first_ask = 1;
     bool ok = true;
     int u = run.unit;
     int64_t u_lo = run.unit_lo;
@@ -179,50 +190,52 @@ __global__ void __launch_bounds__(kThreads, per_sm_of(NT)) attend_quant_kernel(c
         };
         int batch = 0, now = look_up(0), then = look_up(1), next = t0;
         uint32_t absent = 0;   // two bits per slot: blocks that are not there
-        auto ask = [&]() {
-            const uint32_t slot = asked % kSlots;
+        // the warp's blocks of step `next` into slot `to`
+        auto ask = [&](uint32_t to) {
             const int at = 2 * (next - t0);
             if (at >> 5 > batch) {
                 ++batch;
                 now = then;
                 then = look_up(batch + 1);
             }
-            bool there[2];
-            int64_t block[2];
-            uint32_t bytes = 0;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int page = __shfl_sync(0xffffffffu, now, (at + j) & 31);
-                const int key = next * kStepKeys + warp * kChunk + kQuantRows * j;   // (at most 128 past a.hi)
-                there[j] = key < a.hi && page >= 0 && page < p.n_pages;
-                if (key < a.hi && !there[j] && lane == 0) set_status(p.status, KVC_DEV_BAD_PAGE);
-                block[j] = (((int64_t)page << p.shift) + (key & ((1 << p.shift) - 1))) >> 4;
-                bytes += there[j] ? 2 * kBlock : 0;
-            }
-            absent = (absent & ~(3u << 2 * slot)) | (uint32_t)(!there[0] | !there[1] << 1) << 2 * slot;
-            if (lane == 0 && !(p.skip_load && asked == 0)) {
-                uint64_t *bar = &s.full[warp][slot];
-                if (bytes)
-                    mbar_arrive_expect_tx(bar, bytes);
-                else
-                    mbar_arrive(bar);
-                uint8_t *dst = mine + slot * slot_bytes(BITS, G);
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    if (there[j]) {
-                        bulk_load(dst + j * kBlock, static_cast<const uint8_t *>(p.k_pool) + block[j] * kBlock, kBlock, bar);
-                        bulk_load(dst + (2 + j) * kBlock, static_cast<const uint8_t *>(p.v_pool) + block[j] * kBlock, kBlock, bar);
+            const int key = next * kStepKeys + warp * kChunk;   // (its blocks may lie past a.hi)
+            const int page0 = __shfl_sync(0xffffffffu, now, at & 31), page1 = __shfl_sync(0xffffffffu, now, (at + 1) & 31);
+            const bool seen0 = key < a.hi, seen1 = key + kQuantRows < a.hi;
+            const bool there0 = seen0 && (uint32_t)page0 < (uint32_t)p.n_pages, there1 = seen1 && (uint32_t)page1 < (uint32_t)p.n_pages;
+            absent = (absent & ~(3u << 2 * to)) | (uint32_t)(!there0 | !there1 << 1) << 2 * to;
+            if (lane == 0) {
+                if ((seen0 && !there0) || (seen1 && !there1)) set_status(p.status, KVC_DEV_BAD_PAGE);
+                if (!(p.skip_load && first_ask)) {
+                    uint64_t *bar = &s.full[warp][to];
+                    const uint32_t bytes = (there0 + there1) * 2 * kBlock;
+                    if (bytes)
+                        mbar_arrive_expect_tx(bar, bytes);
+                    else
+                        mbar_arrive(bar);
+                    uint8_t *dst = mine + to * slot_bytes(BITS, G);
+                    const int in_page = (key & ((1 << p.shift) - 1)) >> 4;
+                    if (there0) {
+                        const int64_t at0 = ((int64_t)page0 << (p.shift - 4)) + in_page;
+                        bulk_load(dst, static_cast<const uint8_t *>(p.k_pool) + at0 * kBlock, kBlock, bar);
+                        bulk_load(dst + 2 * kBlock, static_cast<const uint8_t *>(p.v_pool) + at0 * kBlock, kBlock, bar);
                     }
+                    if (there1) {   // the next block of the page, or the first of the next page
+                        const int64_t at1 = ((int64_t)page1 << (p.shift - 4)) + (p.shift == 4 ? 0 : in_page + 1);
+                        bulk_load(dst + kBlock, static_cast<const uint8_t *>(p.k_pool) + at1 * kBlock, kBlock, bar);
+                        bulk_load(dst + 3 * kBlock, static_cast<const uint8_t *>(p.v_pool) + at1 * kBlock, kBlock, bar);
+                    }
+                }
             }
-            ++asked;
+            first_ask = 0;
+            ++pending;
             ++next;
         };
-        while (ok && next < min(t1, t0 + kSlots)) ask();
+        for (uint32_t i = 0, to = slot; ok && i < kSlots && next < t1; ++i, to = to + 1 == kSlots ? 0 : to + 1) ask(to);
 
         // ---------------------------------------------------- queries
         // of row 8 nt + r8, piece c of every group, as fp16 over a power of two
         uint32_t q[NT][G][4];
-        float qs[NT][G][2];   // of the lane's two columns: kZero times the group's sum
+        float qs[NT][G][2];   // of the lane's two columns: the group's sum
         float factor[NT][2];  // logit in log2 units of a sum
         int sees[NT][2];
 #pragma unroll
@@ -269,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, per_sm_of(NT)) attend_quant_kernel(c
                 const int from = (2 * c + e) * 4, row = 8 * nt + 2 * c + e;
                 factor[nt][e] = __shfl_sync(0xffffffffu, mul, from);
 #pragma unroll
-                for (int g = 0; g < G; ++g) qs[nt][g][e] = __shfl_sync(0xffffffffu, sum[g], from) * (0x1p-20f * kZero);
+                for (int g = 0; g < G; ++g) qs[nt][g][e] = __shfl_sync(0xffffffffu, sum[g], from) * 0x1p-20f;
                 sees[nt][e] = row < a.rows ? attend_sees(p, a, row) : 0;
             }
         }
@@ -293,34 +306,60 @@ __global__ void __launch_bounds__(kThreads, per_sm_of(NT)) attend_quant_kernel(c
         int top_exp = -127;   // O stands for sum p v / 2^top_exp
 
         for (int t = t0; ok && t < t1; ++t) {
-            const uint32_t slot = used % kSlots;
-            ok = __all_sync(0xffffffffu, mbar_wait(&s.full[warp][slot], (used / kSlots) & 1, stop, p.status));
+            ok = __all_sync(0xffffffffu, mbar_wait(&s.full[warp][slot], round & 1, stop, p.status));
             if (!ok) break;
-            ++used;
+            --pending;
             const uint8_t *k_at = mine + slot * slot_bytes(BITS, G), *v_at = k_at + 2 * kBlock;
             const int key0 = t * kStepKeys + warp * kChunk;
             const uint32_t gone = absent >> 2 * slot & 3;
-            // ------------------------------------------------ steps and zero codes of V, a key per lane
+            // ------------------------------------------------ steps and zero codes, a key per lane
             bool odd = false;
             {
-                const uint8_t *w = v_at + (lane >> 4) * kBlock + kWordsAt + (lane & 15) * quant_words(G);
-                uint32_t word[G / 2];
                 const bool there = key0 + lane < a.hi && !(gone >> (lane >> 4) & 1);
+                const uint32_t is = there ? 0xffffffffu : 0;   // (a row that is not there has steps of zero)
+                const int at = (lane >> 4) * kBlock + kWordsAt + (lane & 15) * quant_words(G);
+                uint32_t kw[G / 2], vw[G / 2];
                 if (G == 4) {
-                    const uint2 x = *reinterpret_cast<const uint2 *>(w);
-                    word[0] = there ? x.x : 0;
-                    word[G / 2 - 1] = there ? x.y : 0;
+                    const uint2 y = *reinterpret_cast<const uint2 *>(k_at + at), z = *reinterpret_cast<const uint2 *>(v_at + at);
+                    kw[0] = y.x & is;
+                    kw[G / 2 - 1] = y.y & is;
+                    vw[0] = z.x & is;
+                    vw[G / 2 - 1] = z.y & is;
                 } else {
-                    word[0] = there ? *reinterpret_cast<const uint32_t *>(w) : 0;
+                    kw[0] = *reinterpret_cast<const uint32_t *>(k_at + at) & is;
+                    vw[0] = *reinterpret_cast<const uint32_t *>(v_at + at) & is;
                 }
                 uint32_t top = 0;
 #pragma unroll
-                for (int g = 0; g < G; ++g) {
-                    const uint32_t e = word[g / 2] >> (16 * (g & 1) + (BITS == 4 ? 7 : 8)) & 0xffu;
-                    odd |= e == 255;
-                    top = max(top, e == 255 ? 0 : e);
+                for (int i = 0; i < G / 2; ++i) {
+                    const uint32_t e0 = vw[i] >> (BITS == 4 ? 7 : 8) & 0xffu, e1 = vw[i] >> (BITS == 4 ? 23 : 24) & 0xffu;
+                    top = max(top, max(e0, e1));
+                    // zero codes as 1 + z / 16 or 1 + z / 256, for want of a cheap conversion
+                    const float s0 = quant_step<BITS>(kw[i] & 0xffffu), s1 = quant_step<BITS>(kw[i] >> 16);
+                    float z0, z1;
+                    if (BITS == 4) {
+                        z0 = fmaf(__uint_as_float((kw[i] << 19 & 0x00780000u) | 0x3f800000u), -16.f, 16.f);
+                        z1 = fmaf(__uint_as_float((kw[i] << 3 & 0x00780000u) | 0x3f800000u), -16.f, 16.f);
+                    } else {
+                        z0 = fmaf(__uint_as_float((kw[i] << 15 & 0x007f8000u) | 0x3f800000u), -256.f, 256.f);
+                        z1 = fmaf(__uint_as_float((kw[i] >> 1 & 0x007f8000u) | 0x3f800000u), -256.f, 256.f);
+                    }
+                    *reinterpret_cast<float4 *>(k_steps + lane * G + 2 * i) = make_float4(s0, s0 * z0, s1, s1 * z1);
                 }
-                odd = __any_sync(0xffffffffu, odd);
+                odd = __any_sync(0xffffffffu, top == 255);
+                if (odd) {   // groups of V that stand for NaN: added below
+                    top = 0;
+#pragma unroll
+                    for (int i = 0; i < G / 2; ++i)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t e = vw[i] >> (16 * h + (BITS == 4 ? 7 : 8)) & 0xffu;
+                            if (e == 255)
+                                vw[i] &= h ? 0xffffu : 0xffff0000u;
+                            else
+                                top = max(top, e);
+                        }
+                }
                 const int e_top = (int)__reduce_max_sync(0xffffffffu, top) - 127;
                 if (e_top > top_exp) {
                     // 2^(old - new), nothing of what was nothing
@@ -337,21 +376,26 @@ __global__ void __launch_bounds__(kThreads, per_sm_of(NT)) attend_quant_kernel(c
                 }
                 const float down = pow2(-top_exp);
 #pragma unroll
-                for (int g = 0; g < G; ++g) {
-                    const uint32_t one = g & 1 ? word[g / 2] >> 16 : word[g / 2] & 0xffffu;
-                    const bool nan = quant_is_nan<BITS>(one);
-                    const float st = nan ? 0.f : quant_step<BITS>(one) * down;
-                    const uint32_t both = pack_f16(st, nan ? 0.f : st * (float)quant_zero<BITS>(one));
-                    const int at = (my_pair * G + g) * 2 + my_half;
-                    reinterpret_cast<uint16_t *>(steps)[at] = (uint16_t)both;
-                    reinterpret_cast<uint16_t *>(zeros)[at] = (uint16_t)(both >> 16);
+                for (int i = 0; i < G / 2; ++i) {
+                    const uint32_t st = pack_f16(quant_step<BITS>(vw[i] & 0xffffu) * down, quant_step<BITS>(vw[i] >> 16) * down);
+                    // 1024 + z - 1024 in fp16
+                    const uint32_t z = sub_f16((vw[i] & (BITS == 4 ? 0x000f000fu : 0x00ff00ffu)) | 0x64006400u, 0x64006400u);
+                    const uint32_t sz = mul_f16(st, z);
+                    uint16_t *s16 = reinterpret_cast<uint16_t *>(steps) + (my_pair * G + 2 * i) * 2 + my_half;
+                    uint16_t *z16 = reinterpret_cast<uint16_t *>(zeros) + (my_pair * G + 2 * i) * 2 + my_half;
+                    s16[0] = (uint16_t)st;
+                    s16[2] = (uint16_t)(st >> 16);
+                    z16[0] = (uint16_t)sz;
+                    z16[2] = (uint16_t)(sz >> 16);
                 }
+                __syncwarp();
             }
             // ------------------------------------------------ logits
             float x[2][NT][4];
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                uint32_t code[2][kCodes / 16], word[2][G / 2];
+                uint32_t code[2][kCodes / 16];
+                float4 st[2][G / 2];   // step and zero code's share, of two groups each
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const uint8_t *at = k_at + b * kBlock + key_of[h] * kRow + c * (kCodes / 4);
@@ -369,16 +413,9 @@ __global__ void __launch_bounds__(kThreads, per_sm_of(NT)) attend_quant_kernel(c
                             code[h][4 * i + 3] = y.w;
                         }
                     }
-                    // (a block that is not there has steps of zero)
-                    const uint8_t *w = k_at + b * kBlock + kWordsAt + key_of[h] * quant_words(G);
-                    const uint32_t is = gone >> b & 1 ? 0 : 0xffffffffu;
-                    if (G == 4) {
-                        const uint2 y = *reinterpret_cast<const uint2 *>(w);
-                        word[h][0] = y.x & is;
-                        word[h][G / 2 - 1] = y.y & is;
-                    } else {
-                        word[h][0] = *reinterpret_cast<const uint32_t *>(w) & is;
-                    }
+#pragma unroll
+                    for (int i = 0; i < G / 2; ++i)
+                        st[h][i] = *reinterpret_cast<const float4 *>(k_steps + (kQuantRows * b + key_of[h]) * G + 2 * i);
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -390,51 +427,43 @@ __global__ void __launch_bounds__(kThreads, per_sm_of(NT)) attend_quant_kernel(c
                     pick<BITS>(code[0][BITS == 4 ? g : 2 * g], code[0][BITS == 4 ? g : 2 * g + 1], e0);
                     pick<BITS>(code[1][BITS == 4 ? g : 2 * g], code[1][BITS == 4 ? g : 2 * g + 1], e1);
                     const uint32_t a0[4] = {e0[0], e1[0], e0[1], e1[1]}, a1[4] = {e0[2], e1[2], e0[3], e1[3]};
-                    float st[2], zf[2];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint32_t w = word[h][g / 2];
-                        if (BITS == 4) {
-                            st[h] = __uint_as_float((g & 1 ? w : w << 16) & 0xfff00000u);
-                            zf[h] = __uint_as_float(((g & 1 ? w << 3 : w << 19) & 0x00780000u) | 0x3f800000u);
-                        } else {
-                            st[h] = __uint_as_float((g & 1 ? w >> 1 : w << 15) & 0x7f800000u);
-                            zf[h] = __uint_as_float(((g & 1 ? w >> 1 : w << 15) & 0x007f8000u) | 0x3f800000u);
-                        }
-                    }
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        float d[4] = {qs[nt][g][0], qs[nt][g][1], qs[nt][g][0], qs[nt][g][1]};
-                        mma16816(d, a0, q[nt][g][0], q[nt][g][1]);
+                        float d[4];
+                        mma16816_zero(d, a0, q[nt][g][0], q[nt][g][1]);
                         mma16816(d, a1, q[nt][g][2], q[nt][g][3]);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const float y = fmaf(-zf[i >> 1], qs[nt][g][i & 1], d[i]);
-                            x[b][nt][i] = fmaf(st[i >> 1], y, x[b][nt][i]);
+                            const float4 &w = st[i >> 1][g / 2];
+                            x[b][nt][i] = fmaf(g & 1 ? w.w : w.y, qs[nt][g][i & 1], fmaf(g & 1 ? w.z : w.x, d[i], x[b][nt][i]));
                         }
                     }
                 }
             }
             // ------------------------------------------------ softmax
-            const bool edge = key0 + kChunk > sees0;
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[b][nt][i] *= factor[nt][i & 1];
+            if (key0 + kChunk > sees0) {
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (key0 + kQuantRows * b + key_of[i >> 1] >= sees[nt][i & 1]) x[b][nt][i] = -INFINITY;
+            }
             bool grow = false;
             float top[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float y = -INFINITY;
-#pragma unroll
-                    for (int b = 0; b < 2; ++b)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            float &v = x[b][nt][2 * h + e];
-                            v *= factor[nt][e];
-                            if (edge && key0 + kQuantRows * b + key_of[h] >= sees[nt][e]) v = -INFINITY;
-                            y = fmaxf(y, v);
-                        }
-                    top[nt][e] = y;
-                    grow |= y > m[nt][e] + kLag;
+                    top[nt][e] = fmaxf(fmaxf(x[0][nt][e], x[0][nt][2 + e]), fmaxf(x[1][nt][e], x[1][nt][2 + e]));
+                    grow |= top[nt][e] > m[nt][e] + kLag;
                 }
             if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
@@ -471,7 +500,6 @@ __global__ void __launch_bounds__(kThreads, per_sm_of(NT)) attend_quant_kernel(c
                         pt[b][nt][h] = turn(pack_f16(p0, p1));
                     }
             }
-            __syncwarp();   // steps and zeros are written
             // ------------------------------------------------ values
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
@@ -552,9 +580,19 @@ __global__ void __launch_bounds__(kThreads, per_sm_of(NT)) attend_quant_kernel(c
                 }
             }
             __syncwarp();   // the slot and the scratch are read
-            if (next < t1) ask();
+            if (next < t1) ask(slot);
+            if (++slot == kSlots) {
+                slot = 0;
+                ++round;
+            }
         }
-        for (; !ok && used < asked; ++used) mbar_drain(&s.full[warp][used % kSlots], (used / kSlots) & 1);   // every copy must land
+        for (; !ok && pending > 0; --pending) {   // every copy must land
+            mbar_drain(&s.full[warp][slot], round & 1);
+            if (++slot == kSlots) {
+                slot = 0;
+                ++round;
+            }
+        }
 
         // ---------------------------------------------------- the warps' results
         const bool whole = t0 == 0 && t1 == a.steps;

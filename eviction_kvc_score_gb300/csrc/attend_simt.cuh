@@ -203,12 +203,10 @@ __global__ void __launch_bounds__(threads_of(ROWS), ROWS == 64 ? 2 : 4) attend_s
                     const int r = kPass * i + (tid >> 3);
                     const QuantRow at = quant_row(BITS, groups, r);
                     for (int u = tid & 7; u < vecs; u += 8) {
-                        float y[8];
-                        quant_values<BITS>(quant_load<BITS>(held + at.codes, groups, u >> 2, u & 3, of_v),
-                                           reinterpret_cast<const uint16_t *>(held + at.words)[u >> 2], y);
-#pragma unroll
-                        for (int e = 0; e < 8; e += 2)
-                            store2(reinterpret_cast<__nv_bfloat16 *>(dst + r * rb) + 8 * u + e, y[e], y[e + 1]);
+                        const uint32_t word = reinterpret_cast<const uint16_t *>(held + at.words)[u >> 2];
+                        uint32_t y[4];
+                        quant_bf16<BITS>(quant_load<BITS>(held + at.codes, groups, u >> 2, u & 3, of_v), word * 0x10001u, y);
+                        *reinterpret_cast<uint4 *>(dst + r * rb + 16 * u) = make_uint4(y[0], y[1], y[2], y[3]);
                     }
                 }
             }

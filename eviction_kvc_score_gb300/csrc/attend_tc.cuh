@@ -316,16 +316,6 @@ struct Walk {
 __device__ __forceinline__ void write16(uint32_t at, const uint32_t (&x)[4]) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]) : "memory");
 }
-__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
 __device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c) {
     uint32_t r;
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
@@ -335,28 +325,6 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
-}
-// Eight channels of K as bf16: codes come as 128 + n (4 bits), where bf16 counts in
-// ones, or 2^23 + n in fp32 (8 bits); the zero code comes off the same way, and times
-// the step it is exact.
-template <int BITS>
-__device__ __forceinline__ void tile_k(uint2 codes, uint32_t word, uint32_t (&y)[4]) {
-    if (BITS == 4) {
-        const uint32_t s = word & 0xfff0fff0u, z = (word & 0x000f000fu) | 0x43004300u;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = mul_bf16x2(sub_bf16x2(((codes.x >> 4 * i) & 0x000f000fu) | 0x43004300u, z), s);
-    } else {
-        const float s = quant_step<8>(word), z = -__uint_as_float(0x4b000000u | (word & 0xffu));
-        const unsigned long long s2 = f2_pack(s, s), z2 = f2_pack(z, z);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t w = i < 2 ? codes.x : codes.y;
-            float a, b;
-            f2_unpack(f2_mul(f2_add(f2_pack(__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440 + 2 * (i & 1))),
-                                            __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7441 + 2 * (i & 1)))), z2), s2), a, b);
-            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y[i]) : "f"(b), "f"(a));
-        }
-    }
 }
 // Eight channels of V over 2^e as fp16: codes come as 16 + n or 1024 + n, where fp16
 // has room for them (n of 4 or 8 bits); off is that of the zero code times the step
@@ -475,8 +443,8 @@ struct HeldRows {
                     tile_v<BITS>(piece<V>(i, 2 * k), __byte_perm(s, 0, 0x1010), __byte_perm(off, 0, 0x1010), y0);
                     tile_v<BITS>(piece<V>(i, 2 * k + 1), __byte_perm(s, 0, 0x3232), __byte_perm(off, 0, 0x3232), y1);
                 } else {
-                    tile_k<BITS>(piece<V>(i, 2 * k), __byte_perm(w, 0, 0x1010), y0);
-                    tile_k<BITS>(piece<V>(i, 2 * k + 1), __byte_perm(w, 0, 0x3232), y1);
+                    quant_bf16<BITS>(piece<V>(i, 2 * k), __byte_perm(w, 0, 0x1010), y0);
+                    quant_bf16<BITS>(piece<V>(i, 2 * k + 1), __byte_perm(w, 0, 0x3232), y1);
                 }
                 const uint32_t to = at + i * 8 * 128 + k * kBox;
                 write16(to, y0);

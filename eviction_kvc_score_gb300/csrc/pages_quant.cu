@@ -27,27 +27,23 @@ __device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&x)[8]) {
         x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
 }
-__device__ __forceinline__ void store8(float *p, const float (&x)[8]) {
-    reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+// Eight channels that come as bf16 pairs.
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, const uint32_t (&y)[4]) {
+    *reinterpret_cast<uint4 *>(p) = make_uint4(y[0], y[1], y[2], y[3]);
 }
-__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&x)[8]) {
-    uint32_t w[4];   // exact: see quant.cuh
+__device__ __forceinline__ void store8(float *p, const uint32_t (&y)[4]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(x[2 * i + 1]), "f"(x[2 * i]));
-    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    for (int i = 0; i < 2; ++i)
+        reinterpret_cast<float4 *>(p)[i] = make_float4(__uint_as_float(y[2 * i] << 16), __uint_as_float(y[2 * i] & 0xffff0000u),
+                                                       __uint_as_float(y[2 * i + 1] << 16), __uint_as_float(y[2 * i + 1] & 0xffff0000u));
 }
 
-// Where a warp's next 32 items (parts of rows) begin: no 64-bit division per step.
-struct Place {
-    int64_t row;
-    int item;
-    __device__ __forceinline__ void next(const Divider &by) {
-        const int rows = by(item += 32);
-        row += rows;
-        item -= rows * (int)by.d;
-    }
-};
+// A warp's rows are looked up 32 at a time, a lane each, and worked on in parts, 32 of
+// any rows at a time: the search for a row's list and pages would cost as much as a
+// part's work (560,000 rows read back: 116 us with a search per part, 62 so).
+__device__ __forceinline__ int64_t of_lane(int64_t x, int lane) {
+    return (int64_t)((uint64_t)__shfl_sync(0xffffffffu, (uint32_t)((uint64_t)x >> 32), lane) << 32 | __shfl_sync(0xffffffffu, (uint32_t)x, lane));
+}
 
 template <typename T>
 struct AppendParams : MoveLists {
@@ -72,47 +68,49 @@ __global__ void __launch_bounds__(kMoveThreads) append_quant_kernel(const __grid
     if (r0 >= r1) return;
     int i = owner(p.s.row_begin, p.n_lists, r0);
     uint32_t bad = 0;
-    const int64_t items = (r1 - r0) * pieces;   // a multiple of four: groups' lanes stay together
-    Place place{r0, 0};
-    for (int64_t base = 0; base < items; base += 32, place.next(p.by_pieces)) {
-        const int it = place.item + lane, dr = p.by_pieces(it), u = it - dr * pieces;
-        const int64_t r = place.row + dr;
-        const bool real = base + lane < items;
-        const unsigned together = __ballot_sync(0xffffffffu, real);
-        if (!real) break;
-        i = owner_from(p.s.row_begin, p.n_lists, r, i);
-        const MovedRow m = moved_row<true>(p, i, r, &bad);
-        const int g = u >> 2, c = u & 3;
-        const QuantRow to = quant_row(BITS, p.groups, m.to);
-        uint2 kc, vc;
-        uint32_t kw, vw;
-        const bool copied = m.own_pool;
-        if (copied) {   // a shared last page's row, as it is
-            const QuantRow from = quant_row(BITS, p.groups, m.from);
-            kc = quant_load<BITS>(p.k_pool + from.codes, p.groups, g, c, false);
-            vc = quant_load<BITS>(p.v_pool + from.codes, p.groups, g, c, true);
-            kw = reinterpret_cast<const uint16_t *>(p.k_pool + from.words)[g];
-            vw = reinterpret_cast<const uint16_t *>(p.v_pool + from.words)[g];
+    for (int64_t at = r0; at < r1; at += 32) {
+        MovedRow m{0, 0, false};
+        if (at + lane < r1) {
+            i = owner_from(p.s.row_begin, p.n_lists, at + lane, i);
+            m = moved_row<true>(p, i, at + lane, &bad);
         }
-        float kx[8] = {}, vx[8] = {};
-        if (!copied && u * 8 < p.dim) {
-            load8(p.k_src + m.from * p.dim + u * 8, kx);
-            load8(p.v_src + m.from * p.dim + u * 8, vx);
+        // in a copied row `from` counts the pool's rows, and is negative here
+        const int64_t from_of = m.own_pool ? -1 - m.from : m.from;
+        const int items = (int)min((int64_t)32, r1 - at) * pieces;   // a multiple of four: groups' lanes stay together
+        for (int base = 0; base < items; base += 32) {
+            const int it = base + lane, dr = p.by_pieces(it), u = it - dr * pieces;
+            const int64_t from = of_lane(from_of, dr & 31), to_row = of_lane(m.to, dr & 31);
+            const unsigned together = __ballot_sync(0xffffffffu, it < items);
+            if (it >= items) continue;
+            const int g = u >> 2, c = u & 3;
+            const QuantRow to = quant_row(BITS, p.groups, to_row);
+            if (from < 0) {   // a shared last page's row, as it is (whole groups of lanes are, or none)
+                const QuantRow held = quant_row(BITS, p.groups, -1 - from);
+                quant_store<BITS>(p.k_pool + to.codes, p.groups, g, c, false, quant_load<BITS>(p.k_pool + held.codes, p.groups, g, c, false));
+                quant_store<BITS>(p.v_pool + to.codes, p.groups, g, c, true, quant_load<BITS>(p.v_pool + held.codes, p.groups, g, c, true));
+                if (c == 0) {
+                    reinterpret_cast<uint16_t *>(p.k_pool + to.words)[g] = reinterpret_cast<const uint16_t *>(p.k_pool + held.words)[g];
+                    reinterpret_cast<uint16_t *>(p.v_pool + to.words)[g] = reinterpret_cast<const uint16_t *>(p.v_pool + held.words)[g];
+                }
+            }
+            const unsigned quad = together & 0xfu << (lane & 28);
+            if (from >= 0) {
+                float kx[8] = {}, vx[8] = {};
+                if (u * 8 < p.dim) {
+                    load8(p.k_src + from * p.dim + u * 8, kx);
+                    load8(p.v_src + from * p.dim + u * 8, vx);
+                }
+                uint32_t kw, vw;
+                const uint2 kc = quant_encode<BITS>(kx, quad, &kw), vc = quant_encode<BITS>(vx, quad, &vw);
+                quant_store<BITS>(p.k_pool + to.codes, p.groups, g, c, false, kc);
+                quant_store<BITS>(p.v_pool + to.codes, p.groups, g, c, true, vc);
+                if (c == 0) {
+                    reinterpret_cast<uint16_t *>(p.k_pool + to.words)[g] = (uint16_t)kw;
+                    reinterpret_cast<uint16_t *>(p.v_pool + to.words)[g] = (uint16_t)vw;
+                }
+            }
         }
-        uint32_t kn, vn;
-        const uint2 ke = quant_encode<BITS>(kx, together, &kn), ve = quant_encode<BITS>(vx, together, &vn);
-        if (!copied) {
-            kc = ke;
-            vc = ve;
-            kw = kn;
-            vw = vn;
-        }
-        quant_store<BITS>(p.k_pool + to.codes, p.groups, g, c, false, kc);
-        quant_store<BITS>(p.v_pool + to.codes, p.groups, g, c, true, vc);
-        if (c == 0) {
-            reinterpret_cast<uint16_t *>(p.k_pool + to.words)[g] = (uint16_t)kw;
-            reinterpret_cast<uint16_t *>(p.v_pool + to.words)[g] = (uint16_t)vw;
-        }
+        __syncwarp();
     }
 }
 
@@ -138,34 +136,40 @@ __global__ void __launch_bounds__(kMoveThreads) compact_quant_kernel(const __gri
     if (r0 >= r1) return;
     int i = owner(p.s.row_begin, p.n_lists, r0);
     uint32_t bad = 0;
-    const int64_t items = (r1 - r0) * p.groups;
     constexpr int kVecs = BITS / 4;
-    Place place{r0, 0};
-    for (int64_t base = 0; base + lane < items; base += 32, place.next(p.by_groups)) {
-        const int it = place.item + lane, dr = p.by_groups(it), g = it - dr * p.groups;
-        const int64_t r = place.row + dr;
-        i = owner_from(p.s.row_begin, p.n_lists, r, i);
-        const MovedRow m = moved_row<false>(p, i, r, &bad);
-        uint4 k[kVecs] = {}, v[kVecs] = {};   // a row of zeros has steps of zero
-        uint16_t kw = 0, vw = 0;
-        if (m.from >= 0) {
-            const QuantRow from = quant_row(BITS, p.groups, m.from);
+    for (int64_t at = r0; at < r1; at += 32) {
+        MovedRow m{-1, 0, true};
+        if (at + lane < r1) {
+            i = owner_from(p.s.row_begin, p.n_lists, at + lane, i);
+            m = moved_row<false>(p, i, at + lane, &bad);
+        }
+        const int items = (int)min((int64_t)32, r1 - at) * p.groups;
+        for (int base = 0; base < items; base += 32) {
+            const int it = base + lane, dr = p.by_groups(it), g = it - dr * p.groups;
+            const int64_t from_row = of_lane(m.from, dr & 31), to_row = of_lane(m.to, dr & 31);
+            if (it >= items) continue;
+            uint4 k[kVecs] = {}, v[kVecs] = {};   // a row of zeros has steps of zero
+            uint16_t kw = 0, vw = 0;
+            if (from_row >= 0) {
+                const QuantRow from = quant_row(BITS, p.groups, from_row);
+#pragma unroll
+                for (int e = 0; e < kVecs; ++e) {
+                    k[e] = reinterpret_cast<const uint4 *>(p.k_pool + from.codes)[g * kVecs + e];
+                    v[e] = reinterpret_cast<const uint4 *>(p.v_pool + from.codes)[g * kVecs + e];
+                }
+                kw = reinterpret_cast<const uint16_t *>(p.k_pool + from.words)[g];
+                vw = reinterpret_cast<const uint16_t *>(p.v_pool + from.words)[g];
+            }
+            const QuantRow to = quant_row(BITS, p.groups, to_row);
 #pragma unroll
             for (int e = 0; e < kVecs; ++e) {
-                k[e] = reinterpret_cast<const uint4 *>(p.k_pool + from.codes)[g * kVecs + e];
-                v[e] = reinterpret_cast<const uint4 *>(p.v_pool + from.codes)[g * kVecs + e];
+                reinterpret_cast<uint4 *>(p.k_pool + to.codes)[g * kVecs + e] = k[e];
+                reinterpret_cast<uint4 *>(p.v_pool + to.codes)[g * kVecs + e] = v[e];
             }
-            kw = reinterpret_cast<const uint16_t *>(p.k_pool + from.words)[g];
-            vw = reinterpret_cast<const uint16_t *>(p.v_pool + from.words)[g];
+            reinterpret_cast<uint16_t *>(p.k_pool + to.words)[g] = kw;
+            reinterpret_cast<uint16_t *>(p.v_pool + to.words)[g] = vw;
         }
-        const QuantRow to = quant_row(BITS, p.groups, m.to);
-#pragma unroll
-        for (int e = 0; e < kVecs; ++e) {
-            reinterpret_cast<uint4 *>(p.k_pool + to.codes)[g * kVecs + e] = k[e];
-            reinterpret_cast<uint4 *>(p.v_pool + to.codes)[g * kVecs + e] = v[e];
-        }
-        reinterpret_cast<uint16_t *>(p.k_pool + to.words)[g] = kw;
-        reinterpret_cast<uint16_t *>(p.v_pool + to.words)[g] = vw;
+        __syncwarp();
     }
     if (bad) set_status(&p.s.head->status, bad);
 }
@@ -237,31 +241,41 @@ __global__ void __launch_bounds__(kMoveThreads) read_quant_kernel(const __grid_c
     if (r0 >= r1) return;
     int i = owner(p.s.row_begin, p.n_lists, r0);
     bool bad = false;
-    const int64_t items = (r1 - r0) * pieces;
-    Place place{r0, 0};
-    for (int64_t base = 0; base + lane < items; base += 32, place.next(p.by_pieces)) {
-        const int it = place.item + lane, dr = p.by_pieces(it), u = it - dr * pieces;
-        const int64_t r = place.row + dr;
-        i = owner_from(p.s.row_begin, p.n_lists, r, i);
-        const int64_t at = r - p.s.row_begin[i];
-        const int row = (p.first ? p.first[i] : 0) + (int)at;
-        const int page = p.table[(int64_t)i * p.max_pages + (row >> p.shift)];
-        const int64_t to = (p.dst_row[i] + at * p.dst_step) * p.dim + u * 8;
-        float k[8] = {}, v[8] = {};
-        if (page >= 0 && page < p.n_pages) {
-            const QuantRow from = quant_row(BITS, p.groups, ((int64_t)page << p.shift) + (row & (ps - 1)));
-            const int g = u >> 2, c = u & 3;
-            if (p.k_dst)
-                quant_values<BITS>(quant_load<BITS>(p.k_pool + from.codes, p.groups, g, c, false),
-                                   reinterpret_cast<const uint16_t *>(p.k_pool + from.words)[g], k);
-            if (p.v_dst)
-                quant_values<BITS>(quant_load<BITS>(p.v_pool + from.codes, p.groups, g, c, true),
-                                   reinterpret_cast<const uint16_t *>(p.v_pool + from.words)[g], v);
-        } else {
-            bad = true;
+    for (int64_t at = r0; at < r1; at += 32) {
+        int64_t from_of = -1, to_of = 0;   // row of the pools, -1: zeros; element of the destination
+        if (at + lane < r1) {
+            const int64_t r = at + lane;
+            i = owner_from(p.s.row_begin, p.n_lists, r, i);
+            const int64_t k = r - p.s.row_begin[i];
+            const int row = (p.first ? p.first[i] : 0) + (int)k;
+            const int page = p.table[(int64_t)i * p.max_pages + (row >> p.shift)];
+            to_of = (p.dst_row[i] + k * p.dst_step) * p.dim;
+            if (page >= 0 && page < p.n_pages)
+                from_of = ((int64_t)page << p.shift) + (row & (ps - 1));
+            else
+                bad = true;
         }
-        if (p.k_dst) store8(p.k_dst + to, k);
-        if (p.v_dst) store8(p.v_dst + to, v);
+        const int items = (int)min((int64_t)32, r1 - at) * pieces;
+#pragma unroll 2
+        for (int base = 0; base < items; base += 32) {
+            const int it = base + lane, dr = p.by_pieces(it), u = it - dr * pieces;
+            const int64_t from = of_lane(from_of, dr & 31), to = of_lane(to_of, dr & 31) + u * 8;
+            if (it >= items) continue;
+            uint32_t k[4] = {}, v[4] = {};
+            if (from >= 0) {
+                const QuantRow held = quant_row(BITS, p.groups, from);
+                const int g = u >> 2, c = u & 3;
+                if (p.k_dst)
+                    quant_bf16<BITS>(quant_load<BITS>(p.k_pool + held.codes, p.groups, g, c, false),
+                                     reinterpret_cast<const uint16_t *>(p.k_pool + held.words)[g] * 0x10001u, k);
+                if (p.v_dst)
+                    quant_bf16<BITS>(quant_load<BITS>(p.v_pool + held.codes, p.groups, g, c, true),
+                                     reinterpret_cast<const uint16_t *>(p.v_pool + held.words)[g] * 0x10001u, v);
+            }
+            if (p.k_dst) store8(p.k_dst + to, k);
+            if (p.v_dst) store8(p.v_dst + to, v);
+        }
+        __syncwarp();
     }
     if (bad) set_status(&p.s.head->status, KVC_DEV_BAD_PAGE);
 }

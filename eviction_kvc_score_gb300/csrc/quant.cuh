@@ -106,39 +106,60 @@ __device__ __forceinline__ void quant_store(uint8_t *codes, int groups, int g, i
     }
 }
 
-// What a piece stands for.
+__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// What a piece stands for, as bf16, which holds it exactly; `word` is the group's,
+// once in either half.  Codes come as 128 + n (4 bits), where bf16 counts in ones, or
+// as 2^23 + n in fp32 (8 bits); the zero code comes off the same way.
 template <int BITS>
-__device__ __forceinline__ void quant_values(uint2 codes, uint32_t word, float (&y)[8]) {
-    const float s = quant_step<BITS>(word);
-    const int z = quant_zero<BITS>(word);
+__device__ __forceinline__ void quant_bf16(uint2 codes, uint32_t word, uint32_t (&y)[4]) {
+    if (BITS == 4) {
+        const uint32_t s = word & 0xfff0fff0u, z = (word & 0x000f000fu) | 0x43004300u;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t n = BITS == 8 ? ((i < 4 ? codes.x : codes.y) >> 8 * (i & 3)) & 0xffu
-                                     : (codes.x >> (4 * (i >> 1) + 16 * (i & 1))) & 0xfu;
-        y[i] = (float)((int)n - z) * s;
+        for (int i = 0; i < 4; ++i) y[i] = mul_bf16x2(sub_bf16x2(((codes.x >> 4 * i) & 0x000f000fu) | 0x43004300u, z), s);
+    } else {
+        const float s = quant_step<8>(word), z = -__uint_as_float(0x4b000000u | (word & 0xffu));
+        const unsigned long long s2 = f2_pack(s, s), z2 = f2_pack(z, z);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t w = i < 2 ? codes.x : codes.y;
+            float a, b;
+            f2_unpack(f2_mul(f2_add(f2_pack(__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440 + 2 * (i & 1))),
+                                            __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7441 + 2 * (i & 1)))), z2), s2), a, b);
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y[i]) : "f"(b), "f"(a));
+        }
     }
 }
 
 // A group's codes and word from its values, eight in each of four neighbouring
-// lanes; the lanes of `mask` call it together.
+// lanes; the lanes of `mask` call it together.  (Rounding by adding 1.5 2^23, where
+// fp32 counts in ones: conversions run at an eighth of the rate.)
 template <int BITS>
 __device__ __forceinline__ uint2 quant_encode(const float (&x)[8], uint32_t mask, uint32_t *word) {
     constexpr int N = (1 << BITS) - 1;
-    float lo = 0.f, hi = 0.f;
-    uint32_t size = 0;   // of fp32 bits without the sign, the largest: a NaN's is above all others
+    constexpr float kOnes = 12582912.f;
+    float lo = fminf(fmin3(x[0], x[1], x[2]), fmin3(x[3], x[4], x[5])), hi = fmaxf(fmax3(x[0], x[1], x[2]), fmax3(x[3], x[4], x[5]));
+    lo = fminf(fmin3(lo, x[6], x[7]), 0.f);
+    hi = fmaxf(fmax3(hi, x[6], x[7]), 0.f);
+    float odd = 0.f;   // stays zero but for infinities and NaN
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        lo = fminf(lo, x[i]);
-        hi = fmaxf(hi, x[i]);
-        size = max(size, __float_as_uint(x[i]) & 0x7fffffffu);
-    }
+    for (int i = 0; i < 8; ++i) odd = fmaf(x[i], 0.f, odd);
+    if (!(odd == 0.f)) hi = INFINITY;
 #pragma unroll
     for (int d = 1; d <= 2; d <<= 1) {
         lo = fminf(lo, __shfl_xor_sync(mask, lo, d));
         hi = fmaxf(hi, __shfl_xor_sync(mask, hi, d));
-        size = max(size, __shfl_xor_sync(mask, size, d));
     }
-    if (size >= __float_as_uint(0x1p126f)) {
+    if (!(fmaxf(-lo, hi) < 0x1p126f)) {
         *word = BITS == 4 ? 0x7fc0u : 0xff00u;
         return make_uint2(0, 0);
     }
@@ -147,18 +168,20 @@ __device__ __forceinline__ uint2 quant_encode(const float (&x)[8], uint32_t mask
     uint32_t s_bits = (__float_as_uint(t) + ((1u << kDropped) - 1u)) >> kDropped << kDropped;
     s_bits = max(s_bits, __float_as_uint(0x1p-126f));
     const float inv = __frcp_rn(__uint_as_float(s_bits));
-    const int z = __float2int_rn(__fmul_rn(-lo, inv));
-    *word = BITS == 4 ? s_bits >> 16 | z : s_bits >> 23 << 8 | z;
-    uint2 r = make_uint2(0, 0);
+    const float z = __fadd_rn(__fadd_rn(__fmul_rn(-lo, inv), kOnes), -kOnes);
+    const uint32_t z_bits = __float_as_uint(z + kOnes) & 0xffu;
+    *word = BITS == 4 ? s_bits >> 16 | z_bits : s_bits >> 23 << 8 | z_bits;
+    uint32_t n[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t n = min(max(__float2int_rn(__fmul_rn(x[i], inv)) + z, 0), N);
-        if (BITS == 8)
-            (i < 4 ? r.x : r.y) |= n << 8 * (i & 3);
-        else
-            r.x |= n << (4 * (i >> 1) + 16 * (i & 1));
-    }
-    return r;
+    for (int i = 0; i < 8; ++i)
+        n[i] = __float_as_uint(fminf(fmaxf(__fadd_rn(__fadd_rn(__fmul_rn(x[i], inv), kOnes), z), kOnes), kOnes + N));
+    if (BITS == 8)
+        return make_uint2(__byte_perm(__byte_perm(n[0], n[1], 0x0040), __byte_perm(n[2], n[3], 0x0040), 0x5410),
+                          __byte_perm(__byte_perm(n[4], n[5], 0x0040), __byte_perm(n[6], n[7], 0x0040), 0x5410));
+    uint32_t r = 0;
+#pragma unroll
+    for (int i = 3; i >= 0; --i) r = r * 16 + __byte_perm(n[2 * i], n[2 * i + 1], 0x5410);
+    return make_uint2(r, 0);
 }
 
 int launch_pages_append_quant(const kvc_cache &c, int bits, const PagesState &s, int32_t *table, int32_t *len,

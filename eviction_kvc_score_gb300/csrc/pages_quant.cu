@@ -101,7 +101,8 @@ __global__ void __launch_bounds__(kMoveThreads) append_quant_kernel(const __grid
                     load8(p.v_src + from * p.dim + u * 8, vx);
                 }
                 uint32_t kw, vw;
-                const uint2 kc = quant_encode<BITS>(kx, quad, &kw), vc = quant_encode<BITS>(vx, quad, &vw);
+                uint2 kc, vc;
+                quant_encode<BITS>(kx, vx, quad, &kc, &kw, &vc, &vw);
                 quant_store<BITS>(p.k_pool + to.codes, p.groups, g, c, false, kc);
                 quant_store<BITS>(p.v_pool + to.codes, p.groups, g, c, true, vc);
                 if (c == 0) {

@@ -140,41 +140,36 @@ __device__ __forceinline__ void quant_bf16(uint2 codes, uint32_t word, uint32_t 
     }
 }
 
-// A group's codes and word from its values, eight in each of four neighbouring
-// lanes; the lanes of `mask` call it together.  (Rounding by adding 1.5 2^23, where
-// fp32 counts in ones: conversions run at an eighth of the rate.)
+// The smallest and largest of eight channels and zero; NaN and infinities make the
+// largest infinite.
+__device__ __forceinline__ void quant_range(const float (&x)[8], float *lo, float *hi) {
+    *lo = fminf(fmin3(fminf(fmin3(x[0], x[1], x[2]), fmin3(x[3], x[4], x[5])), x[6], x[7]), 0.f);
+    *hi = fmaxf(fmax3(fmaxf(fmax3(x[0], x[1], x[2]), fmax3(x[3], x[4], x[5])), x[6], x[7]), 0.f);
+    unsigned long long odd = 0;   // stays zero but for those
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) odd = f2_fma(f2_pack(x[i], x[i + 1]), f2_pack(0.f, 0.f), odd);
+    float a, b;
+    f2_unpack(odd, a, b);
+    if (!(a + b == 0.f)) *hi = INFINITY;
+}
+
+// Codes of eight channels, by 1 / s and z: rounding by adding 1.5 2^23, where fp32
+// counts in ones (conversions run at an eighth of the rate).  rint(x / s) + z is never
+// below 0: lo has the smallest, and -z exactly.
 template <int BITS>
-__device__ __forceinline__ uint2 quant_encode(const float (&x)[8], uint32_t mask, uint32_t *word) {
-    constexpr int N = (1 << BITS) - 1;
-    constexpr float kOnes = 12582912.f;
-    float lo = fminf(fmin3(x[0], x[1], x[2]), fmin3(x[3], x[4], x[5])), hi = fmaxf(fmax3(x[0], x[1], x[2]), fmax3(x[3], x[4], x[5]));
-    lo = fminf(fmin3(lo, x[6], x[7]), 0.f);
-    hi = fmaxf(fmax3(hi, x[6], x[7]), 0.f);
-    float odd = 0.f;   // stays zero but for infinities and NaN
-#pragma unroll
-    for (int i = 0; i < 8; ++i) odd = fmaf(x[i], 0.f, odd);
-    if (!(odd == 0.f)) hi = INFINITY;
-#pragma unroll
-    for (int d = 1; d <= 2; d <<= 1) {
-        lo = fminf(lo, __shfl_xor_sync(mask, lo, d));
-        hi = fmaxf(hi, __shfl_xor_sync(mask, hi, d));
-    }
-    if (!(fmaxf(-lo, hi) < 0x1p126f)) {
-        *word = BITS == 4 ? 0x7fc0u : 0xff00u;
-        return make_uint2(0, 0);
-    }
-    const float t = __fdiv_rn(__fadd_rn(hi * 0.5f, lo * -0.5f), 0.5f * N);
-    constexpr uint32_t kDropped = BITS == 4 ? 20 : 23;   // bits of fp32 that are rounded up
-    uint32_t s_bits = (__float_as_uint(t) + ((1u << kDropped) - 1u)) >> kDropped << kDropped;
-    s_bits = max(s_bits, __float_as_uint(0x1p-126f));
-    const float inv = __frcp_rn(__uint_as_float(s_bits));
-    const float z = __fadd_rn(__fadd_rn(__fmul_rn(-lo, inv), kOnes), -kOnes);
-    const uint32_t z_bits = __float_as_uint(z + kOnes) & 0xffu;
-    *word = BITS == 4 ? s_bits >> 16 | z_bits : s_bits >> 23 << 8 | z_bits;
+__device__ __forceinline__ uint2 quant_codes_of(const float (&x)[8], float inv, float z) {
+    constexpr float kOnes = 12582912.f, kMost = kOnes + (1 << BITS) - 1;
+    const unsigned long long z2 = f2_pack(z, z);
     uint32_t n[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        n[i] = __float_as_uint(fminf(fmaxf(__fadd_rn(__fadd_rn(__fmul_rn(x[i], inv), kOnes), z), kOnes), kOnes + N));
+    for (int i = 0; i < 8; i += 2) {
+        // the product is rounded before the sum (a packed product and sum would be fused)
+        const float p = __fadd_rn(__fmul_rn(x[i], inv), kOnes), q = __fadd_rn(__fmul_rn(x[i + 1], inv), kOnes);
+        float a, b;
+        f2_unpack(f2_add(f2_pack(p, q), z2), a, b);
+        n[i] = __float_as_uint(fminf(a, kMost));
+        n[i + 1] = __float_as_uint(fminf(b, kMost));
+    }
     if (BITS == 8)
         return make_uint2(__byte_perm(__byte_perm(n[0], n[1], 0x0040), __byte_perm(n[2], n[3], 0x0040), 0x5410),
                           __byte_perm(__byte_perm(n[4], n[5], 0x0040), __byte_perm(n[6], n[7], 0x0040), 0x5410));
@@ -182,6 +177,43 @@ __device__ __forceinline__ uint2 quant_encode(const float (&x)[8], uint32_t mask
 #pragma unroll
     for (int i = 3; i >= 0; --i) r = r * 16 + __byte_perm(n[2 * i], n[2 * i + 1], 0x5410);
     return make_uint2(r, 0);
+}
+
+// Codes and words of a group of K and one of V from their values, eight in each of four
+// neighbouring lanes; the lanes of `mask` call it together.  Even lanes work K's step
+// out, odd ones V's.
+template <int BITS>
+__device__ __forceinline__ void quant_encode(const float (&kx)[8], const float (&vx)[8], uint32_t mask, uint2 *kc, uint32_t *kw, uint2 *vc,
+                                             uint32_t *vw) {
+    constexpr int N = (1 << BITS) - 1;
+    constexpr float kOnes = 12582912.f;
+    float klo, khi, vlo, vhi;
+    quant_range(kx, &klo, &khi);
+    quant_range(vx, &vlo, &vhi);
+    // lane c gets the range of its own of the two over lanes c and c ^ 1, then over all
+    const int lane = threadIdx.x & 31, odd = lane & 1;
+    float lo = odd ? vlo : klo, hi = odd ? vhi : khi;
+    lo = fminf(lo, __shfl_xor_sync(mask, odd ? klo : vlo, 1));
+    hi = fmaxf(hi, __shfl_xor_sync(mask, odd ? khi : vhi, 1));
+    lo = fminf(lo, __shfl_xor_sync(mask, lo, 2));
+    hi = fmaxf(hi, __shfl_xor_sync(mask, hi, 2));
+    const bool fine = fmaxf(-lo, hi) < 0x1p126f;
+    const float t = __fdiv_rn(__fadd_rn(hi * 0.5f, lo * -0.5f), 0.5f * N);
+    constexpr uint32_t kDropped = BITS == 4 ? 20 : 23;   // bits of fp32 that are rounded up
+    uint32_t s_bits = (__float_as_uint(t) + ((1u << kDropped) - 1u)) >> kDropped << kDropped;
+    s_bits = max(s_bits, __float_as_uint(0x1p-126f));
+    const float inv = __frcp_rn(__uint_as_float(s_bits)), z = __fadd_rn(__fmul_rn(-lo, inv), kOnes);
+    const uint32_t z_bits = __float_as_uint(z) & 0xffu;
+    const uint32_t word = !fine ? (BITS == 4 ? 0x7fc0u : 0xff00u) : BITS == 4 ? s_bits >> 16 | z_bits : s_bits >> 23 << 8 | z_bits;
+    const int even = lane & ~1;
+    *kw = __shfl_sync(mask, word, even);
+    *vw = __shfl_sync(mask, word, even + 1);
+    const float k_inv = __shfl_sync(mask, inv, even), v_inv = __shfl_sync(mask, inv, even + 1);
+    constexpr uint32_t kZero = BITS == 4 ? 0xfu : 0xffu;
+    *kc = quant_codes_of<BITS>(kx, k_inv, __uint_as_float(__float_as_uint(kOnes) | (*kw & kZero)) - kOnes);
+    *vc = quant_codes_of<BITS>(vx, v_inv, __uint_as_float(__float_as_uint(kOnes) | (*vw & kZero)) - kOnes);
+    if (quant_is_nan<BITS>(*kw)) *kc = make_uint2(0, 0);
+    if (quant_is_nan<BITS>(*vw)) *vc = make_uint2(0, 0);
 }
 
 int launch_pages_append_quant(const kvc_cache &c, int bits, const PagesState &s, int32_t *table, int32_t *len,

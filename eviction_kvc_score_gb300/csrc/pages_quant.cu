@@ -12,21 +12,37 @@ namespace kvc {
 
 namespace {
 
-// Eight channels as floats.
-__device__ __forceinline__ void load8(const float *p, float (&x)[8]) {
-    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&x)[8]) {
-    const uint4 a = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+// Eight channels as they come, and as floats.
+template <typename T>
+struct Eight {
+    uint4 v[sizeof(T) / 2];
+    __device__ __forceinline__ void load(const T *p) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = reinterpret_cast<const uint4 *>(p)[i];
     }
-}
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void floats(float (&x)[8]) const {
+        const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+        if (sizeof(T) == 2) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[2 * i] = __uint_as_float(w[i] << 16);
+                x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            }
+        } else {
+            const uint4 b = v[sizeof(T) / 2 - 1];
+            const uint32_t y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[i] = __uint_as_float(w[i]);
+                x[4 + i] = __uint_as_float(y[i]);
+            }
+        }
+    }
+};
 // Eight channels that come as bf16 pairs.
 __device__ __forceinline__ void store8(__nv_bfloat16 *p, const uint32_t (&y)[4]) {
     *reinterpret_cast<uint4 *>(p) = make_uint4(y[0], y[1], y[2], y[3]);
@@ -37,6 +53,8 @@ __device__ __forceinline__ void store8(float *p, const uint32_t (&y)[4]) {
         reinterpret_cast<float4 *>(p)[i] = make_float4(__uint_as_float(y[2 * i] << 16), __uint_as_float(y[2 * i] & 0xffff0000u),
                                                        __uint_as_float(y[2 * i + 1] << 16), __uint_as_float(y[2 * i + 1] & 0xffff0000u));
 }
+
+constexpr int kAtOnce = 4;   // parts that a lane reads before it goes on with the first
 
 // A warp's rows are looked up 32 at a time, a lane each, and worked on in parts, 32 of
 // any rows at a time: the search for a row's list and pages would cost as much as a
@@ -77,12 +95,32 @@ __global__ void __launch_bounds__(kMoveThreads) append_quant_kernel(const __grid
         // in a copied row `from` counts the pool's rows, and is negative here
         const int64_t from_of = m.own_pool ? -1 - m.from : m.from;
         const int items = (int)min((int64_t)32, r1 - at) * pieces;   // a multiple of four: groups' lanes stay together
+        // the lane's part number base / 32: its source (negative: copied) and values
+        Eight<T> k_next, v_next;
+        int64_t from_next = 0;
+        int u_next = 0, dr_next = 0;
+        auto look = [&](int base) {
+            const int it = base + lane, dr = p.by_pieces(it);
+            u_next = it - dr * pieces;
+            dr_next = dr & 31;
+            from_next = of_lane(from_of, dr_next);
+            k_next.clear();
+            v_next.clear();
+            if (it < items && from_next >= 0 && u_next * 8 < p.dim) {
+                k_next.load(p.k_src + from_next * p.dim + u_next * 8);
+                v_next.load(p.v_src + from_next * p.dim + u_next * 8);
+            }
+        };
+        look(0);
         for (int base = 0; base < items; base += 32) {
-            const int it = base + lane, dr = p.by_pieces(it), u = it - dr * pieces;
-            const int64_t from = of_lane(from_of, dr & 31), to_row = of_lane(m.to, dr & 31);
-            const unsigned together = __ballot_sync(0xffffffffu, it < items);
-            if (it >= items) continue;
-            const int g = u >> 2, c = u & 3;
+            const int64_t from = from_next, to_row = of_lane(m.to, dr_next);
+            const int g = u_next >> 2, c = u_next & 3;
+            float kx[8], vx[8];
+            k_next.floats(kx);
+            v_next.floats(vx);
+            look(base + 32);
+            const unsigned together = __ballot_sync(0xffffffffu, base + lane < items);
+            if (base + lane >= items) continue;
             const QuantRow to = quant_row(BITS, p.groups, to_row);
             if (from < 0) {   // a shared last page's row, as it is (whole groups of lanes are, or none)
                 const QuantRow held = quant_row(BITS, p.groups, -1 - from);
@@ -92,23 +130,16 @@ __global__ void __launch_bounds__(kMoveThreads) append_quant_kernel(const __grid
                     reinterpret_cast<uint16_t *>(p.k_pool + to.words)[g] = reinterpret_cast<const uint16_t *>(p.k_pool + held.words)[g];
                     reinterpret_cast<uint16_t *>(p.v_pool + to.words)[g] = reinterpret_cast<const uint16_t *>(p.v_pool + held.words)[g];
                 }
+                continue;
             }
-            const unsigned quad = together & 0xfu << (lane & 28);
-            if (from >= 0) {
-                float kx[8] = {}, vx[8] = {};
-                if (u * 8 < p.dim) {
-                    load8(p.k_src + from * p.dim + u * 8, kx);
-                    load8(p.v_src + from * p.dim + u * 8, vx);
-                }
-                uint32_t kw, vw;
-                uint2 kc, vc;
-                quant_encode<BITS>(kx, vx, quad, &kc, &kw, &vc, &vw);
-                quant_store<BITS>(p.k_pool + to.codes, p.groups, g, c, false, kc);
-                quant_store<BITS>(p.v_pool + to.codes, p.groups, g, c, true, vc);
-                if (c == 0) {
-                    reinterpret_cast<uint16_t *>(p.k_pool + to.words)[g] = (uint16_t)kw;
-                    reinterpret_cast<uint16_t *>(p.v_pool + to.words)[g] = (uint16_t)vw;
-                }
+            uint32_t kw, vw;
+            uint2 kc, vc;
+            quant_encode<BITS>(kx, vx, together & 0xfu << (lane & 28), &kc, &kw, &vc, &vw);
+            quant_store<BITS>(p.k_pool + to.codes, p.groups, g, c, false, kc);
+            quant_store<BITS>(p.v_pool + to.codes, p.groups, g, c, true, vc);
+            if (c == 0) {
+                reinterpret_cast<uint16_t *>(p.k_pool + to.words)[g] = (uint16_t)kw;
+                reinterpret_cast<uint16_t *>(p.v_pool + to.words)[g] = (uint16_t)vw;
             }
         }
         __syncwarp();
@@ -257,24 +288,44 @@ __global__ void __launch_bounds__(kMoveThreads) read_quant_kernel(const __grid_c
                 bad = true;
         }
         const int items = (int)min((int64_t)32, r1 - at) * pieces;
-#pragma unroll 2
-        for (int base = 0; base < items; base += 32) {
-            const int it = base + lane, dr = p.by_pieces(it), u = it - dr * pieces;
-            const int64_t from = of_lane(from_of, dr & 31), to = of_lane(to_of, dr & 31) + u * 8;
-            if (it >= items) continue;
-            uint32_t k[4] = {}, v[4] = {};
-            if (from >= 0) {
-                const QuantRow held = quant_row(BITS, p.groups, from);
-                const int g = u >> 2, c = u & 3;
-                if (p.k_dst)
-                    quant_bf16<BITS>(quant_load<BITS>(p.k_pool + held.codes, p.groups, g, c, false),
-                                     reinterpret_cast<const uint16_t *>(p.k_pool + held.words)[g] * 0x10001u, k);
-                if (p.v_dst)
-                    quant_bf16<BITS>(quant_load<BITS>(p.v_pool + held.codes, p.groups, g, c, true),
-                                     reinterpret_cast<const uint16_t *>(p.v_pool + held.words)[g] * 0x10001u, v);
+        for (int base = 0; base < items; base += 32 * kAtOnce) {
+            uint2 kc[kAtOnce], vc[kAtOnce];
+            uint32_t kw[kAtOnce], vw[kAtOnce];
+            int64_t to[kAtOnce];
+#pragma unroll
+            for (int e = 0; e < kAtOnce; ++e) {
+                const int it = base + 32 * e + lane, dr = p.by_pieces(it), u = it - dr * pieces;
+                const int64_t from = of_lane(from_of, dr & 31);
+                to[e] = of_lane(to_of, dr & 31) + u * 8;
+                if (it >= items) to[e] = -1;
+                kc[e] = vc[e] = make_uint2(0, 0);
+                kw[e] = vw[e] = 0;   // rows of zeros
+                if (it < items && from >= 0) {
+                    const QuantRow held = quant_row(BITS, p.groups, from);
+                    const int g = u >> 2, c = u & 3;
+                    if (p.k_dst) {
+                        kc[e] = quant_load<BITS>(p.k_pool + held.codes, p.groups, g, c, false);
+                        kw[e] = reinterpret_cast<const uint16_t *>(p.k_pool + held.words)[g];
+                    }
+                    if (p.v_dst) {
+                        vc[e] = quant_load<BITS>(p.v_pool + held.codes, p.groups, g, c, true);
+                        vw[e] = reinterpret_cast<const uint16_t *>(p.v_pool + held.words)[g];
+                    }
+                }
             }
-            if (p.k_dst) store8(p.k_dst + to, k);
-            if (p.v_dst) store8(p.v_dst + to, v);
+#pragma unroll
+            for (int e = 0; e < kAtOnce; ++e) {
+                if (to[e] < 0) continue;
+                uint32_t y[4];
+                if (p.k_dst) {
+                    quant_bf16<BITS>(kc[e], kw[e] * 0x10001u, y);
+                    store8(p.k_dst + to[e], y);
+                }
+                if (p.v_dst) {
+                    quant_bf16<BITS>(vc[e], vw[e] * 0x10001u, y);
+                    store8(p.v_dst + to[e], y);
+                }
+            }
         }
         __syncwarp();
     }

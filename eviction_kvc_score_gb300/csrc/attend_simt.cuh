@@ -22,8 +22,9 @@
 //
 // Rows held in 4 or 8 bits (BITS; quant.cuh) come to shared memory as they are,
 // four blocks of 16 rows a tile, and are written out from there as a tile of bf16,
-// which holds their values exactly; the rest is the same.  Units of their
-// own compile them (attend_simt_quant4.cu, attend_simt_quant8.cu).
+// which holds their values exactly; the rest is the same.  So go lists of up to 16
+// rows; those of more are attend_pieces.cuh's.  Units of their own compile both
+// (attend_simt_quant4.cu, attend_simt_quant8.cu).
 #pragma once
 
 #include <algorithm>
@@ -122,6 +123,27 @@ template <int N>
 __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+
+// Blocks that share a unit have stored their parts: the last to come joins them.
+template <typename T, int THREADS>
+__device__ __forceinline__ void attend_meet(const AttendParams &p, const AttendRun &run, const AttendUnit &a, int64_t u_lo, uint32_t *s_last) {
+    const int c0 = attend_cta_of(run.total, run.grid, u_lo);
+    const int c1 = attend_cta_of(run.total, run.grid, u_lo + a.steps - 1);
+    const int me = blockIdx.x, tid = threadIdx.x, n = c1 - c0 + 1, groups = attend_groups(n);
+    bool last = true;
+    if (groups > 1) {
+        const int g0 = c0 + (me - c0) / kJoinGroup * kJoinGroup, gn = min(kJoinGroup, c1 - g0 + 1);
+        last = attend_block_last(&p.arrived[16 * g0 + 8], gn, s_last);
+        if (last) attend_join<T, 2, 4>(p, a, AttendSpan{c0, g0, 1, gn, false, false}, 0, a.rows, 0, tid, THREADS);
+    }
+    if (last && attend_block_last(&p.arrived[16 * c0], groups > 1 ? groups : n, s_last))
+        attend_join<T, 2, 4>(p, a, AttendSpan{c0, c0, groups > 1 ? kJoinGroup : 1, groups > 1 ? groups : n, groups > 1, true},
+                             0, a.rows, 0, tid, THREADS);
+}
+
+// Many rows over rows held in 4 or 8 bits: attend_pieces.cuh.
+template <typename T, int BITS>
+int launch_pieces(AttendParams &p, int sms, cudaStream_t st);
 
 // A thread's columns: CT chunks of 2 N, CT * TX * 2 N >= D.
 template <typename T, int ROWS, int N, int CT, int BITS>
@@ -388,20 +410,7 @@ __global__ void __launch_bounds__(threads_of(ROWS), ROWS == 64 ? 2 : 4) attend_s
                     p.stat[slot * p.slot_rows + r] = make_float2(m[i], l[i]);
             }
         }
-        if (!whole) {
-            const int c0 = attend_cta_of(run.total, run.grid, u_lo);
-            const int c1 = attend_cta_of(run.total, run.grid, u_lo + a.steps - 1);
-            const int me = blockIdx.x, n = c1 - c0 + 1, groups = attend_groups(n);
-            bool last = true;
-            if (groups > 1) {
-                const int g0 = c0 + (me - c0) / kJoinGroup * kJoinGroup, gn = min(kJoinGroup, c1 - g0 + 1);
-                last = attend_block_last(&p.arrived[16 * g0 + 8], gn, s_last);
-                if (last) attend_join<T, 2, 4>(p, a, AttendSpan{c0, g0, 1, gn, false, false}, 0, a.rows, 0, tid, kThreads);
-            }
-            if (last && attend_block_last(&p.arrived[16 * c0], groups > 1 ? groups : n, s_last))
-                attend_join<T, 2, 4>(p, a, AttendSpan{c0, c0, groups > 1 ? kJoinGroup : 1, groups > 1 ? groups : n, groups > 1, true},
-                                     0, a.rows, 0, tid, kThreads);
-        }
+        if (!whole) attend_meet<T, kThreads>(p, run, a, u_lo, s_last);
         pos = end;
         u_lo += a.steps;
         u = attend_next(p, a, u);
@@ -426,11 +435,14 @@ int launch_type(AttendParams &p, int rows, int sms, cudaStream_t st) {
         return d <= 64    ? launch<T, 16, 1, 1, BITS>(p, sms, st)
                : d <= 128 ? launch<T, 16, 2, 1, BITS>(p, sms, st)
                           : launch<T, 16, 2, 2, BITS>(p, sms, st);
-    return d <= 64    ? launch<T, 64, 2, 1, BITS>(p, sms, st)
-           : d <= 96  ? launch<T, 64, 1, 3, BITS>(p, sms, st)
-           : d <= 128 ? launch<T, 64, 2, 2, BITS>(p, sms, st)
-           : d <= 192 ? launch<T, 64, 2, 3, BITS>(p, sms, st)
-                      : launch<T, 64, 2, 4, BITS>(p, sms, st);
+    if constexpr (BITS != 0)
+        return launch_pieces<T, BITS>(p, sms, st);
+    else
+        return d <= 64    ? launch<T, 64, 2, 1, BITS>(p, sms, st)
+               : d <= 96  ? launch<T, 64, 1, 3, BITS>(p, sms, st)
+               : d <= 128 ? launch<T, 64, 2, 2, BITS>(p, sms, st)
+               : d <= 192 ? launch<T, 64, 2, 3, BITS>(p, sms, st)
+                          : launch<T, 64, 2, 4, BITS>(p, sms, st);
 }
 
 template <int BITS>

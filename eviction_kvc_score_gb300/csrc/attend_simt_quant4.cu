@@ -1,5 +1,5 @@
-// attend_simt_quant4.cu -- the CUDA cores' attention over rows held in 4 bits.
-#include "attend_simt.cuh"
+// attend_simt_quant4.cu -- attention by fp32's accuracy over rows held in 4 bits.
+#include "attend_pieces.cuh"
 
 namespace kvc {
 

@@ -210,14 +210,14 @@ __global__ void __launch_bounds__(kPieceThreads, KS <= 8 ? 3 : 2) attend_pieces_
 #pragma unroll
                     for (int e = 0; e < kPieces; ++e) ldmatrix4(q[e], q_at + e * kPieceRows * rb + 32 * s);
 #pragma unroll
-                    for (int n = 0; n < kPieceKeys / 16; ++n) {
-                        uint32_t k[4];
-                        ldmatrix4(k, k_at + 16 * n * rb + 32 * s);
+                    for (int n = 0; n < kPieceKeys / 16; n += 2) {   // four sums at a time
+                        uint32_t k[2][4];
+                        ldmatrix4(k[0], k_at + 16 * n * rb + 32 * s);
+                        ldmatrix4(k[1], k_at + 16 * (n + 1) * rb + 32 * s);
 #pragma unroll
-                        for (int e = kPieces - 1; e >= 0; --e) {
-                            mma_bf16(x[2 * n], q[e], k[0], k[1]);
-                            mma_bf16(x[2 * n + 1], q[e], k[2], k[3]);
-                        }
+                        for (int e = kPieces - 1; e >= 0; --e)
+#pragma unroll
+                            for (int h = 0; h < 4; ++h) mma_bf16(x[2 * n + h], q[e], k[h >> 1][2 * (h & 1)], k[h >> 1][2 * (h & 1) + 1]);
                     }
                 }
                 const bool edge = j0 + kPieceKeys > sees0;
@@ -267,14 +267,22 @@ __global__ void __launch_bounds__(kPieceThreads, KS <= 8 ? 3 : 2) attend_pieces_
                         e[2][i] = y[2];
                     }
 #pragma unroll
-                    for (int n = 0; n < KS; ++n) {
+                    for (int n = 0; n < KS; n += 2) {
                         if (n >= steps) continue;
-                        uint32_t v[4];
-                        ldmatrix4_turned(v, v_at + 16 * s * rb + 32 * n);
+                        const bool both = n + 1 < steps;
+                        uint32_t v[2][4];
+                        ldmatrix4_turned(v[0], v_at + 16 * s * rb + 32 * n);
+                        if (both) {
+                            ldmatrix4_turned(v[1], v_at + 16 * s * rb + 32 * n + 32);
 #pragma unroll
-                        for (int i = 2; i >= 0; --i) {
-                            mma_bf16(o[2 * n], e[i], v[0], v[1]);
-                            mma_bf16(o[2 * n + 1], e[i], v[2], v[3]);
+                            for (int i = 2; i >= 0; --i)
+#pragma unroll
+                                for (int h = 0; h < 4; ++h) mma_bf16(o[2 * n + h], e[i], v[h >> 1][2 * (h & 1)], v[h >> 1][2 * (h & 1) + 1]);
+                        } else {
+#pragma unroll
+                            for (int i = 2; i >= 0; --i)
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) mma_bf16(o[2 * n + h], e[i], v[0][2 * h], v[0][2 * h + 1]);
                         }
                     }
                 }

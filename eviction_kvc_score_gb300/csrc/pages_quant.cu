@@ -58,7 +58,14 @@ constexpr int kAtOnce = 4;   // parts that a lane reads before it goes on with t
 
 // A warp's rows are looked up 32 at a time, a lane each, and worked on in parts, 32 of
 // any rows at a time: the search for a row's list and pages would cost as much as a
-// part's work (560,000 rows read back: 116 us with a search per part, 62 so).
+// part's work (560,000 rows of 128 read back from 4 bits: 116 us with a search per part,
+// 102 so, 77 with four parts' loads in flight).
+// Eight blocks per SM are launched, of which three to five are resident: the later ones
+// fill what the earlier leave.  As many as are resident took 82 us instead of 77 to read
+// and 113 instead of 106 to append those rows; twice as many, 78 and 109.  Moving rows is
+// one round per warp either way, and gains from fewer (243,000 rows: 23 us, 19 so).
+constexpr int kCompactPerSm = 5;
+
 __device__ __forceinline__ int64_t of_lane(int64_t x, int lane) {
     return (int64_t)((uint64_t)__shfl_sync(0xffffffffu, (uint32_t)((uint64_t)x >> 32), lane) << 32 | __shfl_sync(0xffffffffu, (uint32_t)x, lane));
 }
@@ -155,7 +162,7 @@ struct CompactParams : MoveLists {
 // Rows as they are: a lane moves 16 (4 bits) or 32 bytes of codes of K and of V,
 // and the words of one group.
 template <int BITS>
-__global__ void __launch_bounds__(kMoveThreads) compact_quant_kernel(const __grid_constant__ CompactParams p) {
+__global__ void __launch_bounds__(kMoveThreads, kCompactPerSm) compact_quant_kernel(const __grid_constant__ CompactParams p) {
     let_next_start();
     wait_for_inputs();
     if (!p.s.head->ok) return;
@@ -379,7 +386,7 @@ int launch_pages_compact_quant(const kvc_cache &c, int bits, const PagesState &s
     launch_pages_plan({s, table, len, counts, nullptr, 0, 0, n_lists, c.n_pages, c.max_pages, shift, k_max, false}, st);
     const CompactParams p{{s, table, nullptr, 0, idx, n_lists, c.n_pages, c.max_pages, shift, k_max}, groups,
                           Divider(groups), static_cast<uint8_t *>(k_pool), static_cast<uint8_t *>(v_pool)};
-    launch_early(bits == 4 ? compact_quant_kernel<4> : compact_quant_kernel<8>, sms * 8, kMoveThreads, 0, st, p);
+    launch_early(bits == 4 ? compact_quant_kernel<4> : compact_quant_kernel<8>, sms * kCompactPerSm, kMoveThreads, 0, st, p);
     launch_pages_swap(c, s, table, len, n_lists, counts, st);
     return cache_launched("kvc_pages_compact_quant");
 }

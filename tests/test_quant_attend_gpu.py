@@ -310,3 +310,30 @@ def test_two_calls_at_once():
             c.run(stream=s)
     a.check()
     b.check()
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("bf16", 96), ("f32", 128)])
+@pytest.mark.parametrize("ns", [[3, 1], [200, 64]])
+def test_queries_that_are_no_numbers_spoil_their_own_rows(ns, dtype, d, bits):
+    c = Case(ns=ns, lens=[700, 300], hq=6, h=2, d=d, ps=32, dtype=dtype, bits=bits, seed=d + bits)
+    c.q[1, 2, 5] = math.nan
+    c.q[2, 0, 3], c.q[2, 0, 40] = math.inf, -math.inf   # some key's two terms cancel
+    c.run().check()
+    assert c.out[1, 2].isnan().all() and c.out[2, 0].isnan().all() and int(c.out.isnan().any(-1).sum()) == 2
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("dtype,n", [("bf16", 1), ("bf16", 40), ("f32", 1), ("f32", 40)])
+def test_pages_past_32_bits(n, dtype, bits):
+    """Pages at the end of pools of more than 2^32 bytes."""
+    kvc = K()
+    c = Case(ns=[n], lens=[333], hq=4, h=2, d=128, ps=64, dtype=dtype, bits=bits)
+    few, size = c.kp.shape
+    c.c = kvc.cache(2 ** 32 // size + 1 + few, 64, 128, c.table.shape[1], dtype)
+    move = c.c.n_pages - few
+    pools = [torch.zeros((c.c.n_pages, size), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    pools[0][move:], pools[1][move:] = c.kp, c.vp
+    c.kp, c.vp = pools
+    c.table = torch.where(c.table >= 0, c.table + move, c.table)
+    c.run().check()

@@ -43,8 +43,15 @@ constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kChunk = 32;                 // keys of a warp's step
 constexpr int kStepKeys = kWarps * kChunk;
 constexpr int kSlotRows = 32;
-// Blocks per SM by their registers: 128, 168 or 255 per thread.
-constexpr int per_sm_of(int nt) { return nt == 1 ? 4 : nt == 2 ? 3 : 2; }
+// Blocks per SM by their registers: 128, 168 or 255 per thread.  A head of 64 spills
+// less than its one block more gains (16 rows: 73 us with three, 81 with two, over 64 x 8
+// lists of 500-6,000 rows in 4 bits; 8 rows: 40.7 with four, 41.4 with three, over 3 x 4
+// lists of 60,000-131,000).  One of 128 does not (16 rows: 121 us with three, 109 with
+// two; in 8 bits, 32 x 8 lists, 93 and 73; 8 rows: 79 with four, 77 with three; in 8
+// bits four did not fit shared memory, and 168 registers in place of 128 took 63 to 56).
+constexpr int per_sm_of(int groups, int nt) {
+    return groups == 2 ? (nt == 1 ? 4 : nt == 2 ? 3 : 2) : nt == 1 ? 3 : 2;
+}
 constexpr float kLag = 4.f;                // log2 units m may lag behind
 constexpr float kTop = 11.f;               // log2 of what P has for a probability of 1
 
@@ -69,19 +76,19 @@ struct Shared {
 };
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void mma16816_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
                  : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 // The transpose of an 8 x 8 matrix of 16-bit elements, a pair of a row per lane.
 __device__ __forceinline__ uint32_t turn(uint32_t x) {
     uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
@@ -140,7 +147,7 @@ __device__ __forceinline__ uint4 load_q(const AttendParams &p, const AttendUnit 
 }
 
 template <int G, int BITS, int NT>
-__global__ void __launch_bounds__(kThreads, per_sm_of(NT)) attend_quant_kernel(const __grid_constant__ AttendParams p) {
+__global__ void __launch_bounds__(kThreads, per_sm_of(G, NT)) attend_quant_kernel(const __grid_constant__ AttendParams p) {
     constexpr int D = 32 * G, kSlots = slots_of(BITS, G), kBlock = quant_block(BITS, G), kCodes = quant_codes(BITS, G);
     constexpr int kRow = kCodes, kWordsAt = kQuantRows * kCodes, kOutRow = D + 1;
     extern __shared__ __align__(128) uint8_t raw[];
@@ -694,7 +701,7 @@ int launch(AttendParams &p, int sms, cudaStream_t st) {
     static_assert(bytes <= 232448, "shared memory of one block");
     allow_shared<attend_quant_kernel<G, BITS, NT>>((int)bytes);
     // as many blocks as an SM holds at once (1 KB of shared memory is each block's own cost)
-    const int per_sm = std::max(1, std::min(per_sm_of(NT), (int)(233472 / (bytes + 1024))));
+    const int per_sm = std::max(1, std::min(per_sm_of(G, NT), (int)(233472 / (bytes + 1024))));
     launch_early(attend_quant_kernel<G, BITS, NT>, per_sm * sms, kThreads, bytes, st, p);
     return cache_launched("kvc_attend_quant");
 }

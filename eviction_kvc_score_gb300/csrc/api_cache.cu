@@ -176,9 +176,15 @@ int attend_call(const char *fn, int bits, const kvc_cache *cache, int32_t n_q_he
     p.part = reinterpret_cast<float *>(base + w.part);
     const bool f32 = c.dtype == KVC_F32;
     if (bits != 0 && w.tc) {
-        // Lists of few rows are attend_quant.cu's; where chunks are among them, a token's,
-        // in a launch of their own as in launch_attend_simt.
-        const int few = attend_quant_rows(c.head_dim);
+        // Lists of few rows are attend_quant.cu's: a tile of tcgen05's is 128 rows whoever
+        // fills them, and its keys are written out as bf16 first (us here and there; 64 x 8
+        // lists of 500-6,000 rows of 128 in 4 bits: 4 rows a list 77 and 282, 16 rows 109
+        // and 286, 32 rows 201 and 289; 32 x 8 in 8 bits: 56 and 180, 73 and 184, 127 and
+        // 189; heads of 64, 64 x 8 lists, 32 rows: 114 and 184, in 8 bits 118 and 181; one
+        // sequence of 1,000: 11 and 20).  48 rows would be three units of 16, 300 and 290.
+        // Where chunks are among them, a token's rows go in a launch of their own as in
+        // launch_attend_simt.
+        const int few = attend_quant_rows();
         const int64_t most = (int64_t)max_new * p.group;
         if (most <= few) return launch_attend_quant(p, (int)most, w.needs.grid, stream);
         const int own = p.group <= 8 ? 8 : p.group <= 16 ? 16 : 32;

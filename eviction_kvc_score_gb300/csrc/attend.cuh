@@ -188,8 +188,10 @@ __device__ __forceinline__ AttendRaw attend_raw_of(const AttendRaw &raw, int lan
                      __shfl_sync(0xffffffffu, raw.len, lane)};
 }
 
-// The cost of the lane's list (0 where !real); a list of several units is added
-// up by the whole warp.
+// The cost of the lane's list (0 where !real); a list of many units is added up by
+// the whole warp, of up to kOwnUnits by the lane (512 lists of two, one after the other
+// in four warps: 100 us).
+constexpr int kOwnUnits = 4;
 template <bool kSome>
 __device__ __forceinline__ int64_t attend_list_cost(const AttendParams &p, int list, bool real, AttendRaw *raw) {
     const int lane = threadIdx.x & 31;
@@ -200,6 +202,10 @@ __device__ __forceinline__ int64_t attend_list_cost(const AttendParams &p, int l
         const AttendUnit a = attend_unit<kSome>(p, list * p.blocks, *raw);
         cost = a.cost;
         rows = a.n * p.group;
+        if (p.blocks <= kOwnUnits) {
+            for (int i = 1; i < p.blocks; ++i) cost += attend_unit<kSome>(p, list * p.blocks + i, *raw).cost;
+            rows = 0;
+        }
     }
     for (unsigned left = __ballot_sync(0xffffffffu, rows > p.unit_rows); left; left &= left - 1) {
         const int of = __ffs(left) - 1, u0 = __shfl_sync(0xffffffffu, list, of) * p.blocks;
@@ -535,8 +541,9 @@ int launch_attend_simt(AttendParams &p, bool f32, int grid, cudaStream_t st);
 int launch_attend_simt_quant4(AttendParams &p, bool f32, int grid, cudaStream_t st);
 int launch_attend_simt_quant8(AttendParams &p, bool f32, int grid, cudaStream_t st);
 int launch_attend_tc(AttendParams &p, int grid, cudaStream_t st);
-// Lists of at most `rows` rows (16; 32 where D is 64), on the warp-wide tensor instruction.
-int attend_quant_rows(int dim);
+// Lists of at most `rows` rows, themselves at most attend_quant_rows(), on the warp-wide
+// tensor instruction.
+int attend_quant_rows();
 int launch_attend_quant(AttendParams &p, int rows, int sms, cudaStream_t st);
 // Lists of more than rows_above rows.
 int launch_attend_tc_quant(AttendParams &p, int rows_above, int grid, cudaStream_t st);

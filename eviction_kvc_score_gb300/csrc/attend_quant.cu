@@ -716,7 +716,7 @@ int launch_rows(AttendParams &p, int rows, int sms, cudaStream_t st) {
 
 }  // namespace
 
-int attend_quant_rows(int dim) { return dim == 64 ? 32 : 16; }
+int attend_quant_rows() { return 32; }
 
 int launch_attend_quant(AttendParams &p, int rows, int sms, cudaStream_t st) {
     const char *skip = getenv("KVC_TEST_SKIP_ARRIVE");
@@ -727,8 +727,9 @@ int launch_attend_quant(AttendParams &p, int rows, int sms, cudaStream_t st) {
     own.extra = 0;
     own.slots = 2;
     own.slot_rows = kSlotRows;
-    const int unit = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
-    if (!attend_units(own, unit, 0, unit)) {
+    // (two units of 16 rows for up to 32 of a head of 128, whose sums take the registers)
+    const int unit = rows <= 8 ? 8 : rows <= 16 || p.dim == 128 ? 16 : 32;
+    if (!attend_units(own, unit, 0, rows <= unit ? unit : 2 * unit)) {
         set_error("kvc_attend_quant: n_seqs * n_kv_heads * max_new is too large");
         return KVC_ERR_UNSUPPORTED;
     }

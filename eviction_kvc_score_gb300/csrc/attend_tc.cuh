@@ -326,16 +326,16 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-// Eight channels of V over 2^e as fp16: codes come as 16 + n or 1024 + n, where fp16
-// has room for them (n of 4 or 8 bits); off is that of the zero code times the step
-// with its sign turned, nine or eleven bits, so the fused sum is exact.
+// Eight channels of V over 2^e as fp16: codes come as 64 + n or 1024 + n, where fp16
+// has room for them (n of 4 bits, at bits 4-7, or of 8); off is that of the zero code times
+// the step with its sign turned, eleven bits, so the fused sum is exact.
 template <int BITS>
 __device__ __forceinline__ void tile_v(uint2 codes, uint32_t step, uint32_t off, uint32_t (&y)[4]) {
     if (BITS == 4) {
-        y[0] = fma_f16x2((codes.x << 6 & 0x03c003c0u) | 0x4c004c00u, step, off);
-        y[1] = fma_f16x2((codes.x << 2 & 0x03c003c0u) | 0x4c004c00u, step, off);
-        y[2] = fma_f16x2((codes.x >> 2 & 0x03c003c0u) | 0x4c004c00u, step, off);
-        y[3] = fma_f16x2((codes.x >> 6 & 0x03c003c0u) | 0x4c004c00u, step, off);
+        y[0] = fma_f16x2((codes.x << 4 & 0x00f000f0u) | 0x54005400u, step, off);
+        y[1] = fma_f16x2((codes.x & 0x00f000f0u) | 0x54005400u, step, off);
+        y[2] = fma_f16x2((codes.x >> 4 & 0x00f000f0u) | 0x54005400u, step, off);
+        y[3] = fma_f16x2((codes.x >> 8 & 0x00f000f0u) | 0x54005400u, step, off);
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -396,31 +396,32 @@ struct HeldRows {
     // V: groups that stand for NaN become zeros from row `finite` on (*dirty is set if
     // one of them is before `held`); the exponent of the largest step, or -127.
     __device__ __forceinline__ int exponent(int finite, int held, volatile int *dirty) {
-        const int r8 = row8();
-        uint32_t top = 0;
-        bool odd = false;
+        constexpr uint32_t kExponent = BITS == 4 ? 0x7f80u : 0xff00u;
+        uint32_t most = 0;   // of the upper and of the lower words
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int k = 0; k < KH; ++k)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t e = word[i][k] >> (16 * h + (BITS == 4 ? 7 : 8)) & 0xffu;
-                    odd |= e == 255;
-                    top = max(top, e == 255 ? 0 : e);
-                }
-        if (odd) {
+            for (int k = 0; k < KH; ++k) most = __vmaxu2(most, word[i][k] & (kExponent << 16 | kExponent));
+        uint32_t top = max(most >> 16, most & 0xffffu);
+        if (top == kExponent) {
+            const int r8 = row8();
+            top = 0;
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int k = 0; k < KH; ++k)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        if (quant_is_nan<BITS>(word[i][k] >> 16 * h & 0xffffu) && r8 + 8 * i >= finite) {
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t e = word[i][k] >> 16 * h & kExponent;
+                        if (e != kExponent) {
+                            top = max(top, e);
+                        } else if (r8 + 8 * i >= finite) {
                             word[i][k] &= h ? 0xffffu : 0xffff0000u;
                             if (r8 + 8 * i < held) *dirty = 1;
                         }
+                    }
         }
+        top >>= BITS == 4 ? 7 : 8;
         return (int)__reduce_max_sync(0xffffffffu, top) - 127;
     }
     // To rows row0 .. + 15 of a tile (V: over 2^e).
@@ -439,7 +440,7 @@ struct HeldRows {
                     // both groups' steps over 2^e, and the zero codes' share
                     uint32_t s, off;
                     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(s) : "f"(quant_step<BITS>(w >> 16) * down), "f"(quant_step<BITS>(w & 0xffffu) * down));
-                    off = mul_f16x2(BITS == 4 ? (w << 6 & 0x03c003c0u) | 0xcc00cc00u : (w & 0x00ff00ffu) | 0xe400e400u, s);
+                    off = mul_f16x2(BITS == 4 ? (w << 4 & 0x00f000f0u) | 0xd400d400u : (w & 0x00ff00ffu) | 0xe400e400u, s);
                     tile_v<BITS>(piece<V>(i, 2 * k), __byte_perm(s, 0, 0x1010), __byte_perm(off, 0, 0x1010), y0);
                     tile_v<BITS>(piece<V>(i, 2 * k + 1), __byte_perm(s, 0, 0x3232), __byte_perm(off, 0, 0x3232), y1);
                 } else {

@@ -52,6 +52,10 @@ constexpr int kSlotRows = 32;
 constexpr int per_sm_of(int groups, int nt) {
     return groups == 2 ? (nt == 1 ? 4 : nt == 2 ? 3 : 2) : nt == 1 ? 3 : 2;
 }
+// A unit costs about two steps beside its steps (us with 0, 2, 4 and 6: 64 x 8 lists of
+// 500-6,000 rows in 4 bits 77.4, 75.8, 76.9, 79.3; 32 x 8 in 8 bits 56.3, 53.9, 54.6,
+// 56.8; 12 lists of 60,000-131,000 78.7, 74.8, 73.7, 73.9).
+constexpr int kExtra = 2;
 constexpr float kLag = 4.f;                // log2 units m may lag behind
 constexpr float kTop = 11.f;               // log2 of what P has for a probability of 1
 
@@ -186,8 +190,16 @@ __global__ void __launch_bounds__(kThreads, per_sm_of(G, NT)) attend_quant_kerne
             u = attend_next_seq<true>(p, a.b);
             continue;
         }
-        const int64_t end = min(run.hi, u_lo + a.steps);
-        const int t0 = (int)(pos - u_lo), t1 = (int)(end - u_lo);
+        const int64_t end = min(run.hi, u_lo + a.cost);
+        const int t0 = max(0, (int)(pos - u_lo) - p.extra), t1 = max(0, (int)(end - u_lo) - p.extra);
+        if (t1 <= t0) {   // nothing but what the unit costs beside its steps
+            pos = end;
+            if (end == u_lo + a.cost) {
+                u_lo += a.cost;
+                u = attend_next(p, a, u);
+            }
+            continue;
+        }
         // ---------------------------------------------------- loads
         const int32_t *entry = p.table + (int64_t)a.list * p.max_pages;
         // page numbers of the warp's blocks, 16 steps at a time
@@ -673,8 +685,8 @@ __global__ void __launch_bounds__(kThreads, per_sm_of(G, NT)) attend_quant_kerne
             }
         }
         if (!whole) {
-            const int c0 = attend_cta_of(run.total, run.grid, u_lo);
-            const int c1 = attend_cta_of(run.total, run.grid, u_lo + a.steps - 1);
+            const int c0 = attend_cta_of(run.total, run.grid, u_lo + p.extra);
+            const int c1 = attend_cta_of(run.total, run.grid, u_lo + a.cost - 1);
             const int me = blockIdx.x, n = c1 - c0 + 1, groups = attend_groups(n);
             bool last = true;
             if (groups > 1) {
@@ -690,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, per_sm_of(G, NT)) attend_quant_kerne
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // bulk copies come after what was written here
         __syncthreads();   // the results are read: the ring may be filled again
         pos = end;
-        u_lo += a.steps;
+        u_lo += a.cost;
         u = attend_next(p, a, u);
     }
 }
@@ -724,7 +736,7 @@ int launch_attend_quant(AttendParams &p, int rows, int sms, cudaStream_t st) {
     own.skip_load = skip && skip[0] == '1';
     own.split_rows = 0;
     own.step_keys = kStepKeys;
-    own.extra = 0;
+    own.extra = kExtra;
     own.slots = 2;
     own.slot_rows = kSlotRows;
     // (two units of 16 rows for up to 32 of a head of 128, whose sums take the registers)

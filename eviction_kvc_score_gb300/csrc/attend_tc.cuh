@@ -73,7 +73,7 @@
 // and 15 more per block of K cost 1% of the time.  4,096 tokens x 32 heads over 32,768
 // rows in 4 bits: 1.95 ms, 1,050 TFLOP/s (rows in bf16: 2.01 ms with two terms of P, 1.46
 // with one, whose 8 bits are fewer than the 11 here); six chunks of 1-700 tokens over up to
-// 5,700 rows in 8 bits 215-220 us, 475 TFLOP/s.  Warps 12-19 and not the softmax's own: a
+// 5,700 rows in 8 bits 206-216 us, 485-510 TFLOP/s.  Warps 12-19 and not the softmax's own: a
 // step's tiles would then stand between its softmaxes.
 #pragma once
 
@@ -113,6 +113,10 @@ constexpr int kSlotsTc = 2;
 // A unit costs about 4 steps beside its steps (one term, 12 lists of 60,000-130,000
 // rows: 68 us without, 63 with 4, 62 with 8; 512 short lists: 148, 150 and 152 us).
 constexpr int kExtra = 4;
+// One over held rows of 128 about 8 (us with 4, 8 and 12: 16 chunks of up to 300 tokens
+// in 8 bits 290, 273, 277, in 4 bits 232, 222, 225, six of up to 700 211, 206, 215; of 64,
+// 32 chunks of up to 200: 146, 149, 150).
+constexpr int kExtraHeld = 8;
 constexpr int kDirect = 4;              // shares that are joined from registers
 constexpr int kQueue = 4;               // segments on their way from the walk to the roles
 
@@ -1552,7 +1556,7 @@ bool shape_units(AttendParams &p, int rows_above) {
     const int R = kTile / p.group * p.group;   // whole tokens
     p.split_rows = R;
     p.step_keys = kTile;
-    p.extra = kExtra;
+    p.extra = p.bits != 0 && p.dim == 128 ? kExtraHeld : kExtra;
     if (attend_units(p, 2 * R, rows_above, INT_MAX)) return true;
     set_error("kvc_attend: n_seqs * n_kv_heads * max_new is too large");
     return false;

@@ -1,5 +1,5 @@
-// attend.cuh -- the work split and the joining of partial results that both
-// attention kernels (attend_simt.cuh, attend_tc.cuh) share.
+// attend.cuh -- the work split and the joining of partial results that the attention
+// kernels (attend_simt.cuh, attend_tc.cuh, attend_quant.cu, attend_pieces.cuh) share.
 //
 // Rows: the G query heads of a KV head stand side by side, row r of a list =
 // token r / G, query head r % G of the group, so every key tile is read once

@@ -4,17 +4,23 @@
 // longer lists of rows are attend_tc.cuh's.
 //
 // Reading the cache should bound it: a code may then cost three instructions, so none
-// is spent on taking it out of the packed word but the one that picks it, on its zero
-// code or on its step.  With codes n, step s and zero code z of a key's group, and
-// everything per row (query head) of the list:
+// is spent on taking it out of the packed word but the one that picks it.  With codes n,
+// step s and zero code z of a key's group, and everything per row (query head) of the list:
 //   logit  = sum_g s_g (sum_d q_d n_d - z_g sum_d q_d)
-//   out_d  = sum_t (p_t s_tg) n_td - sum_t p_t (s_tg z_tg)
-// The sums over codes are matrix products (mma.m16n8k16) with the codes as they are:
-// a code picked out of its word by a mask is an fp16 number as it stands, n 2^-24 in
-// bits 0-3 (or 0-7) of a half and n 2^-20 in bits 4-7, exactly; the rows of Q, or of
-// the result, that meet the latter are 2^4 apart.  The groups' steps and zero codes go
-// to the products' 16 x 8 results in fp32 (K), or to the probabilities, one fp16
-// multiplication per key, row and group (V).
+//   out_d  = sum_t (p_t s_tg) (n_td - z_tg)
+// The sums are matrix products (mma.m16n8k16).  K's is with the codes as they are: a code
+// picked out of its word by a mask is an fp16 number as it stands, n 2^-24 in bits 0-3 (or
+// 0-7) of a half and n 2^-20 in bits 4-7, exactly; the rows of Q that meet the latter are
+// 2^4 apart, and the groups' steps and zero codes go to the products' 16 x 8 results in fp32.
+//
+// V's is in bf16, whose exponents are fp32's, so that no value is too large or too small
+// beside another one: a code as it stands is n 2^-133 or n 2^-129 there, and one
+// multiplication and sum makes it (n - z) 2^-6, exactly; a value of 0 is 0 in the product.
+// What a row's probability times the group's step is rounded to is two bf16 numbers,
+// 2^-17 of it away at most, as the tensor cores' other kernels have it.  (One fp16 number
+// instead, steps over the list's largest and the zero codes' share in a product of its own:
+// 7% faster, but 7 to 17% of the outputs were not the nearest number, and what one row
+// held far above the others, seen or not, took their bits.)
 //
 // Fragments: the product of K has 16 keys as its rows and 8 of the list's rows as
 // columns, a step of 16 channels picks two codes per lane out of every key's word, in
@@ -23,9 +29,8 @@
 // are channels.  Key i of a block stands in row pi(i) of both products: pi(2 c) = c,
 // pi(2 c + 1) = 4 + (c ^ 1), for fewer bank conflicts.
 //
-// P: fp16, 2^11 for a probability of 1 (the running maximum may lag behind by 2^4);
-// steps of V are taken over 2^E, the power of two of the largest so far, so that they
-// fit fp16 too.  Smaller numbers lose bits below 2^-35 of the largest product.
+// P: 2^20 for a probability of 1 (the running maximum may lag behind by 2^4), so that
+// rows whose values are near the type's smallest keep the bits of small probabilities.
 //
 // Every warp walks 32 keys of each step of 128 by itself, with a ring of its own that
 // bulk copies fill (a block of K or V of 16 rows each); the warps' results meet in
@@ -68,12 +73,12 @@ constexpr int per_sm_of(int groups, int nt) {
 // 56.8; 12 lists of 60,000-131,000 78.7, 74.8, 73.7, 73.9).
 constexpr int kExtra = 2;
 constexpr float kLag = 4.f;                // log2 units m may lag behind
-constexpr float kTop = 11.f;               // log2 of what P has for a probability of 1
+constexpr float kTop = 20.f;               // log2 of what P has for a probability of 1
 
 // Ring slots of a warp.
 constexpr int slots_of(int bits, int groups) { return bits == 4 && groups == 2 ? 4 : 2; }
 constexpr int slot_bytes(int bits, int groups) { return 4 * quant_block(bits, groups); }   // K K V V
-// K's steps and zero codes in fp32, V's in fp16.
+// K's steps and zero codes in fp32, V's in bf16.
 constexpr int scratch_bytes(int groups) { return kChunk * groups * 8 + 2 * kChunk / 2 * groups * 4; }
 constexpr int out_floats(int groups) { return kWarps * 8 * (32 * groups + 1); }
 constexpr int ring_bytes(int bits, int groups) {
@@ -95,6 +100,11 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma16816_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
 __device__ __forceinline__ void mma16816_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
                  : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
@@ -111,14 +121,14 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-__device__ __forceinline__ uint32_t mul_f16(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-__device__ __forceinline__ uint32_t sub_f16(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
     uint32_t r;
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
     return r;
 }
 __device__ __forceinline__ float2 unpack_f16(uint32_t x) {
@@ -174,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, per_sm_of(G, NT)) attend_quant_kerne
     uint8_t *mine = ring + warp * kSlots * slot_bytes(BITS, G);
     float2 *k_steps = reinterpret_cast<float2 *>(scratch_all + warp * scratch_bytes(G));   // [key][G]: s, -s z
     uint32_t *steps = reinterpret_cast<uint32_t *>(k_steps + kChunk * G);                    // V: [pair of keys][G]
-    uint32_t *zeros = steps + kChunk / 2 * G;                                                // the same of s z
+    uint32_t *zeros = steps + kChunk / 2 * G;                                                // the same of -z 2^-6
     volatile int *stop = &s.stop;
     const int key_of[2] = {(r8 & 1) ? 4 + (r8 >> 1 ^ 1) : r8 >> 1, 8 + ((r8 & 1) ? 4 + (r8 >> 1 ^ 1) : r8 >> 1)};   // of rows r8, r8 + 8
     // the lane's own key of the 32, and its half of its pair's word
@@ -318,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, per_sm_of(G, NT)) attend_quant_kerne
         }
         const int sees0 = attend_sees(p, a, 0);   // the fewest
 
-        float m[NT][2], l[NT][2], o[NT][2 * G][4], zo[NT][4];
+        float m[NT][2], l[NT][2], o[NT][2 * G][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -328,12 +338,10 @@ __global__ void __launch_bounds__(kThreads, per_sm_of(G, NT)) attend_quant_kerne
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                zo[nt][i] = 0.f;
 #pragma unroll
                 for (int mt = 0; mt < 2 * G; ++mt) o[nt][mt][i] = 0.f;
             }
         }
-        int top_exp = -127;   // O stands for sum p v / 2^top_exp
 
         for (int t = t0; ok && t < t1; ++t) {
             ok = __all_sync(0xffffffffu, mbar_wait(&s.full[warp][slot], round & 1, stop, p.status));
@@ -359,11 +367,22 @@ __global__ void __launch_bounds__(kThreads, per_sm_of(G, NT)) attend_quant_kerne
                     kw[0] = *reinterpret_cast<const uint32_t *>(k_at + at) & is;
                     vw[0] = *reinterpret_cast<const uint32_t *>(v_at + at) & is;
                 }
-                uint32_t top = 0;
+                uint32_t nan = 0;
 #pragma unroll
                 for (int i = 0; i < G / 2; ++i) {
-                    const uint32_t e0 = vw[i] >> (BITS == 4 ? 7 : 8) & 0xffu, e1 = vw[i] >> (BITS == 4 ? 23 : 24) & 0xffu;
-                    top = max(top, max(e0, e1));
+                    // V's steps are bf16 numbers
+                    uint32_t vs = BITS == 4 ? vw[i] & 0xfff0fff0u : vw[i] >> 1 & 0x7f807f80u;
+                    const uint32_t none = (vs & 0x7f807f80u) + 0x00800080u & 0x80008000u;   // exponents of ones only
+                    nan |= none;
+                    vs &= ~((none >> 15) * 0xffffu);   // added below
+                    // -z 2^-6: a whole number below 256 is that number times 2^-133 as bf16
+                    const uint32_t vz = mul_bf16x2(vw[i] & (BITS == 4 ? 0x000f000fu : 0x00ff00ffu), 0xff00ff00u);
+                    uint16_t *s16 = reinterpret_cast<uint16_t *>(steps) + (my_pair * G + 2 * i) * 2 + my_half;
+                    uint16_t *z16 = reinterpret_cast<uint16_t *>(zeros) + (my_pair * G + 2 * i) * 2 + my_half;
+                    s16[0] = (uint16_t)vs;
+                    s16[2] = (uint16_t)(vs >> 16);
+                    z16[0] = (uint16_t)vz;
+                    z16[2] = (uint16_t)(vz >> 16);
                     // zero codes as 1 + z / 16 or 1 + z / 256, for want of a cheap conversion
                     const float s0 = quant_step<BITS>(kw[i] & 0xffffu), s1 = quant_step<BITS>(kw[i] >> 16);
                     float z0, z1;
@@ -376,48 +395,7 @@ __global__ void __launch_bounds__(kThreads, per_sm_of(G, NT)) attend_quant_kerne
                     }
                     *reinterpret_cast<float4 *>(k_steps + lane * G + 2 * i) = make_float4(s0, s0 * z0, s1, s1 * z1);
                 }
-                odd = __any_sync(0xffffffffu, top == 255);
-                if (odd) {   // groups of V that stand for NaN: added below
-                    top = 0;
-#pragma unroll
-                    for (int i = 0; i < G / 2; ++i)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const uint32_t e = vw[i] >> (16 * h + (BITS == 4 ? 7 : 8)) & 0xffu;
-                            if (e == 255)
-                                vw[i] &= h ? 0xffffu : 0xffff0000u;
-                            else
-                                top = max(top, e);
-                        }
-                }
-                const int e_top = (int)__reduce_max_sync(0xffffffffu, top) - 127;
-                if (e_top > top_exp) {
-                    // 2^(old - new), nothing of what was nothing
-                    const float down = pow2(max(top_exp - e_top, -127));
-                    top_exp = e_top;
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            zo[nt][i] *= down;
-#pragma unroll
-                            for (int mt = 0; mt < 2 * G; ++mt) o[nt][mt][i] *= down;
-                        }
-                }
-                const float down = pow2(-top_exp);
-#pragma unroll
-                for (int i = 0; i < G / 2; ++i) {
-                    const uint32_t st = pack_f16(quant_step<BITS>(vw[i] & 0xffffu) * down, quant_step<BITS>(vw[i] >> 16) * down);
-                    // 1024 + z - 1024 in fp16
-                    const uint32_t z = sub_f16((vw[i] & (BITS == 4 ? 0x000f000fu : 0x00ff00ffu)) | 0x64006400u, 0x64006400u);
-                    const uint32_t sz = mul_f16(st, z);
-                    uint16_t *s16 = reinterpret_cast<uint16_t *>(steps) + (my_pair * G + 2 * i) * 2 + my_half;
-                    uint16_t *z16 = reinterpret_cast<uint16_t *>(zeros) + (my_pair * G + 2 * i) * 2 + my_half;
-                    s16[0] = (uint16_t)st;
-                    s16[2] = (uint16_t)(st >> 16);
-                    z16[0] = (uint16_t)sz;
-                    z16[2] = (uint16_t)(sz >> 16);
-                }
+                odd = __any_sync(0xffffffffu, nan != 0);   // groups of V that stand for NaN
                 __syncwarp();
             }
             // ------------------------------------------------ logits
@@ -507,8 +485,6 @@ __global__ void __launch_bounds__(kThreads, per_sm_of(G, NT)) attend_quant_kerne
                         const float down = y == -INFINITY ? 1.f : ex2(m[nt][e] - y);
                         m[nt][e] = y;
                         l[nt][e] *= down;
-                        zo[nt][e] *= down;
-                        zo[nt][2 + e] *= down;
 #pragma unroll
                         for (int mt = 0; mt < 2 * G; ++mt) {
                             o[nt][mt][e] *= down;
@@ -516,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, per_sm_of(G, NT)) attend_quant_kerne
                         }
                     }
             }
-            uint32_t pt[2][NT][2];   // P with keys as the inner dimension: [block][..][keys 0-7, 8-15]
+            uint32_t pt[2][NT][2], pl[2][NT][2];   // P in two terms, keys the inner dimension: [block][..][keys 0-7, 8-15]
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 const float n0 = kTop - (m[nt][0] == -INFINITY ? 0.f : m[nt][0]), n1 = kTop - (m[nt][1] == -INFINITY ? 0.f : m[nt][1]);
@@ -527,7 +503,9 @@ __global__ void __launch_bounds__(kThreads, per_sm_of(G, NT)) attend_quant_kerne
                         const float p0 = ex2(x[b][nt][2 * h] + n0), p1 = ex2(x[b][nt][2 * h + 1] + n1);
                         l[nt][0] += p0;
                         l[nt][1] += p1;
-                        pt[b][nt][h] = turn(pack_f16(p0, p1));
+                        const uint32_t hi = pack_bf16(p0, p1);
+                        pt[b][nt][h] = turn(hi);
+                        pl[b][nt][h] = turn(pack_bf16(p0 - __uint_as_float(hi << 16), p1 - __uint_as_float(hi & 0xffff0000u)));
                     }
             }
             // ------------------------------------------------ values
@@ -553,20 +531,21 @@ __global__ void __launch_bounds__(kThreads, per_sm_of(G, NT)) attend_quant_kerne
                         code[j][3 % (kCodes / 32)] = y.w;
                     }
                 }
-                uint32_t st[2][G];
+                uint32_t st[2][G], sz[2][G];   // steps and zero codes
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t *at = steps + (8 * b + 4 * h + c) * G;
+                for (int h = 0; h < 4; ++h) {
+                    const uint32_t *at = (h < 2 ? steps : zeros) + (8 * b + 4 * (h & 1) + c) * G;
+                    uint32_t(&to)[G] = h < 2 ? st[h & 1] : sz[h & 1];
                     if (G == 4) {
                         const uint4 y = *reinterpret_cast<const uint4 *>(at);
-                        st[h][0] = y.x;
-                        st[h][1] = y.y;
-                        st[h][2 % G] = y.z;
-                        st[h][3 % G] = y.w;
+                        to[0] = y.x;
+                        to[1] = y.y;
+                        to[2 % G] = y.z;
+                        to[3 % G] = y.w;
                     } else {
                         const uint2 y = *reinterpret_cast<const uint2 *>(at);
-                        st[h][0] = y.x;
-                        st[h][1] = y.y;
+                        to[0] = y.x;
+                        to[1] = y.y;
                     }
                 }
 #pragma unroll
@@ -581,18 +560,26 @@ __global__ void __launch_bounds__(kThreads, per_sm_of(G, NT)) attend_quant_kerne
                         pick<8>(__byte_perm(code[0][g], code[1][g], 0x5410), __byte_perm(code[0][g], code[1][g], 0x7632), e0);
                         pick<8>(__byte_perm(code[2][g], code[3][g], 0x5410), __byte_perm(code[2][g], code[3][g], 0x7632), e1);
                     }
+                    // (n - z) 2^-6: as bf16 numbers codes are at 2^-133, those in bits 4-7 at 2^-129
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        constexpr uint32_t kUp = 0x7f007f00u, kUp4 = 0x7d007d00u;   // 2^127, 2^123
+                        e0[i] = fma_bf16x2(e0[i], BITS == 4 && (i & 1) ? kUp4 : kUp, sz[0][g]);
+                        e1[i] = fma_bf16x2(e1[i], BITS == 4 && (i & 1) ? kUp4 : kUp, sz[1][g]);
+                    }
                     const uint32_t a0[4] = {e0[0], e0[1], e1[0], e1[1]}, a1[4] = {e0[2], e0[3], e1[2], e1[3]};
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        const uint32_t b0 = mul_f16(pt[b][nt][0], st[0][g]), b1 = mul_f16(pt[b][nt][1], st[1][g]);
-                        mma16816(o[nt][2 * g], a0, b0, b1);
-                        mma16816(o[nt][2 * g + 1], a1, b0, b1);
+                        // p s in two terms: what the first one's rounding leaves is exact
+                        const uint32_t b0 = mul_bf16x2(pt[b][nt][0], st[0][g]), b1 = mul_bf16x2(pt[b][nt][1], st[1][g]);
+                        const uint32_t c0 = fma_bf16x2(pl[b][nt][0], st[0][g], fma_bf16x2(pt[b][nt][0], st[0][g], b0 ^ 0x80008000u));
+                        const uint32_t c1 = fma_bf16x2(pl[b][nt][1], st[1][g], fma_bf16x2(pt[b][nt][1], st[1][g], b1 ^ 0x80008000u));
+                        mma16816_bf16(o[nt][2 * g], a0, b0, b1);
+                        mma16816_bf16(o[nt][2 * g], a0, c0, c1);
+                        mma16816_bf16(o[nt][2 * g + 1], a1, b0, b1);
+                        mma16816_bf16(o[nt][2 * g + 1], a1, c0, c1);
                     }
                 }
-                // rows 0 .. G - 1 of a product of their own: the groups' s z
-                const uint32_t az[4] = {zeros[(8 * b + c) * G + r8 % G], 0, zeros[(8 * b + 4 + c) * G + r8 % G], 0};
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) mma16816(zo[nt], az, pt[b][nt][0], pt[b][nt][1]);
             }
             if (odd) {   // groups of V that stand for NaN, for the rows that see them
                 for (int k = 0; k < kChunk; ++k) {
@@ -627,7 +614,6 @@ __global__ void __launch_bounds__(kThreads, per_sm_of(G, NT)) attend_quant_kerne
         // ---------------------------------------------------- the warps' results
         const bool whole = t0 == 0 && t1 == a.steps;
         const int64_t out_slot = (int64_t)blockIdx.x * p.slots + (t0 == 0 ? kSlotLast : kSlotFirst);
-        const float back = pow2(top_exp);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             __syncthreads();   // every warp's ring is at rest, the rows before are read
@@ -637,16 +623,14 @@ __global__ void __launch_bounds__(kThreads, per_sm_of(G, NT)) attend_quant_kerne
                 float sum = l[nt][e];
 #pragma unroll
                 for (int d = 4; d <= 16; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-                if (r8 == 0) s.stat[warp][2 * c + e] = make_float2(m[nt][e], sum * 0x1p-11f);
+                if (r8 == 0) s.stat[warp][2 * c + e] = make_float2(m[nt][e], sum * 0x1p-20f);
                 float *dst = s_out + (warp * 8 + 2 * c + e) * kOutRow;
 #pragma unroll
                 for (int g = 0; g < G; ++g) {
-                    const float z = __shfl_sync(0xffffffffu, zo[nt][e], g * 4 + c);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float y = o[nt][2 * g + (i >> 1)][2 * (i & 1) + e] * (BITS == 4 && (i & 1) ? 0x1p20f : 0x1p24f) - z;
                         const int ch = BITS == 4 ? 8 * (r8 >> 1) + 2 * i + (r8 & 1) : 4 * r8 + i;
-                        dst[32 * g + ch] = y * 0x1p-11f * back;
+                        dst[32 * g + ch] = o[nt][2 * g + (i >> 1)][2 * (i & 1) + e] * 0x1p-14f;
                     }
                 }
             }

@@ -1,0 +1,107 @@
+"""How exact attention over a cache held in 4 or 8 bits is, beyond the bound per
+element of test_quant_attend_gpu.py: the error's norm, channels that are zero, and rows
+that some tokens do not see."""
+import math
+
+import pytest
+import torch
+
+import quant_ref as ref
+from test_quant_attend_gpu import Case, K
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+    import __graft_entry__
+    __graft_entry__.build()
+    torch.cuda.set_device(0)
+
+
+# Forms of the call: one token, drafts (units of 16 and 32 rows), head sizes of every kernel.
+FORMS = [
+    dict(ns=[1, 1], lens=[700, 2300], hq=8, h=2, d=128, ps=16),
+    dict(ns=[1], lens=[30000], hq=4, h=2, d=64, ps=64),
+    dict(ns=[4, 3], lens=[500, 1800], hq=8, h=2, d=128, ps=32),
+    dict(ns=[7, 5], lens=[1500, 300], hq=8, h=2, d=64, ps=128),
+    dict(ns=[8], lens=[900], hq=8, h=2, d=128, ps=32),
+    dict(ns=[1, 3], lens=[300, 800], hq=4, h=2, d=80, ps=16),
+    dict(ns=[40, 90], lens=[1000, 300], hq=4, h=2, d=96, ps=32),
+]
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("i", range(len(FORMS)))
+def test_channels_that_are_zero_stay_zero(i, dtype, bits):
+    """V's channels 3, 32 and the last are 0 in every row, in groups whose other values
+    lie to one side of zero or to both: (n - z) s is 0, and so are the outputs, exactly."""
+    d = FORMS[i]["d"]
+    zero = [3, 32, d - 1]
+
+    def change(k, v):
+        for j, x in enumerate(v):
+            if j % 2:
+                x.sub_(4)
+            x[:, zero] = 0
+    c = Case(**FORMS[i], dtype=dtype, bits=bits, seed=i, change=change)
+    assert any(ref.quantise(x, bits)[2][:, zero].amax() > 0 for x in c.v)
+    c.run().check()
+    assert (c.out[..., zero] == 0).all()
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("i", range(len(FORMS)))
+def test_errors_norm(i, dtype, bits):
+    c = Case(**FORMS[i], dtype=dtype, bits=bits, seed=100 + i).run()
+    torch.cuda.synchronize()
+    want = ref.attend(c.q, c.start, c.k, c.v, c.scale, bits)["out"]
+    assert ref.near(c.out, want) is None
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("bf16", 80), ("f32", 128)])
+@pytest.mark.parametrize("ns", [[4, 3], [8, 2]])
+def test_values_that_a_token_does_not_see_leave_no_trace(ns, dtype, d, bits):
+    """The last token's own row of V is 2^40 to 2^99 times as large as the others, in one group of channels or
+    in all: the tokens before it get the very bits that they get without it."""
+    c = Case(ns=ns, lens=[[300, 777], [129, 1000]], hq=8, h=2, d=d, ps=16, dtype=dtype, bits=bits)
+    c.run().check()
+    calm = c.out.clone(), c.lse.clone()
+
+    def change(k, v):
+        v[0][-1] *= 2.0 ** 40
+        v[1][-1, :32] = 2.0 ** 99
+        v[2][-1, 32:] *= -(2.0 ** 60)
+        v[3][-1, 5] = 2.0 ** 45
+    c = Case(ns=ns, lens=[[300, 777], [129, 1000]], hq=8, h=2, d=d, ps=16, dtype=dtype, bits=bits, change=change)
+    c.run()
+    torch.cuda.synchronize()
+    before = [t for t in range(sum(ns)) if t + 1 not in c.start]
+    assert len(before) > 3
+    assert torch.equal(c.out[before], calm[0][before]) and torch.equal(c.lse, calm[1])
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("bf16", 80), ("f32", 128)])
+@pytest.mark.parametrize("ns", [[1, 1], [8, 5]])
+def test_rows_small_in_value_and_probability_keep_their_bits(ns, dtype, d, bits):
+    """Channels 32 to 63 of V are 2^-30 of the others and half of the rows have 2^-25 of the others' probability (their
+    values, 2^25 times as large there, decide those channels as much as the likely rows do): their outputs are as near to
+    the definition as anybody's."""
+    def change(k, v):
+        for x, y in zip(k, v):
+            x.copy_(torch.randn_like(x.float()) / 64)
+            x[::2, 0], x[1::2, 0] = 8, -8
+            y[:, 32:64] *= 2.0 ** -30
+            y[1::2, 32:64] *= 2.0 ** 25
+    c = Case(ns=ns, lens=[500, 900], hq=8, h=2, d=d, ps=32, dtype=dtype, bits=bits, change=change)
+    c.q[..., 0] = 1.08 * math.sqrt(d)    # logits of +-8.64: e^-17.3 between the halves
+    c.run()
+    torch.cuda.synchronize()
+    want = ref.attend(c.q, c.start, c.k, c.v, c.scale, bits)["out"]
+    assert ref.near(c.out[..., 32:64], want[..., 32:64], logit=8.64) is None

@@ -57,24 +57,19 @@
 //
 // Rows held in 4 or 8 bits (BITS; quant.cuh; attend_tc_quant.cu): warps 12-19 make
 // the tiles.  Warp 11 brings blocks of 16 rows to shared memory, a bulk copy each;
-// each of the eight warps takes a block of every tile and writes it out in the layout
-// that TMA would have left: K as bf16, exactly; V as fp16, (n - z) times the step, the
-// step over 2^e with e the exponent of the block's largest.  The
-// probabilities of their columns are multiplied by 2^(e - E), E the largest e
-// so far, and rounded to one fp16 number: 11 bits where bf16 has 8, so there is no
-// second term.  O stands for sum p v / 2^E, rescaled when E grows by more than one.
-// p = 1 with e = E is held as 2^6: m's 8 and E's 1 leave it below fp16's 2^16, and
-// numbers down to 2^-30 of that are not lost.  Groups of V that stand for NaN are
-// taken out by the warps that write the tile.
+// each of the eight warps takes a block of every tile and writes it out as bf16, which
+// holds (n - z) s exactly, in the layout that TMA would have left.  The rest is as with
+// rows in bf16, two terms of P included; groups of V that stand for NaN are taken out by
+// the warps that write the tile.  (V as fp16 over a power of two and P as one fp16 number
+// took 216 us for the chunks and 1.95 ms for the long one below, but every power had to
+// fit a tile's largest value: one seen by some tokens only took the others' bits.)
 //
-// What bounds them: issue slots, and shared memory beside the MMAs that read it.  A step
-// of two halves takes 5,000 clocks where its MMAs take 2,048; of 11,500 instructions a
-// step the tiles are 4,400 (a block of K 187, of V 200 a warp), the two softmaxes 3,500,
-// and 15 more per block of K cost 1% of the time.  4,096 tokens x 32 heads over 32,768
-// rows in 4 bits: 1.95 ms, 1,050 TFLOP/s (rows in bf16: 2.01 ms with two terms of P, 1.46
-// with one, whose 8 bits are fewer than the 11 here); six chunks of 1-700 tokens over up to
-// 5,700 rows in 8 bits 206-216 us, 485-510 TFLOP/s.  Warps 12-19 and not the softmax's own: a
-// step's tiles would then stand between its softmaxes.
+// What bounds them: the chain S -> softmax -> P V, whose softmax shares its issue slots
+// with the writing of the tiles.  A step of two halves takes 6,200 clocks where its MMAs
+// take 3,072.  4,096 tokens x 32 heads over 32,768 rows in 4 bits: 2.40 ms, 860 TFLOP/s
+// (rows in bf16: 2.01 ms; without the MMAs of the second term 2.28); six chunks of 1-700
+// tokens over up to 5,700 rows in 8 bits 240 us, 437 TFLOP/s.  Warps 12-19 and not the
+// softmax's own: a step's tiles would then stand between its softmaxes.
 #pragma once
 
 #include <cudaTypedefs.h>
@@ -95,12 +90,13 @@ namespace {
 // the loading and issuing warpgroup to the two that hold a row of 128 logits
 // per thread.  256 x 208 + 128 x 88 = 384 x 168: the launch checks the 168,
 // because an increase beyond what the block was launched with never returns.
-// With two warpgroups more: 256 x 128 + 128 x 64 + 256 x 80 = 640 x 96.
+// With two warpgroups more: 256 x 144 + 128 x 64 + 256 x 64 = 640 x 96 (with 128 and 80
+// the second term spills twice as much: a long chunk takes 2.48 ms, and 2.40 so).
 template <int BITS>
 struct Shape {
     static constexpr int kThreads = BITS == 0 ? 384 : 640;
-    static constexpr int kRegsLaunch = BITS == 0 ? 168 : 96, kRegsSoftmax = BITS == 0 ? 208 : 128;
-    static constexpr int kRegsOther = BITS == 0 ? 88 : 64, kRegsTiles = BITS == 0 ? 0 : 80;
+    static constexpr int kRegsLaunch = BITS == 0 ? 168 : 96, kRegsSoftmax = BITS == 0 ? 208 : 144;
+    static constexpr int kRegsOther = BITS == 0 ? 88 : 64, kRegsTiles = BITS == 0 ? 0 : 64;
     static_assert(256 * kRegsSoftmax + 128 * kRegsOther + 256 * kRegsTiles <= kThreads * kRegsLaunch, "register split");
     static constexpr int kReaders = BITS == 0 ? 12 : 20;   // warps that read the queue
 };
@@ -157,9 +153,7 @@ struct Bars {
     Work work[kQueue];
     float2 other[kTile];  // half 1's (max, sum) of a split unit
     int64_t plan[Shape<BITS>::kThreads / 32 + 4];
-    // held rows: exponents of a stage's blocks, those of half 1's O, blocks that have come and gone
-    alignas(16) int exps[BITS == 0 ? 1 : STAGES][8];
-    int other_exp[4];
+    // held rows: blocks that have come and gone
     uint64_t raw_full[BITS == 0 ? 1 : RAW], raw_empty[BITS == 0 ? 1 : RAW];
     volatile int raw_there[BITS == 0 ? 1 : RAW];   // blocks that a page of the pool holds
 };
@@ -329,33 +323,6 @@ struct Walk {
 __device__ __forceinline__ void write16(uint32_t at, const uint32_t (&x)[4]) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]) : "memory");
 }
-__device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c) {
-    uint32_t r;
-    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
-    return r;
-}
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-// Eight channels of V over 2^e as fp16: codes come as 64 + n or 1024 + n, where fp16
-// has room for them (n of 4 bits, at bits 4-7, or of 8); off is that of the zero code times
-// the step with its sign turned, eleven bits, so the fused sum is exact.
-template <int BITS>
-__device__ __forceinline__ void tile_v(uint2 codes, uint32_t step, uint32_t off, uint32_t (&y)[4]) {
-    if (BITS == 4) {
-        y[0] = fma_f16x2((codes.x << 4 & 0x00f000f0u) | 0x54005400u, step, off);
-        y[1] = fma_f16x2((codes.x & 0x00f000f0u) | 0x54005400u, step, off);
-        y[2] = fma_f16x2((codes.x >> 4 & 0x00f000f0u) | 0x54005400u, step, off);
-        y[3] = fma_f16x2((codes.x >> 8 & 0x00f000f0u) | 0x54005400u, step, off);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            y[i] = fma_f16x2(__byte_perm(i < 2 ? codes.x : codes.y, 0x64646464u, i & 1 ? 0x4342 : 0x4140), step, off);
-    }
-}
-
 // A block of 16 rows as it is held, in a warp's registers: lane 4 j + c has piece c of
 // all groups of rows r8 and r8 + 8, r8 = 0, 4, 1, 5, 2, 6, 3, 7 for j = 0 .. 7: the
 // eight lanes whose 16 bytes are stored at a time hit eight places of the swizzle.
@@ -406,42 +373,32 @@ struct HeldRows {
         // halves of the group from two places
         return make_uint2(__byte_perm(code[i][g / 2], code[i][KH + g / 2], g & 1 ? 0x7632 : 0x5410), 0);
     }
-    // V: groups that stand for NaN become zeros from row `finite` on (*dirty is set if
-    // one of them is before `held`); the exponent of the largest step, or -127.
-    __device__ __forceinline__ int exponent(int finite, int held, volatile int *dirty) {
+    // V: groups that stand for NaN become zeros from row `finite` on; *dirty is set if
+    // one of them is before `held`.
+    __device__ __forceinline__ void clean(int finite, int held, volatile int *dirty) {
         constexpr uint32_t kExponent = BITS == 4 ? 0x7f80u : 0xff00u;
         uint32_t most = 0;   // of the upper and of the lower words
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int k = 0; k < KH; ++k) most = __vmaxu2(most, word[i][k] & (kExponent << 16 | kExponent));
-        uint32_t top = max(most >> 16, most & 0xffffu);
-        if (top == kExponent) {
-            const int r8 = row8();
-            top = 0;
+        if (max(most >> 16, most & 0xffffu) != kExponent) return;
+        const int r8 = row8();
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int k = 0; k < KH; ++k)
+            for (int k = 0; k < KH; ++k)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint32_t e = word[i][k] >> 16 * h & kExponent;
-                        if (e != kExponent) {
-                            top = max(top, e);
-                        } else if (r8 + 8 * i >= finite) {
-                            word[i][k] &= h ? 0xffffu : 0xffff0000u;
-                            if (r8 + 8 * i < held) *dirty = 1;
-                        }
+                for (int h = 0; h < 2; ++h)
+                    if ((word[i][k] >> 16 * h & kExponent) == kExponent && r8 + 8 * i >= finite) {
+                        word[i][k] &= h ? 0xffffu : 0xffff0000u;
+                        if (r8 + 8 * i < held) *dirty = 1;
                     }
-        }
-        top >>= BITS == 4 ? 7 : 8;
-        return (int)__reduce_max_sync(0xffffffffu, top) - 127;
     }
-    // To rows row0 .. + 15 of a tile (V: over 2^e).
+    // To rows row0 .. + 15 of a tile.
     template <bool V>
-    __device__ __forceinline__ void write(uint32_t tile, int row0, int e) const {
+    __device__ __forceinline__ void write(uint32_t tile, int row0) const {
         const int r8 = row8(), c = threadIdx.x & 3;
-        const float down = V ? __uint_as_float((uint32_t)(127 - e) << 23) : 1.f;
         const uint32_t at = tile + (row0 + r8) * 128 + ((c ^ r8) << 4);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -449,17 +406,8 @@ struct HeldRows {
             for (int k = 0; k < KH; ++k) {
                 const uint32_t w = word[i][k];
                 uint32_t y0[4], y1[4];
-                if (V) {
-                    // both groups' steps over 2^e, and the zero codes' share
-                    uint32_t s, off;
-                    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(s) : "f"(quant_step<BITS>(w >> 16) * down), "f"(quant_step<BITS>(w & 0xffffu) * down));
-                    off = mul_f16x2(BITS == 4 ? (w << 4 & 0x00f000f0u) | 0xd400d400u : (w & 0x00ff00ffu) | 0xe400e400u, s);
-                    tile_v<BITS>(piece<V>(i, 2 * k), __byte_perm(s, 0, 0x1010), __byte_perm(off, 0, 0x1010), y0);
-                    tile_v<BITS>(piece<V>(i, 2 * k + 1), __byte_perm(s, 0, 0x3232), __byte_perm(off, 0, 0x3232), y1);
-                } else {
-                    quant_bf16<BITS>(piece<V>(i, 2 * k), __byte_perm(w, 0, 0x1010), y0);
-                    quant_bf16<BITS>(piece<V>(i, 2 * k + 1), __byte_perm(w, 0, 0x3232), y1);
-                }
+                quant_bf16<BITS>(piece<V>(i, 2 * k), __byte_perm(w, 0, 0x1010), y0);
+                quant_bf16<BITS>(piece<V>(i, 2 * k + 1), __byte_perm(w, 0, 0x3232), y1);
                 const uint32_t to = at + i * 8 * 128 + k * kBox;
                 write16(to, y0);
                 write16(to ^ 0x40, y1);
@@ -586,11 +534,11 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1)
                     if (!(ok = fill < kStages || warp_wait(&b.empty[st], (fill / kStages - 1) & 1, stop, p.status))) break;
                     const uint32_t to = smem_u32(ring) + st * kStageBytes;
                     if (is_v) {
-                        const int key = key0 + tile * kTile, e = rows.exponent(from - key, len - key, &b.dirty);
-                        rows.template write<true>(to, kQuantRows * part, e);
-                        if (lane == 0) b.exps[st][part] = e;
+                        const int key = key0 + tile * kTile;
+                        rows.clean(from - key, len - key, &b.dirty);
+                        rows.template write<true>(to, kQuantRows * part);
                     } else {
-                        rows.template write<false>(to, kQuantRows * part, 0);
+                        rows.template write<false>(to, kQuantRows * part);
                     }
                     if (l + 1 < 2 * g.n) ok = read(l + 1);
                     __threadfence_block();   // what was taken out is noted
@@ -808,8 +756,7 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1)
         // ------------------------------------------------ MMA issue, a warp per half
         if (elect_one()) {
             constexpr uint32_t kIdS = idesc_bf16_f32(kTile, kTile);
-            // B MN-major; A and B are fp16 (format 0) where V is
-            constexpr uint32_t kIdO = (idesc_bf16_f32(kTile, D) | (1u << 16)) & ~(BITS == 0 ? 0u : 1u << 7 | 1u << 10);
+            constexpr uint32_t kIdO = idesc_bf16_f32(kTile, D) | (1u << 16);   // B MN-major
             const int t = warp - kMmaWarp;
             const uint32_t col_s = tmem + kColS + t * 128, col_o = tmem + kColO + t * 128;
             uint32_t use = 0, segs = 0, np = 0;   // ring stages passed, segments, P tiles seen
@@ -833,17 +780,18 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1)
                 }
                 tc_commit(&b.s_full[t]);
             };
-            // keys 0-63 or 64-127 of the tile.  (Held rows: the upper ones come first, their P
-            // from S's upper columns; the first group of a unit's first tile does not add.)
+            // keys 0-63 or 64-127 of the tile; the first group of a unit's first tile does not
+            // add.  (Held rows: the upper ones come first, and each 64 keys' P lies over their
+            // own S, the second term behind the first.)
             auto issue_o = [&](uint32_t f, auto second, bool add) {
                 constexpr bool kUpper = decltype(second)::value == (BITS == 0);
-                constexpr int k0 = kUpper ? 4 : 0, kP = BITS != 0 && kUpper ? 32 : 0;
+                constexpr int k0 = kUpper ? 4 : 0, kP = BITS != 0 && kUpper ? 32 : 0, kSecond = BITS != 0 ? 32 : 64;
                 const uint64_t v = desc_sw128(smem_u32(ring) + (f % kStages) * kStageBytes, kBox, 1024);
 #pragma unroll
                 for (int ks = k0; ks < k0 + 4; ++ks) {
                     const uint64_t at = v + (uint64_t)(ks * (16 * 128 >> 4));
                     tc_mma_bf16_tmem_a(col_o, col_s + kP + ks * 8, at, kIdO, add || ks > k0);
-                    if (TWO) tc_mma_bf16_tmem_a(col_o, col_s + 64 + ks * 8, at, kIdO, 1);
+                    if (TWO) tc_mma_bf16_tmem_a(col_o, col_s + kP + kSecond + ks * 8, at, kIdO, 1);
                 }
             };
             // The halves' groups (O of a tile, S of the next) go to the tensor
@@ -943,7 +891,6 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1)
             const int sees0 = attend_sees(p, a, g.split ? 0 : t * R);   // the tile's first row's
             const int from = attend_sees(p, a, 0);                      // the unit's
             float m = -INFINITY, l = 0.f;
-            int top_exp = -127;   // held rows: O stands for sum p v / 2^top_exp
             const int cnt = g.cnt[t];
             for (int i = 0; i < cnt; ++i) {
                 const int ti = g.split ? 2 * i + t : i;
@@ -989,17 +936,6 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1)
                     fence_async_shared();
                     // lane 0 says for all 32 rows that they are clean
                     __syncwarp();
-                }
-                int exps[BITS == 0 ? 1 : 8] = {};
-                if constexpr (BITS != 0) {
-                    if (any) {
-                        const uint32_t f = filled + v_at(g, ti);
-                        if (!(ok = warp_wait(&b.full[f % kStages], (f / kStages) & 1, stop, p.status))) break;
-                        const int4 x = *reinterpret_cast<const int4 *>(b.exps[f % kStages]);
-                        const int4 y = *reinterpret_cast<const int4 *>(b.exps[f % kStages] + 4);
-                        exps[0] = x.x; exps[1] = x.y; exps[2] = x.z; exps[3] = x.w;
-                        exps[4] = y.x; exps[5] = y.y; exps[6] = y.z; exps[7] = y.w;
-                    }
                 }
                 // slow: some row of the tile sees only part of it, or the scale is
                 // not positive; two copies, because a select per logit costs as much
@@ -1140,22 +1076,14 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1)
                         }
                     }
                     const float top = fmaxf(fmax3(x[0], x[1], x[2]), x[3]) * (kSlow ? 1.f : c);
-                    int e_top = exps[0];
-#pragma unroll
-                    for (int q = 1; q < 8; ++q) e_top = max(e_top, exps[q % (BITS == 0 ? 1 : 8)]);
                     if (i == 0) {
                         m = top;
-                        top_exp = e_top;
                     } else {
                         const bool grow = top > m + kGrow;
-                        if (__any_sync(0xffffffffu, grow || e_top > top_exp + 1)) {
-                            float down = grow ? ex2(m - top) : 1.f;
+                        if (__any_sync(0xffffffffu, grow)) {
+                            const float down = grow ? ex2(m - top) : 1.f;
                             if (grow) m = top;
                             l *= down;
-                            if (e_top > top_exp + 1) {   // 2^(top_exp - e_top)
-                                down *= __uint_as_float((uint32_t)max(127 + top_exp - e_top, 0) << 23);
-                                top_exp = e_top;
-                            }
 #pragma unroll 1
                             for (int d = 0; d < D; d += 16) {
                                 float o[16];
@@ -1172,42 +1100,40 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1)
                         }
                     }
                     const float nm = m == -INFINITY ? 0.f : -m;
-                    float sum = 0.f;
+                    const unsigned long long nm2 = f2_pack(nm, nm);
+                    unsigned long long sum2[2] = {0, 0};
                     // keys 32 q .. + 31 of the tile from y, the slow way already scaled or not
                     auto weigh = [&](int q, float(&y)[32], auto scaled) {
-                        uint32_t pw[16];
 #pragma unroll
-                        for (int b16 = 0; b16 < 2; ++b16) {
-                            // P is p 2^shift, shift = e - E + 6 of the block of 16 columns;
-                            // far below, where that rounds to zero, p still counts in l
-                            const int shift = max(exps[(2 * q + b16) % (BITS == 0 ? 1 : 8)] - top_exp + 6, -60);
-                            const float at = nm + (float)shift;
-                            const unsigned long long at2 = f2_pack(at, at);
-                            unsigned long long sum2 = 0;
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t pw[8], lo[8];
 #pragma unroll
-                            for (int j = 8 * b16; j < 8 * b16 + 8; ++j) {
-                                float y0 = y[2 * j], y1 = y[2 * j + 1];
+                            for (int j = 0; j < 8; ++j) {
+                                float y0 = y[16 * h + 2 * j], y1 = y[16 * h + 2 * j + 1];
                                 if (kSlow) {
                                     if (!decltype(scaled)::value) {
-                                        y0 = seen(q * 32 + 2 * j, y0);
-                                        y1 = seen(q * 32 + 2 * j + 1, y1);
+                                        y0 = seen(q * 32 + 16 * h + 2 * j, y0);
+                                        y1 = seen(q * 32 + 16 * h + 2 * j + 1, y1);
                                     }
-                                    y0 += at;
-                                    y1 += at;
+                                    f2_unpack(f2_add(f2_pack(y0, y1), nm2), y0, y1);
                                 } else {
-                                    f2_unpack(f2_fma(f2_pack(y0, y1), c2, at2), y0, y1);
+                                    f2_unpack(f2_fma(f2_pack(y0, y1), c2, nm2), y0, y1);
                                 }
-                                y0 = ex2(y0);
-                                y1 = ex2(y1);
-                                sum2 = j == 8 * b16 ? f2_pack(y0, y1) : f2_add(sum2, f2_pack(y0, y1));
-                                asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pw[j]) : "f"(y1), "f"(y0));
+                                const float p0 = ex2(y0), p1 = ex2(y1);
+                                const unsigned long long pp = f2_pack(p0, p1);
+                                sum2[j & 1] = f2_add(sum2[j & 1], pp);
+                                // the upper 16 bits, and what is left of the rest
+                                const uint32_t b0 = __float_as_uint(p0), b1 = __float_as_uint(p1);
+                                pw[j] = __byte_perm(b0, b1, 0x7632);
+                                float r0, r1;
+                                f2_unpack(f2_add(pp, f2_pack(-__uint_as_float(b0 & 0xffff0000u), -__uint_as_float(b1 & 0xffff0000u))), r0, r1);
+                                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(lo[j]) : "f"(r1), "f"(r0));
                             }
-                            float s0, s1;
-                            f2_unpack(sum2, s0, s1);
-                            sum = fmaf(s0 + s1, __uint_as_float((uint32_t)(127 - shift) << 23), sum);
+                            // over logits that are in registers or read for the last time
+                            const uint32_t to = cs + (q < 2 ? 0 : 32) + 16 * q + 8 * h;
+                            tmem_st8(to, pw);
+                            tmem_st8(to + 32, lo);
                         }
-                        // over logits that are in registers or read for the last time
-                        tmem_st16(cs + (q < 2 ? 0 : 32) + 16 * q, pw);
                     };
                     auto handed = [&](int h) {
                         tmem_st_wait();
@@ -1226,7 +1152,9 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1)
                     weigh(0, v[0], std::false_type{});
                     weigh(1, v[1], std::false_type{});
                     handed(1);
-                    l += sum;
+                    float s0, s1;
+                    f2_unpack(f2_add(sum2[0], sum2[1]), s0, s1);
+                    l += s0 + s1;
                 };
                 if (any) {
                     if constexpr (BITS != 0) {
@@ -1255,7 +1183,6 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1)
                 // the other half takes these rows over, O straight from TMEM
                 if (cnt > 0) {
                     b.other[r] = make_float2(m, l);
-                    if (BITS != 0 && lane == 0) b.other_exp[quarter] = top_exp;
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&b.half_full);
@@ -1266,8 +1193,6 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1)
             }
             const bool take = g.split && g.cnt[1] > 0;
             float w_mine = 1.f, w_other = 0.f;
-            // held rows: 2^top_exp, of this half and of the other
-            float up = __uint_as_float((uint32_t)(127 + top_exp) << 23), up_other = 0.f;
             if (take) {
                 if (!(ok = warp_wait(&b.half_full, handed++ & 1, stop, p.status))) break;
                 tc_fence_after();
@@ -1277,7 +1202,6 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1)
                 w_other = ex2(st.x - ref);
                 l = l * w_mine + st.y * w_other;
                 m = top;
-                if (BITS != 0) up_other = __uint_as_float((uint32_t)(127 + b.other_exp[quarter]) << 23);
             }
             const int64_t slot = ((int64_t)blockIdx.x * kSlotsTc + (g.begins ? kSlotLast : kSlotFirst)) * p.slot_rows +
                                  t * kTile + r;
@@ -1330,22 +1254,11 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1)
                             tmem_ld_wait();
                             reg_fence(o);
                             reg_fence(y);
-                            if (BITS != 0) {
-#pragma unroll
-                                for (int j = 0; j < 32; ++j) {
-                                    o[j] = o[j] * 0x1p-6f * up;
-                                    y[j] = y[j] * 0x1p-6f * up_other;
-                                }
-                            }
 #pragma unroll
                             for (int j = 0; j < 32; ++j) o[j] = fmaf(o[j], w_mine, y[j] * w_other);
                         } else {
                             tmem_ld_wait();
                             reg_fence(o);
-                            if (BITS != 0) {
-#pragma unroll
-                                for (int j = 0; j < 32; ++j) o[j] = o[j] * 0x1p-6f * up;
-                            }
                         }
                     } else {
 #pragma unroll

@@ -622,11 +622,8 @@ int kvc_pages_read_quant(const kvc_cache *cache, int32_t bits, const int32_t *ta
 
 /* kvc_attend over what the rows of such pools stand for, with its arguments and
  * guarantees; a row's NaN reaches the tokens that see it, and no others.  On the
- * tensor cores (as there: bf16, D 64 or 128) probabilities are rounded to fp16, 11
- * bits, for the product with V, and taken times the rows' steps in fp16: what a row
- * adds is then right to 2^-10 of (n + z) s where its step is above 2^-20 of the
- * list's largest and its probability above 2^-20 of the row's largest, and to 2^-30
- * of those two below. */
+ * tensor cores (as there: bf16, D 64 or 128) queries of lists of few rows are held
+ * beside their token's and head's largest element: 2^-34 of that is lost. */
 size_t kvc_attend_quant_workspace_size(const kvc_cache *cache, int32_t bits, int32_t n_q_heads, int32_t n_kv_heads,
                                        int32_t n_seqs, int32_t max_new);
 int kvc_attend_quant(const kvc_cache *cache, int32_t bits, int32_t n_q_heads, int32_t n_kv_heads, int32_t n_seqs,

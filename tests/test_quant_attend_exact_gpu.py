@@ -21,13 +21,18 @@ def _built():
     torch.cuda.set_device(0)
 
 
-# Forms of the call: one token, drafts (units of 16 and 32 rows), head sizes of every kernel.
+# Each form of the call: one token, drafts (units of 16 and 32 rows), chunks, single tokens
+# beside a chunk, head sizes of every kernel.
 FORMS = [
     dict(ns=[1, 1], lens=[700, 2300], hq=8, h=2, d=128, ps=16),
     dict(ns=[1], lens=[30000], hq=4, h=2, d=64, ps=64),
     dict(ns=[4, 3], lens=[500, 1800], hq=8, h=2, d=128, ps=32),
     dict(ns=[7, 5], lens=[1500, 300], hq=8, h=2, d=64, ps=128),
     dict(ns=[8], lens=[900], hq=8, h=2, d=128, ps=32),
+    dict(ns=[1], lens=[900], hq=64, h=1, d=128, ps=32),
+    dict(ns=[90, 200], lens=[1500, 300], hq=4, h=2, d=128, ps=64),
+    dict(ns=[150], lens=[4000], hq=6, h=2, d=64, ps=16),
+    dict(ns=[1, 70, 1], lens=[1200, 900, 40], hq=8, h=2, d=128, ps=16),
     dict(ns=[1, 3], lens=[300, 800], hq=4, h=2, d=80, ps=16),
     dict(ns=[40, 90], lens=[1000, 300], hq=4, h=2, d=96, ps=32),
 ]
@@ -65,7 +70,7 @@ def test_errors_norm(i, dtype, bits):
 
 @pytest.mark.parametrize("bits", [4, 8])
 @pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("bf16", 80), ("f32", 128)])
-@pytest.mark.parametrize("ns", [[4, 3], [8, 2]])
+@pytest.mark.parametrize("ns", [[4, 3], [8, 2], [12, 9], [70, 200]])
 def test_values_that_a_token_does_not_see_leave_no_trace(ns, dtype, d, bits):
     """The last token's own row of V is 2^40 to 2^99 times as large as the others, in one group of channels or
     in all: the tokens before it get the very bits that they get without it."""
@@ -88,7 +93,7 @@ def test_values_that_a_token_does_not_see_leave_no_trace(ns, dtype, d, bits):
 
 @pytest.mark.parametrize("bits", [4, 8])
 @pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("bf16", 80), ("f32", 128)])
-@pytest.mark.parametrize("ns", [[1, 1], [8, 5]])
+@pytest.mark.parametrize("ns", [[1, 1], [8, 5], [70, 90]])
 def test_rows_small_in_value_and_probability_keep_their_bits(ns, dtype, d, bits):
     """Channels 32 to 63 of V are 2^-30 of the others and half of the rows have 2^-25 of the others' probability (their
     values, 2^25 times as large there, decide those channels as much as the likely rows do): their outputs are as near to

@@ -490,11 +490,19 @@ int kvc_attend_quant(const kvc_cache *cache, int32_t bits, int32_t n_q_heads, in
                      int32_t max_new, int64_t n_tokens, const void *q, int64_t q_stride, const int32_t *q_start,
                      const int32_t *table, const int32_t *len, const void *k_pool, const void *v_pool, float scale,
                      void *out, float *lse, void *ws, size_t ws_bytes, cudaStream_t stream) {
+    return kvc_attend_quant_ex(cache, bits, n_q_heads, n_kv_heads, n_seqs, max_new, n_tokens, q, q_stride, q_start,
+                               table, len, k_pool, v_pool, scale, out, lse, 0, ws, ws_bytes, stream);
+}
+
+int kvc_attend_quant_ex(const kvc_cache *cache, int32_t bits, int32_t n_q_heads, int32_t n_kv_heads, int32_t n_seqs,
+                        int32_t max_new, int64_t n_tokens, const void *q, int64_t q_stride, const int32_t *q_start,
+                        const int32_t *table, const int32_t *len, const void *k_pool, const void *v_pool, float scale,
+                        void *out, float *lse, uint32_t flags, void *ws, size_t ws_bytes, cudaStream_t stream) {
     const char *fn = "kvc_attend_quant";
     NvtxRange nvtx_range(fn);
     if (!bits_ok(bits, fn)) return KVC_ERR_INVALID_ARG;
     return attend_call(fn, bits, cache, n_q_heads, n_kv_heads, n_seqs, max_new, n_tokens, q, q_stride, q_start, table,
-                       len, k_pool, v_pool, scale, out, lse, 0, ws, ws_bytes, stream);
+                       len, k_pool, v_pool, scale, out, lse, flags, ws, ws_bytes, stream);
 }
 
 }  // extern "C"

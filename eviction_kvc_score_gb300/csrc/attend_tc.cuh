@@ -67,8 +67,8 @@
 // What bounds them: the chain S -> softmax -> P V, whose softmax shares its issue slots
 // with the writing of the tiles.  A step of two halves takes 6,200 clocks where its MMAs
 // take 3,072.  4,096 tokens x 32 heads over 32,768 rows in 4 bits: 2.40 ms, 860 TFLOP/s
-// (rows in bf16: 2.01 ms; without the MMAs of the second term 2.28); six chunks of 1-700
-// tokens over up to 5,700 rows in 8 bits 240 us, 437 TFLOP/s.  Warps 12-19 and not the
+// (rows in bf16: 2.01 ms); six chunks of 1-700 tokens over up to 5,700 rows in 8 bits 238
+// us, 441 TFLOP/s; one term of P, 1.81 ms and 200 us.  Warps 12-19 and not the
 // softmax's own: a step's tiles would then stand between its softmaxes.
 #pragma once
 
@@ -1106,7 +1106,8 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1)
                     auto weigh = [&](int q, float(&y)[32], auto scaled) {
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            uint32_t pw[8], lo[8];
+                            uint32_t pw[8];
+                            [[maybe_unused]] uint32_t lo[8];
 #pragma unroll
                             for (int j = 0; j < 8; ++j) {
                                 float y0 = y[16 * h + 2 * j], y1 = y[16 * h + 2 * j + 1];
@@ -1122,17 +1123,21 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1)
                                 const float p0 = ex2(y0), p1 = ex2(y1);
                                 const unsigned long long pp = f2_pack(p0, p1);
                                 sum2[j & 1] = f2_add(sum2[j & 1], pp);
-                                // the upper 16 bits, and what is left of the rest
-                                const uint32_t b0 = __float_as_uint(p0), b1 = __float_as_uint(p1);
-                                pw[j] = __byte_perm(b0, b1, 0x7632);
-                                float r0, r1;
-                                f2_unpack(f2_add(pp, f2_pack(-__uint_as_float(b0 & 0xffff0000u), -__uint_as_float(b1 & 0xffff0000u))), r0, r1);
-                                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(lo[j]) : "f"(r1), "f"(r0));
+                                if constexpr (TWO) {
+                                    // the upper 16 bits, and what is left of the rest
+                                    const uint32_t b0 = __float_as_uint(p0), b1 = __float_as_uint(p1);
+                                    pw[j] = __byte_perm(b0, b1, 0x7632);
+                                    float r0, r1;
+                                    f2_unpack(f2_add(pp, f2_pack(-__uint_as_float(b0 & 0xffff0000u), -__uint_as_float(b1 & 0xffff0000u))), r0, r1);
+                                    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(lo[j]) : "f"(r1), "f"(r0));
+                                } else {
+                                    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(pw[j]) : "f"(p1), "f"(p0));
+                                }
                             }
                             // over logits that are in registers or read for the last time
                             const uint32_t to = cs + (q < 2 ? 0 : 32) + 16 * q + 8 * h;
                             tmem_st8(to, pw);
-                            tmem_st8(to + 32, lo);
+                            if constexpr (TWO) tmem_st8(to + 32, lo);
                         }
                     };
                     auto handed = [&](int h) {

@@ -631,6 +631,14 @@ int kvc_attend_quant(const kvc_cache *cache, int32_t bits, int32_t n_q_heads, in
                      const int32_t *table, const int32_t *len, const void *k_pool, const void *v_pool, float scale,
                      void *out, float *lse, void *ws, size_t ws_bytes, cudaStream_t stream);
 
+/* kvc_attend_quant with kvc_attend_ex's flags.  Where no sequence may have more than 32
+ * rows (max_new times the query heads of a KV head), nothing changes with
+ * KVC_ATTEND_BF16_P. */
+int kvc_attend_quant_ex(const kvc_cache *cache, int32_t bits, int32_t n_q_heads, int32_t n_kv_heads, int32_t n_seqs,
+                        int32_t max_new, int64_t n_tokens, const void *q, int64_t q_stride, const int32_t *q_start,
+                        const int32_t *table, const int32_t *len, const void *k_pool, const void *v_pool, float scale,
+                        void *out, float *lse, uint32_t flags, void *ws, size_t ws_bytes, cudaStream_t stream);
+
 const char *kvc_status_string(int status);
 
 /* Message for the last error returned on the calling thread ("" if none). */

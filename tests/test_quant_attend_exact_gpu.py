@@ -110,3 +110,26 @@ def test_rows_small_in_value_and_probability_keep_their_bits(ns, dtype, d, bits)
     torch.cuda.synchronize()
     want = ref.attend(c.q, c.start, c.k, c.v, c.scale, bits)["out"]
     assert ref.near(c.out[..., 32:64], want[..., 32:64], logit=8.64) is None
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("bf16", 80), ("f32", 64)])
+@pytest.mark.parametrize("ns", [[1, 3], [200, 60]])
+def test_one_bf16_probability_is_the_callers_choice(dtype, d, ns, bits):
+    """In tcgen05's kernel 2^-8 of a probability may be lost then; in the others nothing changes."""
+    c = Case(ns=ns, lens=[700, 300], hq=4, h=2, d=d, ps=32, dtype=dtype, bits=bits, seed=d)
+    c.run()
+    out, lse = c.out.clone(), c.lse.clone()
+    c.out.fill_(7)
+    K().kvc_attend_quant_ex(c.c, bits, c.q, c.q_start, c.table, c.len, c.kp, c.vp, c.max_new, c.out, K().ATTEND_BF16_P, c.ws,
+                            lse=c.lse, scale=c.scale)
+    torch.cuda.synchronize()
+    one = dtype == "bf16" and d != 80 and ns[0] > 16
+    assert torch.equal(c.lse, lse) and torch.equal(c.out, out) != one
+    if one:
+        r = ref.attend(c.q, c.start, c.k, c.v, c.scale, bits)
+        # both sums' weights move by the logits' error (as in Case.check); p is rounded to nearest, the output once more
+        dx = (2 * (d + 18) * r["logit_w"] + 2.0 ** 3) * 2.0 ** -24
+        tol = (2 * dx[..., None] + 2.0 ** -9 + 2.0 ** -14) * r["reach"] + 2.0 ** -9 * r["out"].abs() * 1.01
+        assert ((c.out.double() - r["out"]).abs() <= tol).all()
+        assert (c.out.double() - r["out"]).norm() > 1.1 * (out.double() - r["out"]).norm()

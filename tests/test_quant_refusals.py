@@ -115,3 +115,11 @@ def test_binding_refuses_wrong_tensors(kvc):
                  lambda: kvc.kvc_attend_quant(c, 4, x.view(9, 1, 64), torch.tensor([0, 9], dtype=torch.int32), table, i, pool, pool, 9, x, pool)):
         with pytest.raises(ValueError):    # tensors of the host
             call()
+
+
+@pytest.mark.parametrize("flags", [2, 3, 1 << 31])
+def test_attend_refuses_unknown_flags(kvc, flags):
+    c = cache(kvc)
+    assert kvc._lib.kvc_attend_quant_ex(C.byref(c), 4, 8, 2, 1, 1, 4, FAKE, 512, FAKE, FAKE, FAKE, FAKE, FAKE, 0.1, FAKE, NUL, flags, FAKE,
+                                        BIG, NUL) == -1
+    assert "flags" in kvc.kvc_last_error() and "kvc_attend_quant" in kvc.kvc_last_error()

@@ -278,6 +278,8 @@ __global__ void __launch_bounds__(kThreads, per_sm_of(G, NT)) attend_quant_kerne
         float qs[NT][G][2];   // of the lane's two columns: the group's sum
         float factor[NT][2];  // logit in log2 units of a sum
         int sees[NT][2];
+        float mul[NT];        // the lane's row's
+        bool far = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             uint4 x[G];
@@ -316,16 +318,24 @@ __global__ void __launch_bounds__(kThreads, per_sm_of(G, NT)) attend_quant_kerne
                 sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
                 sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 2);
             }
-            const float mul = p.scale_log2 * 0x1p20f * pow2(-f);   // codes times q are at 2^-20
+            mul[nt] = p.scale_log2 * pow2(-f);
+            far |= !isfinite(mul[nt] * 0x1p20f);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int from = (2 * c + e) * 4, row = 8 * nt + 2 * c + e;
-                factor[nt][e] = __shfl_sync(0xffffffffu, mul, from);
 #pragma unroll
                 for (int g = 0; g < G; ++g) qs[nt][g][e] = __shfl_sync(0xffffffffu, sum[g], from) * 0x1p-20f;
                 sees[nt][e] = row < a.rows ? attend_sees(p, a, row) : 0;
             }
         }
+        // codes times q are at 2^-20, which the factor takes back; that of queries of 2^120
+        // would not be a number, so K's steps do
+        const float up = __any_sync(0xffffffffu, far) ? 0x1p20f : 1.f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                factor[nt][e] = __shfl_sync(0xffffffffu, mul[nt] * (up == 1.f ? 0x1p20f : 1.f), (2 * c + e) * 4);
         const int sees0 = attend_sees(p, a, 0);   // the fewest
 
         float m[NT][2], l[NT][2], o[NT][2 * G][4];
@@ -384,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, per_sm_of(G, NT)) attend_quant_kerne
                     z16[0] = (uint16_t)vz;
                     z16[2] = (uint16_t)(vz >> 16);
                     // zero codes as 1 + z / 16 or 1 + z / 256, for want of a cheap conversion
-                    const float s0 = quant_step<BITS>(kw[i] & 0xffffu), s1 = quant_step<BITS>(kw[i] >> 16);
+                    const float s0 = quant_step<BITS>(kw[i] & 0xffffu) * up, s1 = quant_step<BITS>(kw[i] >> 16) * up;
                     float z0, z1;
                     if (BITS == 4) {
                         z0 = fmaf(__uint_as_float((kw[i] << 19 & 0x00780000u) | 0x3f800000u), -16.f, 16.f);

@@ -623,7 +623,8 @@ int kvc_pages_read_quant(const kvc_cache *cache, int32_t bits, const int32_t *ta
 /* kvc_attend over what the rows of such pools stand for, with its arguments and
  * guarantees; a row's NaN reaches the tokens that see it, and no others.  On the
  * tensor cores (as there: bf16, D 64 or 128) queries of lists of few rows are held
- * beside their token's and head's largest element: 2^-34 of that is lost. */
+ * beside their token's and head's largest element: 2^-34 of that is lost.  fp32
+ * queries may lose what is below 2^-133. */
 size_t kvc_attend_quant_workspace_size(const kvc_cache *cache, int32_t bits, int32_t n_q_heads, int32_t n_kv_heads,
                                        int32_t n_seqs, int32_t max_new);
 int kvc_attend_quant(const kvc_cache *cache, int32_t bits, int32_t n_q_heads, int32_t n_kv_heads, int32_t n_seqs,

@@ -133,3 +133,32 @@ def test_one_bf16_probability_is_the_callers_choice(dtype, d, ns, bits):
         tol = (2 * dx[..., None] + 2.0 ** -9 + 2.0 ** -14) * r["reach"] + 2.0 ** -9 * r["out"].abs() * 1.01
         assert ((c.out.double() - r["out"]).abs() <= tol).all()
         assert (c.out.double() - r["out"]).norm() > 1.1 * (out.double() - r["out"]).norm()
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("bf16", 96), ("f32", 64)])
+@pytest.mark.parametrize("ns", [[1, 1], [6, 4], [70, 40]])
+def test_largest_and_smallest_queries(ns, dtype, d, bits):
+    """Queries of 2^123 over keys that are 2^-123 of the usual ones or nothing, and the other way round:
+    logits are ordinary numbers, and 0 of a row of zeros."""
+    tiny = -123 if dtype == "bf16" else -100    # three bf16 pieces end at 2^-133
+    for big, small in ((2.0 ** 123, 2.0 ** -123), (2.0 ** tiny, 2.0 ** (-3 - tiny))):
+        def change(k, v):
+            for x in k:
+                x.mul_(small)
+                x[3::7] = 0
+        c = Case(ns=ns, lens=[300, 170], hq=4, h=2, d=d, ps=16, dtype=dtype, bits=bits, change=change)
+        c.q.mul_(big)
+        assert c.q.isfinite().all() and all(x.isfinite().all() for x in c.k)
+        c.run().check()
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n,power", [(1, 121), (6, 121)])
+def test_huge_queries_over_ordinary_keys(n, d, bits, power):
+    """Logits of 2^120 and more: one row has all of the weight."""
+    c = Case(ns=[n], lens=[300], hq=4, h=2, d=d, ps=16, dtype="bf16", bits=bits)
+    c.q.mul_(2.0 ** power)
+    assert c.q.isfinite().all()
+    c.run().check()

@@ -90,13 +90,14 @@ namespace {
 // the loading and issuing warpgroup to the two that hold a row of 128 logits
 // per thread.  256 x 208 + 128 x 88 = 384 x 168: the launch checks the 168,
 // because an increase beyond what the block was launched with never returns.
-// With two warpgroups more: 256 x 144 + 128 x 64 + 256 x 64 = 640 x 96 (with 128 and 80
-// the second term spills twice as much: a long chunk takes 2.48 ms, and 2.40 so).
+// With two warpgroups more: 256 x 152 + 128 x 64 + 256 x 56 = 640 x 96 (of what the
+// softmax and the tiles share, 128 and 80 let the second term spill: a long chunk took
+// 2.48 ms; 144 and 64 2.40, so 2.37).
 template <int BITS>
 struct Shape {
     static constexpr int kThreads = BITS == 0 ? 384 : 640;
-    static constexpr int kRegsLaunch = BITS == 0 ? 168 : 96, kRegsSoftmax = BITS == 0 ? 208 : 144;
-    static constexpr int kRegsOther = BITS == 0 ? 88 : 64, kRegsTiles = BITS == 0 ? 0 : 64;
+    static constexpr int kRegsLaunch = BITS == 0 ? 168 : 96, kRegsSoftmax = BITS == 0 ? 208 : 152;
+    static constexpr int kRegsOther = BITS == 0 ? 88 : 64, kRegsTiles = BITS == 0 ? 0 : 56;
     static_assert(256 * kRegsSoftmax + 128 * kRegsOther + 256 * kRegsTiles <= kThreads * kRegsLaunch, "register split");
     static constexpr int kReaders = BITS == 0 ? 12 : 20;   // warps that read the queue
 };
@@ -888,7 +889,7 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1)
             const bool real = r < R && rt < a.rows;
             const bool any = __any_sync(0xffffffffu, real);
             const int sees = real ? attend_sees(p, a, rt) : 0;
-            const int sees0 = attend_sees(p, a, g.split ? 0 : t * R);   // the tile's first row's
+            int sees0 = attend_sees(p, a, g.split ? 0 : t * R);   // the tile's first row's
             const int from = attend_sees(p, a, 0);                      // the unit's
             float m = -INFINITY, l = 0.f;
             const int cnt = g.cnt[t];
@@ -939,7 +940,10 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1)
                 }
                 // slow: some row of the tile sees only part of it, or the scale is
                 // not positive; two copies, because a select per logit costs as much
-                // as the rest
+                // as the rest.  The other way takes S c - m in one step, which is 2^-24 of m
+                // off the product m: a row whose m would be beyond 2^24 goes the slow way, where
+                // S c is rounded as m was, and the other returns without having done anything.
+                auto far = [&](float top) { return __any_sync(0xffffffffu, sees > 0 && fabsf(top) > 0x1p24f); };
                 auto soften = [&](auto slow) {
                     constexpr bool kSlow = decltype(slow)::value;
                     unsigned long long mul2 = c2;
@@ -980,11 +984,12 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1)
                     }
                     const float s_top = fmaxf(fmax3(x[0], x[1], x[2]), x[3]);
                     const float top = s_top * mul;
-                    if (i == 0) {
-                        m = top;
-                    } else {
-                        const bool grow = top > m + kGrow;
-                        if (__any_sync(0xffffffffu, grow)) {
+                    const bool grow = top > m + kGrow;
+                    if (i == 0 || __any_sync(0xffffffffu, grow)) {
+                        if (!kSlow && far(top)) return false;
+                        if (i == 0) {
+                            m = top;
+                        } else {
                             // every product of this half up to the tile before is done: S came after it
                             const float down = grow ? ex2(m - top) : 1.f;
                             if (grow) m = top;
@@ -1045,6 +1050,7 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1)
                     float s0, s1;
                     f2_unpack(f2_add(sum2[0], sum2[1]), s0, s1);
                     l += s0 + s1;
+                    return true;
                 };
                 // held rows: 64 logits at a time for want of registers.  The maximum of
                 // keys 0-63, that of keys 64-127, whose probabilities come first, and then
@@ -1076,11 +1082,12 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1)
                         }
                     }
                     const float top = fmaxf(fmax3(x[0], x[1], x[2]), x[3]) * (kSlow ? 1.f : c);
-                    if (i == 0) {
-                        m = top;
-                    } else {
-                        const bool grow = top > m + kGrow;
-                        if (__any_sync(0xffffffffu, grow)) {
+                    const bool grow = top > m + kGrow;
+                    if (i == 0 || __any_sync(0xffffffffu, grow)) {
+                        if (!kSlow && far(top)) return false;
+                        if (i == 0) {
+                            m = top;
+                        } else {
                             const float down = grow ? ex2(m - top) : 1.f;
                             if (grow) m = top;
                             l *= down;
@@ -1160,18 +1167,22 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1)
                     float s0, s1;
                     f2_unpack(f2_add(sum2[0], sum2[1]), s0, s1);
                     l += s0 + s1;
+                    return true;
                 };
                 if (any) {
+                    bool slow = edge || !plain;
                     if constexpr (BITS != 0) {
-                        if (edge || !plain)
-                            soften_held(std::true_type{});
-                        else
-                            soften_held(std::false_type{});
+                        if (!slow && !soften_held(std::false_type{})) {
+                            slow = true;
+                            sees0 = 0;   // and the tiles behind it
+                        }
+                        if (slow) soften_held(std::true_type{});
                     } else {
-                        if (edge || !plain)
-                            soften(std::true_type{});
-                        else
-                            soften(std::false_type{});
+                        if (!slow && !soften(std::false_type{})) {
+                            slow = true;
+                            sees0 = 0;
+                        }
+                        if (slow) soften(std::true_type{});
                     }
                 } else if (lane == 0) {
                     mbar_arrive(&b.p_full[t][0]);

@@ -224,3 +224,14 @@ def test_ranges_of_tokens_are_cut_as_described(dtype, d, most, starts):
         ok[a:b] = near
         claims[guard + a:guard + b] += 1
     assert bool(ok[claims[guard:-guard] == 1].all()) and (out[claims == 0] == 7).all() and (lse[claims == 0] == 7).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n,power", [(1, 24), (1, 40), (1, 117), (300, 28), (300, 40), (300, 117)])
+def test_huge_logits(n, d, power):
+    """One row has all of the weight: logits beyond 2^24, where product and difference in one step are not the
+    difference of the rounded product."""
+    c = Case(ns=[n], lens=[1000 + n], hq=4, h=2, d=d, ps=16, dtype="bf16", seed=d + n)
+    c.q.mul_(2.0 ** power)
+    assert c.q.isfinite().all()
+    c.run().check()

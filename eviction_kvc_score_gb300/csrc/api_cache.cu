@@ -183,12 +183,12 @@ int attend_call(const char *fn, int bits, const kvc_cache *cache, int32_t n_q_he
         // 189; heads of 64, 64 x 8 lists, 32 rows: 114 and 184, in 8 bits 118 and 181; one
         // sequence of 1,000: 11 and 20).  48 rows would be three units of 16, 300 and 290.
         // Where chunks are among them, a token's rows go in a launch of their own as in
-        // launch_attend_simt.
+        // launch_attend_simt, unless a token has more.
         const int few = attend_quant_rows();
         const int64_t most = (int64_t)max_new * p.group;
         if (most <= few) return launch_attend_quant(p, (int)most, w.needs.grid, stream);
         const int own = p.group <= 8 ? 8 : p.group <= 16 ? 16 : 32;
-        const bool both = own <= few && n_tokens * p.group <= 128 * (int64_t)n_seqs;
+        const bool both = p.group <= few && n_tokens * p.group <= 128 * (int64_t)n_seqs;
         if (both) {
             const int rc = launch_attend_quant(p, own, w.needs.grid, stream);
             if (rc) return rc;

@@ -536,6 +536,8 @@ inline bool attend_units(AttendParams &p, int unit_rows, int rows_above, int row
     p.by_quads = Divider((uint32_t)p.dim / 4);
     return n < INT_MAX;
 }
+// The call that a launch's messages name.
+inline const char *attend_name(const AttendParams &p) { return p.bits != 0 ? "kvc_attend_quant" : "kvc_attend"; }
 // All set the units' shape.
 int launch_attend_simt(AttendParams &p, bool f32, int grid, cudaStream_t st);
 int launch_attend_simt_quant4(AttendParams &p, bool f32, int grid, cudaStream_t st);

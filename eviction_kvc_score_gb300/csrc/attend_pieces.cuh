@@ -368,7 +368,7 @@ int launch_pieces_of(AttendParams &p, int sms, cudaStream_t st) {
     // as many blocks as an SM holds at once (1 KB of shared memory is each block's own cost)
     const int per_sm = std::max(1, std::min(piece_blocks(KS), (int)(233472 / (bytes + 1024))));
     launch_early(kernel, per_sm * sms, kPieceThreads, bytes, st, p);
-    return cache_launched("kvc_attend");
+    return cache_launched(attend_name(p));
 }
 
 template <typename T, int BITS>

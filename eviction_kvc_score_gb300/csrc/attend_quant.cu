@@ -720,7 +720,7 @@ int launch(AttendParams &p, int sms, cudaStream_t st) {
     // as many blocks as an SM holds at once (1 KB of shared memory is each block's own cost)
     const int per_sm = std::max(1, std::min(per_sm_of(G, NT), (int)(233472 / (bytes + 1024))));
     launch_early(attend_quant_kernel<G, BITS, NT>, per_sm * sms, kThreads, bytes, st, p);
-    return cache_launched("kvc_attend_quant");
+    return cache_launched(attend_name(p));
 }
 
 template <int G, int BITS>
@@ -747,7 +747,7 @@ int launch_attend_quant(AttendParams &p, int rows, int sms, cudaStream_t st) {
     // (two units of 16 rows for up to 32 of a head of 128, whose sums take the registers)
     const int unit = rows <= 8 ? 8 : rows <= 16 || p.dim == 128 ? 16 : 32;
     if (!attend_units(own, unit, 0, rows <= unit ? unit : 2 * unit)) {
-        set_error("kvc_attend_quant: n_seqs * n_kv_heads * max_new is too large");
+        set_error("%s: n_seqs * n_kv_heads * max_new is too large", attend_name(p));
         return KVC_ERR_UNSUPPORTED;
     }
     if (p.bits == 4) return p.dim == 64 ? launch_rows<2, 4>(own, unit, sms, st) : launch_rows<4, 4>(own, unit, sms, st);

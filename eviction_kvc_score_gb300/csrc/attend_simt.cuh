@@ -432,7 +432,7 @@ int launch(AttendParams &p, int sms, cudaStream_t st) {
     // as many blocks as an SM holds at once (1 KB of shared memory is each block's own cost)
     const int per_sm = std::max(1, std::min(ROWS == 64 ? 2 : 4, (int)(233472 / (bytes + 1024))));
     launch_early(kernel, per_sm * sms, threads_of(ROWS), bytes, st, p);
-    return cache_launched("kvc_attend");
+    return cache_launched(attend_name(p));
 }
 
 template <typename T, int BITS>
@@ -469,7 +469,7 @@ int launch_all(AttendParams &p, bool f32, int grid, cudaStream_t st) {
         const bool large = rows == 64;
         p.extra = large ? piece_extra<BITS>() : 0;
         if (!attend_units(p, rows, large && both ? 16 : 0, large ? INT_MAX : 16)) {
-            set_error("kvc_attend: n_seqs * n_kv_heads * max_new is too large");
+            set_error("%s: n_seqs * n_kv_heads * max_new is too large", attend_name(p));
             return KVC_ERR_UNSUPPORTED;
         }
         const int rc = f32 ? launch_type<float, BITS>(p, rows, sms, st)

@@ -1450,7 +1450,7 @@ int launch(AttendParams &p, int grid, cudaStream_t st) {
     if (!make_q_map(&tq, p.q, dims, strides, box) ||
         (BITS == 0 && (!make_tma_map(&tk, p.k_pool, D, ps, (uint64_t)p.n_pages, (uint32_t)ps) ||
                        !make_tma_map(&tv, p.v_pool, D, ps, (uint64_t)p.n_pages, (uint32_t)ps)))) {
-        set_error("kvc_attend: cuTensorMapEncodeTiled failed (alignment or driver)");
+        set_error("%s: cuTensorMapEncodeTiled failed (alignment or driver)", attend_name(p));
         return KVC_ERR_CUDA;
     }
     constexpr size_t bytes = smem_bytes<KH, BITS>();
@@ -1464,18 +1464,18 @@ int launch(AttendParams &p, int grid, cudaStream_t st) {
     });
     if (err != cudaSuccess) {
         cudaGetLastError();
-        set_error("kvc_attend: the tensor-core kernel's attributes: %s", cudaGetErrorString(err));
+        set_error("%s: the tensor-core kernel's attributes: %s", attend_name(p), cudaGetErrorString(err));
         return KVC_ERR_CUDA;
     }
     // (of a library built by the compiler it was measured with, these are 168 or 96)
     if (regs != Shape<BITS>::kRegsLaunch) {
-        set_error("kvc_attend: the tensor-core kernel has %d registers per thread, its split needs %d", regs,
+        set_error("%s: the tensor-core kernel has %d registers per thread, its split needs %d", attend_name(p), regs,
                   Shape<BITS>::kRegsLaunch);
         return KVC_ERR_UNSUPPORTED;
     }
     allow_shared<attend_tc_kernel<KH, TWO, BITS>>((int)bytes);
     launch_early(attend_tc_kernel<KH, TWO, BITS>, grid, Shape<BITS>::kThreads, bytes, st, tq, tk, tv, p);
-    return cache_launched("kvc_attend");
+    return cache_launched(attend_name(p));
 }
 
 // The units' shape for lists of more than rows_above rows; false if there are too many.
@@ -1487,7 +1487,7 @@ bool shape_units(AttendParams &p, int rows_above) {
     p.step_keys = kTile;
     p.extra = p.bits != 0 && p.dim == 128 ? kExtraHeld : kExtra;
     if (attend_units(p, 2 * R, rows_above, INT_MAX)) return true;
-    set_error("kvc_attend: n_seqs * n_kv_heads * max_new is too large");
+    set_error("%s: n_seqs * n_kv_heads * max_new is too large", attend_name(p));
     return false;
 }
 

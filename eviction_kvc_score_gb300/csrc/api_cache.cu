@@ -189,11 +189,9 @@ int attend_call(const char *fn, int bits, const kvc_cache *cache, int32_t n_q_he
         if (most <= few) return launch_attend_quant(p, (int)most, w.needs.grid, stream);
         const int own = p.group <= 8 ? 8 : p.group <= 16 ? 16 : 32;
         const bool both = p.group <= few && n_tokens * p.group <= 128 * (int64_t)n_seqs;
-        if (both) {
-            const int rc = launch_attend_quant(p, own, w.needs.grid, stream);
-            if (rc) return rc;
-        }
-        return launch_attend_tc_quant(p, both ? own : 0, w.needs.grid, stream);
+        // (the one that may be refused comes first: then nothing has been written)
+        const int rc = launch_attend_tc_quant(p, both ? own : 0, w.needs.grid, stream);
+        return rc || !both ? rc : launch_attend_quant(p, own, w.needs.grid, stream);
     }
     if (bits != 0)
         return bits == 4 ? launch_attend_simt_quant4(p, f32, w.needs.grid, stream)

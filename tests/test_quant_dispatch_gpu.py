@@ -81,3 +81,13 @@ def test_refused_launches_name_the_call(dtype, d):
             m.quant(bits)
     with pytest.raises(K().KvcError, match="kvc_attend: n_seqs . n_kv_heads . max_new is too large"):
         m.plain()
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("bf16", 80), ("f32", 64)])
+def test_refused_launches_write_nothing(dtype, d):
+    m = Many(dtype, d, 8, 1 << 22)
+    for bits in (4, 8):
+        with pytest.raises(K().KvcError):
+            m.quant(bits)
+    torch.cuda.synchronize()
+    assert (m.out == 7).all()

@@ -131,6 +131,13 @@ __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t 
     asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
     return r;
 }
+// What (hi + lo) s has beside `product`, the rounded hi s: with 8 bits s is a power of two
+// and hi s is exact.
+template <int BITS>
+__device__ __forceinline__ uint32_t rest_of(uint32_t hi, uint32_t lo, uint32_t s, uint32_t product) {
+    if (BITS == 8) return mul_bf16x2(lo, s);
+    return fma_bf16x2(lo, s, fma_bf16x2(hi, s, product ^ 0x80008000u));
+}
 __device__ __forceinline__ float2 unpack_f16(uint32_t x) {
     float2 r;
     asm("{\n\t.reg .f16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}" : "=f"(r.x), "=f"(r.y) : "r"(x));
@@ -582,8 +589,8 @@ __global__ void __launch_bounds__(kThreads, per_sm_of(G, NT)) attend_quant_kerne
                     for (int nt = 0; nt < NT; ++nt) {
                         // p s in two terms: what the first one's rounding leaves is exact
                         const uint32_t b0 = mul_bf16x2(pt[b][nt][0], st[0][g]), b1 = mul_bf16x2(pt[b][nt][1], st[1][g]);
-                        const uint32_t c0 = fma_bf16x2(pl[b][nt][0], st[0][g], fma_bf16x2(pt[b][nt][0], st[0][g], b0 ^ 0x80008000u));
-                        const uint32_t c1 = fma_bf16x2(pl[b][nt][1], st[1][g], fma_bf16x2(pt[b][nt][1], st[1][g], b1 ^ 0x80008000u));
+                        const uint32_t c0 = rest_of<BITS>(pt[b][nt][0], pl[b][nt][0], st[0][g], b0);
+                        const uint32_t c1 = rest_of<BITS>(pt[b][nt][1], pl[b][nt][1], st[1][g], b1);
                         mma16816_bf16(o[nt][2 * g], a0, b0, b1);
                         mma16816_bf16(o[nt][2 * g], a0, c0, c1);
                         mma16816_bf16(o[nt][2 * g + 1], a1, b0, b1);

@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, per_sm_of(G, NT)) attend_quant_kerne
             }
         }
         // codes times q are at 2^-20, which the factor takes back; that of queries of 2^120
-        // would not be a number, so K's steps do
+        // would not be a number, so logits and m stay 2^-20 of what they are until the exponentials
         const float up = __any_sync(0xffffffffu, far) ? 0x1p20f : 1.f;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, per_sm_of(G, NT)) attend_quant_kerne
                     z16[0] = (uint16_t)vz;
                     z16[2] = (uint16_t)(vz >> 16);
                     // zero codes as 1 + z / 16 or 1 + z / 256, for want of a cheap conversion
-                    const float s0 = quant_step<BITS>(kw[i] & 0xffffu) * up, s1 = quant_step<BITS>(kw[i] >> 16) * up;
+                    const float s0 = quant_step<BITS>(kw[i] & 0xffffu), s1 = quant_step<BITS>(kw[i] >> 16);
                     float z0, z1;
                     if (BITS == 4) {
                         z0 = fmaf(__uint_as_float((kw[i] << 19 & 0x00780000u) | 0x3f800000u), -16.f, 16.f);
@@ -488,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, per_sm_of(G, NT)) attend_quant_kerne
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     top[nt][e] = fmaxf(fmaxf(x[0][nt][e], x[0][nt][2 + e]), fmaxf(x[1][nt][e], x[1][nt][2 + e]));
-                    grow |= top[nt][e] > m[nt][e] + kLag;
+                    grow |= fmaf(top[nt][e] - m[nt][e], up, -kLag) > 0.f;
                 }
             if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
@@ -499,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, per_sm_of(G, NT)) attend_quant_kerne
 #pragma unroll
                         for (int d = 4; d <= 16; d <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
                         y = fmaxf(y, m[nt][e]);
-                        const float down = y == -INFINITY ? 1.f : ex2(m[nt][e] - y);
+                        const float down = y == -INFINITY ? 1.f : ex2((m[nt][e] - y) * up);
                         m[nt][e] = y;
                         l[nt][e] *= down;
 #pragma unroll
@@ -512,12 +512,12 @@ __global__ void __launch_bounds__(kThreads, per_sm_of(G, NT)) attend_quant_kerne
             uint32_t pt[2][NT][2], pl[2][NT][2];   // P in two terms, keys the inner dimension: [block][..][keys 0-7, 8-15]
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const float n0 = kTop - (m[nt][0] == -INFINITY ? 0.f : m[nt][0]), n1 = kTop - (m[nt][1] == -INFINITY ? 0.f : m[nt][1]);
+                const float n0 = m[nt][0] == -INFINITY ? kTop : fmaf(-m[nt][0], up, kTop), n1 = m[nt][1] == -INFINITY ? kTop : fmaf(-m[nt][1], up, kTop);
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const float p0 = ex2(x[b][nt][2 * h] + n0), p1 = ex2(x[b][nt][2 * h + 1] + n1);
+                        const float p0 = ex2(fmaf(x[b][nt][2 * h], up, n0)), p1 = ex2(fmaf(x[b][nt][2 * h + 1], up, n1));
                         l[nt][0] += p0;
                         l[nt][1] += p1;
                         const uint32_t hi = pack_bf16(p0, p1);
@@ -640,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, per_sm_of(G, NT)) attend_quant_kerne
                 float sum = l[nt][e];
 #pragma unroll
                 for (int d = 4; d <= 16; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-                if (r8 == 0) s.stat[warp][2 * c + e] = make_float2(m[nt][e], sum * 0x1p-20f);
+                if (r8 == 0) s.stat[warp][2 * c + e] = make_float2(m[nt][e] * up, sum * 0x1p-20f);
                 float *dst = s_out + (warp * 8 + 2 * c + e) * kOutRow;
 #pragma unroll
                 for (int g = 0; g < G; ++g) {

@@ -163,3 +163,26 @@ def test_huge_queries_over_ordinary_keys(n, d, bits, power):
     c.q.mul_(2.0 ** power)
     assert c.q.isfinite().all()
     c.run().check()
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("d,n", [(128, 1), (64, 3), (128, 4)])
+@pytest.mark.parametrize("odd", [2.0 ** 124, math.inf, math.nan])
+def test_huge_queries_leave_the_others_alone(odd, d, n, bits):
+    """Rows beside a query that is huge or no number get the very bits that they get beside an ordinary one, also over
+    keys of 2^110."""
+    for size in (1.0, 2.0 ** 110):
+        def change(k, v):
+            for x in k:
+                x.mul_(size)
+        c = Case(ns=[n], lens=[300], hq=8, h=2, d=d, ps=16, dtype="bf16", bits=bits, change=change)
+        if size > 1:
+            c.q.mul_(2.0 ** -108)
+        c.run().check()
+        out, lse = c.out.clone(), c.lse.clone()
+        c.q[0, 2, 5] = odd
+        c.run()
+        torch.cuda.synchronize()
+        others = torch.ones(c.lse.shape, dtype=torch.bool)
+        others[0, 2] = False
+        assert torch.equal(c.out[others], out[others]) and torch.equal(c.lse[others], lse[others])

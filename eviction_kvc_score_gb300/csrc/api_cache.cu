@@ -178,10 +178,11 @@ int attend_call(const char *fn, int bits, const kvc_cache *cache, int32_t n_q_he
     if (bits != 0 && w.tc) {
         // Lists of few rows are attend_quant.cu's: a tile of tcgen05's is 128 rows whoever
         // fills them, and its keys are written out as bf16 first (us here and there; 64 x 8
-        // lists of 500-6,000 rows of 128 in 4 bits: 4 rows a list 77 and 282, 16 rows 109
-        // and 286, 32 rows 201 and 289; 32 x 8 in 8 bits: 56 and 180, 73 and 184, 127 and
-        // 189; heads of 64, 64 x 8 lists, 32 rows: 114 and 184, in 8 bits 118 and 181; one
-        // sequence of 1,000: 11 and 20).  48 rows would be three units of 16, 300 and 290.
+        // lists of 500-6,000 rows of 128 in 4 bits: 4 rows a list 82 and 299, 16 rows 120
+        // and 301, 32 rows 225 and 308; 32 x 8 in 8 bits: 58 and 198, 75 and 202, 130 and
+        // 214; heads of 64, 64 x 8 lists, 32 rows: 126 and 199, in 8 bits 128 and 207; one
+        // sequence of 1,000: 12 and 19).  48 rows would be three units of 16, where two take
+        // 225, and are 317 there.
         // Where chunks are among them, a token's rows go in a launch of their own as in
         // launch_attend_simt, unless a token has more.
         const int few = attend_quant_rows();

@@ -19,7 +19,7 @@
 // What a row's probability times the group's step is rounded to is two bf16 numbers,
 // 2^-17 of it away at most, as the tensor cores' other kernels have it.  (One fp16 number
 // instead, steps over the list's largest and the zero codes' share in a product of its own:
-// 7% faster, but 7 to 17% of the outputs were not the nearest number, and what one row
+// 7-9% less time, but 7 to 17% of the outputs were not the nearest number, and what one row
 // held far above the others, seen or not, took their bits.)
 //
 // Fragments: the product of K has 16 keys as its rows and 8 of the list's rows as
@@ -38,14 +38,15 @@
 //
 // What bounds it, measured on one GB300 (measured copy rate 6,776 GB/s):
 // - 8 bits: reading the cache, once lists are long.  32 sequences x 8 KV heads over
-//   4,000-48,000 rows: 288 us, 6.3 TB/s, 92%; over 500-6,000: 54 us, 4.2 TB/s, the rest
+//   4,000-48,000 rows: 315 us, 5.7 TB/s, 85%; over 500-6,000: 57-58 us, 3.9 TB/s, the rest
 //   of which is about 20 us of plan (7), first loads (6) and joining at lists' ends.
-// - 4 bits: instructions, about 940 per 32 keys, warp and 128 channels (K 200, V 175,
-//   steps and zero codes 140, the softmax and the loads the rest).  64 x 8 lists of
-//   500-6,000: 76 us, 3.2 TB/s, 47%; of 4,000-48,000: 460 us, 4.2 TB/s.
-// - 17 to 32 rows: instructions and the latency between the products; registers leave 8
-//   warps to an SM.  3 x 4 lists of 60,000-131,000 rows, 28 rows, heads of 64: 77 us.
-// - one sequence of 1,000 rows: latency, 11 us.
+// - 4 bits: instructions and the latency between them.  About 950 per 32 keys, warp and 128
+//   channels would take 44 us of issue for 64 x 8 lists of 500-6,000 rows; the twelve warps
+//   that an SM holds issue at half that rate: 82 us, 2.9 TB/s, 43%; of 4,000-48,000: 510
+//   us, 3.8 TB/s.
+// - 17 to 32 rows: the same with 8 warps to an SM, for the registers.  3 x 4 lists of
+//   60,000-131,000 rows, 28 rows, heads of 64: 84-86 us.
+// - one sequence of 1,000 rows: latency, 11-12 us.
 #include <climits>
 
 #include "attend.cuh"
@@ -60,17 +61,16 @@ constexpr int kChunk = 32;                 // keys of a warp's step
 constexpr int kStepKeys = kWarps * kChunk;
 constexpr int kSlotRows = 32;
 // Blocks per SM by their registers: 128, 168 or 255 per thread.  A head of 64 spills
-// less than its one block more gains (16 rows: 73 us with three, 81 with two, over 64 x 8
-// lists of 500-6,000 rows in 4 bits; 8 rows: 40.7 with four, 41.4 with three, over 3 x 4
-// lists of 60,000-131,000).  One of 128 does not (16 rows: 121 us with three, 109 with
-// two; in 8 bits, 32 x 8 lists, 93 and 73; 8 rows: 79 with four, 77 with three; in 8
-// bits four did not fit shared memory, and 168 registers in place of 128 took 63 to 56).
+// less than its one block more gains (64 x 8 lists of 500-6,000 rows in 4 bits: 16 rows 79
+// us with three, 85 with two; 8 rows 58 with four, 60 with three).  One of 128 does not (16
+// rows: 136 us with three, 120 with two; in 8 bits, 32 x 8 lists, 97 and 75; 8 rows: 91
+// with four, 82 with three, 90 with two; in 8 bits 70, 58 and 62).
 constexpr int per_sm_of(int groups, int nt) {
     return groups == 2 ? (nt == 1 ? 4 : nt == 2 ? 3 : 2) : nt == 1 ? 3 : 2;
 }
 // A unit costs about two steps beside its steps (us with 0, 2, 4 and 6: 64 x 8 lists of
-// 500-6,000 rows in 4 bits 77.4, 75.8, 76.9, 79.3; 32 x 8 in 8 bits 56.3, 53.9, 54.6,
-// 56.8; 12 lists of 60,000-131,000 78.7, 74.8, 73.7, 73.9).
+// 500-6,000 rows in 4 bits 83.4, 82.3, 84.1, 87.3; 32 x 8 in 8 bits 61.0, 58.9, 60.3,
+// 62.9; 12 lists of 60,000-131,000 88.3, 83.6, 82.9, 82.9).
 constexpr int kExtra = 2;
 constexpr float kLag = 4.f;                // log2 units m may lag behind
 constexpr float kTop = 20.f;               // log2 of what P has for a probability of 1

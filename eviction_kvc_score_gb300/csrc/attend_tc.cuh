@@ -14,8 +14,8 @@
 // rounded once; with two it is the same.  The second term costs half as many
 // products again, and four instructions per pair of probabilities, which in a
 // decode step one scheduler of four issues for both halves (their rows lie in the
-// same quarter of TMEM): 16.7 us against 14.5 for one sequence of 1,000 rows, 172
-// against 152 for the batch below, 2.01 ms against 1.46 for the chunk.
+// same quarter of TMEM): 16.9 us against 14.6 for one sequence of 1,000 rows, 170
+// against 153 for the batch below, 1.99 ms against 1.41 for the chunk.
 // The reference m only follows the running maximum when that has grown by more
 // than 8 (p then stays below 2^8, far from any limit of bf16 or fp32); O and l
 // are rescaled then, which after the first tiles hardly ever happens.
@@ -48,12 +48,12 @@
 // What bounds it, measured on one GB300:
 // - chunks: the MMAs of a step of two halves take 3,072 clocks (128 x 128 x 16 in
 //   64 clocks; one term: 2,048), the chain S -> softmax -> P V the rest.  4,096
-//   tokens x 32 heads behind 28,672 cached rows: 2.01 ms back to back, 1,540
-//   TFLOP/s of products or 91% of the measured sustained rate; one term 1.46.
+//   tokens x 32 heads behind 28,672 cached rows: 1.99 ms back to back, 1,550
+//   TFLOP/s of products or 91% of the measured sustained rate; one term 1.41.
 // - decode: reading the cache, and the softmax of one warp between K and V.  64
-//   sequences x 8 KV heads of 500-6,000 rows in 16-row pages, 853 MB: 172 us, 5.0
-//   TB/s or 73% of the measured copy rate; one term 152 us, 83%.
-// - short calls: latency.  One sequence of 1,000 rows: 16.7 us; one term 14.5.
+//   sequences x 8 KV heads of 500-6,000 rows in 16-row pages, 853 MB: 170 us, 5.0
+//   TB/s or 74% of the measured copy rate; one term 153 us, 82%.
+// - short calls: latency.  One sequence of 1,000 rows: 16.9 us; one term 14.6.
 //
 // Rows held in 4 or 8 bits (BITS; quant.cuh; attend_tc_quant.cu): warps 12-19 make
 // the tiles.  Warp 11 brings blocks of 16 rows to shared memory, a bulk copy each;
@@ -65,10 +65,11 @@
 // fit a tile's largest value: one seen by some tokens only took the others' bits.)
 //
 // What bounds them: the chain S -> softmax -> P V, whose softmax shares its issue slots
-// with the writing of the tiles.  A step of two halves takes 6,200 clocks where its MMAs
-// take 3,072.  4,096 tokens x 32 heads over 32,768 rows in 4 bits: 2.40 ms, 860 TFLOP/s
-// (rows in bf16: 2.01 ms); six chunks of 1-700 tokens over up to 5,700 rows in 8 bits 238
-// us, 441 TFLOP/s; one term of P, 1.81 ms and 200 us.  Warps 12-19 and not the
+// with the writing of the tiles.  A step of two halves takes 6,300 clocks where its MMAs
+// take 3,072; of some 13,400 instructions a step (44% of the issue slots) the tiles are a
+// third.  4,096 tokens x 32 heads over 32,768 rows in 4 bits: 2.47 ms, 833 TFLOP/s (rows in
+// bf16: 1.99 ms); six chunks of 1-700 tokens over up to 5,700 rows in 8 bits 239 us, 438
+// TFLOP/s; one term of P, 1.82 ms and 210 us.  Warps 12-19 and not the
 // softmax's own: a step's tiles would then stand between its softmaxes.
 #pragma once
 
@@ -111,8 +112,10 @@ constexpr int kSlotsTc = 2;
 // rows: 68 us without, 63 with 4, 62 with 8; 512 short lists: 148, 150 and 152 us).
 constexpr int kExtra = 4;
 // One over held rows of 128 about 8 (us with 4, 8 and 12: 16 chunks of up to 300 tokens
-// in 8 bits 290, 273, 277, in 4 bits 232, 222, 225, six of up to 700 211, 206, 215; of 64,
-// 32 chunks of up to 200: 146, 149, 150).
+// in 8 bits 302, 289, 296, in 4 bits 256, 252, 253, six of up to 700 234, 237, 234; of 64,
+// with 2, 4 and 8, 32 chunks of up to 200: 166, 166, 172).  Units of one tile's rows, whose
+// halves take every other key tile, would do with less (64 rows a list: 32 x 8 lists in 8
+// bits 194, 222, 235, 64 x 8 in 4 bits 312, 317, 319).
 constexpr int kExtraHeld = 8;
 constexpr int kDirect = 4;              // shares that are joined from registers
 constexpr int kQueue = 4;               // segments on their way from the walk to the roles

@@ -15,7 +15,7 @@
 //
 // V's is in bf16, whose exponents are fp32's, so that no value is too large or too small
 // beside another one: a code as it stands is n 2^-133 or n 2^-129 there, and one
-// multiplication and sum makes it (n - z) 2^-6, exactly; a value of 0 is 0 in the product.
+// multiplication and sum makes it (n - z) 2^-20, exactly; a value of 0 is 0 in the product.
 // What a row's probability times the group's step is rounded to is two bf16 numbers,
 // 2^-17 of it away at most, as the tensor cores' other kernels have it.  (One fp16 number
 // instead, steps over the list's largest and the zero codes' share in a product of its own:
@@ -29,8 +29,9 @@
 // are channels.  Key i of a block stands in row pi(i) of both products: pi(2 c) = c,
 // pi(2 c + 1) = 4 + (c ^ 1), for fewer bank conflicts.
 //
-// P: 2^20 for a probability of 1 (the running maximum may lag behind by 2^4), so that
-// rows whose values are near the type's smallest keep the bits of small probabilities.
+// P: 2^24 for a probability of 1 (the running maximum may lag behind by 2^4), so that
+// rows whose values are near the type's smallest keep the bits of small probabilities; with
+// the values' 2^-20 the sums stand 2^4 above the outputs, and values of 2^100 fit them.
 //
 // Every warp walks 32 keys of each step of 128 by itself, with a ring of its own that
 // bulk copies fill (a block of K or V of 16 rows each); the warps' results meet in
@@ -73,7 +74,7 @@ constexpr int per_sm_of(int groups, int nt) {
 // 62.9; 12 lists of 60,000-131,000 88.3, 83.6, 82.9, 82.9).
 constexpr int kExtra = 2;
 constexpr float kLag = 4.f;                // log2 units m may lag behind
-constexpr float kTop = 20.f;               // log2 of what P has for a probability of 1
+constexpr float kTop = 24.f;               // log2 of what P has for a probability of 1
 
 // Ring slots of a warp.
 constexpr int slots_of(int bits, int groups) { return bits == 4 && groups == 2 ? 4 : 2; }
@@ -191,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, per_sm_of(G, NT)) attend_quant_kerne
     uint8_t *mine = ring + warp * kSlots * slot_bytes(BITS, G);
     float2 *k_steps = reinterpret_cast<float2 *>(scratch_all + warp * scratch_bytes(G));   // [key][G]: s, -s z
     uint32_t *steps = reinterpret_cast<uint32_t *>(k_steps + kChunk * G);                    // V: [pair of keys][G]
-    uint32_t *zeros = steps + kChunk / 2 * G;                                                // the same of -z 2^-6
+    uint32_t *zeros = steps + kChunk / 2 * G;                                                // the same of -z 2^-20
     volatile int *stop = &s.stop;
     const int key_of[2] = {(r8 & 1) ? 4 + (r8 >> 1 ^ 1) : r8 >> 1, 8 + ((r8 & 1) ? 4 + (r8 >> 1 ^ 1) : r8 >> 1)};   // of rows r8, r8 + 8
     // the lane's own key of the 32, and its half of its pair's word
@@ -392,8 +393,8 @@ __global__ void __launch_bounds__(kThreads, per_sm_of(G, NT)) attend_quant_kerne
                     const uint32_t none = (vs & 0x7f807f80u) + 0x00800080u & 0x80008000u;   // exponents of ones only
                     nan |= none;
                     vs &= ~((none >> 15) * 0xffffu);   // added below
-                    // -z 2^-6: a whole number below 256 is that number times 2^-133 as bf16
-                    const uint32_t vz = mul_bf16x2(vw[i] & (BITS == 4 ? 0x000f000fu : 0x00ff00ffu), 0xff00ff00u);
+                    // -z 2^-20: a whole number below 256 is that number times 2^-133 as bf16
+                    const uint32_t vz = mul_bf16x2(vw[i] & (BITS == 4 ? 0x000f000fu : 0x00ff00ffu), 0xf800f800u);
                     uint16_t *s16 = reinterpret_cast<uint16_t *>(steps) + (my_pair * G + 2 * i) * 2 + my_half;
                     uint16_t *z16 = reinterpret_cast<uint16_t *>(zeros) + (my_pair * G + 2 * i) * 2 + my_half;
                     s16[0] = (uint16_t)vs;
@@ -577,10 +578,10 @@ __global__ void __launch_bounds__(kThreads, per_sm_of(G, NT)) attend_quant_kerne
                         pick<8>(__byte_perm(code[0][g], code[1][g], 0x5410), __byte_perm(code[0][g], code[1][g], 0x7632), e0);
                         pick<8>(__byte_perm(code[2][g], code[3][g], 0x5410), __byte_perm(code[2][g], code[3][g], 0x7632), e1);
                     }
-                    // (n - z) 2^-6: as bf16 numbers codes are at 2^-133, those in bits 4-7 at 2^-129
+                    // (n - z) 2^-20: as bf16 numbers codes are at 2^-133, those in bits 4-7 at 2^-129
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        constexpr uint32_t kUp = 0x7f007f00u, kUp4 = 0x7d007d00u;   // 2^127, 2^123
+                        constexpr uint32_t kUp = 0x78007800u, kUp4 = 0x76007600u;   // 2^113, 2^109
                         e0[i] = fma_bf16x2(e0[i], BITS == 4 && (i & 1) ? kUp4 : kUp, sz[0][g]);
                         e1[i] = fma_bf16x2(e1[i], BITS == 4 && (i & 1) ? kUp4 : kUp, sz[1][g]);
                     }
@@ -640,14 +641,14 @@ __global__ void __launch_bounds__(kThreads, per_sm_of(G, NT)) attend_quant_kerne
                 float sum = l[nt][e];
 #pragma unroll
                 for (int d = 4; d <= 16; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-                if (r8 == 0) s.stat[warp][2 * c + e] = make_float2(m[nt][e] * up, sum * 0x1p-20f);
+                if (r8 == 0) s.stat[warp][2 * c + e] = make_float2(m[nt][e] * up, sum * 0x1p-24f);
                 float *dst = s_out + (warp * 8 + 2 * c + e) * kOutRow;
 #pragma unroll
                 for (int g = 0; g < G; ++g) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int ch = BITS == 4 ? 8 * (r8 >> 1) + 2 * i + (r8 & 1) : 4 * r8 + i;
-                        dst[32 * g + ch] = o[nt][2 * g + (i >> 1)][2 * (i & 1) + e] * 0x1p-14f;
+                        dst[32 * g + ch] = o[nt][2 * g + (i >> 1)][2 * (i & 1) + e] * 0x1p-4f;
                     }
                 }
             }

@@ -186,3 +186,46 @@ def test_huge_queries_leave_the_others_alone(odd, d, n, bits):
         others = torch.ones(c.lse.shape, dtype=torch.bool)
         others[0, 2] = False
         assert torch.equal(c.out[others], out[others]) and torch.equal(c.lse[others], lse[others])
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("i", range(len(FORMS)))
+@pytest.mark.parametrize("power", [100, -100])
+def test_largest_and_smallest_values(power, i, dtype, bits):
+    """Values up to 2^100, which sums over the longest lists may not pass, all of one sign so that they add up; and
+    values of 2^-100."""
+    def change(k, v):
+        for x, y in zip(k, v):
+            x.mul_(0.01)
+            y.copy_((torch.rand_like(y.float()) * 0.5 + 0.5).clamp(max=0.99) * 2.0 ** power)
+    c = Case(**FORMS[i], dtype=dtype, bits=bits, seed=i, change=change).run()
+    c.check()
+    want = ref.attend(c.q, c.start, c.k, c.v, c.scale, bits)["out"]
+    assert want.abs().max() > 2.0 ** (power - 1) and ref.near(c.out, want) is None
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("dtype,d,n", [("bf16", 64, 1), ("bf16", 128, 8), ("f32", 64, 1), ("bf16", 80, 1)])
+def test_large_values_of_lists_that_one_block_adds_up(dtype, d, n, bits):
+    """So many lists that a list is one block's, of 131,072 rows each with values of up to 2^100, alike and all of them seen
+    alike: the outputs are their mean.  (All lists are the same pages.)"""
+    lists, rows = 600, 131072
+
+    def change(k, v):
+        k[0].zero_()
+        v[0].copy_((torch.rand_like(v[0].float()) * 0.5 + 0.5).clamp(max=0.99) * 2.0 ** 100)
+    c = Case(ns=[n], lens=[rows], hq=1, h=1, d=d, ps=128, dtype=dtype, bits=bits, change=change)
+    kvc = K()
+    q = c.q.repeat(lists, 1, 1)
+    q_start = torch.arange(lists + 1, dtype=torch.int32, device="cuda") * n
+    ws = torch.empty(kvc.kvc_attend_quant_workspace_size(c.c, bits, 1, 1, lists, n), dtype=torch.uint8, device="cuda")
+    kvc.kvc_workspace_init(ws)
+    out = torch.full_like(q, 7.0)
+    kvc.kvc_attend_quant(c.c, bits, q, q_start, c.table.repeat(lists, 1), c.len.repeat(lists), c.kp, c.vp, n, out, ws)
+    torch.cuda.synchronize()
+    assert kvc.kvc_workspace_status(ws) == 0
+    v = ref.stands(c.v[0], bits).cumsum(0)
+    want = torch.stack([v[rows - n + t] / (rows - n + t + 1) for t in range(n)])[:, None].repeat(lists, 1, 1)
+    # T positive terms, added up by 128 or more partial sums; the output rounded once
+    assert ((out.double() - want).abs() <= want * (2 * (rows / 128 + 64) * 2.0 ** -24 + torch.finfo(out.dtype).eps / 2)).all()

@@ -65,8 +65,8 @@
 // fit a tile's largest value: one seen by some tokens only took the others' bits.)
 //
 // What bounds them: the chain S -> softmax -> P V, whose softmax shares its issue slots
-// with the writing of the tiles.  A step of two halves takes 6,300 clocks where its MMAs
-// take 3,072; of some 13,400 instructions a step (44% of the issue slots) the tiles are a
+// with the writing of the tiles.  A step of two halves takes 6,300 clocks, twice what its
+// MMAs take; of some 13,400 instructions a step (44% of the issue slots) the tiles are a
 // third.  4,096 tokens x 32 heads over 32,768 rows in 4 bits: 2.47 ms, 833 TFLOP/s (rows in
 // bf16: 1.99 ms); six chunks of 1-700 tokens over up to 5,700 rows in 8 bits 239 us, 438
 // TFLOP/s; one term of P, 1.82 ms and 210 us.  Warps 12-19 and not the
